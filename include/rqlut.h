@@ -410,6 +410,89 @@ RQ_API int rq_prepare_rot10(const uint16_t *codes_u16, rq_dims d, uint8_t *out,
                             uint64_t *stats, void *stream);
 
 /*
+ * Losses of the RQ-coded head and their gradients, without its logits being
+ * kept (training and scoring; the pages train and score the compressed head
+ * but state no calls for it, so these are the plain readings).  With
+ * y[n][v] = softcap(<h_n, E_v>) as in rq_lut_logits, T the temperature (1 for
+ * cross entropy):
+ *   lse[n]  = log sum_v exp(y[n][v] / T)
+ *   rq_xent     loss[n] = lse[n] - y[n][target[n]]
+ *   rq_distill  q[n][j] = softmax over the row's listed entries of
+ *               teacher_val[n][j] / T,
+ *               loss[n] = T^2 sum_j q[n][j] (log q[n][j]
+ *                         - y[n][teacher_idx[n][j]] / T + lse[n])
+ * and for an upstream gradient weight[n] of loss[n] (NULL: all 1)
+ *   dy[n][v] = weight[n] T (exp(y[n][v] / T - lse[n]) - q_n(v)),
+ *   dz = dy (1 - (y / softcap)^2)   (dz = dy with the softcap off),
+ *   dh[n] = sum_v dz[n][v] E_v,
+ *   dC[m][l][k] = sum of dE_v, subspace m, over the rows v whose code (m, l)
+ *                 is k, with dE_v = sum_n dz[n][v] h_n.
+ * q_n(v) is 1 at the target, or the sum of the q[n][j] listed for v (an id
+ * may be listed twice).  An id below 0 stands for none (padding, masked
+ * tokens, short lists), so does a teacher's logit of -inf; an id >= V is
+ * taken for none and sets RQ_DEVERR_BAD_ID.  A row with no entry left has
+ * loss 0 and no gradient; its lse is written all the same.  Hidden states,
+ * codebooks, weights and teacher's logits are finite otherwise (a NaN gives
+ * NaN in the rows it reaches).
+ *   h       (device) [N][D]: float, or bf16 bit patterns with h_bf16 = 1
+ *   C, codes, fmt, d, softcap: as for rq_logits_from_hidden, every layout
+ *   target  (device) int32 [N]; teacher_val (device) float [N][k] and
+ *           teacher_idx (device) int32 [N][k], e.g. of rq_topk_sample,
+ *           1 <= k <= min(V, 1024), in any order
+ *   loss, lse (device) float [N]; the gradients take the lse that the loss
+ *           call wrote for the same inputs
+ *   dh      (device) [N][D] in h's type, or NULL; dC (device) float
+ *           [M][L][K][ds], or NULL; at least one of the two.  Both are
+ *           overwritten and must not overlap an input.
+ *   index   (device) as written by rq_prepare_grad for the codes
+ *   ws      (device) >= rq_loss_workspace_bytes(d, N, fmt, k, grad) bytes,
+ *           256-byte aligned, contents need no initialisation (k = 1 for
+ *           cross entropy; grad = 1: enough for the gradient and the loss)
+ * Precision: losses, statistics and sums are fp32; for more than a few tokens
+ * the products run on the tensor cores on fp16 hi / lo splits with
+ * power-of-two scales (about 2^-22 per product).  dC and, for float h, dh
+ * carry fp32 accuracy; a bf16 dh is rounded once.  Sums run in a fixed order:
+ * the same call gives the same bits.
+ * Errors: RQ_ERR_INVALID_ARGUMENT (null pointer, N < 1, k, T or h_bf16 out of
+ * range, bad dims or format), RQ_ERR_UNSUPPORTED (the format cannot hold the
+ * shape, k > 1024; gradients: K > 4096), RQ_ERR_MISALIGNED,
+ * RQ_ERR_WORKSPACE_TOO_SMALL, RQ_ERR_CUDA.
+ */
+RQ_API size_t rq_loss_workspace_bytes(rq_dims d, int N, int fmt, int k, int grad);
+RQ_API int rq_xent(const void *h, int h_bf16, const float *C, const void *codes, int fmt,
+                   rq_dims d, int N, float softcap, const int32_t *target, float *loss,
+                   float *lse, void *ws, size_t ws_bytes, void *stream);
+RQ_API int rq_xent_grad(const void *h, int h_bf16, const float *C, const void *codes, int fmt,
+                        rq_dims d, int N, float softcap, const int32_t *target,
+                        const float *lse, const float *weight, const void *index, void *dh,
+                        float *dC, void *ws, size_t ws_bytes, void *stream);
+RQ_API int rq_distill(const void *h, int h_bf16, const float *C, const void *codes, int fmt,
+                      rq_dims d, int N, float softcap, const float *teacher_val,
+                      const int32_t *teacher_idx, int k, float temperature, float *loss,
+                      float *lse, void *ws, size_t ws_bytes, void *stream);
+RQ_API int rq_distill_grad(const void *h, int h_bf16, const float *C, const void *codes, int fmt,
+                           rq_dims d, int N, float softcap, const float *teacher_val,
+                           const int32_t *teacher_idx, int k, float temperature,
+                           const float *lse, const float *weight, const void *index, void *dh,
+                           float *dC, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * rq_prepare_grad -- the rows of the vocabulary ordered by code, per column of
+ * the code matrix, which the gradients above sum by.  A layout of this
+ * library; run once per artifact (the codes stay fixed while codebooks and
+ * hidden states train).
+ *   codes (device) in format fmt, 16-byte aligned; index (device)
+ *   rq_grad_index_bytes(d) bytes (about 2 bytes per code plus 4 K per 8192
+ *   rows and column), 16-byte aligned, not overlapping codes.  An index holds
+ *   for every layout of the same codes.
+ * Supported: K <= 4096 (rq_grad_index_bytes is 0 above).
+ * Errors: RQ_ERR_INVALID_ARGUMENT, RQ_ERR_UNSUPPORTED, RQ_ERR_MISALIGNED,
+ * RQ_ERR_CUDA.
+ */
+RQ_API size_t rq_grad_index_bytes(rq_dims d);
+RQ_API int rq_prepare_grad(const void *codes, int fmt, rq_dims d, void *index, void *stream);
+
+/*
  * Greedy pick over a vocabulary split across ranks ("Gemma-2 runtime
  * compression: NF4 + LUT serving", LUT section: argmax of the softcapped
  * logits of every vocabulary row; rows are independent, so rank g may hold

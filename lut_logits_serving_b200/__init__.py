@@ -13,6 +13,10 @@ names:
   (``rq_logits_from_hidden_path`` picks tables, FP32 or tensor cores)
 * ``rq_decode_rows`` -- bf16 input rows rebuilt on demand
 * ``rq_pack10`` -- uint16 codes -> 10-bit packed rows
+* ``rq_xent``, ``rq_distill`` -- cross entropy and distillation from a
+  teacher's top logits on the head, without keeping its logits;
+  ``rq_xent_grad``, ``rq_distill_grad`` -- their gradients with respect to
+  the hidden states and the codebooks (``rq_prepare_grad`` once per artifact)
 * ``rq_prepare_sched``, ``rq_prepare_rot10`` -- the batch-1 layouts of
   uint16 and 10-bit codes (bank-scheduled, rotated slices)
 
@@ -35,7 +39,8 @@ __all__ = [
     "rq_pack10", "rq_device_error", "rq_set_profile_events", "rq_lut_logits_static",
     "rq_greedy_step", "rq_encode", "rq_topk_workspace_bytes", "rq_topk_sample",
     "rq_last_cuda_error", "rq_cuda_error_name", "PATH_AUTO", "PATH_TABLES", "PATH_DECODE_FP32",
-    "PATH_DECODE_TC", "rq_argmax_candidates", "rq_argmax_merge", "shard_rows", "rq_sharded_logits",
+    "PATH_DECODE_TC", "rq_loss_workspace_bytes", "rq_xent", "rq_xent_grad", "rq_distill",
+    "rq_distill_grad", "rq_grad_index_bytes", "rq_prepare_grad", "rq_argmax_candidates", "rq_argmax_merge", "shard_rows", "rq_sharded_logits",
 ]
 
 U16 = 0
@@ -109,6 +114,15 @@ _SIGNATURES = {
     "rq_prepare_rot10": (_i, [_p, RqDims, _p, _p, _p]),
     "rq_lut_logits_static": (_i, [_p, _i, RqDims, _p, _i, _f, _p, _p, _p]),
     "rq_greedy_step": (_i, [_p, _p, _p, _i, RqDims, _i, _f, _p, _p, _f, _p, _p, _sz, _p]),
+    "rq_loss_workspace_bytes": (_sz, [RqDims, _i, _i, _i, _i]),
+    "rq_xent": (_i, [_p, _i, _p, _p, _i, RqDims, _i, _f, _p, _p, _p, _p, _sz, _p]),
+    "rq_xent_grad": (_i, [_p, _i, _p, _p, _i, RqDims, _i, _f, _p, _p, _p, _p, _p, _p, _p, _sz,
+                          _p]),
+    "rq_distill": (_i, [_p, _i, _p, _p, _i, RqDims, _i, _f, _p, _p, _i, _f, _p, _p, _p, _sz, _p]),
+    "rq_distill_grad": (_i, [_p, _i, _p, _p, _i, RqDims, _i, _f, _p, _p, _i, _f, _p, _p, _p, _p,
+                             _p, _p, _sz, _p]),
+    "rq_grad_index_bytes": (_sz, [RqDims]),
+    "rq_prepare_grad": (_i, [_p, _i, RqDims, _p, _p]),
     "rq_argmax_candidates": (_i, [_p, _p, _i, _i64, _i64, _p, _p, _p]),
     "rq_argmax_merge": (_i, [_p, _p, _i, _i, _p, _p]),
 }
@@ -460,6 +474,155 @@ def rq_pack8(codes_u16, d: RqDims, out=None, stream=None):
         _cuda(codes_u16, torch.uint16, "codes_u16", rq_codes_bytes(d, U16)), d,
         _cuda(out, torch.uint8, "packed", rq_codes_bytes(d, U8)), _stream(stream)))
     return out
+
+
+# ------------------------------------------------------------ losses
+
+def rq_loss_workspace_bytes(d: RqDims, N: int, fmt: int, k: int = 1, grad: bool = False) -> int:
+    """Workspace of a loss on N tokens (and, with grad, of its gradient);
+    k entries per teacher's list (0 or 1 for cross entropy)."""
+    return int(lib().rq_loss_workspace_bytes(d, N, fmt, k, int(bool(grad))))
+
+
+def rq_grad_index_bytes(d: RqDims) -> int:
+    return int(lib().rq_grad_index_bytes(d))
+
+
+@contextlib.contextmanager
+def _on(stream, like, *others):
+    """Current device and stream of a call on `like`: every tensor of it lives
+    on one device, and what the call allocates belongs to its stream."""
+    torch = _torch()
+    for t in others:
+        if t is not None and t.device != like.device:
+            raise ValueError(f"tensors on {t.device} and {like.device}: one device expected")
+    if not like.is_cuda:          # a CPU tensor is refused by name below
+        yield stream
+        return
+    with torch.cuda.device(like.device):
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            yield torch.cuda.current_stream()
+
+
+def _hidden(h, d):
+    """(pointer, bf16 flag, N) of hidden states [N, D] float32 or bfloat16."""
+    torch = _torch()
+    if h.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"h: dtype {h.dtype}, expected float32 or bfloat16")
+    N = _tokens(h, d)
+    return _cuda(h, h.dtype, "h"), int(h.dtype == torch.bfloat16), N
+
+
+def _lists(val, idx, N):
+    """k of a teacher's lists [N, k]."""
+    if idx.dim() != 2 or idx.shape[0] != N or tuple(val.shape) != tuple(idx.shape):
+        raise ValueError(f"teacher_val, teacher_idx: [{N}, k] expected")
+    return idx.shape[1]
+
+
+def _run_loss(fn, h, C, codes, fmt, d, extra, k, tensors, softcap, loss, lse, ws, stream):
+    torch = _torch()
+    with _on(stream, h, C, codes, loss, lse, ws, *tensors) as s:
+        hp, hb, N = _hidden(h, d)
+        if loss is None:
+            loss = _empty((N,), torch.float32, h)
+        if lse is None:
+            lse = _empty((N,), torch.float32, h)
+        wp, wn, ws = _workspace(rq_loss_workspace_bytes(d, N, fmt, k), h, ws)
+        _check(fn, getattr(lib(), fn)(
+            hp, hb, _cuda(C, torch.float32, "C", _book_bytes(d)),
+            _cuda(codes, _codes_dtype(fmt), "codes", rq_codes_bytes(d, fmt)), fmt, d, N,
+            float(softcap), *extra(N), _cuda(loss, torch.float32, "loss", N * 4),
+            _cuda(lse, torch.float32, "lse", N * 4), wp, wn, _stream(s)))
+    return loss, lse, ws
+
+
+def _run_grad(fn, h, C, codes, fmt, d, extra, k, tensors, lse, index, weight, softcap, want_dh,
+              want_dC, dh, dC, ws, stream):
+    torch = _torch()
+    with _on(stream, h, C, codes, lse, index, weight, dh, dC, ws, *tensors) as s:
+        hp, hb, N = _hidden(h, d)
+        if want_dh and dh is None:
+            dh = _empty((N, d.D), h.dtype, h)
+        if want_dC and dC is None:
+            dC = _empty((d.M, d.L, d.K, d.D // d.M), torch.float32, h)
+        wp, wn, ws = _workspace(rq_loss_workspace_bytes(d, N, fmt, k, True), h, ws)
+        _check(fn, getattr(lib(), fn)(
+            hp, hb, _cuda(C, torch.float32, "C", _book_bytes(d)),
+            _cuda(codes, _codes_dtype(fmt), "codes", rq_codes_bytes(d, fmt)), fmt, d, N,
+            float(softcap), *extra(N), _cuda(lse, torch.float32, "lse", N * 4),
+            _ptr_or_null(weight, torch.float32, "weight", N * 4),
+            _cuda(index, torch.uint8, "index", rq_grad_index_bytes(d)),
+            _ptr_or_null(dh, h.dtype, "dh", N * d.D * h.element_size()),
+            _ptr_or_null(dC, torch.float32, "dC", _book_bytes(d)), wp, wn, _stream(s)))
+    return dh, dC, ws
+
+
+def rq_prepare_grad(codes, fmt: int, d: RqDims, out=None, stream=None):
+    """Codes in any layout -> the index uint8 [rq_grad_index_bytes(d)] that
+    the gradients of the losses sum the vocabulary's rows by."""
+    torch = _torch()
+    with _on(stream, codes, out) as s:
+        nbytes = rq_grad_index_bytes(d)
+        if out is None:
+            out = _empty((nbytes,), torch.uint8, codes)
+        _check("rq_prepare_grad", lib().rq_prepare_grad(
+            _cuda(codes, _codes_dtype(fmt), "codes", rq_codes_bytes(d, fmt)), fmt, d,
+            _cuda(out, torch.uint8, "index", nbytes), _stream(s)))
+    return out
+
+
+def rq_xent(h, C, codes, fmt: int, d: RqDims, target, softcap: float = 30.0, loss=None, lse=None,
+            ws=None, stream=None):
+    """Softmax cross entropy of the head against target ids int32 [N] (below
+    0: none, loss 0), h [N, D] float32 or bfloat16.  Returns (loss float32
+    [N], lse float32 [N], ws)."""
+    torch = _torch()
+    return _run_loss("rq_xent", h, C, codes, fmt, d,
+                     lambda N: (_cuda(target, torch.int32, "target", N * 4),), 1, (target,),
+                     softcap, loss, lse, ws, stream)
+
+
+def rq_xent_grad(h, C, codes, fmt: int, d: RqDims, target, lse, index, weight=None,
+                 softcap: float = 30.0, want_dh: bool = True, want_dC: bool = True, dh=None,
+                 dC=None, ws=None, stream=None):
+    """Gradient of sum_n weight[n] loss[n] of rq_xent (weight float32 [N],
+    None: all 1), from its lse and rq_prepare_grad's index.  Returns (dh [N, D]
+    in h's type or None, dC float32 [M, L, K, ds] or None, ws)."""
+    torch = _torch()
+    return _run_grad("rq_xent_grad", h, C, codes, fmt, d,
+                     lambda N: (_cuda(target, torch.int32, "target", N * 4),), 1, (target,), lse,
+                     index, weight, softcap, want_dh, want_dC, dh, dC, ws, stream)
+
+
+def rq_distill(h, C, codes, fmt: int, d: RqDims, teacher_val, teacher_idx,
+               temperature: float = 1.0, softcap: float = 30.0, loss=None, lse=None, ws=None,
+               stream=None):
+    """Distillation from a teacher's top logits float32 [N, k] at ids int32
+    [N, k] (below 0: none), as rq_topk_sample returns them.  Returns (loss
+    float32 [N], lse float32 [N] at the temperature, ws)."""
+    torch = _torch()
+    k = _lists(teacher_val, teacher_idx, _tokens(h, d))
+    return _run_loss("rq_distill", h, C, codes, fmt, d,
+                     lambda N: (_cuda(teacher_val, torch.float32, "teacher_val"),
+                                _cuda(teacher_idx, torch.int32, "teacher_idx"), k,
+                                float(temperature)),
+                     k, (teacher_val, teacher_idx), softcap, loss, lse, ws, stream)
+
+
+def rq_distill_grad(h, C, codes, fmt: int, d: RqDims, teacher_val, teacher_idx, lse, index,
+                    weight=None, temperature: float = 1.0, softcap: float = 30.0,
+                    want_dh: bool = True, want_dC: bool = True, dh=None, dC=None, ws=None,
+                    stream=None):
+    """Gradient of sum_n weight[n] loss[n] of rq_distill; see rq_xent_grad."""
+    torch = _torch()
+    k = _lists(teacher_val, teacher_idx, _tokens(h, d))
+    return _run_grad("rq_distill_grad", h, C, codes, fmt, d,
+                     lambda N: (_cuda(teacher_val, torch.float32, "teacher_val"),
+                                _cuda(teacher_idx, torch.int32, "teacher_idx"), k,
+                                float(temperature)),
+                     k, (teacher_val, teacher_idx), lse, index, weight, softcap, want_dh, want_dC,
+                     dh, dC, ws, stream)
 
 
 def rq_device_error(clear: bool = True) -> int:

@@ -1,0 +1,205 @@
+// loss_common.cuh -- shared by the loss kernels (cross entropy and
+// distillation on the RQ-coded head, and their gradients).  Not part of the
+// public ABI.
+#pragma once
+
+#include <cfloat>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "rq_common.cuh"
+
+namespace rq {
+
+// Rows of the vocabulary that one block of the gradient index covers: their
+// local numbers fit 16 bits, and 6 floats of each fit shared memory.
+constexpr int kGradRows = 8192;
+
+// Code p of row v in any layout, safe for codes >= K (see CodeFix).
+struct CodeSrc {
+  const void *codes;
+  int fmt;
+  int64_t V;
+  int P, K;
+  CodeFix fix;
+  __device__ __forceinline__ uint32_t operator()(int64_t v, int p) const {
+    uint32_t c;
+    if (fmt == RQ_CODES_U16) c = __ldg(static_cast<const uint16_t *>(codes) + v * P + p);
+    else if (fmt == RQ_CODES_U8) c = __ldg(static_cast<const uint8_t *>(codes) + v * P + p);
+    else if (fmt == RQ_CODES_SCHED)
+      c = sched_code(static_cast<const uint16_t *>(codes), V, v, p, sched_shift(K));
+    else if (fmt == RQ_CODES_PACKED10_ROT)
+      c = rot10_code(static_cast<const uint8_t *>(codes), V, P, v, p);
+    else
+      c = packed10_code(static_cast<const uint8_t *>(codes) + v * ((10LL * P + 7) / 8), p);
+    return fix(c);
+  }
+};
+
+// ------------------------------------------------------------- fp16 splits
+//
+// An fp32 operand x of the tensor-core products is scaled by a power of two s
+// (exact) with |x| s <= 2^14 and split into hi = fp16_rn(x s) and lo =
+// fp16_rn(x s - hi): x s = hi + lo within 2^-22 |x s| as long as lo stays a
+// normal number, and within 2^-25 absolutely below that, 2^-39 of the
+// largest element.  a b = a_hi b_hi + a_lo b_hi + a_hi b_lo + (dropped
+// a_lo b_lo, 2^-22 |a b|).
+
+// Largest magnitudes found by loss_amax_kernel: kAmaxBlocks partial maxima
+// each of |h|, of |C| and of |weight|.
+constexpr int kAmaxBlocks = 64;
+enum { kAmaxH = 0, kAmaxC = 1, kAmaxW = 2 };
+
+// Largest power of two s (clamped to 2^-60 .. 2^60) with bound s < 2^14; 1 for
+// a bound that is zero, infinite or NaN.
+__device__ __forceinline__ float pow2_scale(float bound) {
+  if (!(bound > 0.f) || !(bound <= FLT_MAX)) return 1.f;
+  int e;
+  frexpf(bound, &e);
+  int k = 14 - e;
+  k = k < -60 ? -60 : (k > 60 ? 60 : k);
+  return ldexpf(1.f, k);
+}
+
+// Maximum of the kAmaxBlocks partials of kind `which`; a whole warp calls it.
+__device__ __forceinline__ float warp_amax(const float *amax, int which) {
+  const int lane = threadIdx.x & 31;
+  float m = 0.f;
+  for (int i = lane; i < kAmaxBlocks; i += 32) m = fmaxf(m, amax[which * kAmaxBlocks + i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+// The scales of the three operands: hidden states, decoded rows (a sum of L
+// codewords), gradients of the logits (|w| T times a difference of two
+// probabilities).
+__device__ __forceinline__ float scale_h(const float *amax) {
+  return pow2_scale(warp_amax(amax, kAmaxH));
+}
+__device__ __forceinline__ float scale_e(const float *amax, int L) {
+  return pow2_scale(warp_amax(amax, kAmaxC) * (float)L);
+}
+__device__ __forceinline__ float scale_z(const float *amax, float T) {
+  return pow2_scale(warp_amax(amax, kAmaxW) * T);
+}
+
+__device__ __forceinline__ void split_f16(float x, __half &hi, __half &lo) {
+  hi = __float2half_rn(x);
+  lo = __float2half_rn(__fsub_rn(x, __half2float(hi)));
+}
+
+__device__ __forceinline__ float load_h(const void *h, int bf16, int64_t i) {
+  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(h)[i])
+              : static_cast<const float *>(h)[i];
+}
+
+// ------------------------------------------------------------- launchers
+
+// Tensor-core products of the loss kernels (loss_gemm.cu).
+enum LossGemm {
+  kGemmStats = 0,   // y = softcap(h E^T): per (row, 128 columns) max and sum of exp(y / T)
+  kGemmGrad = 1,    // y again, gradients of the logits as fp16 hi / lo planes
+  kGemmDh = 2,      // dz E, fp32, split over the vocabulary
+  kGemmDw = 3       // (h^T dz), fp32 [D][rows]
+};
+
+struct GemmPlanes {          // row-major fp16 planes; lo may be null
+  const void *hi, *lo;
+  int64_t rows, cols, pitch; // extents and row pitch in elements (pitch % 8 == 0)
+};
+
+struct GemmArgs {
+  int m_tiles, n_tiles, splits, kblocks;
+  int a_planes, b_planes, chain, stages;
+  int rows, cols;            // output extents
+  // scales
+  const float *amax;
+  int L;
+  // epilogues
+  float inv_cap, cap, beta, T;
+  float2 *stat;              // [parts][stat_ld] (max, sum)
+  int stat_ld;
+  int stat_part0;            // first part of this launch
+  const float *lse, *f;      // per row: log-sum-exp, w T (0: no gradient)
+  __half *dz_hi, *dz_lo;
+  int64_t dz_pitch;
+  float *out;                // fp32 output
+  int64_t out_pitch, out_split;   // row pitch; stride between splits
+  int accumulate;
+  unsigned *err;
+};
+
+cudaError_t launch_loss_gemm(int mode, const GemmPlanes &A, const GemmPlanes &B, GemmArgs a,
+                             const DevInfo &di, cudaStream_t s);
+
+// Rows of a piece decoded into fp16 hi / lo planes and the other row-wise
+// kernels (loss_rows.cu).
+cudaError_t launch_loss_amax(const void *h, int bf16, int64_t nh, const float *C, int64_t nc,
+                             const float *w, int64_t nw, float *amax, cudaStream_t s);
+cudaError_t launch_loss_split_h(const void *h, int bf16, int64_t N, int D, int64_t pitch,
+                                const float *amax, __half *hi, __half *lo, cudaStream_t s);
+cudaError_t launch_loss_widen_h(const void *h, int64_t n, float *out, cudaStream_t s);
+cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, int ds, int64_t v0,
+                               int64_t rows, int64_t pitch, const float *amax, __half *hi,
+                               __half *lo, const DevInfo &di, cudaStream_t s);
+// y[n][j] = softcapped logit of id[n][j] (0 where id < 0 or >= V)
+cudaError_t launch_loss_pick(const void *h, int bf16, const CodeSrc &cs, const float *C, int D,
+                             int M, int L, const int32_t *id, int64_t N, int k, float cap,
+                             float *y, cudaStream_t s);
+// (max, sum) parts of logits [N][V] at 1 / T = beta
+int loss_stat_parts(int64_t V);
+cudaError_t launch_loss_logit_stats(const float *logits, int64_t N, int64_t V, float beta,
+                                    float2 *stat, int stat_ld, cudaStream_t s);
+
+// The sparse probabilities of a loss: target ids (k = 1, val null) or a
+// teacher's lists.
+struct LossTargets {
+  const int32_t *id;     // [N][k]
+  const float *val;      // [N][k] or null
+  int k;
+  float T, beta;
+};
+// lse and loss from the parts and the picked logits: y[n * k + j], or, with
+// y_is_logits, y[n * V + id].
+cudaError_t launch_loss_finish(const float2 *stat, int parts, int stat_ld, int64_t N, int64_t V,
+                               const LossTargets &t, const float *y, bool y_is_logits, float *loss,
+                               float *lse, unsigned *err, cudaStream_t s);
+// q, merged ids and f = w T (0 for rows without a target)
+cudaError_t launch_loss_sparse(const LossTargets &t, int64_t N, int64_t V, const float *w,
+                               int32_t *sid, float *sq, float *f, unsigned *err, cudaStream_t s);
+// dz planes at the listed ids of rows [v0, v0 + rows)
+cudaError_t launch_loss_fix_planes(const int32_t *sid, const float *sq, const float *y, int k,
+                                   int64_t N, int64_t v0, int64_t rows, const float *lse,
+                                   const float *f, const float *amax, float T, float beta,
+                                   float cap, __half *hi, __half *lo, int64_t pitch,
+                                   cudaStream_t s);
+// logits [N][V] -> gradients in groups of W tokens, [ceil(N / W)][V][W], with
+// the listed ids' corrections
+cudaError_t launch_loss_dz_small(const float *logits, int64_t N, int64_t V, const int32_t *sid,
+                                 const float *sq, int k, const float *lse, const float *f,
+                                 float beta, float cap, int W, float *dz, cudaStream_t s);
+cudaError_t launch_loss_dh_sum(const float *part, int splits, int64_t stride, int64_t pitch,
+                               int64_t N, int D, int bf16, void *dh, cudaStream_t s);
+
+// Rows by code (loss_codebook.cu).
+size_t grad_index_bytes(int64_t V, int P, int K);
+cudaError_t launch_prepare_grad(const CodeSrc &cs, void *index, const DevInfo &di, cudaStream_t s);
+// dC (+)= the columns of dwt [D][pitch] (rows v0 .. v0 + rows of the
+// vocabulary, v0 % kGradRows == 0) summed by code
+cudaError_t launch_codebook_rows(const float *dwt, int64_t pitch, int64_t v0, int64_t rows,
+                                 const void *index, int64_t V, int M, int L, int K, int ds,
+                                 bool accumulate, float *dC, const DevInfo &di, cudaStream_t s);
+// S[split][p][k][W] = sums of dz [V][W] by code
+int codebook_sum_splits(int64_t V, int P, int K, int W, const DevInfo &di);
+cudaError_t launch_codebook_sums(const float *dz, int W, const void *index, int64_t V, int P, int K,
+                                 int splits, float *S, const DevInfo &di, cudaStream_t s);
+// from S of tokens [t0, t0 + nt): dC (+)= S h, dhp[p][t][ds] = S C
+cudaError_t launch_codebook_finish(const float *S, int splits, int W, const void *h, int bf16,
+                                   int t0, int nt, const float *C, int D, int M, int L, int K,
+                                   bool accumulate, float *dC, float *dhp, cudaStream_t s);
+cudaError_t launch_codebook_dh(const float *dhp, int W, int t0, int nt, int D, int M, int L,
+                               int bf16, void *dh, cudaStream_t s);
+
+}  // namespace rq

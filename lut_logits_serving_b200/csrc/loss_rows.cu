@@ -1,0 +1,678 @@
+// loss_rows.cu -- the row-wise kernels of the losses on the RQ-coded head:
+// operand scales and fp16 splits, decoding a piece of the vocabulary for the
+// tensor cores, the logits at the listed ids, log-sum-exp and losses, and the
+// sparse part of the logits' gradient.
+//
+//   lse_n = log sum_v exp(y[n,v] / T)
+//   cross entropy  loss_n = lse_n - y[n, t_n]
+//   distillation   q = softmax(teacher / T) over the listed ids,
+//                  loss_n = T^2 sum_j q_j (log q_j - y[n, id_j] / T + lse_n)
+//   dy[n,v] = w_n T (exp(y[n,v] / T - lse_n) - q_n[v])
+//
+// The statistics are kept in fp32 as (maximum, sum of exp) parts that are
+// joined in a fixed order, so every result is the same from run to run.
+#include "loss_common.cuh"
+
+namespace rq {
+
+namespace {
+
+// ------------------------------------------------------------- scales
+
+__device__ __forceinline__ float block_max(float m, float *red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) red[warp] = m;
+  __syncthreads();
+  m = threadIdx.x < (blockDim.x >> 5) ? red[threadIdx.x] : 0.f;
+  if (warp == 0) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+  return m;
+}
+
+// Blocks [0, 64): |h|, [64, 128): |C|, [128, 192): |w| (1 without weights).
+__global__ void __launch_bounds__(512) loss_amax_kernel(const void *h, int bf16, int64_t nh,
+                                                        const float *__restrict__ C, int64_t nc,
+                                                        const float *__restrict__ w, int64_t nw,
+                                                        float *__restrict__ amax) {
+  __shared__ float red[32];
+  const int kind = blockIdx.x / kAmaxBlocks, b = blockIdx.x % kAmaxBlocks;
+  const int64_t stride = (int64_t)kAmaxBlocks * blockDim.x;
+  const int64_t i0 = (int64_t)b * blockDim.x + threadIdx.x;
+  float m = 0.f;
+  if (kind == kAmaxH) {
+#pragma unroll 8
+    for (int64_t i = i0; i < nh; i += stride) m = fmaxf(m, fabsf(load_h(h, bf16, i)));
+  } else if (kind == kAmaxC) {
+#pragma unroll 8
+    for (int64_t i = i0; i < nc; i += stride) m = fmaxf(m, fabsf(C[i]));
+  } else if (w != nullptr) {
+    for (int64_t i = i0; i < nw; i += stride) m = fmaxf(m, fabsf(w[i]));
+  } else {
+    m = 1.f;
+  }
+  m = block_max(m, red);
+  if (threadIdx.x == 0) amax[blockIdx.x] = m;
+}
+
+__global__ void __launch_bounds__(256) loss_split_h_kernel(const void *h, int bf16, int64_t N,
+                                                           int D, int64_t pitch,
+                                                           const float *__restrict__ amax,
+                                                           __half *__restrict__ hi,
+                                                           __half *__restrict__ lo) {
+  const float s = scale_h(amax);
+  const int64_t n = blockIdx.x;
+  for (int i = threadIdx.x; i < D; i += blockDim.x) {
+    __half a, b;
+    split_f16(__fmul_rn(load_h(h, bf16, n * D + i), s), a, b);
+    hi[n * pitch + i] = a;
+    if (lo) lo[n * pitch + i] = b;
+  }
+}
+
+__global__ void __launch_bounds__(256) loss_widen_h_kernel(const __nv_bfloat16 *__restrict__ h,
+                                                           int64_t n, float *__restrict__ out) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * blockDim.x)
+    out[i] = __bfloat162float(h[i]);
+}
+
+// ------------------------------------------------------------- row decode
+//
+// Rows v0 .. v0 + rows of E as scaled fp16 hi / lo planes.  A CTA keeps the
+// codebooks of a group of GS subspaces in shared memory and walks a share of
+// the piece's (group, row) space, so the books are loaded at most a few times
+// per CTA while each row costs L codes and L gathers of ds floats a subspace.
+// A lane has one (row, subspace): GS lanes share a row, its results go through
+// a strip of shared memory and leave as full 16-byte vectors of GS ds halves.
+// Bound by the random shared-memory gathers (about three passes a load).
+struct DecodeArgs {
+  CodeSrc cs;
+  const float *C;
+  int M, L, ds, gs, groups;
+  int64_t v0, rows, pitch;
+  const float *amax;
+  __half *hi, *lo;
+  int vec;             // 16: strips leave as 16-byte vectors, else 2
+  int book;            // floats of one subspace's codebooks, L K ds
+  int strip;           // halves of one row's strip, padded
+  int quad;            // codebooks may be copied 16 bytes at a time
+  int direct;          // wide subspaces (ds > 32): no strips, each lane writes its own
+};
+
+constexpr int kDecThreads = 512;
+
+template <int DS, bool SMEM>
+__global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int ds = DS > 0 ? DS : a.ds, gs = a.gs, L = a.L, K = a.cs.K;
+  float *books = reinterpret_cast<float *>(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rw = 32 / gs;                           // rows a warp takes at once
+  const size_t book_bytes = SMEM ? ((size_t)gs * a.book * 4 + 15) / 16 * 16 : 0;
+  __half *strip = reinterpret_cast<__half *>(smem + book_bytes) + (size_t)warp * 2 * rw * a.strip;
+  const float se = scale_e(a.amax, L);
+  const int sub = lane % gs, lrow = lane / gs;
+  // this CTA's share of the (group, row) space, in row blocks of the CTA
+  const int rb = rw * (kDecThreads / 32);
+  const int64_t blocks = (a.rows + rb - 1) / rb, total = blocks * a.groups;
+  const int64_t u1 = total * (blockIdx.x + 1) / gridDim.x;
+  int have = -1;
+  for (int64_t u = total * blockIdx.x / gridDim.x; u < u1;) {
+    const int g = (int)(u / blocks);
+    const int64_t b0 = u % blocks, b1 = b0 + (u1 - u) < blocks ? b0 + (u1 - u) : blocks;
+    const int m0 = g * gs, ms = a.M - m0 < gs ? a.M - m0 : gs;
+    if (SMEM && g != have) {
+      __syncthreads();
+      const float *src = a.C + (size_t)m0 * a.book;
+      const int n = ms * a.book;
+      if (a.quad) {
+        for (int i = tid; i < n / 4; i += kDecThreads)
+          reinterpret_cast<float4 *>(books)[i] = __ldg(reinterpret_cast<const float4 *>(src) + i);
+        for (int i = n / 4 * 4 + tid; i < n; i += kDecThreads) books[i] = src[i];
+      } else {
+        for (int i = tid; i < n; i += kDecThreads) books[i] = src[i];
+      }
+      have = g;
+      __syncthreads();
+    }
+    const int m = m0 + sub;
+    const bool on = sub < ms;
+    const float *book = SMEM ? books + (size_t)sub * a.book : a.C + (size_t)m * a.book;
+    // codes of the row ahead, so their latency hides behind this row's gathers
+    uint32_t cn[4];
+    auto fetch = [&](int64_t b) {
+      const int64_t r = b * rb + warp * rw + lrow;
+      if (!on || b >= b1 || r >= a.rows) return;
+      const int64_t v = a.v0 + r;
+      if (a.cs.fmt == RQ_CODES_U16 && L == 2) {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(a.cs.codes) + v * a.M + m);
+        cn[0] = a.cs.fix(w & 0xFFFFu);
+        cn[1] = a.cs.fix(w >> 16);
+      } else {
+#pragma unroll
+        for (int l = 0; l < 4; ++l)
+          if (l < L) cn[l] = a.cs(v, m * L + l);
+      }
+    };
+    cn[0] = cn[1] = cn[2] = cn[3] = 0;
+    fetch(b0);
+    for (int64_t b = b0; b < b1; ++b) {
+      uint32_t c[4];
+#pragma unroll
+      for (int l = 0; l < 4; ++l) c[l] = cn[l];
+      fetch(b + 1);
+      const int64_t r0 = b * rb + warp * rw;        // first row of this warp
+      const int64_t r = r0 + lrow;
+      if (on && r < a.rows) {
+        __half *oh = DS == 0 && a.direct ? a.hi + r * a.pitch + (int64_t)m * ds
+                                         : strip + (size_t)lrow * a.strip + sub * ds;
+        __half *ol = DS == 0 && a.direct ? a.lo + r * a.pitch + (int64_t)m * ds
+                                         : oh + (size_t)rw * a.strip;
+        if (DS > 0) {
+          float e[DS > 0 ? DS : 1];
+#pragma unroll
+          for (int j = 0; j < DS; ++j) e[j] = 0.f;
+          for (int l = 0; l < L; ++l) {
+            const uint32_t cl = l == 0 ? c[0] : l == 1 ? c[1] : l == 2 ? c[2] : l == 3 ? c[3]
+                                              : a.cs(a.v0 + r, m * L + l);
+            const float *w = book + ((size_t)l * K + cl) * DS;
+            if (SMEM && DS % 2 == 0) {
+#pragma unroll
+              for (int j = 0; j < DS; j += 2) {
+                const float2 x = *reinterpret_cast<const float2 *>(w + j);
+                e[j] = __fadd_rn(e[j], x.x);
+                e[j + 1 < DS ? j + 1 : j] = __fadd_rn(e[j + 1 < DS ? j + 1 : j], x.y);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < DS; ++j) e[j] = __fadd_rn(e[j], w[j]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < DS; ++j) split_f16(__fmul_rn(e[j], se), oh[j], ol[j]);
+        } else {
+          for (int j = 0; j < ds; ++j) {
+            float e = 0.f;
+            for (int l = 0; l < L; ++l) {
+              const uint32_t cl = l == 0 ? c[0] : l == 1 ? c[1] : l == 2 ? c[2] : l == 3 ? c[3]
+                                                : a.cs(a.v0 + r, m * L + l);
+              e = __fadd_rn(e, book[((size_t)l * K + cl) * ds + j]);
+            }
+            split_f16(__fmul_rn(e, se), oh[j], ol[j]);
+          }
+        }
+      }
+      if (DS == 0 && a.direct) continue;
+      __syncwarp();
+      // the strips out: `n` halves a row and plane from column m0 ds on
+      const int n = ms * ds;
+      if (a.vec == 16 && ms == gs) {
+        const int per = n / 8, both = 2 * rw * per;
+        for (int i = lane; i < both; i += 32) {
+          const int pl = i / (rw * per), x = i - pl * rw * per, lr = x / per, q = x - lr * per;
+          if (r0 + lr < a.rows) {
+            __half *o = (pl ? a.lo : a.hi) + (r0 + lr) * a.pitch + (int64_t)m0 * ds + q * 8;
+            *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(
+                strip + ((size_t)pl * rw + lr) * a.strip + q * 8);
+          }
+        }
+      } else {
+        const int both = 2 * rw * n;
+        for (int i = lane; i < both; i += 32) {
+          const int pl = i / (rw * n), x = i - pl * rw * n, lr = x / n, q = x - lr * n;
+          if (r0 + lr < a.rows)
+            ((pl ? a.lo : a.hi) + (r0 + lr) * a.pitch + (int64_t)m0 * ds)[q] =
+                strip[((size_t)pl * rw + lr) * a.strip + q];
+        }
+      }
+      __syncwarp();
+    }
+    u += b1 - b0;
+  }
+}
+
+// ------------------------------------------------------------- picked logits
+
+// One warp per (token, list entry): <h_n, E_id> in fp32.
+__global__ void __launch_bounds__(256) loss_pick_kernel(const void *h, int bf16, const CodeSrc cs,
+                                                        const float *__restrict__ C, int D, int M,
+                                                        int L, const int32_t *__restrict__ id,
+                                                        int64_t count, int k, float cap,
+                                                        float *__restrict__ y) {
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, ds = D / M;
+  if (i >= count) return;
+  const int32_t v = id[i];
+  float z = 0.f;
+  if (v >= 0 && v < cs.V) {
+    const int64_t n = i / k;
+    for (int m = lane; m < M; m += 32) {
+      const int64_t hm = n * D + (int64_t)m * ds;
+      if (ds == 6 && L == 2) {
+        const float *w0 = C + ((size_t)(2 * m) * cs.K + cs(v, 2 * m)) * 6;
+        const float *w1 = C + ((size_t)(2 * m + 1) * cs.K + cs(v, 2 * m + 1)) * 6;
+#pragma unroll
+        for (int j = 0; j < 6; ++j)
+          z = fmaf(load_h(h, bf16, hm + j), __fadd_rn(__ldg(w0 + j), __ldg(w1 + j)), z);
+      } else {
+        for (int j = 0; j < ds; ++j) {
+          float e = 0.f;
+          for (int l = 0; l < L; ++l)
+            e = __fadd_rn(e, __ldg(C + ((size_t)(m * L + l) * cs.K + cs(v, m * L + l)) * ds + j));
+          z = fmaf(load_h(h, bf16, hm + j), e, z);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  }
+  if (lane == 0) y[i] = softcap_f(z, cap);
+}
+
+// ------------------------------------------------------------- statistics
+
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  if (!(m > -INFINITY)) return make_float2(m, a.y + b.y);
+  return make_float2(m, a.y * expf(a.x - m) + b.y * expf(b.x - m));
+}
+
+constexpr int kStatCols = 2048;   // logits one block folds into a part
+
+__global__ void __launch_bounds__(256) loss_logit_stats_kernel(const float *__restrict__ logits,
+                                                               int64_t V, float beta,
+                                                               float2 *__restrict__ stat,
+                                                               int stat_ld) {
+  __shared__ float2 red[8];
+  const int64_t n = blockIdx.y, c0 = (int64_t)blockIdx.x * kStatCols;
+  float x[kStatCols / 256], m = -INFINITY, s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kStatCols / 256; ++i) {
+    const int64_t c = c0 + i * 256 + threadIdx.x;
+    x[i] = c < V ? logits[n * V + c] * beta : -INFINITY;
+    m = fmaxf(m, x[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kStatCols / 256; ++i)
+    s += m > -INFINITY ? expf(x[i] - m) : (x[i] != x[i] ? x[i] : 0.f);
+  float2 p = make_float2(m, s);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    p = join(p, make_float2(__shfl_xor_sync(0xffffffffu, p.x, o),
+                            __shfl_xor_sync(0xffffffffu, p.y, o)));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = p;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 8; ++w) p = join(p, red[w]);
+    stat[(int64_t)blockIdx.x * stat_ld + n] = p;
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// An id of the lists counts when it lies in [0, V) and, for a teacher, its
+// logit is above -inf.
+__device__ __forceinline__ bool listed(int32_t id, int64_t V) { return id >= 0 && id < V; }
+
+// Rows 32 b .. 32 b + 31: the parts joined by 32 threads a row, then one warp
+// per row forms the loss.
+__global__ void __launch_bounds__(1024) loss_finish_kernel(const float2 *__restrict__ stat,
+                                                           int parts, int stat_ld, int64_t N,
+                                                           int64_t V, const LossTargets t,
+                                                           const float *__restrict__ y,
+                                                           int y_is_logits,
+                                                           float *__restrict__ loss,
+                                                           float *__restrict__ lse, unsigned *err) {
+  __shared__ float2 red[32][33];
+  const int r = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t row = (int64_t)blockIdx.x * 32 + r;
+  float2 p = make_float2(-INFINITY, 0.f);
+  if (row < N) {
+#pragma unroll 4
+    for (int i = w; i < parts; i += 32) p = join(p, stat[(int64_t)i * stat_ld + row]);
+  }
+  red[w][r] = p;
+  __syncthreads();
+  const int64_t n = (int64_t)blockIdx.x * 32 + w;   // this warp's row
+  if (n >= N) return;
+  p = red[r][w];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    p = join(p, make_float2(__shfl_xor_sync(0xffffffffu, p.x, o),
+                            __shfl_xor_sync(0xffffffffu, p.y, o)));
+  const float l = p.x + logf(p.y);
+  const int32_t *id = t.id + n * t.k;
+  auto logit = [&](int j) { return y_is_logits ? y[n * V + id[j]] : y[n * t.k + j]; };
+  float out = 0.f;
+  if (t.val == nullptr) {
+    if (r == 0) {
+      if (id[0] >= V) atomicOr(err, RQ_DEVERR_BAD_ID);
+      if (listed(id[0], V)) out = l - logit(0);
+    }
+  } else {
+    const float *val = t.val + n * t.k;
+    float m = -INFINITY;
+    for (int j = r; j < t.k; j += 32) {
+      if (id[j] >= V) atomicOr(err, RQ_DEVERR_BAD_ID);
+      if (listed(id[j], V)) m = fmaxf(m, val[j] * t.beta);
+    }
+    m = warp_max(m);
+    float z = 0.f, a = 0.f;
+    if (m > -INFINITY) {
+      for (int j = r; j < t.k; j += 32)
+        if (listed(id[j], V)) z += expf(val[j] * t.beta - m);
+      z = warp_sum(z);
+      const float logz = logf(z);
+      for (int j = r; j < t.k; j += 32) {
+        if (!listed(id[j], V)) continue;
+        const float d = val[j] * t.beta - m, e = expf(d);
+        if (e > 0.f || e != e) a = fmaf(e, (d - logz) - logit(j) * t.beta + l, a);
+      }
+      out = warp_sum(a) / z * t.T * t.T;
+    }
+  }
+  if (r == 0) {
+    loss[n] = out;
+    lse[n] = l;
+  }
+}
+
+// ------------------------------------------------------------- gradient, sparse part
+
+// One block per row: q_j of the listed ids, an id listed twice merged into its
+// first place (so each id is corrected once, by one thread), and f = w T.
+__global__ void __launch_bounds__(128) loss_sparse_kernel(const LossTargets t, int64_t V,
+                                                          const float *__restrict__ w,
+                                                          int32_t *__restrict__ sid,
+                                                          float *__restrict__ sq,
+                                                          float *__restrict__ f, unsigned *err) {
+  extern __shared__ float lists[];                 // [k] q, [k] id
+  __shared__ float red[4], red2[4];
+  const int64_t n = blockIdx.x;
+  const int tid = threadIdx.x, k = t.k;
+  float *q = lists;
+  int *ids = reinterpret_cast<int *>(lists + k);
+  const int32_t *id = t.id + n * k;
+  float m = -INFINITY;
+  for (int j = tid; j < k; j += 128) {
+    int32_t v = id[j];
+    float x = t.val ? t.val[n * k + j] * t.beta : 0.f;
+    if (v >= V) atomicOr(err, RQ_DEVERR_BAD_ID);
+    if (!listed(v, V)) {
+      v = -1;
+      x = -INFINITY;
+    }
+    ids[j] = v;
+    q[j] = x;
+    m = fmaxf(m, x);
+  }
+  m = warp_max(m);
+  if ((tid & 31) == 0) red[tid >> 5] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  float z = 0.f;
+  if (m > -INFINITY)
+    for (int j = tid; j < k; j += 128) {
+      const float e = ids[j] >= 0 ? expf(q[j] - m) : 0.f;
+      q[j] = e;
+      z += e;
+    }
+  z = warp_sum(z);
+  if ((tid & 31) == 0) red2[tid >> 5] = z;
+  __syncthreads();
+  z = (red2[0] + red2[1]) + (red2[2] + red2[3]);
+  const bool some = m > -INFINITY;
+  for (int j = tid; j < k; j += 128) {
+    int v = some ? ids[j] : -1;
+    float s = 0.f;
+    if (v >= 0) {
+      for (int i = 0; i < j; ++i)
+        if (ids[i] == v) {
+          v = -1;
+          break;
+        }
+      if (v >= 0) {
+        s = q[j];
+        for (int i = j + 1; i < k; ++i)
+          if (ids[i] == v) s += q[i];
+      }
+    }
+    sid[n * k + j] = v;
+    sq[n * k + j] = v >= 0 ? s / z : 0.f;
+  }
+  if (tid == 0) f[n] = some ? (w ? w[n] : 1.f) * t.T : 0.f;
+}
+
+__device__ __forceinline__ float dz_at(float y, float q, float lse, float f, float beta,
+                                       float cap) {
+  const float th = cap > 0.f ? y / cap : 0.f;
+  return f != 0.f ? (expf(y * beta - lse) - q) * (1.f - th * th) * f : 0.f;
+}
+
+__global__ void __launch_bounds__(256) loss_fix_planes_kernel(
+    const int32_t *__restrict__ sid, const float *__restrict__ sq, const float *__restrict__ y,
+    int k, int64_t count, int64_t v0, int64_t rows, const float *__restrict__ lse,
+    const float *__restrict__ f, const float *__restrict__ amax, float T, float beta, float cap,
+    __half *__restrict__ hi, __half *__restrict__ lo, int64_t pitch) {
+  const float sz = scale_z(amax, T);
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= count) return;
+  const int64_t v = (int64_t)sid[i] - v0;
+  if (sid[i] < 0 || v < 0 || v >= rows) return;
+  const int64_t n = i / k;
+  __half a, b;
+  split_f16(dz_at(y[i], sq[i], lse[n], f[n] * sz, beta, cap), a, b);
+  hi[n * pitch + v] = a;
+  lo[n * pitch + v] = b;
+}
+
+// ------------------------------------------------------------- few tokens
+
+template <int W>
+__global__ void __launch_bounds__(256) loss_dz_small_kernel(const float *__restrict__ logits,
+                                                            int64_t N, int64_t V,
+                                                            const float *__restrict__ lse,
+                                                            const float *__restrict__ f, float beta,
+                                                            float cap, float *__restrict__ dz) {
+  const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x, g = blockIdx.y;
+  if (v >= V) return;
+  float d[W];
+#pragma unroll
+  for (int t = 0; t < W; ++t) {
+    const int64_t n = g * W + t;
+    d[t] = n < N ? dz_at(logits[n * V + v], 0.f, lse[n], f[n], beta, cap) : 0.f;
+  }
+  float *o = dz + (g * V + v) * W;
+  if (W == 4) *reinterpret_cast<float4 *>(o) = make_float4(d[0], d[W > 1 ? 1 : 0], d[W > 2 ? 2 : 0], d[W > 3 ? 3 : 0]);
+  else if (W == 2) *reinterpret_cast<float2 *>(o) = make_float2(d[0], d[W > 1 ? 1 : 0]);
+  else o[0] = d[0];
+}
+
+__global__ void __launch_bounds__(256) loss_fix_small_kernel(
+    const int32_t *__restrict__ sid, const float *__restrict__ sq, const float *__restrict__ logits,
+    int k, int64_t count, int64_t V, const float *__restrict__ lse, const float *__restrict__ f,
+    float beta, float cap, int W, float *__restrict__ dz) {
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= count || sid[i] < 0) return;
+  const int64_t n = i / k, v = sid[i];
+  dz[((n / W) * V + v) * W + n % W] = dz_at(logits[n * V + v], sq[i], lse[n], f[n], beta, cap);
+}
+
+__global__ void __launch_bounds__(256) loss_dh_sum_kernel(const float *__restrict__ part,
+                                                          int splits, int64_t stride,
+                                                          int64_t pitch, int64_t N, int D,
+                                                          int bf16, void *__restrict__ dh) {
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= N * D) return;
+  const int64_t n = i / D, c = i - n * D;
+  float s = 0.f;
+  for (int p = 0; p < splits; ++p) s += part[p * stride + n * pitch + c];
+  if (bf16) static_cast<__nv_bfloat16 *>(dh)[i] = __float2bfloat16_rn(s);
+  else static_cast<float *>(dh)[i] = s;
+}
+
+unsigned blocks_of(int64_t n, int per) { return (unsigned)((n + per - 1) / per); }
+
+}  // namespace
+
+cudaError_t launch_loss_amax(const void *h, int bf16, int64_t nh, const float *C, int64_t nc,
+                             const float *w, int64_t nw, float *amax, cudaStream_t s) {
+  loss_amax_kernel<<<3 * kAmaxBlocks, 512, 0, s>>>(h, bf16, nh, C, nc, w, nw, amax);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_loss_split_h(const void *h, int bf16, int64_t N, int D, int64_t pitch,
+                                const float *amax, __half *hi, __half *lo, cudaStream_t s) {
+  loss_split_h_kernel<<<(unsigned)N, 256, 0, s>>>(h, bf16, N, D, pitch, amax, hi, lo);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_loss_widen_h(const void *h, int64_t n, float *out, cudaStream_t s) {
+  loss_widen_h_kernel<<<blocks_of(n, 1024), 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(h), n,
+                                                         out);
+  return cudaGetLastError();
+}
+
+namespace {
+template <bool SMEM>
+const void *decode_fn(int ds) {
+  switch (ds) {
+    case 2: return reinterpret_cast<const void *>(&loss_decode_kernel<2, SMEM>);
+    case 3: return reinterpret_cast<const void *>(&loss_decode_kernel<3, SMEM>);
+    case 4: return reinterpret_cast<const void *>(&loss_decode_kernel<4, SMEM>);
+    case 5: return reinterpret_cast<const void *>(&loss_decode_kernel<5, SMEM>);
+    case 6: return reinterpret_cast<const void *>(&loss_decode_kernel<6, SMEM>);
+    case 8: return reinterpret_cast<const void *>(&loss_decode_kernel<8, SMEM>);
+  }
+  return reinterpret_cast<const void *>(&loss_decode_kernel<0, SMEM>);
+}
+}  // namespace
+
+cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, int ds, int64_t v0,
+                               int64_t rows, int64_t pitch, const float *amax, __half *hi,
+                               __half *lo, const DevInfo &di, cudaStream_t s) {
+  DecodeArgs a;
+  a.cs = cs;
+  a.C = C;
+  a.M = M;
+  a.L = L;
+  a.ds = ds;
+  a.v0 = v0;
+  a.rows = rows;
+  a.pitch = pitch;
+  a.amax = amax;
+  a.hi = hi;
+  a.lo = lo;
+  const int64_t book = (int64_t)L * cs.K * ds;
+  const bool in_smem = book * 4 <= 200 * 1024;
+  // as many subspaces (a power of two up to a warp's lanes) as their
+  // codebooks fit beside the strips
+  int gs = 1;
+  size_t smem = 0;
+  auto strip_of = [&](int g) { return (g * ds + 7) / 8 * 8; };
+  auto bytes_of = [&](int g) {
+    return (in_smem ? ((size_t)g * book * 4 + 15) / 16 * 16 : 0) +
+           (ds > 32 ? 0 : (size_t)(kDecThreads / 32) * 2 * (32 / g) * strip_of(g) * 2);
+  };
+  while (gs < 32 && gs * 2 <= M && bytes_of(gs * 2) <= 220 * 1024) gs *= 2;
+  smem = bytes_of(gs);
+  if (smem > 225 * 1024) return cudaErrorInvalidValue;
+  a.gs = gs;
+  a.direct = ds > 32;
+  a.groups = (M + gs - 1) / gs;
+  a.book = in_smem ? (int)book : 0;
+  if (!in_smem && book > 0x7fffffff) return cudaErrorInvalidValue;
+  if (!in_smem) a.book = (int)book;
+  a.strip = strip_of(gs);
+  a.vec = (gs * ds) % 8 == 0 ? 16 : 2;
+  a.quad = (reinterpret_cast<uintptr_t>(C) & 15) == 0 && (gs * book) % 4 == 0;
+  const void *fn = in_smem ? decode_fn<true>(ds) : decode_fn<false>(ds);
+  cudaError_t e = ensure_smem_limit(fn, di.device, smem);
+  if (e != cudaSuccess) return e;
+  const int occ = occupancy_cached(fn, di.device, kDecThreads, smem);
+  const int rb = 32 / gs * (kDecThreads / 32);
+  const int64_t total = (rows + rb - 1) / rb * a.groups;
+  const int64_t cap = (int64_t)di.sms * occ;
+  void *args[] = {&a};
+  return launch_maybe_pdl(fn, dim3((unsigned)(total < cap ? total : cap)), dim3(kDecThreads), smem,
+                          s, args, false);
+}
+
+cudaError_t launch_loss_pick(const void *h, int bf16, const CodeSrc &cs, const float *C, int D,
+                             int M, int L, const int32_t *id, int64_t N, int k, float cap,
+                             float *y, cudaStream_t s) {
+  loss_pick_kernel<<<blocks_of(N * k, 8), 256, 0, s>>>(h, bf16, cs, C, D, M, L, id, N * k, k, cap,
+                                                       y);
+  return cudaGetLastError();
+}
+
+int loss_stat_parts(int64_t V) { return (int)((V + kStatCols - 1) / kStatCols); }
+
+cudaError_t launch_loss_logit_stats(const float *logits, int64_t N, int64_t V, float beta,
+                                    float2 *stat, int stat_ld, cudaStream_t s) {
+  loss_logit_stats_kernel<<<dim3(loss_stat_parts(V), (unsigned)N), 256, 0, s>>>(logits, V, beta,
+                                                                               stat, stat_ld);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_loss_finish(const float2 *stat, int parts, int stat_ld, int64_t N, int64_t V,
+                               const LossTargets &t, const float *y, bool y_is_logits, float *loss,
+                               float *lse, unsigned *err, cudaStream_t s) {
+  loss_finish_kernel<<<blocks_of(N, 32), 1024, 0, s>>>(stat, parts, stat_ld, N, V, t, y,
+                                                       y_is_logits, loss, lse, err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_loss_sparse(const LossTargets &t, int64_t N, int64_t V, const float *w,
+                               int32_t *sid, float *sq, float *f, unsigned *err, cudaStream_t s) {
+  loss_sparse_kernel<<<(unsigned)N, 128, (size_t)t.k * 8, s>>>(t, V, w, sid, sq, f, err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_loss_fix_planes(const int32_t *sid, const float *sq, const float *y, int k,
+                                   int64_t N, int64_t v0, int64_t rows, const float *lse,
+                                   const float *f, const float *amax, float T, float beta,
+                                   float cap, __half *hi, __half *lo, int64_t pitch,
+                                   cudaStream_t s) {
+  loss_fix_planes_kernel<<<blocks_of(N * k, 256), 256, 0, s>>>(sid, sq, y, k, N * k, v0, rows, lse,
+                                                               f, amax, T, beta, cap, hi, lo,
+                                                               pitch);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_loss_dz_small(const float *logits, int64_t N, int64_t V, const int32_t *sid,
+                                 const float *sq, int k, const float *lse, const float *f,
+                                 float beta, float cap, int W, float *dz, cudaStream_t s) {
+  const dim3 grid(blocks_of(V, 256), (unsigned)((N + W - 1) / W));
+  if (W == 1) loss_dz_small_kernel<1><<<grid, 256, 0, s>>>(logits, N, V, lse, f, beta, cap, dz);
+  else if (W == 2) loss_dz_small_kernel<2><<<grid, 256, 0, s>>>(logits, N, V, lse, f, beta, cap, dz);
+  else if (W == 4) loss_dz_small_kernel<4><<<grid, 256, 0, s>>>(logits, N, V, lse, f, beta, cap, dz);
+  else return cudaErrorInvalidValue;
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  loss_fix_small_kernel<<<blocks_of(N * k, 256), 256, 0, s>>>(sid, sq, logits, k, N * k, V, lse, f,
+                                                              beta, cap, W, dz);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_loss_dh_sum(const float *part, int splits, int64_t stride, int64_t pitch,
+                               int64_t N, int D, int bf16, void *dh, cudaStream_t s) {
+  loss_dh_sum_kernel<<<blocks_of(N * D, 256), 256, 0, s>>>(part, splits, stride, pitch, N, D, bf16,
+                                                           dh);
+  return cudaGetLastError();
+}
+
+}  // namespace rq

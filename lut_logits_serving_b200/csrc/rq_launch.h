@@ -64,6 +64,9 @@ struct DevInfo {
 
 cudaError_t dev_info(DevInfo *out);
 
+// The status of a CUDA result; an error is kept for rq_last_cuda_error.
+int note_cuda_error(cudaError_t e);
+
 // Raises the dynamic shared-memory limit of kernel `fn` on `device` (the
 // current device) to at least `smem` bytes.  The limit set so far is kept per
 // (kernel, device) under a lock, so concurrent host threads may launch.

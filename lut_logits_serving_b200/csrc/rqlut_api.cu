@@ -334,6 +334,8 @@ int run_fused(const float *h, const float *C, const void *codes, int fmt, const 
 }  // namespace
 
 namespace rq {
+int note_cuda_error(cudaError_t e) { return status_of(e); }
+
 // Greedy pick over a vocabulary split across ranks (shard_argmax.cu).
 cudaError_t launch_argmax_candidates(const float *logits, const int32_t *argmax, int B, int64_t V,
                                      int64_t row0, float *val, int32_t *gidx, cudaStream_t s);
