@@ -13,16 +13,15 @@ using namespace rq;
 
 namespace {
 
-constexpr int64_t kPieceRows = 32768;     // rows of the vocabulary per piece (a multiple of kGradRows)
+constexpr int64_t kPieceRows = 4 * kGradRows;   // rows of the vocabulary per piece
 constexpr int kTokenChunk = 4096;         // tokens per sweep over the vocabulary
 constexpr int kFewTokens = 64;            // up to here a loss takes the serving kernels' logits
 constexpr int kFewTokensGrad = 16;        // and a gradient the sums by code
+constexpr int kSms = 148;                 // sizes do not depend on the current device
 constexpr int kMaxSplits = 32;            // of the vocabulary in dz E
 constexpr int kChain = 4;                 // blocks of 64 per accumulation chain
 constexpr int kMaxList = 1024;            // a teacher's entries per token
 constexpr int kMaxGradK = 4096;           // codewords per codebook, gradients
-
-static_assert(kPieceRows % kGradRows == 0, "pieces are whole index blocks");
 
 bool dims_valid(const rq_dims &d) { return rq_lut_bytes(d, 1) != 0; }
 
@@ -88,9 +87,9 @@ int total_parts(const rq_dims &d) {
 
 // Splits of dz E over the vocabulary: enough that its 128 x 256 tiles fill the
 // SMs.
-int dh_splits(const rq_dims &d, int64_t n, int sms) {
+int dh_splits(const rq_dims &d, int64_t n) {
   const int64_t tiles = (n + 127) / 128 * ((d.D + 255) / 256);
-  int64_t s = sms / tiles;
+  int64_t s = kSms / tiles;
   const int64_t kb = (piece_rows(d) + 63) / 64;
   if (s > kb) s = kb;
   if (s > kMaxSplits) s = kMaxSplits;
@@ -102,10 +101,9 @@ int group_width(int N) { return N == 1 ? 1 : N == 2 ? 2 : 4; }
 
 struct FewLayout {
   size_t logits, stat, wide, sid, sq, f, dz, S, dhp, fused, fused_bytes, total;
-  int splits;
 };
 
-FewLayout few_layout(const rq_dims &d, int N, int fmt, int k, bool grad, const DevInfo &di) {
+FewLayout few_layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
   FewLayout x{};
   Arena a;
   x.logits = a.take((int64_t)N * d.V * 4);
@@ -117,8 +115,7 @@ FewLayout few_layout(const rq_dims &d, int N, int fmt, int k, bool grad, const D
     x.sq = a.take((int64_t)N * k * 4);
     x.f = a.take((int64_t)N * 4);
     x.dz = a.take((int64_t)G * d.V * W * 4);
-    x.splits = codebook_sum_splits(d.V, P, d.K, W, di);
-    x.S = a.take((int64_t)x.splits * P * d.K * W * 4);
+    x.S = a.take((int64_t)codebook_sum_slots(d.V, P) * P * d.K * W * 4);
     x.dhp = a.take((int64_t)P * W * (d.D / d.M) * 4);
   }
   x.fused_bytes = rq_fused_workspace_bytes(d, N, fmt, 0);
@@ -133,7 +130,7 @@ struct ManyLayout {
   int64_t chunk;       // tokens per sweep
 };
 
-ManyLayout many_layout(const rq_dims &d, int N, int k, bool grad, int sms) {
+ManyLayout many_layout(const rq_dims &d, int N, int k, bool grad) {
   ManyLayout x{};
   Arena a;
   const int64_t n = N < kTokenChunk ? N : kTokenChunk, rows = piece_rows(d);
@@ -156,9 +153,9 @@ ManyLayout many_layout(const rq_dims &d, int N, int k, bool grad, int sms) {
     x.zl = a.take(n * x.zp * 2);
     x.dw = a.take((int64_t)d.D * x.zp * 4);
     // the last sweep may have fewer tokens and with them more splits
-    int64_t part = dh_splits(d, n, sms) * n;
+    int64_t part = dh_splits(d, n) * n;
     const int64_t last = N % n == 0 ? n : N % n;
-    const int64_t p2 = dh_splits(d, last, sms) * last;
+    const int64_t p2 = dh_splits(d, last) * last;
     if (p2 > part) part = p2;
     x.part = a.take(part * x.hp * 4);
   }
@@ -166,18 +163,9 @@ ManyLayout many_layout(const rq_dims &d, int N, int k, bool grad, int sms) {
   return x;
 }
 
-// The B200's figures, so that sizes do not depend on the current device.
-DevInfo nominal() {
-  DevInfo d{};
-  d.sms = 148;
-  d.max_smem_optin = 232448;
-  return d;
-}
-
 size_t loss_bytes(const rq_dims &d, int N, int fmt, int k, bool grad) {
-  const DevInfo di = nominal();
-  if (grad ? few_grad(d, N) : few_loss(d, N)) return few_layout(d, N, fmt, k, grad, di).total;
-  return many_layout(d, N, k, grad, di.sms).total;
+  if (grad ? few_grad(d, N) : few_loss(d, N)) return few_layout(d, N, fmt, k, grad).total;
+  return many_layout(d, N, k, grad).total;
 }
 
 #define RQ_TRY(call)                           \
@@ -285,7 +273,7 @@ cudaError_t many_grad(const Problem &q, const ManyLayout &x, const float *lse, c
     LossTargets t = q.t;
     t.id += n0 * t.k;
     if (t.val) t.val += n0 * t.k;
-    const int splits = dh_splits(d, n, 148);
+    const int splits = dh_splits(d, n);
     RQ_TRY(launch_loss_split_h(h, q.bf16, n, d.D, x.hp, amax, hh, hl, s));
     RQ_TRY(launch_loss_sparse(t, n, d.V, w ? w + n0 : nullptr, sid, sq, f, di.err, s));
     RQ_TRY(launch_loss_pick(h, q.bf16, q.src(), q.C, d.D, d.M, d.L, sid, n, t.k, q.cap, y, s));
@@ -351,9 +339,8 @@ cudaError_t few_gradients(const Problem &q, const FewLayout &x, const float *lse
                               q.cap, W, dz, s));
   for (int g = 0; g < G; ++g) {
     const int t0 = g * W, nt = q.N - t0 < W ? q.N - t0 : W;
-    RQ_TRY(launch_codebook_sums(dz + (size_t)g * d.V * W, W, index, d.V, P, d.K, x.splits, S, di,
-                                s));
-    RQ_TRY(launch_codebook_finish(S, x.splits, W, q.h, q.bf16, t0, nt, q.C, d.D, d.M, d.L, d.K,
+    RQ_TRY(launch_codebook_sums(dz + (size_t)g * d.V * W, W, index, d.V, P, d.K, S, di, s));
+    RQ_TRY(launch_codebook_finish(S, d.V, W, q.h, q.bf16, t0, nt, q.C, d.D, d.M, d.L, d.K,
                                   g > 0, dC, dhp, s));
     if (dh) RQ_TRY(launch_codebook_dh(dhp, W, t0, nt, d.D, d.M, d.L, q.bf16, dh, s));
   }
@@ -388,10 +375,10 @@ int run_loss(const Problem &q, float *loss, float *lse, void *ws, size_t ws_byte
   if (e != cudaSuccess) return status_of(e);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!few_loss(q.d, q.N)) {
-    const ManyLayout x = many_layout(q.d, q.N, q.t.k, false, 148);
+    const ManyLayout x = many_layout(q.d, q.N, q.t.k, false);
     return status_of(many_loss(q, x, loss, lse, ws, di, s));
   }
-  const FewLayout x = few_layout(q.d, q.N, q.fmt, q.t.k, false, nominal());
+  const FewLayout x = few_layout(q.d, q.N, q.fmt, q.t.k, false);
   const int st = few_logits(q, x, ws, s, &e);
   if (st != RQ_OK) return e != cudaSuccess ? status_of(e) : st;
   e = launch_loss_logit_stats(at<float>(ws, x.logits), q.N, q.d.V, q.t.beta, at<float2>(ws, x.stat),
@@ -417,10 +404,10 @@ int run_grad(const Problem &q, const float *lse, const float *w, const void *ind
   if (e != cudaSuccess) return status_of(e);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!few_grad(q.d, q.N)) {
-    const ManyLayout x = many_layout(q.d, q.N, q.t.k, true, 148);
+    const ManyLayout x = many_layout(q.d, q.N, q.t.k, true);
     return status_of(many_grad(q, x, lse, w, index, dh, dC, ws, di, s));
   }
-  const FewLayout x = few_layout(q.d, q.N, q.fmt, q.t.k, true, nominal());
+  const FewLayout x = few_layout(q.d, q.N, q.fmt, q.t.k, true);
   const int st = few_logits(q, x, ws, s, &e);
   if (st != RQ_OK) return e != cudaSuccess ? status_of(e) : st;
   return status_of(few_gradients(q, x, lse, w, index, dh, dC, ws, di, s));

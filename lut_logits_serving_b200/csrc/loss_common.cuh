@@ -13,7 +13,8 @@
 namespace rq {
 
 // Rows of the vocabulary that one block of the gradient index covers: their
-// local numbers fit 16 bits, and 6 floats of each fit shared memory.
+// local numbers fit 16 bits, and 3 floats of each, with the sums of 1024 codes,
+// fit half an SM's shared memory.
 constexpr int kGradRows = 8192;
 
 // Code p of row v in any layout, safe for codes >= K (see CodeFix).
@@ -191,12 +192,13 @@ cudaError_t launch_prepare_grad(const CodeSrc &cs, void *index, const DevInfo &d
 cudaError_t launch_codebook_rows(const float *dwt, int64_t pitch, int64_t v0, int64_t rows,
                                  const void *index, int64_t V, int M, int L, int K, int ds,
                                  bool accumulate, float *dC, const DevInfo &di, cudaStream_t s);
-// S[split][p][k][W] = sums of dz [V][W] by code
-int codebook_sum_splits(int64_t V, int P, int K, int W, const DevInfo &di);
+// S[slot][p][k][W] = sums of dz [V][W] by code; a column's blocks may be
+// shared by up to codebook_sum_slots CTAs, each with a slot of its own
+int codebook_sum_slots(int64_t V, int P);
 cudaError_t launch_codebook_sums(const float *dz, int W, const void *index, int64_t V, int P, int K,
-                                 int splits, float *S, const DevInfo &di, cudaStream_t s);
+                                 float *S, const DevInfo &di, cudaStream_t s);
 // from S of tokens [t0, t0 + nt): dC (+)= S h, dhp[p][t][ds] = S C
-cudaError_t launch_codebook_finish(const float *S, int splits, int W, const void *h, int bf16,
+cudaError_t launch_codebook_finish(const float *S, int64_t V, int W, const void *h, int bf16,
                                    int t0, int nt, const float *C, int D, int M, int L, int K,
                                    bool accumulate, float *dC, float *dhp, cudaStream_t s);
 cudaError_t launch_codebook_dh(const float *dhp, int W, int t0, int nt, int D, int M, int L,

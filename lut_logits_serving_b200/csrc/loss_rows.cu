@@ -83,27 +83,55 @@ __global__ void __launch_bounds__(256) loss_widen_h_kernel(const __nv_bfloat16 *
 // ------------------------------------------------------------- row decode
 //
 // Rows v0 .. v0 + rows of E as scaled fp16 hi / lo planes.  A CTA keeps the
-// codebooks of a group of GS subspaces in shared memory and walks a share of
-// the piece's (group, row) space, so the books are loaded at most a few times
-// per CTA while each row costs L codes and L gathers of ds floats a subspace.
-// A lane has one (row, subspace): GS lanes share a row, its results go through
-// a strip of shared memory and leave as full 16-byte vectors of GS ds halves.
-// Bound by the random shared-memory gathers (about three passes a load).
+// (scaled) codebooks of a group of gs subspaces in shared memory while it walks
+// a chunk of rows; each row costs L codes and L gathers of ds floats a
+// subspace.  The items go chunk by chunk, all groups of a chunk at about the
+// same time: a group writes 2 gs ds bytes of a row, and the L2 joins them to
+// whole sectors and lines only if the row's other groups follow before it
+// evicts them (groups at unrelated rows: 474 us for 32768 rows of 2304, of
+// which 320 were the scattered writes).  A lane has one subspace of two rows at a time: gs lanes share a
+// row, its results go through a strip of shared memory and leave as 16-byte
+// vectors; the codes of the next rows are fetched meanwhile.  Bound by the
+// random shared-memory gathers (16 lanes' 8-byte words meet about three times
+// in the fullest bank pair).
 struct DecodeArgs {
   CodeSrc cs;
   const float *C;
   int M, L, ds, gs, groups;
+  int chunk, items;    // rows of an item (whole CTA blocks), (chunk, group) items
   int64_t v0, rows, pitch;
   const float *amax;
   __half *hi, *lo;
-  int vec;             // 16: strips leave as 16-byte vectors, else 2
+  int vec;             // strips leave as 16-byte vectors
   int book;            // floats of one subspace's codebooks, L K ds
   int strip;           // halves of one row's strip, padded
   int quad;            // codebooks may be copied 16 bytes at a time
   int direct;          // wide subspaces (ds > 32): no strips, each lane writes its own
 };
 
-constexpr int kDecThreads = 512;
+constexpr int kDecThreads = 1024;  // 512 with two rows a lane: 256 us where this takes 185
+constexpr int kDecU = 1;           // rows a lane has in flight
+
+// The (up to four) codes of subspace m of row v.
+__device__ __forceinline__ void row_codes(const CodeSrc &cs, int L, int M, int64_t v, int m,
+                                          uint32_t (&c)[4]) {
+  if (L == 2 && cs.fmt == RQ_CODES_U16) {
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(cs.codes) + v * M + m);
+    c[0] = cs.fix(w & 0xFFFFu);
+    c[1] = cs.fix(w >> 16);
+  } else if (L == 2 && cs.fmt == RQ_CODES_PACKED10) {
+    // bits [20 m, 20 m + 20) of the row, in three bytes
+    const uint8_t *b = static_cast<const uint8_t *>(cs.codes) + v * ((20LL * M + 7) / 8) + (20 * m >> 3);
+    const uint32_t w = ((uint32_t)__ldg(b) | (uint32_t)__ldg(b + 1) << 8 | (uint32_t)__ldg(b + 2) << 16) >>
+                       ((m & 1) * 4);
+    c[0] = cs.fix(w & 1023u);
+    c[1] = cs.fix(w >> 10 & 1023u);
+  } else {
+#pragma unroll
+    for (int l = 0; l < 4; ++l)
+      if (l < L) c[l] = cs(v, m * L + l);
+  }
+}
 
 template <int DS, bool SMEM>
 __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeArgs a) {
@@ -111,127 +139,137 @@ __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeAr
   const int ds = DS > 0 ? DS : a.ds, gs = a.gs, L = a.L, K = a.cs.K;
   float *books = reinterpret_cast<float *>(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rw = 32 / gs;                           // rows a warp takes at once
+  const int lr = 32 / gs, rw = lr * kDecU;          // rows a warp takes at once
   const size_t book_bytes = SMEM ? ((size_t)gs * a.book * 4 + 15) / 16 * 16 : 0;
   __half *strip = reinterpret_cast<__half *>(smem + book_bytes) + (size_t)warp * 2 * rw * a.strip;
   const float se = scale_e(a.amax, L);
   const int sub = lane % gs, lrow = lane / gs;
-  // this CTA's share of the (group, row) space, in row blocks of the CTA
   const int rb = rw * (kDecThreads / 32);
-  const int64_t blocks = (a.rows + rb - 1) / rb, total = blocks * a.groups;
-  const int64_t u1 = total * (blockIdx.x + 1) / gridDim.x;
-  int have = -1;
-  for (int64_t u = total * blockIdx.x / gridDim.x; u < u1;) {
-    const int g = (int)(u / blocks);
-    const int64_t b0 = u % blocks, b1 = b0 + (u1 - u) < blocks ? b0 + (u1 - u) : blocks;
+  // 16-byte vectors of a plane's strip: this lane's first, and the step to its next
+  const int per = gs * ds / 8, vecs = rw * per;
+  const int q0 = per > 0 ? lane % per : 0, x0 = per > 0 ? lane / per : 0;
+  const int dq = per > 0 ? 32 % per : 0, dx = per > 0 ? 32 / per : 0;
+  for (int u = blockIdx.x; u < a.items; u += gridDim.x) {
+    const int g = u % a.groups;
+    const int64_t b0 = (int64_t)(u / a.groups) * (a.chunk / rb), b1 = b0 + a.chunk / rb;
     const int m0 = g * gs, ms = a.M - m0 < gs ? a.M - m0 : gs;
-    if (SMEM && g != have) {
+    if (SMEM) {
       __syncthreads();
       const float *src = a.C + (size_t)m0 * a.book;
       const int n = ms * a.book;
+      int i0 = 0;
       if (a.quad) {
-        for (int i = tid; i < n / 4; i += kDecThreads)
-          reinterpret_cast<float4 *>(books)[i] = __ldg(reinterpret_cast<const float4 *>(src) + i);
-        for (int i = n / 4 * 4 + tid; i < n; i += kDecThreads) books[i] = src[i];
-      } else {
-        for (int i = tid; i < n; i += kDecThreads) books[i] = src[i];
+        i0 = n / 4 * 4;
+        for (int i = tid; i < n / 4; i += kDecThreads) {
+          float4 x = __ldg(reinterpret_cast<const float4 *>(src) + i);
+          x.x *= se;
+          x.y *= se;
+          x.z *= se;
+          x.w *= se;
+          reinterpret_cast<float4 *>(books)[i] = x;
+        }
       }
-      have = g;
+      for (int i = i0 + tid; i < n; i += kDecThreads) books[i] = src[i] * se;
       __syncthreads();
     }
     const int m = m0 + sub;
     const bool on = sub < ms;
     const float *book = SMEM ? books + (size_t)sub * a.book : a.C + (size_t)m * a.book;
-    // codes of the row ahead, so their latency hides behind this row's gathers
-    uint32_t cn[4];
+    uint32_t cn[kDecU][4];
     auto fetch = [&](int64_t b) {
-      const int64_t r = b * rb + warp * rw + lrow;
-      if (!on || b >= b1 || r >= a.rows) return;
-      const int64_t v = a.v0 + r;
-      if (a.cs.fmt == RQ_CODES_U16 && L == 2) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(a.cs.codes) + v * a.M + m);
-        cn[0] = a.cs.fix(w & 0xFFFFu);
-        cn[1] = a.cs.fix(w >> 16);
-      } else {
 #pragma unroll
-        for (int l = 0; l < 4; ++l)
-          if (l < L) cn[l] = a.cs(v, m * L + l);
+      for (int i = 0; i < kDecU; ++i) {
+        const int64_t r = b * rb + warp * rw + i * lr + lrow;
+        if (on && b < b1 && r < a.rows) row_codes(a.cs, L, a.M, a.v0 + r, m, cn[i]);
       }
     };
-    cn[0] = cn[1] = cn[2] = cn[3] = 0;
-    fetch(b0);
-    for (int64_t b = b0; b < b1; ++b) {
-      uint32_t c[4];
 #pragma unroll
-      for (int l = 0; l < 4; ++l) c[l] = cn[l];
+    for (int i = 0; i < kDecU; ++i) cn[i][0] = cn[i][1] = cn[i][2] = cn[i][3] = 0;
+    fetch(b0);
+    for (int64_t b = b0; b < b1 && b * rb < a.rows; ++b) {
+      uint32_t c[kDecU][4];
+#pragma unroll
+      for (int i = 0; i < kDecU; ++i)
+#pragma unroll
+        for (int l = 0; l < 4; ++l) c[i][l] = cn[i][l];
       fetch(b + 1);
       const int64_t r0 = b * rb + warp * rw;        // first row of this warp
-      const int64_t r = r0 + lrow;
-      if (on && r < a.rows) {
+#pragma unroll
+      for (int i = 0; i < kDecU; ++i) {
+        const int x = i * lr + lrow;
+        const int64_t r = r0 + x;
+        if (!on || r >= a.rows) continue;
         __half *oh = DS == 0 && a.direct ? a.hi + r * a.pitch + (int64_t)m * ds
-                                         : strip + (size_t)lrow * a.strip + sub * ds;
+                                         : strip + (size_t)x * a.strip + sub * ds;
         __half *ol = DS == 0 && a.direct ? a.lo + r * a.pitch + (int64_t)m * ds
                                          : oh + (size_t)rw * a.strip;
-        if (DS > 0) {
-          float e[DS > 0 ? DS : 1];
+        auto code = [&](int l) {
+          return l == 0 ? c[i][0] : l == 1 ? c[i][1] : l == 2 ? c[i][2] : l == 3 ? c[i][3]
+                                                 : a.cs(a.v0 + r, m * L + l);
+        };
+        if (DS > 0 && DS % 2 == 0) {
+          float2 e[DS > 1 ? DS / 2 : 1];
 #pragma unroll
-          for (int j = 0; j < DS; ++j) e[j] = 0.f;
+          for (int j = 0; j < DS / 2; ++j) e[j] = make_float2(0.f, 0.f);
+#pragma unroll 2
           for (int l = 0; l < L; ++l) {
-            const uint32_t cl = l == 0 ? c[0] : l == 1 ? c[1] : l == 2 ? c[2] : l == 3 ? c[3]
-                                              : a.cs(a.v0 + r, m * L + l);
-            const float *w = book + ((size_t)l * K + cl) * DS;
-            if (SMEM && DS % 2 == 0) {
+            const float *w = book + ((size_t)l * K + code(l)) * DS;
 #pragma unroll
-              for (int j = 0; j < DS; j += 2) {
-                const float2 x = *reinterpret_cast<const float2 *>(w + j);
-                e[j] = __fadd_rn(e[j], x.x);
-                e[j + 1 < DS ? j + 1 : j] = __fadd_rn(e[j + 1 < DS ? j + 1 : j], x.y);
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < DS; ++j) e[j] = __fadd_rn(e[j], w[j]);
+            for (int j = 0; j < DS / 2; ++j) {
+              const float2 y = SMEM ? *reinterpret_cast<const float2 *>(w + 2 * j)
+                                    : make_float2(w[2 * j], w[2 * j + 1]);
+              e[j].x = __fadd_rn(e[j].x, y.x);
+              e[j].y = __fadd_rn(e[j].y, y.y);
             }
           }
 #pragma unroll
-          for (int j = 0; j < DS; ++j) split_f16(__fmul_rn(e[j], se), oh[j], ol[j]);
+          for (int j = 0; j < DS / 2; ++j) {
+            if (!SMEM) e[j] = make_float2(__fmul_rn(e[j].x, se), __fmul_rn(e[j].y, se));
+            const __half2 h = __floats2half2_rn(e[j].x, e[j].y);
+            const float2 f = __half22float2(h);
+            reinterpret_cast<__half2 *>(oh)[j] = h;
+            reinterpret_cast<__half2 *>(ol)[j] =
+                __floats2half2_rn(__fsub_rn(e[j].x, f.x), __fsub_rn(e[j].y, f.y));
+          }
         } else {
+#pragma unroll(DS > 0 ? DS : 1)
           for (int j = 0; j < ds; ++j) {
             float e = 0.f;
-            for (int l = 0; l < L; ++l) {
-              const uint32_t cl = l == 0 ? c[0] : l == 1 ? c[1] : l == 2 ? c[2] : l == 3 ? c[3]
-                                                : a.cs(a.v0 + r, m * L + l);
-              e = __fadd_rn(e, book[((size_t)l * K + cl) * ds + j]);
-            }
-            split_f16(__fmul_rn(e, se), oh[j], ol[j]);
+            for (int l = 0; l < L; ++l) e = __fadd_rn(e, book[((size_t)l * K + code(l)) * ds + j]);
+            split_f16(SMEM ? e : __fmul_rn(e, se), oh[j], ol[j]);
           }
         }
       }
       if (DS == 0 && a.direct) continue;
       __syncwarp();
-      // the strips out: `n` halves a row and plane from column m0 ds on
-      const int n = ms * ds;
-      if (a.vec == 16 && ms == gs) {
-        const int per = n / 8, both = 2 * rw * per;
-        for (int i = lane; i < both; i += 32) {
-          const int pl = i / (rw * per), x = i - pl * rw * per, lr = x / per, q = x - lr * per;
-          if (r0 + lr < a.rows) {
-            __half *o = (pl ? a.lo : a.hi) + (r0 + lr) * a.pitch + (int64_t)m0 * ds + q * 8;
-            *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(
-                strip + ((size_t)pl * rw + lr) * a.strip + q * 8);
+      // the strips out, from column m0 ds on
+      if (a.vec && ms == gs) {
+        int q = q0, x = x0;
+        for (int i = lane; i < vecs; i += 32) {
+          if (r0 + x < a.rows) {
+            const int64_t o = (r0 + x) * a.pitch + (int64_t)m0 * ds + q * 8;
+            const uint4 *src = reinterpret_cast<const uint4 *>(strip) + i;
+            *reinterpret_cast<uint4 *>(a.hi + o) = src[0];
+            *reinterpret_cast<uint4 *>(a.lo + o) = src[vecs];
+          }
+          q += dq;
+          x += dx;
+          if (q >= per) {
+            q -= per;
+            ++x;
           }
         }
       } else {
-        const int both = 2 * rw * n;
+        const int n = ms * ds, both = 2 * rw * n;
         for (int i = lane; i < both; i += 32) {
-          const int pl = i / (rw * n), x = i - pl * rw * n, lr = x / n, q = x - lr * n;
-          if (r0 + lr < a.rows)
-            ((pl ? a.lo : a.hi) + (r0 + lr) * a.pitch + (int64_t)m0 * ds)[q] =
-                strip[((size_t)pl * rw + lr) * a.strip + q];
+          const int pl = i / (rw * n), y = i - pl * rw * n, x = y / n, q = y - x * n;
+          if (r0 + x < a.rows)
+            ((pl ? a.lo : a.hi) + (r0 + x) * a.pitch + (int64_t)m0 * ds)[q] =
+                strip[((size_t)pl * rw + x) * a.strip + q];
         }
       }
       __syncwarp();
     }
-    u += b1 - b0;
   }
 }
 
@@ -577,15 +615,16 @@ cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, 
   a.hi = hi;
   a.lo = lo;
   const int64_t book = (int64_t)L * cs.K * ds;
-  const bool in_smem = book * 4 <= 200 * 1024;
+  const auto strips = [&](int g) -> size_t {
+    return ds > 32 ? 0 : (size_t)(kDecThreads / 32) * 2 * kDecU * (32 / g) * ((g * ds + 7) / 8 * 8) * 2;
+  };
+  const bool in_smem = (size_t)book * 4 + strips(1) <= 220 * 1024;
   // as many subspaces (a power of two up to a warp's lanes) as their
   // codebooks fit beside the strips
   int gs = 1;
   size_t smem = 0;
-  auto strip_of = [&](int g) { return (g * ds + 7) / 8 * 8; };
   auto bytes_of = [&](int g) {
-    return (in_smem ? ((size_t)g * book * 4 + 15) / 16 * 16 : 0) +
-           (ds > 32 ? 0 : (size_t)(kDecThreads / 32) * 2 * (32 / g) * strip_of(g) * 2);
+    return (in_smem ? ((size_t)g * book * 4 + 15) / 16 * 16 : 0) + strips(g);
   };
   while (gs < 32 && gs * 2 <= M && bytes_of(gs * 2) <= 220 * 1024) gs *= 2;
   smem = bytes_of(gs);
@@ -596,18 +635,32 @@ cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, 
   a.book = in_smem ? (int)book : 0;
   if (!in_smem && book > 0x7fffffff) return cudaErrorInvalidValue;
   if (!in_smem) a.book = (int)book;
-  a.strip = strip_of(gs);
-  a.vec = (gs * ds) % 8 == 0 ? 16 : 2;
+  a.strip = (gs * ds + 7) / 8 * 8;
+  a.vec = (gs * ds) % 8 == 0;
   a.quad = (reinterpret_cast<uintptr_t>(C) & 15) == 0 && (gs * book) % 4 == 0;
   const void *fn = in_smem ? decode_fn<true>(ds) : decode_fn<false>(ds);
   cudaError_t e = ensure_smem_limit(fn, di.device, smem);
   if (e != cudaSuccess) return e;
   const int occ = occupancy_cached(fn, di.device, kDecThreads, smem);
-  const int rb = 32 / gs * (kDecThreads / 32);
-  const int64_t total = (rows + rb - 1) / rb * a.groups;
-  const int64_t cap = (int64_t)di.sms * occ;
+  const int rb = kDecU * (32 / gs) * (kDecThreads / 32);
+  const int64_t ctas = (int64_t)di.sms * occ, blocks = (rows + rb - 1) / rb;
+  // rows per chunk: the fewest steps of the last CTA, with the load of the
+  // books (about 300 rows' worth) counted per item
+  int64_t best = 0, chunk = 1;
+  for (int64_t c = 1; c <= blocks && c * rb <= 4096; ++c) {
+    const int64_t waves = ((blocks + c - 1) / c * a.groups + ctas - 1) / ctas;
+    const int64_t cost = waves * (c * rb + 300);
+    if (best == 0 || cost < best) {
+      best = cost;
+      chunk = c;
+    }
+  }
+  a.chunk = (int)(chunk * rb);
+  const int64_t items = (blocks + chunk - 1) / chunk * a.groups;
+  if (items > 0x7fffffff) return cudaErrorInvalidValue;
+  a.items = (int)items;
   void *args[] = {&a};
-  return launch_maybe_pdl(fn, dim3((unsigned)(total < cap ? total : cap)), dim3(kDecThreads), smem,
+  return launch_maybe_pdl(fn, dim3((unsigned)(items < ctas ? items : ctas)), dim3(kDecThreads), smem,
                           s, args, false);
 }
 

@@ -109,7 +109,7 @@ FEW = [
 MANY = [
     (4096, 32, 6, 2, 256, 33, "f", "u8", 1.0, 30.0),
     (4099, 32, 6, 2, 1024, 65, "f", "u16", 1.0, 30.0),
-    (33000, 24, 8, 2, 100, 128, "b", "u16", 1.0, 30.0),
+    (32768, 24, 8, 2, 100, 128, "b", "u16", 1.0, 30.0),
     (40961, 16, 5, 3, 200, 129, "f", "u16", 1.3, 0.0),
     (1, 4, 2, 1, 1, 70, "f", "u16", 1.0, 30.0),
     (300, 7, 3, 1, 16, 200, "b", "u16", 4.0, 30.0),
@@ -208,23 +208,51 @@ def test_one_code_for_every_row(N):
     x.check()
 
 
-def test_index():
+@pytest.mark.parametrize("K,skew", [(40, 0.0), (600, 0.0), (600, 0.5), (3, 0.9)])
+def test_index(K, skew):
     """The index lists each row once per column, under its code, in order."""
-    x = Head(8192 + 77, 3, 2, 1, 40, 1)
-    raw = x.index.cpu().numpy()
-    unit, off_at, code_at = 16384 + 96 + 80, 16384, 16384 + 96
-    assert raw.size == 2 * 3 * unit
-    codes = x.codes.view(x.V, 3).cpu().numpy()
-    for b, n in ((0, 8192), (1, 77)):
-        for p in range(3):
-            u = raw[(b * 3 + p) * unit:][:unit]
-            lst, off = u[:2 * n].view(np.uint16), u[off_at:off_at + 82].view(np.uint16)
-            code = u[code_at:code_at + 80].view(np.uint16)
-            assert sorted(code) == list(range(40)) and off[0] == 0 and off[40] == n
-            assert (np.diff(np.diff(off.astype(int))) <= 0).all()
-            for s in range(40):
-                want = np.nonzero(codes[b * 8192:b * 8192 + n, p] == code[s])[0]
-                assert np.array_equal(lst[off[s]:off[s + 1]], want)
+    R, cap, P = 8192, 32, 3
+    x = Head(R + 77, P, 2, 1, K, 1)
+    codes = x.codes.view(x.V, P)
+    codes[torch.rand(x.V, P, generator=x.g, device="cuda") < skew] = K // 2
+    x.packed = codes.to(torch.int16).view(torch.uint16)
+    raw = rq.rq_prepare_grad(x.packed, rq.U16, x.d).cpu().numpy()
+    up = lambda n, a: (n + a - 1) // a * a  # noqa: E731
+    g = 1
+    while g < 32 and K * g < 512:
+        g *= 2
+    ns = (K * g + 31) // 32
+    code_at = up(2 * ns + 2, 16)
+    over_at = code_at + up(2 * K, 16)
+    entry_at = up(over_at + 2 * (R // (g * (cap - 1) + 1) + 2), 64)
+    unit = entry_at + up(2 * (R + 32 * cap + (32 * ns if g > 1 else 0)), 64)
+    assert raw.size == 2 * P * unit == rq.rq_grad_index_bytes(x.d)
+    codes = codes.cpu().numpy()
+    for b, n in ((0, R), (1, 77)):
+        for p in range(P):
+            u = raw[(b * P + p) * unit:][:unit].view(np.uint16)
+            off, code, over = u[:ns + 1].astype(int), u[code_at // 2:][:K], u[over_at // 2:]
+            entry = u[entry_at // 2:]
+            assert sorted(code) == list(range(K)) and off[0] == 0
+            seen = 0
+            for s in range(K):
+                lanes = []
+                for vl in range(s * g, s * g + g):
+                    sl = vl // 32
+                    lane = entry[32 * off[sl]:32 * off[sl + 1]].reshape(-1, 32)[:, vl % 32]
+                    lanes.append(lane[lane < R])
+                    assert (lane[len(lanes[-1]):] == R).all()
+                got = np.full(g * max(map(len, lanes)) if lanes else 0, R)
+                for i, lane in enumerate(lanes):
+                    got[i::g][:len(lane)] = lane
+                got = got[got < R]
+                if s < over[0]:
+                    rest = entry[32 * off[ns]:][over[1 + s]:over[2 + s]]
+                    got = np.concatenate([got, rest])
+                want = np.nonzero(codes[b * R:b * R + n, p] == code[s])[0]
+                assert np.array_equal(got, want)
+                seen += len(got)
+            assert seen == n
 
 
 @pytest.mark.parametrize("N", [3, 150])
