@@ -40,7 +40,6 @@ struct Problem {
   float cap;
   LossTargets t;
   int ds() const { return d.D / d.M; }
-  int P() const { return d.M * d.L; }
   CodeSrc src() const {
     CodeSrc c;
     c.codes = codes;
@@ -71,7 +70,7 @@ bool few_ok(const rq_dims &d, int N, int limit) {
   return (size_t)rq_lut_token_stride(g) * (d.D / d.M) * 4 <= 48 * 1024;
 }
 bool few_loss(const rq_dims &d, int N) { return few_ok(d, N, kFewTokens); }
-bool few_grad(const rq_dims &d, int N) { return few_ok(d, N, kFewTokensGrad) && d.D / d.M <= 256; }
+bool few_grad(const rq_dims &d, int N) { return few_ok(d, N, kFewTokensGrad) && d.D / d.M <= 128; }
 
 int64_t piece_rows(const rq_dims &d) { return d.V < kPieceRows ? d.V : kPieceRows; }
 int64_t pitch8(int64_t n) { return align_up(n, 8); }
@@ -96,11 +95,9 @@ int dh_splits(const rq_dims &d, int64_t n) {
   return s < 1 ? 1 : (int)s;
 }
 
-// Tokens in groups of W share one pass of the sums by code.
-int group_width(int N) { return N == 1 ? 1 : N == 2 ? 2 : 4; }
-
 struct FewLayout {
   size_t logits, stat, wide, sid, sq, f, dz, S, dhp, fused, fused_bytes, total;
+  int splits;
 };
 
 FewLayout few_layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
@@ -110,13 +107,14 @@ FewLayout few_layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
   x.stat = a.take((int64_t)loss_stat_parts(d.V) * N * 8);
   x.wide = a.take((int64_t)N * d.D * 4);
   if (grad) {
-    const int W = group_width(N), G = (N + W - 1) / W, P = d.M * d.L;
+    const int P = d.M * d.L;
+    x.splits = codebook_sum_splits(d.V, d.M, d.L, d.K, N);
     x.sid = a.take((int64_t)N * k * 4);
     x.sq = a.take((int64_t)N * k * 4);
     x.f = a.take((int64_t)N * 4);
-    x.dz = a.take((int64_t)G * d.V * W * 4);
-    x.S = a.take((int64_t)codebook_sum_slots(d.V, P) * P * d.K * W * 4);
-    x.dhp = a.take((int64_t)P * W * (d.D / d.M) * 4);
+    x.dz = a.take((int64_t)N * pitch8(d.V) * 4);
+    x.S = a.take((int64_t)(N + 1) / 2 * x.splits * P * d.K * 8);
+    x.dhp = a.take((int64_t)P * N * (d.D / d.M) * 4);
   }
   x.fused_bytes = rq_fused_workspace_bytes(d, N, fmt, 0);
   x.fused = a.take((int64_t)x.fused_bytes);
@@ -125,9 +123,10 @@ FewLayout few_layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
 }
 
 struct ManyLayout {
-  size_t amax, hh, hl, wh, wl, stat, y, sid, sq, f, zh, zl, dw, part, total;
+  size_t amax, hh, hl, wh, wl, stat, y, sid, sq, f, zh, zl, dw, cpart, part, total;
   int64_t hp, zp;      // row pitches: D and the piece's rows, in elements
   int64_t chunk;       // tokens per sweep
+  int csplits;         // shares of the codebooks' sums
 };
 
 ManyLayout many_layout(const rq_dims &d, int N, int k, bool grad) {
@@ -152,6 +151,8 @@ ManyLayout many_layout(const rq_dims &d, int N, int k, bool grad) {
     x.zh = a.take(n * x.zp * 2);
     x.zl = a.take(n * x.zp * 2);
     x.dw = a.take((int64_t)d.D * x.zp * 4);
+    x.csplits = codebook_rows_splits(d.V, rows, d.M, d.L, d.K, d.D / d.M);
+    x.cpart = a.take(x.csplits > 1 ? (int64_t)x.csplits * d.M * d.L * d.K * (d.D / d.M) * 4 : 0);
     // the last sweep may have fewer tokens and with them more splits
     int64_t part = dh_splits(d, n) * n;
     const int64_t last = N % n == 0 ? n : N % n;
@@ -316,13 +317,17 @@ cudaError_t many_grad(const Problem &q, const ManyLayout &x, const float *lse, c
         RQ_TRY(launch_loss_gemm(kGemmDw, planes(hh, hl, n, d.D, x.hp), planes(zh, zl, n, rows, x.zp),
                                 p, di, s));
         RQ_TRY(launch_codebook_rows(at<float>(ws, x.dw), x.zp, v0, rows, index, d.V, d.M, d.L, d.K,
-                                    q.ds(), n0 > 0 || v0 > 0, dC, di, s));
+                                    q.ds(), x.csplits, n0 > 0 || v0 > 0,
+                                    x.csplits > 1 ? at<float>(ws, x.cpart) : dC, di, s));
       }
     }
     if (dh)
       RQ_TRY(launch_loss_dh_sum(at<float>(ws, x.part), splits, n * x.hp, x.hp, n, d.D, q.bf16,
                                 static_cast<char *>(dh) + n0 * d.D * esz, s));
   }
+  if (dC && x.csplits > 1)
+    RQ_TRY(launch_codebook_join(at<float>(ws, x.cpart), x.csplits,
+                                (int64_t)d.M * d.L * d.K * q.ds(), dC, s));
   return cudaSuccess;
 }
 
@@ -330,20 +335,16 @@ cudaError_t few_gradients(const Problem &q, const FewLayout &x, const float *lse
                           const void *index, void *dh, float *dC, void *ws, const DevInfo &di,
                           cudaStream_t s) {
   const rq_dims &d = q.d;
-  const int W = group_width(q.N), G = (q.N + W - 1) / W, P = q.P();
+  const int64_t pitch = pitch8(d.V);
   int32_t *sid = at<int32_t>(ws, x.sid);
   float *sq = at<float>(ws, x.sq), *f = at<float>(ws, x.f), *dz = at<float>(ws, x.dz);
   float *S = at<float>(ws, x.S), *dhp = dh ? at<float>(ws, x.dhp) : nullptr;
   RQ_TRY(launch_loss_sparse(q.t, q.N, d.V, w, sid, sq, f, di.err, s));
   RQ_TRY(launch_loss_dz_small(at<float>(ws, x.logits), q.N, d.V, sid, sq, q.t.k, lse, f, q.t.beta,
-                              q.cap, W, dz, s));
-  for (int g = 0; g < G; ++g) {
-    const int t0 = g * W, nt = q.N - t0 < W ? q.N - t0 : W;
-    RQ_TRY(launch_codebook_sums(dz + (size_t)g * d.V * W, W, index, d.V, P, d.K, S, di, s));
-    RQ_TRY(launch_codebook_finish(S, d.V, W, q.h, q.bf16, t0, nt, q.C, d.D, d.M, d.L, d.K,
-                                  g > 0, dC, dhp, s));
-    if (dh) RQ_TRY(launch_codebook_dh(dhp, W, t0, nt, d.D, d.M, d.L, q.bf16, dh, s));
-  }
+                              q.cap, dz, pitch, s));
+  RQ_TRY(launch_codebook_sums(dz, pitch, q.N, index, d.V, d.M, d.L, d.K, S, di, s));
+  RQ_TRY(launch_codebook_finish(S, x.splits, q.h, q.bf16, q.N, q.C, d.D, d.M, d.L, d.K, dC, dhp, s));
+  if (dh) RQ_TRY(launch_codebook_dh(dhp, q.N, d.D, d.M, d.L, q.bf16, dh, s));
   return cudaSuccess;
 }
 

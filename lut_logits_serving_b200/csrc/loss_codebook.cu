@@ -26,15 +26,12 @@
 //                            entries that follow the slices
 //   uint16 entry[]           rows, local numbers, ascending per lane
 //
-// Two uses.  launch_codebook_rows sums the rows of a piece's dE^T [D][rows]
-// (the tensor cores' h^T dz); launch_codebook_sums, for a few tokens, sums the
-// logits' gradients themselves, S[p][k][t] = sum of dz[v][t], from which both
-// gradients follow without the V x D matrix of either kind:
+// Two uses of one kernel.  launch_codebook_rows sums the rows of a piece's
+// dE^T [D][rows] (the tensor cores' h^T dz); launch_codebook_sums, for a few
+// tokens, sums the logits' gradients themselves, S[p][k][t] = sum of dz[t][v],
+// from which both gradients follow without the V x D matrix of either kind:
 //   dC[m][l][k] = sum_t S[p][k][t] h_t (subspace m)
 //   dh_t (subspace m) = sum_l sum_k S[p][k][t] C[m][l][k]
-// Both keep the block's values in shared memory and gather them from there;
-// the gathers' bank conflicts (random rows: about 3.4 passes per word) bound
-// them.
 #include "loss_common.cuh"
 
 namespace rq {
@@ -69,21 +66,6 @@ __host__ __device__ inline IndexShape index_shape(int64_t V, int P, int K) {
   x.unit = x.entry_at +
            (size_t)align_up((rows + 32 * kCap + (x.lanes > 1 ? 32 * x.slices : 0)) * 2, 64);
   return x;
-}
-
-struct Unit {
-  const uint16_t *off, *code, *over, *entry;
-};
-
-__device__ __forceinline__ Unit unit_at(const void *index, const IndexShape &x, int block, int p) {
-  const unsigned char *b =
-      static_cast<const unsigned char *>(index) + ((size_t)block * x.P + p) * x.unit;
-  Unit u;
-  u.off = reinterpret_cast<const uint16_t *>(b);
-  u.code = reinterpret_cast<const uint16_t *>(b + x.code_at);
-  u.over = reinterpret_cast<const uint16_t *>(b + x.over_at);
-  u.entry = reinterpret_cast<const uint16_t *>(b + x.entry_at);
-  return u;
 }
 
 // One block takes `cols` adjacent columns of a block of rows, staged column by
@@ -211,288 +193,315 @@ __global__ void __launch_bounds__(256) prepare_grad_kernel(const CodeSrc cs, con
   });
 }
 
-// Sums by code of one unit into stage [K][W]: get(row, acc) adds a row's W
-// values.  Called by every thread of the block; the stage may be read after
-// it, up to the next __syncthreads.  (Sums added to global memory code by code
-// from here cost several times the gathers: every lane its own sector.  The
-// stage lets them go out in code order, whole lines at a time.)
-template <int W, int THREADS, typename Get>
-__device__ __forceinline__ void unit_sums(const Unit &u, const IndexShape &x, float *stage,
-                                          Get &&get) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = x.lanes;
-  const int full = __ldg(u.over);
-  for (int sl = warp; sl < x.slices; sl += THREADS / 32) {
-    const int a = __ldg(u.off + sl), n = __ldg(u.off + sl + 1) - a;
-    const uint16_t *e = u.entry + a * 32 + lane;
-    const int s = (sl * 32 + lane) / g;
-    const int c = s < x.K ? __ldg(u.code + s) : 0;
-    float acc[W];
-#pragma unroll
-    for (int j = 0; j < W; ++j) acc[j] = 0.f;
-    // eight entries at a time, those past the slice's end naming the zero row
-    for (int i = 0; i < n; i += 8) {
-      int r[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) r[q] = i + q < n ? __ldg(e + (i + q) * 32) : kGradRows;
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (i + q < n) get(r[q], acc);
-    }
-    for (int o = g / 2; o > 0; o >>= 1)
-#pragma unroll
-      for (int j = 0; j < W; ++j) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
-    if (lane % g == 0 && s < x.K) {
-#pragma unroll
-      for (int j = 0; j < W; ++j) stage[c * W + j] = acc[j];
-    }
-  }
-  __syncthreads();
-  if (full == 0) return;
-  const uint16_t *rest = u.entry + __ldg(u.off + x.slices) * 32;
-  for (int s = warp; s < full; s += THREADS / 32) {
-    const int a = __ldg(u.over + 1 + s), b = __ldg(u.over + 2 + s);
-    if (a == b) continue;
-    float acc[W];
-#pragma unroll
-    for (int j = 0; j < W; ++j) acc[j] = 0.f;
-    for (int i = a + lane; i < b; i += 32) get(__ldg(rest + i), acc);
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
-    if (lane == 0) {
-      const int c = __ldg(u.code + s);
-#pragma unroll
-      for (int j = 0; j < W; ++j) stage[c * W + j] += acc[j];
-    }
-  }
-  __syncthreads();
-}
-
-// ------------------------------------------------------------- rows of dE^T
+// ------------------------------------------------------------- sums by code
 //
-// CTA (subspace m, slab of up to 3 dims[, level]): walks the piece's blocks,
-// copies the slab's rows of dE^T (contiguous, kGradRows floats a dim) into
-// shared memory and, per level, sums them by code into dC, whose part of this
-// CTA nobody else touches.  Slabs of 3 dims leave room for two CTAs per SM, so
-// one copies while the other gathers.
-constexpr int kSlab = 3;
-constexpr int kSlabPitch = kGradRows + 4;    // the row of zeros, vectors kept whole
-constexpr int kGatherThreads = 512;
+// A CTA takes a pair of value rows [2][V] (two dims of a subspace, or two
+// tokens) and the subspace's L columns, and walks the blocks: per block the
+// values (64 KB) and per column the unit (21 KB at K = 1024) arrive by bulk
+// copies, each into the buffer that the step before last left, so that the
+// copies run under the gathers.  A warp has a slice, a lane a list; the sums
+// of all blocks are kept in shared memory and leave once.  (First version,
+// sums added in global memory list by list: 3.8 ms where the gathers alone
+// need 0.5; without the pipeline 2.3 ms for the 768 columns and 2304 dims of
+// 256000 rows.)
+constexpr int kPairPitch = kGradRows + 4;    // the row of zeros, vectors kept whole
+constexpr int kGatherThreads = 1024;
 
-struct RowsArgs {
-  const float *dwt;
+struct GatherArgs {
+  const float *vals;        // value rows, `pitch` floats apart
   int64_t pitch;
-  int block0, blocks;
-  int64_t rows;         // of the piece
   const void *index;
   IndexShape x;
-  int L, ds, slabs, accumulate, by_level;
-  float *dC;
+  int64_t rows;             // of the values
+  int block0, blocks;       // index blocks they cover
+  int ds, pairs;            // value rows of one source, pairs of them
+  int L, by_level, splits;  // columns of a subspace, a unit per column, shares of the blocks
+  int per_subspace;         // value rows belong to the subspace (dims), else to all (tokens)
+  int units;
+  float *out;
+  int64_t out_p, out_k, out_split;   // strides: column, code, share
+  int64_t out_pair;                  // pair (0: its two columns lie at 2 pair)
+  int accumulate;
+  unsigned *err;
 };
 
-template <int W>
-__device__ __forceinline__ void rows_block(const RowsArgs &a, const float *vals, float *stage,
-                                           int b, int p, int j0) {
-  unit_sums<W, kGatherThreads>(unit_at(a.index, a.x, a.block0 + b, p), a.x, stage,
-                               [&](int r, float (&acc)[W]) {
-#pragma unroll
-                                 for (int j = 0; j < W; ++j) acc[j] += vals[j * kSlabPitch + r];
-                               });
-  float *dst = a.dC + (size_t)p * a.x.K * a.ds + j0;
-  const bool old = a.accumulate || b > 0;
-  const int n = a.x.K * W;
-#pragma unroll 6
-  for (int i = threadIdx.x; i < n; i += kGatherThreads) {
-    const int c = i / W, j = i - c * W;
-    float *d = dst + (size_t)c * a.ds + j;
-    *d = old ? *d + stage[i] : stage[i];
+struct GatherPos {          // one step: unit (subspace, pair, level range, share), block, level
+  int u, b, l, m, j, l0, l1, b0, b1;
+  __device__ __forceinline__ void unit(const GatherArgs &a, int unit) {
+    for (u = unit; u < a.units; u += gridDim.x) {
+      int r = u;
+      const int sp = r % a.splits;
+      r /= a.splits;
+      l0 = 0;
+      l1 = a.L;
+      if (a.by_level) {
+        l0 = r % a.L;
+        l1 = l0 + 1;
+        r /= a.L;
+      }
+      j = r % a.pairs * 2;
+      m = r / a.pairs;
+      b0 = a.blocks * sp / a.splits;
+      b1 = a.blocks * (sp + 1) / a.splits;
+      b = b0;
+      l = l0;
+      if (b0 < b1) return;      // a short last piece leaves shares empty
+    }
   }
+  __device__ __forceinline__ void next(const GatherArgs &a) {
+    if (++l < l1) return;
+    l = l0;
+    if (++b < b1) return;
+    unit(a, u + gridDim.x);
+  }
+};
+
+__global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(const GatherArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int K = a.x.K, g = a.x.lanes;
+  unsigned char *units = smem;                                     // [2] units
+  float *vals = reinterpret_cast<float *>(smem + 2 * a.x.unit);    // [2][2][kPairPitch]
+  float *stage = vals + 4 * kPairPitch;                            // [levels][K][2]
+  __shared__ uint64_t bars[4];                                     // units, values
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) mbar_init(smem_addr(&bars[i]), 1);
+    fence_mbar_init();
+  }
+  if (tid < 4) vals[tid * kPairPitch + kGradRows] = 0.f;
   __syncthreads();
-}
-
-__global__ void __launch_bounds__(kGatherThreads, 2) codebook_rows_kernel(const RowsArgs a) {
-  extern __shared__ __align__(16) float vals[];     // [kSlab][kSlabPitch], stage [K][kSlab]
-  float *stage = vals + kSlab * kSlabPitch;
-  const int tid = threadIdx.x;
-  const int m = blockIdx.x / a.slabs, j0 = blockIdx.x % a.slabs * kSlab;
-  const int w = a.ds - j0 < kSlab ? a.ds - j0 : kSlab;
-  const int l0 = a.by_level ? blockIdx.y : 0, l1 = a.by_level ? l0 + 1 : a.L;
-  if (tid < kSlab) vals[tid * kSlabPitch + kGradRows] = 0.f;
-  for (int b = 0; b < a.blocks; ++b) {
-    const int64_t r0 = (int64_t)b * kGradRows;
-    const int n = (int)(a.rows - r0 < kGradRows ? a.rows - r0 : kGradRows);
-    __syncthreads();
-    for (int j = 0; j < w; ++j) {
-      const float *src = a.dwt + (int64_t)(m * a.ds + j0 + j) * a.pitch + r0;
-#pragma unroll 5
-      for (int i = tid * 4; i < n; i += kGatherThreads * 4)   // the pitch covers whole vectors
-        *reinterpret_cast<float4 *>(vals + j * kSlabPitch + i) =
-            __ldg(reinterpret_cast<const float4 *>(src + i));
-    }
-    __syncthreads();
-    for (int l = l0; l < l1; ++l) {
-      const int p = m * a.L + l;
-      if (w == 3) rows_block<3>(a, vals, stage, b, p, j0);
-      else if (w == 2) rows_block<2>(a, vals, stage, b, p, j0);
-      else rows_block<1>(a, vals, stage, b, p, j0);
-    }
-  }
-}
-
-// ------------------------------------------------------------- sums of dz
-//
-// The (column, block) pairs, column by column, are dealt evenly to the CTAs; a
-// CTA goes through the blocks, holds one block's dz [rows][W] in shared memory
-// at a time and sums it for those of its columns whose share has the block.
-// A column that spans CTAs has a slot of S for each.
-struct SumsArgs {
-  const float *dz;
-  const void *index;
-  IndexShape x;
-  float *S;
-};
-
-constexpr int kSumsThreads = 1024;
-
-// CTA that holds pair i of `total` dealt to `ctas`.
-__host__ __device__ __forceinline__ int owner_of(int64_t i, int64_t total, int ctas) {
-  return (int)(((i + 1) * ctas - 1) / total);
-}
-__host__ __device__ __forceinline__ int sum_ctas(int64_t total) {
-  return (int)(total < 148 ? total : 148);
-}
-
-template <int W>
-__global__ void __launch_bounds__(kSumsThreads) codebook_sums_kernel(const SumsArgs a) {
-  extern __shared__ __align__(16) float vals[];     // [kGradRows + 1][W], stage [K][W]
-  float *stage = vals + (kGradRows + 1) * W;
-  const int tid = threadIdx.x, K = a.x.K, nb = a.x.blocks;
-  const int64_t total = (int64_t)a.x.P * nb;
-  const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
-  const int p0 = (int)(lo / nb), p1 = (int)((hi - 1) / nb);
-  if (tid < W) vals[kGradRows * W + tid] = 0.f;
-  for (int b = 0; b < nb; ++b) {
-    bool any = false;
-    for (int p = p0; p <= p1 && !any; ++p) {
-      const int64_t i = (int64_t)p * nb + b;
-      any = i >= lo && i < hi;
-    }
-    if (!any) continue;
-    const int64_t v0 = (int64_t)b * kGradRows;
-    const int n = (int)((a.x.V - v0 < kGradRows ? a.x.V - v0 : kGradRows) * W);
-    __syncthreads();
-    const float *src = a.dz + v0 * W;
-    for (int i = tid * 4; i + 3 < n; i += kSumsThreads * 4)
-      *reinterpret_cast<float4 *>(vals + i) = __ldg(reinterpret_cast<const float4 *>(src + i));
-    for (int i = n / 4 * 4 + tid; i < n; i += kSumsThreads) vals[i] = src[i];
-    __syncthreads();
-    for (int p = p0; p <= p1; ++p) {
-      const int64_t i = (int64_t)p * nb + b;
-      if (i < lo || i >= hi) continue;
-      const int mine = owner_of((int64_t)p * nb, total, gridDim.x);
-      float *S = a.S + ((size_t)(blockIdx.x - mine) * a.x.P + p) * K * W;
-      const bool old = i > lo && b > 0;            // this CTA has been here before
-      unit_sums<W, kSumsThreads>(
-          unit_at(a.index, a.x, b, p), a.x, stage, [&](int r, float (&acc)[W]) {
-            if (W == 4) {
-              const float4 y = *reinterpret_cast<const float4 *>(vals + r * 4);
-              acc[0] += y.x;
-              acc[W > 1 ? 1 : 0] += y.y;
-              acc[W > 2 ? 2 : 0] += y.z;
-              acc[W > 3 ? 3 : 0] += y.w;
-            } else if (W == 2) {
-              const float2 y = *reinterpret_cast<const float2 *>(vals + r * 2);
-              acc[0] += y.x;
-              acc[W > 1 ? 1 : 0] += y.y;
-            } else {
-              acc[0] += vals[r];
-            }
-          });
+  // copies of step `t` (values at a block's first level, `vt` blocks before)
+  auto issue = [&](const GatherPos &q, int t, int vt) {
+    const uint32_t ub = smem_addr(&bars[t & 1]);
+    mbar_arrive_expect_tx(ub, (uint32_t)a.x.unit);
+    bulk_g2s(smem_addr(units + (t & 1) * a.x.unit),
+             static_cast<const unsigned char *>(a.index) +
+                 ((size_t)(a.block0 + q.b) * a.x.P + q.m * a.L + q.l) * a.x.unit,
+             (uint32_t)a.x.unit, ub);
+    if (q.l != q.l0) return;
+    const int64_t r0 = (int64_t)q.b * kGradRows, left = a.rows - r0;
+    const uint32_t bytes = (uint32_t)align_up(left < kGradRows ? left : kGradRows, 4) * 4;
+    const int w = a.ds - q.j < 2 ? 1 : 2;
+    const uint32_t vb = smem_addr(&bars[2 + (vt & 1)]);
+    mbar_arrive_expect_tx(vb, bytes * w);
+    for (int i = 0; i < w; ++i)
+      bulk_g2s(smem_addr(vals + ((vt & 1) * 2 + i) * kPairPitch),
+               a.vals + (int64_t)((a.per_subspace ? q.m * a.ds : 0) + q.j + i) * a.pitch + r0, bytes,
+               vb);
+  };
+  GatherPos q, ahead;        // `ahead` is one step ahead (thread 0 issues for it)
+  q.unit(a, blockIdx.x);
+  ahead = q;
+  int t = 0, vt = 0, at_v = 0;   // steps, value blocks; value blocks issued
+  if (tid == 0 && q.u < a.units) issue(q, 0, 0);
+  bool to = false;
+  for (; q.u < a.units; ++t) {
+    // the next step's copies go into the buffers that the last step left
+    ahead.next(a);
+    if (ahead.u < a.units && ahead.l == ahead.l0) ++at_v;
+    if (tid == 0 && ahead.u < a.units) issue(ahead, t + 1, at_v);
+    const bool fresh = q.l == q.l0;
+    bool ok = mbar_wait_bounded(smem_addr(&bars[t & 1]), (uint32_t)(t >> 1) & 1u);
+    if (fresh)
+      ok = ok && mbar_wait_bounded(smem_addr(&bars[2 + (vt & 1)]), (uint32_t)(vt >> 1) & 1u);
+    const unsigned char *ub = units + (t & 1) * a.x.unit;
+    const uint16_t *off = reinterpret_cast<const uint16_t *>(ub);
+    const uint16_t *code = reinterpret_cast<const uint16_t *>(ub + a.x.code_at);
+    const uint16_t *over = reinterpret_cast<const uint16_t *>(ub + a.x.over_at);
+    const uint16_t *entry = reinterpret_cast<const uint16_t *>(ub + a.x.entry_at);
+    const float *v0 = vals + (vt & 1) * 2 * kPairPitch, *v1 = v0 + kPairPitch;
+    const bool two = a.ds - q.j > 1, first = q.b == q.b0;
+    float2 *st = reinterpret_cast<float2 *>(stage) + (size_t)(q.l - q.l0) * K;
+    int full = 0;
+    if (ok) {
+      full = over[0];
+      for (int sl = warp; sl < a.x.slices; sl += kGatherThreads / 32) {
+        const int e0 = off[sl], n = off[sl + 1] - e0;
+        const uint16_t *e = entry + e0 * 32 + lane;
+        const int s = (sl * 32 + lane) / g;
+        const int c = s < K ? code[s] : 0;
+        float s0 = 0.f, s1 = 0.f;
+        if (two) {
 #pragma unroll 4
-      for (int j = tid; j < K * W; j += kSumsThreads) S[j] = old ? S[j] + stage[j] : stage[j];
-      __syncthreads();
-    }
-  }
-}
-
-// One block per column p: S summed over its splits, dC (+)= S h and the
-// column's share of dh.
-template <int W>
-__global__ void __launch_bounds__(256) codebook_finish_kernel(
-    const float *__restrict__ S, int blocks, const void *h, int bf16, int t0, int nt,
-    const float *__restrict__ C, int D, int L, int K, int P, int ds, int accumulate, float *dC,
-    float *dhp) {
-  extern __shared__ float fin[];                    // [W][ds] hidden slices, [8][W][ds] partials
-  const int p = blockIdx.x, m = p / L, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t total = (int64_t)P * blocks, i0 = (int64_t)p * blocks;
-  const int ctas = sum_ctas(total);
-  const int slots = owner_of(i0 + blocks - 1, total, ctas) - owner_of(i0, total, ctas) + 1;
-  for (int i = tid; i < W * ds; i += 256) {
-    const int t = i / ds, j = i % ds;
-    fin[i] = t < nt ? load_h(h, bf16, (int64_t)(t0 + t) * D + (int64_t)m * ds + j) : 0.f;
-  }
-  __syncthreads();
-  // dims in steps of 2 so that their sums stay in registers
-  for (int j0 = 0; j0 < ds; j0 += 2) {
-    const int w = ds - j0 < 2 ? 1 : 2;
-    float part[W][2];
-#pragma unroll
-    for (int t = 0; t < W; ++t) part[t][0] = part[t][1] = 0.f;
-    for (int k = tid; k < K; k += 256) {
-      float s[W];
-#pragma unroll
-      for (int t = 0; t < W; ++t) s[t] = 0.f;
-      for (int x = 0; x < slots; ++x)
-#pragma unroll
-        for (int t = 0; t < W; ++t) s[t] += S[(((size_t)x * P + p) * K + k) * W + t];
-      for (int j = 0; j < w; ++j) {
-        const size_t at = ((size_t)p * K + k) * ds + j0 + j;
-        if (dC) {
-          float d = accumulate ? dC[at] : 0.f;
-#pragma unroll
-          for (int t = 0; t < W; ++t) d = fmaf(s[t], fin[t * ds + j0 + j], d);
-          dC[at] = d;
+          for (int i = 0; i < n; ++i) {
+            const int r = e[i * 32];
+            s0 += v0[r];
+            s1 += v1[r];
+          }
+        } else {
+#pragma unroll 4
+          for (int i = 0; i < n; ++i) s0 += v0[e[i * 32]];
         }
-        if (dhp) {
-          const float c = C[at];
+        for (int o = g / 2; o > 0; o >>= 1) {
+          s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+          s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+        }
+        if (lane % g == 0 && s < K) {
+          float2 d = first ? make_float2(0.f, 0.f) : st[c];
+          d.x += s0;
+          d.y += s1;
+          st[c] = d;
+        }
+      }
+      if (full > 0) {      // uniform: every thread reads the same unit
+        __syncthreads();
+        const uint16_t *rest = entry + off[a.x.slices] * 32;
+        for (int s = warp; s < full; s += kGatherThreads / 32) {
+          float s0 = 0.f, s1 = 0.f;
+          for (int i = over[1 + s] + lane; i < over[2 + s]; i += 32) {
+            const int r = rest[i];
+            s0 += v0[r];
+            if (two) s1 += v1[r];
+          }
 #pragma unroll
-          for (int t = 0; t < W; ++t) part[t][j] = fmaf(s[t], c, part[t][j]);
+          for (int o = 16; o > 0; o >>= 1) {
+            s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+            s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+          }
+          if (lane == 0) {
+            float2 d = st[code[s]];
+            d.x += s0;
+            d.y += s1;
+            st[code[s]] = d;
+          }
         }
       }
     }
-    if (dhp) {
-#pragma unroll
-      for (int t = 0; t < W; ++t)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float x = part[t][j];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-          if (lane == 0 && j < w) fin[(1 + warp) * W * ds + t * ds + j0 + j] = x;
-        }
+    if (__syncthreads_or(!ok)) {
+      to = true;
+      break;
     }
+    const GatherPos now = q;
+    q.next(a);
+    if (q.l == q.l0) ++vt;
+    if (q.u == now.u) continue;
+    // the unit's sums out, in code order
+    const int w = two ? 2 : 1, sp = now.u % a.splits;
+    for (int l = now.l0; l < now.l1; ++l) {
+      float *o = a.out + sp * a.out_split + (int64_t)(now.m * a.L + l) * a.out_p +
+                 (a.out_pair > 0 ? now.j / 2 * a.out_pair : now.j);
+      const float *src = stage + (size_t)(l - now.l0) * K * 2;
+#pragma unroll 2
+      for (int i = tid; i < K * w; i += kGatherThreads) {
+        const int c = w == 2 ? i >> 1 : i, j = w == 2 ? i & 1 : 0;
+        float *d = o + (int64_t)c * a.out_k + j;
+        *d = a.accumulate ? *d + src[c * 2 + j] : src[c * 2 + j];
+      }
+    }
+    __syncthreads();
   }
-  if (!dhp) return;
-  __syncthreads();
-  for (int i = tid; i < W * ds; i += 256) {
-    float x = 0.f;
-    for (int v = 0; v < 8; ++v) x += fin[(1 + v) * W * ds + i];
-    dhp[(size_t)p * W * ds + i] = x;
+  if (to && tid == 0) {
+    // the copies in flight land before the shared memory goes
+    mbar_wait_bounded(smem_addr(&bars[t & 1]), (uint32_t)(t >> 1) & 1u);
+    mbar_wait_bounded(smem_addr(&bars[2 + (vt & 1)]), (uint32_t)(vt >> 1) & 1u);
+    if (ahead.u < a.units) {
+      mbar_wait_bounded(smem_addr(&bars[(t + 1) & 1]), (uint32_t)((t + 1) >> 1) & 1u);
+      mbar_wait_bounded(smem_addr(&bars[2 + (at_v & 1)]), (uint32_t)(at_v >> 1) & 1u);
+    }
+    atomicOr(a.err, RQ_DEVERR_TIMEOUT);
   }
 }
 
-__global__ void __launch_bounds__(256) codebook_dh_kernel(const float *__restrict__ dhp, int W,
-                                                          int t0, int nt, int D, int L, int ds,
-                                                          int bf16, void *dh) {
+// out[i] (+)= sum over the shares of part[share][i]
+__global__ void __launch_bounds__(256) codebook_join_kernel(const float *__restrict__ part,
+                                                            int splits, int64_t n,
+                                                            float *__restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float s = part[i];
+  for (int x = 1; x < splits; ++x) s += part[x * n + i];
+  out[i] = s;
+}
+
+// One block per column p, for tokens [0, nt) in pairs: S [pair][split][p][K][2]
+// summed over its splits; dC = S h and the column's share of dh,
+// dhp[p][t][ds].
+constexpr int kFinThreads = 256;
+constexpr int kFinTokens = 4;        // tokens whose sums a thread holds at once
+
+__global__ void __launch_bounds__(kFinThreads) codebook_finish_kernel(
+    const float *__restrict__ S, int splits, const void *h, int bf16, int nt,
+    const float *__restrict__ C, int D, int L, int K, int P, int ds, float *dC, float *dhp) {
+  extern __shared__ float fin[];     // [nt][ds] hidden slices, [8][kFinTokens][ds] partials
+  const int p = blockIdx.x, m = p / L, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float *part = fin + nt * ds;
+  for (int i = tid; i < nt * ds; i += kFinThreads)
+    fin[i] = load_h(h, bf16, (int64_t)(i / ds) * D + (int64_t)m * ds + i % ds);
+  __syncthreads();
+  const int64_t pair = (int64_t)splits * P * K * 2;
+  for (int t0 = 0; t0 < nt; t0 += kFinTokens) {
+    const int n = nt - t0 < kFinTokens ? nt - t0 : kFinTokens;
+    // dims in steps of 2 so that their sums stay in registers
+    for (int j0 = 0; j0 < ds; j0 += 2) {
+      const int w = ds - j0 < 2 ? 1 : 2;
+      float dh[kFinTokens][2];
+#pragma unroll
+      for (int t = 0; t < kFinTokens; ++t) dh[t][0] = dh[t][1] = 0.f;
+      for (int k = tid; k < K; k += kFinThreads) {
+        float s[kFinTokens];
+#pragma unroll
+        for (int t = 0; t < kFinTokens; t += 2) {
+          float2 y = make_float2(0.f, 0.f);
+          if (t < n) {
+            const float *src = S + (t0 + t) / 2 * pair + ((int64_t)p * K + k) * 2;
+            for (int x = 0; x < splits; ++x) {
+              const float2 z = *reinterpret_cast<const float2 *>(src + (int64_t)x * P * K * 2);
+              y.x += z.x;
+              y.y += z.y;
+            }
+          }
+          s[t] = y.x;
+          s[t + 1] = t + 1 < n ? y.y : 0.f;
+        }
+        for (int j = 0; j < w; ++j) {
+          const int64_t at = ((int64_t)p * K + k) * ds + j0 + j;
+          if (dC) {
+            float d = t0 > 0 ? dC[at] : 0.f;
+#pragma unroll
+            for (int t = 0; t < kFinTokens; ++t)
+              if (t < n) d = fmaf(s[t], fin[(t0 + t) * ds + j0 + j], d);
+            dC[at] = d;
+          }
+          if (dhp) {
+            const float c = C[at];
+#pragma unroll
+            for (int t = 0; t < kFinTokens; ++t) dh[t][j] = fmaf(s[t], c, dh[t][j]);
+          }
+        }
+      }
+      if (dhp) {
+#pragma unroll
+        for (int t = 0; t < kFinTokens; ++t)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float x = dh[t][j];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (lane == 0 && j < w) part[(warp * kFinTokens + t) * ds + j0 + j] = x;
+          }
+      }
+    }
+    if (!dhp) continue;
+    __syncthreads();
+    for (int i = tid; i < n * ds; i += kFinThreads) {
+      float x = 0.f;
+      for (int v = 0; v < kFinThreads / 32; ++v) x += part[v * kFinTokens * ds + i];
+      dhp[((int64_t)p * nt + t0) * ds + i] = x;
+    }
+    __syncthreads();
+  }
+}
+
+__global__ void __launch_bounds__(256) codebook_dh_kernel(const float *__restrict__ dhp, int nt,
+                                                          int D, int L, int ds, int bf16,
+                                                          void *dh) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= (int64_t)nt * D) return;
   const int t = (int)(i / D), c = (int)(i % D), m = c / ds, j = c % ds;
   float x = 0.f;
-  for (int l = 0; l < L; ++l) x += dhp[((size_t)(m * L + l) * W + t) * ds + j];
-  const int64_t o = (int64_t)(t0 + t) * D + c;
-  if (bf16) static_cast<__nv_bfloat16 *>(dh)[o] = __float2bfloat16_rn(x);
-  else static_cast<float *>(dh)[o] = x;
+  for (int l = 0; l < L; ++l) x += dhp[((int64_t)(m * L + l) * nt + t) * ds + j];
+  if (bf16) static_cast<__nv_bfloat16 *>(dh)[i] = __float2bfloat16_rn(x);
+  else static_cast<float *>(dh)[i] = x;
 }
 
 }  // namespace
@@ -520,80 +529,131 @@ cudaError_t launch_prepare_grad(const CodeSrc &cs, void *index, const DevInfo &d
   return cudaGetLastError();
 }
 
-cudaError_t launch_codebook_rows(const float *dwt, int64_t pitch, int64_t v0, int64_t rows,
-                                 const void *index, int64_t V, int M, int L, int K, int ds,
-                                 bool accumulate, float *dC, const DevInfo &di, cudaStream_t s) {
-  RowsArgs a;
-  a.dwt = dwt;
-  a.pitch = pitch;
-  a.block0 = (int)(v0 / kGradRows);
-  a.blocks = (int)((rows + kGradRows - 1) / kGradRows);
-  a.rows = rows;
-  a.index = index;
-  a.x = index_shape(V, M * L, K);
-  a.L = L;
-  a.ds = ds;
-  a.slabs = (ds + kSlab - 1) / kSlab;
-  a.accumulate = accumulate ? 1 : 0;
-  a.dC = dC;
-  // few subspaces: a CTA per level, so that more SMs have work
-  a.by_level = M * a.slabs < 2 * di.sms ? 1 : 0;
-  const size_t smem = (size_t)kSlab * (kSlabPitch + K) * 4;
-  const void *fn = reinterpret_cast<const void *>(&codebook_rows_kernel);
-  cudaError_t e = ensure_smem_limit(fn, di.device, smem);
-  if (e != cudaSuccess) return e;
-  codebook_rows_kernel<<<dim3((unsigned)(M * a.slabs), a.by_level ? L : 1), kGatherThreads, smem,
-                         s>>>(a);
-  return cudaGetLastError();
+namespace {
+
+// Units of a gather and how they split: a column of its own where a subspace's
+// L sums do not fit, or where whole subspaces would leave SMs idle; then
+// shares of the blocks.
+struct GatherPlan {
+  bool by_level;
+  int splits;
+  int64_t units;
+  size_t smem;
+};
+
+GatherPlan gather_plan(const IndexShape &x, int blocks, int sources, int pairs, int L) {
+  GatherPlan p;
+  const auto bytes = [&](int levels) {
+    return 2 * x.unit + (size_t)4 * kPairPitch * 4 + (size_t)levels * x.K * 8;
+  };
+  p.units = (int64_t)sources * pairs;
+  p.by_level = L > 1 && (bytes(L) > 224 * 1024 || p.units < 148);
+  if (p.by_level) p.units *= L;
+  p.smem = bytes(p.by_level ? 1 : L);
+  p.splits = 1;
+  if (p.units < 148) {
+    const int64_t n = 148 / p.units;
+    p.splits = (int)(n < blocks ? n : blocks);
+  }
+  p.units *= p.splits;
+  return p;
 }
 
-int codebook_sum_slots(int64_t V, int P) {
-  const int blocks = (int)((V + kGradRows - 1) / kGradRows);
-  const int ctas = sum_ctas((int64_t)P * blocks);
-  return (ctas + P - 1) / P + 1;
-}
-
-cudaError_t launch_codebook_sums(const float *dz, int W, const void *index, int64_t V, int P, int K,
-                                 float *S, const DevInfo &di, cudaStream_t s) {
-  SumsArgs a;
-  a.dz = dz;
-  a.index = index;
-  a.x = index_shape(V, P, K);
-  a.S = S;
-  const size_t smem = (size_t)(kGradRows + 1 + K) * W * 4;
-  const void *fn = W == 1   ? reinterpret_cast<const void *>(&codebook_sums_kernel<1>)
-                   : W == 2 ? reinterpret_cast<const void *>(&codebook_sums_kernel<2>)
-                            : reinterpret_cast<const void *>(&codebook_sums_kernel<4>);
-  cudaError_t e = ensure_smem_limit(fn, di.device, smem);
+cudaError_t launch_gather(GatherArgs a, const GatherPlan &p, const DevInfo &di, cudaStream_t s) {
+  if (p.units > 0x7fffffff || p.smem > 226 * 1024) return cudaErrorInvalidValue;
+  a.by_level = p.by_level ? 1 : 0;
+  a.splits = p.splits;
+  a.units = (int)p.units;
+  a.err = di.err;
+  const void *fn = reinterpret_cast<const void *>(&codebook_gather_kernel);
+  cudaError_t e = ensure_smem_limit(fn, di.device, p.smem);
   if (e != cudaSuccess) return e;
   void *args[] = {&a};
-  return launch_maybe_pdl(fn, dim3((unsigned)sum_ctas((int64_t)P * a.x.blocks)), dim3(kSumsThreads),
-                          smem, s, args, false);
+  return launch_maybe_pdl(fn, dim3((unsigned)(p.units < di.sms ? p.units : di.sms)),
+                          dim3(kGatherThreads), p.smem, s, args, false);
 }
 
-cudaError_t launch_codebook_finish(const float *S, int64_t V, int W, const void *h, int bf16,
-                                   int t0, int nt, const float *C, int D, int M, int L, int K,
-                                   bool accumulate, float *dC, float *dhp, cudaStream_t s) {
-  const int ds = D / M, P = M * L, acc = accumulate ? 1 : 0;
-  const int blocks = (int)((V + kGradRows - 1) / kGradRows);
-  const size_t smem = (size_t)9 * W * ds * 4;
-  if (W == 1)
-    codebook_finish_kernel<1><<<P, 256, smem, s>>>(S, blocks, h, bf16, t0, nt, C, D, L, K, P, ds,
-                                                   acc, dC, dhp);
-  else if (W == 2)
-    codebook_finish_kernel<2><<<P, 256, smem, s>>>(S, blocks, h, bf16, t0, nt, C, D, L, K, P, ds,
-                                                   acc, dC, dhp);
-  else
-    codebook_finish_kernel<4><<<P, 256, smem, s>>>(S, blocks, h, bf16, t0, nt, C, D, L, K, P, ds,
-                                                   acc, dC, dhp);
+int blocks_of(int64_t rows) { return (int)((rows + kGradRows - 1) / kGradRows); }
+
+}  // namespace
+
+int codebook_rows_splits(int64_t V, int64_t rows, int M, int L, int K, int ds) {
+  return gather_plan(index_shape(V, M * L, K), blocks_of(rows), M, (ds + 1) / 2, L).splits;
+}
+
+cudaError_t launch_codebook_rows(const float *dwt, int64_t pitch, int64_t v0, int64_t rows,
+                                 const void *index, int64_t V, int M, int L, int K, int ds,
+                                 int splits, bool accumulate, float *out, const DevInfo &di,
+                                 cudaStream_t s) {
+  GatherArgs a = {};
+  a.vals = dwt;
+  a.pitch = pitch;
+  a.index = index;
+  a.x = index_shape(V, M * L, K);
+  a.rows = rows;
+  a.block0 = (int)(v0 / kGradRows);
+  a.blocks = blocks_of(rows);
+  a.ds = ds;
+  a.pairs = (ds + 1) / 2;
+  a.L = L;
+  a.per_subspace = 1;
+  a.out = out;
+  a.out_p = (int64_t)K * ds;
+  a.out_k = ds;
+  a.out_split = (int64_t)M * L * K * ds;
+  a.accumulate = accumulate ? 1 : 0;
+  GatherPlan p = gather_plan(a.x, a.blocks, M, a.pairs, L);
+  // a last piece of fewer blocks keeps the first piece's shares, some empty
+  p.units = p.units / p.splits * splits;
+  p.splits = splits;
+  return launch_gather(a, p, di, s);
+}
+
+cudaError_t launch_codebook_join(const float *part, int splits, int64_t n, float *dC,
+                                 cudaStream_t s) {
+  codebook_join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(part, splits, n, dC);
   return cudaGetLastError();
 }
 
-cudaError_t launch_codebook_dh(const float *dhp, int W, int t0, int nt, int D, int M, int L,
-                               int bf16, void *dh, cudaStream_t s) {
-  const int64_t n = (int64_t)nt * D;
-  codebook_dh_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(dhp, W, t0, nt, D, L, D / M, bf16,
-                                                                dh);
+int codebook_sum_splits(int64_t V, int M, int L, int K, int N) {
+  return gather_plan(index_shape(V, M * L, K), blocks_of(V), M, (N + 1) / 2, L).splits;
+}
+
+cudaError_t launch_codebook_sums(const float *dz, int64_t pitch, int N, const void *index, int64_t V,
+                                 int M, int L, int K, float *S, const DevInfo &di, cudaStream_t s) {
+  GatherArgs a = {};
+  a.vals = dz;
+  a.pitch = pitch;
+  a.index = index;
+  a.x = index_shape(V, M * L, K);
+  a.rows = V;
+  a.blocks = blocks_of(V);
+  a.ds = N;
+  a.pairs = (N + 1) / 2;
+  a.L = L;
+  a.out = S;
+  const GatherPlan p = gather_plan(a.x, a.blocks, M, a.pairs, L);
+  a.out_k = 2;
+  a.out_p = (int64_t)K * 2;
+  a.out_split = (int64_t)M * L * K * 2;
+  a.out_pair = p.splits * a.out_split;
+  return launch_gather(a, p, di, s);
+}
+
+cudaError_t launch_codebook_finish(const float *S, int splits, const void *h, int bf16, int N,
+                                   const float *C, int D, int M, int L, int K, float *dC,
+                                   float *dhp, cudaStream_t s) {
+  const int ds = D / M, P = M * L;
+  const size_t smem = (size_t)(N + kFinThreads / 32 * kFinTokens) * ds * 4;
+  codebook_finish_kernel<<<P, kFinThreads, smem, s>>>(S, splits, h, bf16, N, C, D, L, K, P, ds, dC,
+                                                      dhp);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_codebook_dh(const float *dhp, int N, int D, int M, int L, int bf16, void *dh,
+                               cudaStream_t s) {
+  const int64_t n = (int64_t)N * D;
+  codebook_dh_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(dhp, N, D, L, D / M, bf16, dh);
   return cudaGetLastError();
 }
 

@@ -176,32 +176,36 @@ cudaError_t launch_loss_fix_planes(const int32_t *sid, const float *sq, const fl
                                    const float *f, const float *amax, float T, float beta,
                                    float cap, __half *hi, __half *lo, int64_t pitch,
                                    cudaStream_t s);
-// logits [N][V] -> gradients in groups of W tokens, [ceil(N / W)][V][W], with
-// the listed ids' corrections
+// logits [N][V] -> their gradients [N][pitch], with the listed ids' corrections
 cudaError_t launch_loss_dz_small(const float *logits, int64_t N, int64_t V, const int32_t *sid,
                                  const float *sq, int k, const float *lse, const float *f,
-                                 float beta, float cap, int W, float *dz, cudaStream_t s);
+                                 float beta, float cap, float *dz, int64_t pitch, cudaStream_t s);
 cudaError_t launch_loss_dh_sum(const float *part, int splits, int64_t stride, int64_t pitch,
                                int64_t N, int D, int bf16, void *dh, cudaStream_t s);
 
 // Rows by code (loss_codebook.cu).
 size_t grad_index_bytes(int64_t V, int P, int K);
 cudaError_t launch_prepare_grad(const CodeSrc &cs, void *index, const DevInfo &di, cudaStream_t s);
-// dC (+)= the columns of dwt [D][pitch] (rows v0 .. v0 + rows of the
-// vocabulary, v0 % kGradRows == 0) summed by code
+// out[split] (+)= the columns of dwt [D][pitch] (rows v0 .. v0 + rows of the
+// vocabulary, v0 % kGradRows == 0) summed by code, each share of the piece's
+// blocks in an array like dC; with one share out is dC itself, else
+// launch_codebook_join adds them up
+int codebook_rows_splits(int64_t V, int64_t rows, int M, int L, int K, int ds);
 cudaError_t launch_codebook_rows(const float *dwt, int64_t pitch, int64_t v0, int64_t rows,
                                  const void *index, int64_t V, int M, int L, int K, int ds,
-                                 bool accumulate, float *dC, const DevInfo &di, cudaStream_t s);
-// S[slot][p][k][W] = sums of dz [V][W] by code; a column's blocks may be
-// shared by up to codebook_sum_slots CTAs, each with a slot of its own
-int codebook_sum_slots(int64_t V, int P);
-cudaError_t launch_codebook_sums(const float *dz, int W, const void *index, int64_t V, int P, int K,
-                                 float *S, const DevInfo &di, cudaStream_t s);
-// from S of tokens [t0, t0 + nt): dC (+)= S h, dhp[p][t][ds] = S C
-cudaError_t launch_codebook_finish(const float *S, int64_t V, int W, const void *h, int bf16,
-                                   int t0, int nt, const float *C, int D, int M, int L, int K,
-                                   bool accumulate, float *dC, float *dhp, cudaStream_t s);
-cudaError_t launch_codebook_dh(const float *dhp, int W, int t0, int nt, int D, int M, int L,
-                               int bf16, void *dh, cudaStream_t s);
+                                 int splits, bool accumulate, float *out, const DevInfo &di,
+                                 cudaStream_t s);
+cudaError_t launch_codebook_join(const float *part, int splits, int64_t n, float *dC,
+                                 cudaStream_t s);
+// S[pair][split][p][k][2] = sums of dz [N][pitch] by code, tokens in pairs
+int codebook_sum_splits(int64_t V, int M, int L, int K, int N);
+cudaError_t launch_codebook_sums(const float *dz, int64_t pitch, int N, const void *index, int64_t V,
+                                 int M, int L, int K, float *S, const DevInfo &di, cudaStream_t s);
+// from S: dC = S h, dhp[p][t][ds] = S C; dh from dhp
+cudaError_t launch_codebook_finish(const float *S, int splits, const void *h, int bf16, int N,
+                                   const float *C, int D, int M, int L, int K, float *dC,
+                                   float *dhp, cudaStream_t s);
+cudaError_t launch_codebook_dh(const float *dhp, int N, int D, int M, int L, int bf16, void *dh,
+                               cudaStream_t s);
 
 }  // namespace rq

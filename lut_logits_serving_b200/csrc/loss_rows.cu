@@ -519,34 +519,26 @@ __global__ void __launch_bounds__(256) loss_fix_planes_kernel(
 
 // ------------------------------------------------------------- few tokens
 
-template <int W>
 __global__ void __launch_bounds__(256) loss_dz_small_kernel(const float *__restrict__ logits,
-                                                            int64_t N, int64_t V,
+                                                            int64_t V,
                                                             const float *__restrict__ lse,
                                                             const float *__restrict__ f, float beta,
-                                                            float cap, float *__restrict__ dz) {
-  const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x, g = blockIdx.y;
-  if (v >= V) return;
-  float d[W];
-#pragma unroll
-  for (int t = 0; t < W; ++t) {
-    const int64_t n = g * W + t;
-    d[t] = n < N ? dz_at(logits[n * V + v], 0.f, lse[n], f[n], beta, cap) : 0.f;
-  }
-  float *o = dz + (g * V + v) * W;
-  if (W == 4) *reinterpret_cast<float4 *>(o) = make_float4(d[0], d[W > 1 ? 1 : 0], d[W > 2 ? 2 : 0], d[W > 3 ? 3 : 0]);
-  else if (W == 2) *reinterpret_cast<float2 *>(o) = make_float2(d[0], d[W > 1 ? 1 : 0]);
-  else o[0] = d[0];
+                                                            float cap, float *__restrict__ dz,
+                                                            int64_t pitch) {
+  const int64_t n = blockIdx.y;
+  const float l = lse[n], w = f[n];
+  for (int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x; v < pitch; v += (int64_t)gridDim.x * 256)
+    dz[n * pitch + v] = v < V ? dz_at(logits[n * V + v], 0.f, l, w, beta, cap) : 0.f;
 }
 
 __global__ void __launch_bounds__(256) loss_fix_small_kernel(
     const int32_t *__restrict__ sid, const float *__restrict__ sq, const float *__restrict__ logits,
     int k, int64_t count, int64_t V, const float *__restrict__ lse, const float *__restrict__ f,
-    float beta, float cap, int W, float *__restrict__ dz) {
+    float beta, float cap, float *__restrict__ dz, int64_t pitch) {
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= count || sid[i] < 0) return;
   const int64_t n = i / k, v = sid[i];
-  dz[((n / W) * V + v) * W + n % W] = dz_at(logits[n * V + v], sq[i], lse[n], f[n], beta, cap);
+  dz[n * pitch + v] = dz_at(logits[n * V + v], sq[i], lse[n], f[n], beta, cap);
 }
 
 __global__ void __launch_bounds__(256) loss_dh_sum_kernel(const float *__restrict__ part,
@@ -708,16 +700,13 @@ cudaError_t launch_loss_fix_planes(const int32_t *sid, const float *sq, const fl
 
 cudaError_t launch_loss_dz_small(const float *logits, int64_t N, int64_t V, const int32_t *sid,
                                  const float *sq, int k, const float *lse, const float *f,
-                                 float beta, float cap, int W, float *dz, cudaStream_t s) {
-  const dim3 grid(blocks_of(V, 256), (unsigned)((N + W - 1) / W));
-  if (W == 1) loss_dz_small_kernel<1><<<grid, 256, 0, s>>>(logits, N, V, lse, f, beta, cap, dz);
-  else if (W == 2) loss_dz_small_kernel<2><<<grid, 256, 0, s>>>(logits, N, V, lse, f, beta, cap, dz);
-  else if (W == 4) loss_dz_small_kernel<4><<<grid, 256, 0, s>>>(logits, N, V, lse, f, beta, cap, dz);
-  else return cudaErrorInvalidValue;
+                                 float beta, float cap, float *dz, int64_t pitch, cudaStream_t s) {
+  loss_dz_small_kernel<<<dim3(blocks_of(pitch, 1024), (unsigned)N), 256, 0, s>>>(
+      logits, V, lse, f, beta, cap, dz, pitch);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   loss_fix_small_kernel<<<blocks_of(N * k, 256), 256, 0, s>>>(sid, sq, logits, k, N * k, V, lse, f,
-                                                              beta, cap, W, dz);
+                                                              beta, cap, dz, pitch);
   return cudaGetLastError();
 }
 
