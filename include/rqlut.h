@@ -482,7 +482,7 @@ RQ_API int rq_distill_grad(const void *h, int h_bf16, const float *C, const void
  * library; run once per artifact (the codes stay fixed while codebooks and
  * hidden states train).
  *   codes (device) in format fmt, 16-byte aligned; index (device)
- *   rq_grad_index_bytes(d) bytes (about 2.4 per code plus 2 K per 8192
+ *   rq_grad_index_bytes(d) bytes (about 2.5 per code plus 2 K per 8192
  *   rows and column), 16-byte aligned, not overlapping codes.  An index holds
  *   for every layout of the same codes.
  * Supported: K <= 4096 (rq_grad_index_bytes is 0 above).

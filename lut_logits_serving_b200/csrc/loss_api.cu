@@ -73,7 +73,7 @@ bool few_loss(const rq_dims &d, int N) { return few_ok(d, N, kFewTokens); }
 bool few_grad(const rq_dims &d, int N) { return few_ok(d, N, kFewTokensGrad) && d.D / d.M <= 128; }
 
 int64_t piece_rows(const rq_dims &d) { return d.V < kPieceRows ? d.V : kPieceRows; }
-int64_t pitch8(int64_t n) { return align_up(n, 8); }
+int64_t pitch16(int64_t n) { return align_up(n, 16); }   // fp16 rows of whole sectors
 
 int total_parts(const rq_dims &d) {
   int n = 0;
@@ -112,7 +112,7 @@ FewLayout few_layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
     x.sid = a.take((int64_t)N * k * 4);
     x.sq = a.take((int64_t)N * k * 4);
     x.f = a.take((int64_t)N * 4);
-    x.dz = a.take((int64_t)N * pitch8(d.V) * 4);
+    x.dz = a.take((int64_t)N * pitch16(d.V) * 4);
     x.S = a.take((int64_t)(N + 1) / 2 * x.splits * P * d.K * 8);
     x.dhp = a.take((int64_t)P * N * (d.D / d.M) * 4);
   }
@@ -134,8 +134,8 @@ ManyLayout many_layout(const rq_dims &d, int N, int k, bool grad) {
   Arena a;
   const int64_t n = N < kTokenChunk ? N : kTokenChunk, rows = piece_rows(d);
   x.chunk = n;
-  x.hp = pitch8(d.D);
-  x.zp = pitch8(rows);
+  x.hp = pitch16(d.D);
+  x.zp = pitch16(rows);
   x.amax = a.take(3 * kAmaxBlocks * 4);
   x.hh = a.take(n * x.hp * 2);
   x.hl = a.take(n * x.hp * 2);
@@ -335,7 +335,7 @@ cudaError_t few_gradients(const Problem &q, const FewLayout &x, const float *lse
                           const void *index, void *dh, float *dC, void *ws, const DevInfo &di,
                           cudaStream_t s) {
   const rq_dims &d = q.d;
-  const int64_t pitch = pitch8(d.V);
+  const int64_t pitch = pitch16(d.V);
   int32_t *sid = at<int32_t>(ws, x.sid);
   float *sq = at<float>(ws, x.sq), *f = at<float>(ws, x.f), *dz = at<float>(ws, x.dz);
   float *S = at<float>(ws, x.S), *dhp = dh ? at<float>(ws, x.dhp) : nullptr;

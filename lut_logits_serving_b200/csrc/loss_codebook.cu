@@ -10,21 +10,21 @@
 //
 // Index.  The vocabulary is cut into blocks of kGradRows rows.  In a (block,
 // column) unit the rows of a code are dealt in turn to the code's g lanes (g a
-// power of two, so that K g fills some hundred lanes), the lanes are ordered by
+// power of two, so that K g fills a block's lanes), the lanes are ordered by
 // falling length and cut into slices of 32, one per warp, and a slice is
-// stored step by step: entry i of its 32 lanes side by side, a lane without an
-// i-th row naming row kGradRows, which holds zeros.  So a warp reads its
-// entries as whole 64-byte rows, ahead of their use, no lane waits for a
-// longer one (with K = 1024 a list has 9 rows on average; in code order the
-// longest of 32 would have 17), and there is no branch.  A lane holds at most
+// stored step by step: entries 2 i and 2 i + 1 of its 32 lanes side by side as
+// 32-bit words, a lane without a row there naming row kGradRows, which holds
+// zeros.  So a warp reads two entries a lane with one access and no conflict,
+// no lane waits for a longer one (with K = 1024 a list has 8 rows on average;
+// in code order the longest of 32 would have 16), and there is no branch.  A lane holds at most
 // kCap entries; what a code has beyond its g kCap (skewed codes) follows as a
 // plain list that one warp adds at the end.
-//   uint16 off[slices + 1]   in rows of 32 entries
+//   uint16 off[slices + 1]   in rows of 64 entries
 //   uint16 code[K]           slot s = lanes [s g, (s + 1) g)
 //   uint16 over[1 + n + 1]   over[0] = n codes (the first n slots) may have
 //                            more; theirs are [over[1 + s], over[2 + s]) of the
 //                            entries that follow the slices
-//   uint16 entry[]           rows, local numbers, ascending per lane
+//   uint16 entry[]           4 x the rows' local numbers, ascending per lane
 //
 // Two uses of one kernel.  launch_codebook_rows sums the rows of a piece's
 // dE^T [D][rows] (the tensor cores' h^T dz); launch_codebook_sums, for a few
@@ -53,18 +53,18 @@ __host__ __device__ inline IndexShape index_shape(int64_t V, int P, int K) {
   x.K = K;
   x.blocks = (int)((V + kGradRows - 1) / kGradRows);
   x.lanes = 1;
-  while (x.lanes < 32 && K * x.lanes < 512) x.lanes *= 2;
+  while (x.lanes < 32 && K * x.lanes < 1024) x.lanes *= 2;
   x.slices = (K * x.lanes + 31) / 32;
   const int rows = (int)(V < kGradRows ? V : kGradRows);
   x.most = rows / (x.lanes * (kCap - 1) + 1);
   x.code_at = (size_t)align_up((x.slices + 1) * 2, 16);
   x.over_at = x.code_at + (size_t)align_up(K * 2, 16);
-  x.entry_at = (size_t)align_up((int64_t)x.over_at + (x.most + 2) * 2, 64);
+  x.entry_at = (size_t)align_up((int64_t)x.over_at + (x.most + 2) * 2, 128);
   // a slice is as long as its first lane, no longer than the lanes of the slice
-  // before, give or take one where codes share lanes: rows + the first slice's
-  // padding + one row per slice
+  // before, give or take one where codes share lanes, and even: rows + the
+  // first slice's padding + 32 per slice, or 64
   x.unit = x.entry_at +
-           (size_t)align_up((rows + 32 * kCap + (x.lanes > 1 ? 32 * x.slices : 0)) * 2, 64);
+           (size_t)align_up((rows + 32 * kCap + (x.lanes > 1 ? 64 : 32) * x.slices) * 2, 128);
   return x;
 }
 
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(256) prepare_grad_kernel(const CodeSrc cs, con
   }
   __threadfence_block();
   __syncwarp();
-  const int total = scan(x.slices, [&](int s) { return kCap - key(code[s * 32 / g]); },
+  const int total = scan(x.slices, [&](int s) { return (kCap - key(code[s * 32 / g]) + 1) / 2; },
                          [&](int s, int at) { off[s] = (uint16_t)at; });
   if (lane == 0) off[x.slices] = (uint16_t)total;
   const int more = scan(full,
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(256) prepare_grad_kernel(const CodeSrc cs, con
     over[0] = (uint16_t)full;
     over[1 + full] = (uint16_t)more;
   }
-  for (int i = lane; i < total * 32; i += 32) entry[i] = (uint16_t)kGradRows;
+  for (int i = lane; i < total * 64; i += 32) entry[i] = (uint16_t)(4 * kGradRows);
   for (int i = lane; i < x.K; i += 32) cnt[i] = 0;
   __threadfence_block();
   __syncwarp();
@@ -183,12 +183,12 @@ __global__ void __launch_bounds__(256) prepare_grad_kernel(const CodeSrc cs, con
     __syncwarp(same);
     int at;
     if (e < g * kCap) {
-      const int vl = s * g + e % g;
-      at = (off[vl >> 5] + e / g) * 32 + (vl & 31);
+      const int vl = s * g + e % g, i = e / g;
+      at = ((off[vl >> 5] + i / 2) * 32 + (vl & 31)) * 2 + (i & 1);
     } else {
-      at = total * 32 + over[1 + s] + e - g * kCap;
+      at = total * 64 + over[1 + s] + e - g * kCap;
     }
-    entry[at] = (uint16_t)r;
+    entry[at] = (uint16_t)(4 * r);
     if ((same & below) == 0) cnt[c] = (uint16_t)(e + __popc(same));
   });
 }
@@ -200,7 +200,9 @@ __global__ void __launch_bounds__(256) prepare_grad_kernel(const CodeSrc cs, con
 // values (64 KB) and per column the unit (21 KB at K = 1024) arrive by bulk
 // copies, each into the buffer that the step before last left, so that the
 // copies run under the gathers.  A warp has a slice, a lane a list; the sums
-// of all blocks are kept in shared memory and leave once.  (First version,
+// of all blocks are kept in shared memory and leave once.  An odd last row is
+// gathered beside what its buffer's other half holds (finite or not, it is
+// not stored).  (First version,
 // sums added in global memory list by list: 3.8 ms where the gathers alone
 // need 0.5; without the pipeline 2.3 ms for the 768 columns and 2304 dims of
 // 256000 rows.)
@@ -225,162 +227,203 @@ struct GatherArgs {
   unsigned *err;
 };
 
-struct GatherPos {          // one step: unit (subspace, pair, level range, share), block, level
-  int u, b, l, m, j, l0, l1, b0, b1;
-  __device__ __forceinline__ void unit(const GatherArgs &a, int unit) {
-    for (u = unit; u < a.units; u += gridDim.x) {
-      int r = u;
-      const int sp = r % a.splits;
-      r /= a.splits;
-      l0 = 0;
-      l1 = a.L;
-      if (a.by_level) {
-        l0 = r % a.L;
-        l1 = l0 + 1;
-        r /= a.L;
-      }
-      j = r % a.pairs * 2;
-      m = r / a.pairs;
-      b0 = a.blocks * sp / a.splits;
-      b1 = a.blocks * (sp + 1) / a.splits;
-      b = b0;
-      l = l0;
-      if (b0 < b1) return;      // a short last piece leaves shares empty
+struct GatherUnit {         // subspace, pair, levels, share of the blocks
+  int m, j, l0, l1, b0, b1, share;
+  __device__ __forceinline__ bool set(const GatherArgs &a, int u) {   // false: an empty share
+    share = u % a.splits;
+    int r = u / a.splits;
+    l0 = 0;
+    l1 = a.L;
+    if (a.by_level) {
+      l0 = r % a.L;
+      l1 = l0 + 1;
+      r /= a.L;
     }
+    j = r % a.pairs * 2;
+    m = r / a.pairs;
+    b0 = a.blocks * share / a.splits;
+    b1 = a.blocks * (share + 1) / a.splits;
+    return b0 < b1;
   }
-  __device__ __forceinline__ void next(const GatherArgs &a) {
-    if (++l < l1) return;
-    l = l0;
-    if (++b < b1) return;
-    unit(a, u + gridDim.x);
+};
+
+// The issuing thread's place in the same walk.
+struct GatherAhead {
+  GatherUnit q;
+  int u, b, l;
+  __device__ __forceinline__ void unit(const GatherArgs &a, int from) {
+    for (u = from; u < a.units; u += gridDim.x)
+      if (q.set(a, u)) break;      // a short last piece leaves shares empty
+    b = q.b0;
+    l = q.l0;
+  }
+  __device__ __forceinline__ void block(const GatherArgs &a) {
+    l = q.l0;
+    if (++b == q.b1) unit(a, u + gridDim.x);
+  }
+  __device__ __forceinline__ void step(const GatherArgs &a) {
+    if (++l == q.l1) block(a);
   }
 };
 
 __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(const GatherArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int K = a.x.K, g = a.x.lanes;
+  const int K = a.x.K, g = a.x.lanes, gsh = __ffs(g) - 1;
   unsigned char *units = smem;                                     // [2] units
   float *vals = reinterpret_cast<float *>(smem + 2 * a.x.unit);    // [2][2][kPairPitch]
-  float *stage = vals + 4 * kPairPitch;                            // [levels][K][2]
+  float2 *stage = reinterpret_cast<float2 *>(vals + 4 * kPairPitch);   // [levels][K]
   __shared__ uint64_t bars[4];                                     // units, values
+  __shared__ volatile int abort_flag;
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) mbar_init(smem_addr(&bars[i]), 1);
     fence_mbar_init();
+    abort_flag = 0;
   }
   if (tid < 4) vals[tid * kPairPitch + kGradRows] = 0.f;
   __syncthreads();
-  // copies of step `t` (values at a block's first level, `vt` blocks before)
-  auto issue = [&](const GatherPos &q, int t, int vt) {
-    const uint32_t ub = smem_addr(&bars[t & 1]);
-    mbar_arrive_expect_tx(ub, (uint32_t)a.x.unit);
-    bulk_g2s(smem_addr(units + (t & 1) * a.x.unit),
+  // thread 0 keeps the copies a step (units) and a block (values) ahead
+  GatherAhead nu, nv;
+  int it = 0, iv = 0;        // copies issued
+  auto issue_unit = [&]() {
+    if (nu.u >= a.units) return;
+    const uint32_t b = smem_addr(&bars[it & 1]);
+    mbar_arrive_expect_tx(b, (uint32_t)a.x.unit);
+    bulk_g2s(smem_addr(units + (it & 1) * a.x.unit),
              static_cast<const unsigned char *>(a.index) +
-                 ((size_t)(a.block0 + q.b) * a.x.P + q.m * a.L + q.l) * a.x.unit,
-             (uint32_t)a.x.unit, ub);
-    if (q.l != q.l0) return;
-    const int64_t r0 = (int64_t)q.b * kGradRows, left = a.rows - r0;
-    const uint32_t bytes = (uint32_t)align_up(left < kGradRows ? left : kGradRows, 4) * 4;
-    const int w = a.ds - q.j < 2 ? 1 : 2;
-    const uint32_t vb = smem_addr(&bars[2 + (vt & 1)]);
-    mbar_arrive_expect_tx(vb, bytes * w);
-    for (int i = 0; i < w; ++i)
-      bulk_g2s(smem_addr(vals + ((vt & 1) * 2 + i) * kPairPitch),
-               a.vals + (int64_t)((a.per_subspace ? q.m * a.ds : 0) + q.j + i) * a.pitch + r0, bytes,
-               vb);
+                 ((size_t)(a.block0 + nu.b) * a.x.P + nu.q.m * a.L + nu.l) * a.x.unit,
+             (uint32_t)a.x.unit, b);
+    ++it;
+    nu.step(a);
   };
-  GatherPos q, ahead;        // `ahead` is one step ahead (thread 0 issues for it)
-  q.unit(a, blockIdx.x);
-  ahead = q;
-  int t = 0, vt = 0, at_v = 0;   // steps, value blocks; value blocks issued
-  if (tid == 0 && q.u < a.units) issue(q, 0, 0);
-  bool to = false;
-  for (; q.u < a.units; ++t) {
-    // the next step's copies go into the buffers that the last step left
-    ahead.next(a);
-    if (ahead.u < a.units && ahead.l == ahead.l0) ++at_v;
-    if (tid == 0 && ahead.u < a.units) issue(ahead, t + 1, at_v);
-    const bool fresh = q.l == q.l0;
-    bool ok = mbar_wait_bounded(smem_addr(&bars[t & 1]), (uint32_t)(t >> 1) & 1u);
-    if (fresh)
-      ok = ok && mbar_wait_bounded(smem_addr(&bars[2 + (vt & 1)]), (uint32_t)(vt >> 1) & 1u);
-    const unsigned char *ub = units + (t & 1) * a.x.unit;
-    const uint16_t *off = reinterpret_cast<const uint16_t *>(ub);
-    const uint16_t *code = reinterpret_cast<const uint16_t *>(ub + a.x.code_at);
-    const uint16_t *over = reinterpret_cast<const uint16_t *>(ub + a.x.over_at);
-    const uint16_t *entry = reinterpret_cast<const uint16_t *>(ub + a.x.entry_at);
-    const float *v0 = vals + (vt & 1) * 2 * kPairPitch, *v1 = v0 + kPairPitch;
-    const bool two = a.ds - q.j > 1, first = q.b == q.b0;
-    float2 *st = reinterpret_cast<float2 *>(stage) + (size_t)(q.l - q.l0) * K;
-    int full = 0;
-    if (ok) {
-      full = over[0];
-      for (int sl = warp; sl < a.x.slices; sl += kGatherThreads / 32) {
-        const int e0 = off[sl], n = off[sl + 1] - e0;
-        const uint16_t *e = entry + e0 * 32 + lane;
-        const int s = (sl * 32 + lane) / g;
-        const int c = s < K ? code[s] : 0;
-        float s0 = 0.f, s1 = 0.f;
-        if (two) {
-#pragma unroll 4
-          for (int i = 0; i < n; ++i) {
-            const int r = e[i * 32];
-            s0 += v0[r];
-            s1 += v1[r];
+  auto issue_vals = [&]() {
+    if (nv.u >= a.units) return;
+    const int64_t r0 = (int64_t)nv.b * kGradRows, left = a.rows - r0;
+    const uint32_t bytes = (uint32_t)align_up(left < kGradRows ? left : kGradRows, 4) * 4;
+    const int w = a.ds - nv.q.j < 2 ? 1 : 2;
+    const uint32_t b = smem_addr(&bars[2 + (iv & 1)]);
+    mbar_arrive_expect_tx(b, bytes * w);
+    for (int i = 0; i < w; ++i)
+      bulk_g2s(smem_addr(vals + ((iv & 1) * 2 + i) * kPairPitch),
+               a.vals + (int64_t)((a.per_subspace ? nv.q.m * a.ds : 0) + nv.q.j + i) * a.pitch + r0,
+               bytes, b);
+    ++iv;
+    nv.block(a);
+  };
+  if (tid == 0) {
+    nu.unit(a, blockIdx.x);
+    nv = nu;
+    issue_unit();
+    issue_vals();
+  }
+  int t = 0, vt = 0;         // steps and blocks done
+  bool ok = true;
+  auto wait = [&](int i, int n) {
+    const uint32_t b = smem_addr(&bars[i]), parity = (uint32_t)(n >> 1) & 1u;
+    if (ok && !mbar_try_wait(b, parity) && !mbar_wait_bounded(b, parity)) {
+      ok = false;
+      abort_flag = 1;
+    }
+  };
+  for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
+    GatherUnit q;
+    if (!q.set(a, u)) continue;
+    const bool two = a.ds - q.j > 1;
+    for (int b = q.b0; b < q.b1; ++b, ++vt) {
+      for (int l = q.l0; l < q.l1; ++l, ++t) {
+        // the next copies go into the buffers that the last step (block) left
+        if (tid == 0) {
+          issue_unit();
+          if (l == q.l0) issue_vals();
+        }
+        wait(t & 1, t);
+        if (l == q.l0) wait(2 + (vt & 1), vt);
+        const unsigned char *ub = units + (t & 1) * a.x.unit;
+        const uint16_t *off = reinterpret_cast<const uint16_t *>(ub);
+        const uint16_t *code = reinterpret_cast<const uint16_t *>(ub + a.x.code_at);
+        const uint16_t *over = reinterpret_cast<const uint16_t *>(ub + a.x.over_at);
+        const uint32_t *entry = reinterpret_cast<const uint32_t *>(ub + a.x.entry_at) + lane;
+        const unsigned char *v0 =
+            reinterpret_cast<const unsigned char *>(vals + (vt & 1) * 2 * kPairPitch);
+        float2 *st = stage + (size_t)(l - q.l0) * K;
+        // one word of entries: two rows of either value row
+        auto add = [&](uint32_t w, float &s0, float &s1) {
+          const unsigned char *p = v0 + (w & 0xFFFFu), *r = v0 + (w >> 16);
+          s0 += *reinterpret_cast<const float *>(p);
+          s1 += *reinterpret_cast<const float *>(p + 4 * kPairPitch);
+          s0 += *reinterpret_cast<const float *>(r);
+          s1 += *reinterpret_cast<const float *>(r + 4 * kPairPitch);
+        };
+        int full = 0;
+        if (ok) {
+          full = over[0];
+          for (int sl = warp; sl < a.x.slices; sl += kGatherThreads / 32) {
+            const int e0 = off[sl], n = off[sl + 1] - e0;
+            const uint32_t *e = entry + e0 * 32;
+            const int s = (sl * 32 + lane) >> gsh;
+            float s0 = 0.f, s1 = 0.f;
+            int i = 0;
+            for (; i + 4 <= n; i += 4, e += 128) {
+              const uint32_t w0 = e[0], w1 = e[32], w2 = e[64], w3 = e[96];
+              add(w0, s0, s1);
+              add(w1, s0, s1);
+              add(w2, s0, s1);
+              add(w3, s0, s1);
+            }
+            if (i + 2 <= n) {
+              const uint32_t w0 = e[0], w1 = e[32];
+              add(w0, s0, s1);
+              add(w1, s0, s1);
+              e += 64;
+            }
+            if (n & 1) add(e[0], s0, s1);
+            for (int o = g >> 1; o > 0; o >>= 1) {
+              s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+              s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+            }
+            if ((lane & (g - 1)) == 0 && s < K) {
+              const int c = code[s];
+              if (b > q.b0) {
+                const float2 d = st[c];
+                s0 += d.x;
+                s1 += d.y;
+              }
+              st[c] = make_float2(s0, s1);
+            }
           }
-        } else {
-#pragma unroll 4
-          for (int i = 0; i < n; ++i) s0 += v0[e[i * 32]];
-        }
-        for (int o = g / 2; o > 0; o >>= 1) {
-          s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-          s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-        }
-        if (lane % g == 0 && s < K) {
-          float2 d = first ? make_float2(0.f, 0.f) : st[c];
-          d.x += s0;
-          d.y += s1;
-          st[c] = d;
-        }
-      }
-      if (full > 0) {      // uniform: every thread reads the same unit
-        __syncthreads();
-        const uint16_t *rest = entry + off[a.x.slices] * 32;
-        for (int s = warp; s < full; s += kGatherThreads / 32) {
-          float s0 = 0.f, s1 = 0.f;
-          for (int i = over[1 + s] + lane; i < over[2 + s]; i += 32) {
-            const int r = rest[i];
-            s0 += v0[r];
-            if (two) s1 += v1[r];
-          }
+          if (full > 0) {      // uniform: every thread reads the same unit
+            __syncthreads();
+            const uint16_t *rest =
+                reinterpret_cast<const uint16_t *>(ub + a.x.entry_at) + off[a.x.slices] * 64;
+            for (int s = warp; s < full; s += kGatherThreads / 32) {
+              float s0 = 0.f, s1 = 0.f;
+              for (int i = over[1 + s] + lane; i < over[2 + s]; i += 32) {
+                const unsigned char *p = v0 + rest[i];
+                s0 += *reinterpret_cast<const float *>(p);
+                s1 += *reinterpret_cast<const float *>(p + 4 * kPairPitch);
+              }
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-            s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-          }
-          if (lane == 0) {
-            float2 d = st[code[s]];
-            d.x += s0;
-            d.y += s1;
-            st[code[s]] = d;
+              for (int o = 16; o > 0; o >>= 1) {
+                s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+                s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+              }
+              if (lane == 0) {
+                const float2 d = st[code[s]];
+                st[code[s]] = make_float2(d.x + s0, d.y + s1);
+              }
+            }
           }
         }
+        __syncthreads();
+        if (abort_flag) goto out;
       }
     }
-    if (__syncthreads_or(!ok)) {
-      to = true;
-      break;
-    }
-    const GatherPos now = q;
-    q.next(a);
-    if (q.l == q.l0) ++vt;
-    if (q.u == now.u) continue;
     // the unit's sums out, in code order
-    const int w = two ? 2 : 1, sp = now.u % a.splits;
-    for (int l = now.l0; l < now.l1; ++l) {
-      float *o = a.out + sp * a.out_split + (int64_t)(now.m * a.L + l) * a.out_p +
-                 (a.out_pair > 0 ? now.j / 2 * a.out_pair : now.j);
-      const float *src = stage + (size_t)(l - now.l0) * K * 2;
+    const int w = two ? 2 : 1;
+    for (int l = q.l0; l < q.l1; ++l) {
+      float *o = a.out + q.share * a.out_split + (int64_t)(q.m * a.L + l) * a.out_p +
+                 (a.out_pair > 0 ? q.j / 2 * a.out_pair : q.j);
+      const float *src = reinterpret_cast<const float *>(stage + (size_t)(l - q.l0) * K);
 #pragma unroll 2
       for (int i = tid; i < K * w; i += kGatherThreads) {
         const int c = w == 2 ? i >> 1 : i, j = w == 2 ? i & 1 : 0;
@@ -390,13 +433,13 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
     }
     __syncthreads();
   }
-  if (to && tid == 0) {
+out:
+  if (abort_flag && tid == 0) {
     // the copies in flight land before the shared memory goes
-    mbar_wait_bounded(smem_addr(&bars[t & 1]), (uint32_t)(t >> 1) & 1u);
-    mbar_wait_bounded(smem_addr(&bars[2 + (vt & 1)]), (uint32_t)(vt >> 1) & 1u);
-    if (ahead.u < a.units) {
-      mbar_wait_bounded(smem_addr(&bars[(t + 1) & 1]), (uint32_t)((t + 1) >> 1) & 1u);
-      mbar_wait_bounded(smem_addr(&bars[2 + (at_v & 1)]), (uint32_t)(at_v >> 1) & 1u);
+    for (int i = 1; i <= 2; ++i) {
+      if (it >= i) mbar_wait_bounded(smem_addr(&bars[(it - i) & 1]), (uint32_t)((it - i) >> 1) & 1u);
+      if (iv >= i)
+        mbar_wait_bounded(smem_addr(&bars[2 + ((iv - i) & 1)]), (uint32_t)((iv - i) >> 1) & 1u);
     }
     atomicOr(a.err, RQ_DEVERR_TIMEOUT);
   }

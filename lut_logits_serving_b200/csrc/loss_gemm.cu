@@ -92,6 +92,13 @@ __device__ __forceinline__ void st16(uint32_t t, const float *r) {
       "f"(r[15]));
 }
 
+// 32 bytes, a whole sector, at once
+__device__ __forceinline__ void stg32(void *p, const uint32_t *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 __device__ __forceinline__ void wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -365,14 +372,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
               }
               if (in) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  if (col0 + j0 + 8 * j < g.dz_pitch) {
-                    *reinterpret_cast<uint4 *>(g.dz_hi + at + j0 + 8 * j) =
-                        *reinterpret_cast<uint4 *>(hi + 4 * j);
-                    *reinterpret_cast<uint4 *>(g.dz_lo + at + j0 + 8 * j) =
-                        *reinterpret_cast<uint4 *>(lo + 4 * j);
-                  }
+                if (col0 + j0 < g.dz_pitch) {      // the pitch is whole sectors
+                  stg32(g.dz_hi + at + j0, reinterpret_cast<const uint32_t *>(hi));
+                  stg32(g.dz_lo + at + j0, reinterpret_cast<const uint32_t *>(lo));
                 }
               }
             }
@@ -386,18 +388,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if ((MODE == kGemmDh || MODE == kGemmDw) && row < g.rows) {
         float *o = g.out + (int64_t)sp * g.out_split + (int64_t)row * g.out_pitch + col0;
 #pragma unroll
-        for (int j = 0; j < 128; j += 4) {
+        for (int j = 0; j < 128; j += 8) {
           if (col0 + j < g.out_pitch) {
-            float4 v = make_float4(acc[j] * inv, acc[j + 1] * inv, acc[j + 2] * inv,
-                                   acc[j + 3] * inv);
+            float v[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[x] = acc[j + x] * inv;
             if (MODE == kGemmDh && g.accumulate) {
-              const float4 w = *reinterpret_cast<const float4 *>(o + j);
-              v.x += w.x;
-              v.y += w.y;
-              v.z += w.z;
-              v.w += w.w;
+#pragma unroll
+              for (int x = 0; x < 8; x += 4) {
+                const float4 w = *reinterpret_cast<const float4 *>(o + j + x);
+                v[x] += w.x;
+                v[x + 1] += w.y;
+                v[x + 2] += w.z;
+                v[x + 3] += w.w;
+              }
             }
-            *reinterpret_cast<float4 *>(o + j) = v;
+            stg32(o + j, reinterpret_cast<const uint32_t *>(v));
           }
         }
       }

@@ -84,82 +84,96 @@ __global__ void __launch_bounds__(256) loss_widen_h_kernel(const __nv_bfloat16 *
 //
 // Rows v0 .. v0 + rows of E as scaled fp16 hi / lo planes.  A CTA keeps the
 // (scaled) codebooks of a group of gs subspaces in shared memory while it walks
-// a chunk of rows; each row costs L codes and L gathers of ds floats a
-// subspace.  The items go chunk by chunk, all groups of a chunk at about the
-// same time: a group writes 2 gs ds bytes of a row, and the L2 joins them to
-// whole sectors and lines only if the row's other groups follow before it
-// evicts them (groups at unrelated rows: 474 us for 32768 rows of 2304, of
-// which 320 were the scattered writes).  A lane has one subspace of two rows at a time: gs lanes share a
-// row, its results go through a strip of shared memory and leave as 16-byte
-// vectors; the codes of the next rows are fetched meanwhile.  Bound by the
-// random shared-memory gathers (16 lanes' 8-byte words meet about three times
-// in the fullest bank pair).
+// a chunk of rows.  A thread has one pair of dims of the group, the same for
+// all its rows: it fetches the row's L codes (a few rows ahead), gathers and
+// adds the pair's L codeword parts, splits the sums and stores one word to
+// each plane.  Neighbouring lanes read neighbouring words of a codeword (three
+// lanes for ds = 6), which spreads a warp's words over the banks better than a
+// lane per codeword, and their stores join; nothing is passed between threads.
+// The items go chunk by chunk, all groups of a chunk at about the same time: a
+// group writes 2 gs ds bytes of a row, and the L2 joins them to whole sectors
+// and lines only if the row's other groups follow before it evicts them
+// (groups at unrelated rows: 474 us for 32768 rows of 2304, of which 320 were
+// the scattered writes; a lane per codeword, results through a strip of shared
+// memory: 185 us).  Bound by the random shared-memory gathers.
 struct DecodeArgs {
   CodeSrc cs;
   const float *C;
   int M, L, ds, gs, groups;
-  int chunk, items;    // rows of an item (whole CTA blocks), (chunk, group) items
+  int chunk, items;    // rows of an item, (chunk, group) items
   int64_t v0, rows, pitch;
   const float *amax;
   __half *hi, *lo;
-  int vec;             // strips leave as 16-byte vectors
-  int book;            // floats of one subspace's codebooks, L K ds
-  int strip;           // halves of one row's strip, padded
+  int64_t book;        // floats of one subspace's codebooks, L K ds
   int quad;            // codebooks may be copied 16 bytes at a time
-  int direct;          // wide subspaces (ds > 32): no strips, each lane writes its own
 };
 
-constexpr int kDecThreads = 1024;  // 512 with two rows a lane: 256 us where this takes 185
-constexpr int kDecU = 1;           // rows a lane has in flight
+constexpr int kDecThreads = 1024;
+constexpr int kDecU = 4;           // rows a thread has in flight
 
-// The (up to four) codes of subspace m of row v.
-__device__ __forceinline__ void row_codes(const CodeSrc &cs, int L, int M, int64_t v, int m,
-                                          uint32_t (&c)[4]) {
-  if (L == 2 && cs.fmt == RQ_CODES_U16) {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(cs.codes) + v * M + m);
-    c[0] = cs.fix(w & 0xFFFFu);
-    c[1] = cs.fix(w >> 16);
-  } else if (L == 2 && cs.fmt == RQ_CODES_PACKED10) {
-    // bits [20 m, 20 m + 20) of the row, in three bytes
-    const uint8_t *b = static_cast<const uint8_t *>(cs.codes) + v * ((20LL * M + 7) / 8) + (20 * m >> 3);
-    const uint32_t w = ((uint32_t)__ldg(b) | (uint32_t)__ldg(b + 1) << 8 | (uint32_t)__ldg(b + 2) << 16) >>
-                       ((m & 1) * 4);
-    c[0] = cs.fix(w & 1023u);
-    c[1] = cs.fix(w >> 10 & 1023u);
-  } else {
+// The codes of subspace m of a row, fetched ahead: load() only issues loads
+// (an instruction on what they bring would wait for it), get() makes codes of
+// them.  LL = 0 (many levels): nothing is kept, codes are fetched when used.
+template <int LL>
+struct RowCodes {
+  uint32_t raw[LL == 0 ? 1 : LL == 2 ? 3 : LL];
+  __device__ __forceinline__ void load(const CodeSrc &cs, int M, int64_t v, int m) {
+    if (LL == 2 && cs.fmt == RQ_CODES_U16) {
+      raw[0] = __ldg(static_cast<const uint32_t *>(cs.codes) + v * M + m);
+    } else if (LL == 2 && cs.fmt == RQ_CODES_PACKED10) {
+      // bits [20 m, 20 m + 20) of the row, in three bytes
+      const uint8_t *b =
+          static_cast<const uint8_t *>(cs.codes) + v * ((20LL * M + 7) / 8) + (20 * m >> 3);
 #pragma unroll
-    for (int l = 0; l < 4; ++l)
-      if (l < L) c[l] = cs(v, m * L + l);
+      for (int i = 0; i < (LL == 2 ? 3 : 0); ++i) raw[i] = __ldg(b + i);
+    } else if (cs.fmt == RQ_CODES_U16) {
+#pragma unroll
+      for (int l = 0; l < LL; ++l)
+        raw[l] = __ldg(static_cast<const uint16_t *>(cs.codes) + v * cs.P + m * LL + l);
+    } else if (cs.fmt == RQ_CODES_U8) {
+#pragma unroll
+      for (int l = 0; l < LL; ++l)
+        raw[l] = __ldg(static_cast<const uint8_t *>(cs.codes) + v * cs.P + m * LL + l);
+    } else {
+#pragma unroll
+      for (int l = 0; l < LL; ++l) raw[l] = cs(v, m * LL + l);
+    }
   }
-}
+  __device__ __forceinline__ uint32_t get(const CodeSrc &cs, int m, int l) const {
+    if (LL == 2 && cs.fmt == RQ_CODES_U16) return cs.fix(l == 0 ? raw[0] & 0xFFFFu : raw[0] >> 16);
+    if (LL == 2 && cs.fmt == RQ_CODES_PACKED10) {
+      const uint32_t w = (raw[0] | raw[LL == 2 ? 1 : 0] << 8 | raw[LL == 2 ? 2 : 0] << 16) >> ((m & 1) * 4);
+      return cs.fix(w >> (10 * l) & 1023u);
+    }
+    return cs.fix(raw[LL > 0 ? l : 0]);
+  }
+};
 
-template <int DS, bool SMEM>
+// EVEN: ds is even, so the pair lies in one subspace; else its dims may belong
+// to two, and each fetches its own codes.
+template <int LL, bool EVEN, bool SMEM>
 __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeArgs a) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  const int ds = DS > 0 ? DS : a.ds, gs = a.gs, L = a.L, K = a.cs.K;
-  float *books = reinterpret_cast<float *>(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int lr = 32 / gs, rw = lr * kDecU;          // rows a warp takes at once
-  const size_t book_bytes = SMEM ? ((size_t)gs * a.book * 4 + 15) / 16 * 16 : 0;
-  __half *strip = reinterpret_cast<__half *>(smem + book_bytes) + (size_t)warp * 2 * rw * a.strip;
-  const float se = scale_e(a.amax, L);
-  const int sub = lane % gs, lrow = lane / gs;
-  const int rb = rw * (kDecThreads / 32);
-  // 16-byte vectors of a plane's strip: this lane's first, and the step to its next
-  const int per = gs * ds / 8, vecs = rw * per;
-  const int q0 = per > 0 ? lane % per : 0, x0 = per > 0 ? lane / per : 0;
-  const int dq = per > 0 ? 32 % per : 0, dx = per > 0 ? 32 / per : 0;
+  extern __shared__ __align__(16) float books[];
+  const int ds = a.ds, L = LL > 0 ? LL : a.L, K = a.cs.K, tid = threadIdx.x;
+  const float se = scale_e(a.amax, a.L);
+  const int words = (a.gs * ds + 1) / 2;            // pairs of a row's group
+  const int rstep = kDecThreads / words;            // rows the CTA takes at once
+  const int w = tid % words, lrow = tid / words;
+  const int sub = 2 * w / ds, sub1 = EVEN ? sub : (2 * w + 1) / ds;
+  const int j = 2 * w - sub * ds, j1 = 2 * w + 1 - sub1 * ds;
   for (int u = blockIdx.x; u < a.items; u += gridDim.x) {
     const int g = u % a.groups;
-    const int64_t b0 = (int64_t)(u / a.groups) * (a.chunk / rb), b1 = b0 + a.chunk / rb;
-    const int m0 = g * gs, ms = a.M - m0 < gs ? a.M - m0 : gs;
+    const int64_t r0 = (int64_t)(u / a.groups) * a.chunk;
+    const int64_t r1 = r0 + a.chunk < a.rows ? r0 + a.chunk : a.rows;
+    const int m0 = g * a.gs, ms = a.M - m0 < a.gs ? a.M - m0 : a.gs;
     if (SMEM) {
       __syncthreads();
-      const float *src = a.C + (size_t)m0 * a.book;
-      const int n = ms * a.book;
+      const float *src = a.C + m0 * a.book;
+      const int n = (int)(ms * a.book);
       int i0 = 0;
       if (a.quad) {
         i0 = n / 4 * 4;
+#pragma unroll 4
         for (int i = tid; i < n / 4; i += kDecThreads) {
           float4 x = __ldg(reinterpret_cast<const float4 *>(src) + i);
           x.x *= se;
@@ -172,103 +186,68 @@ __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeAr
       for (int i = i0 + tid; i < n; i += kDecThreads) books[i] = src[i] * se;
       __syncthreads();
     }
-    const int m = m0 + sub;
-    const bool on = sub < ms;
-    const float *book = SMEM ? books + (size_t)sub * a.book : a.C + (size_t)m * a.book;
-    uint32_t cn[kDecU][4];
-    auto fetch = [&](int64_t b) {
+    if (lrow >= rstep || sub >= ms) continue;
+    const bool second = EVEN || sub1 < ms;          // an odd last pair has one dim
+    const float *b0 = (SMEM ? books + sub * a.book : a.C + (m0 + sub) * a.book) + j;
+    const float *b1 = (SMEM ? books + sub1 * a.book : a.C + (m0 + sub1) * a.book) + j1;
+    const int m = m0 + sub, m1 = m0 + sub1;
+    __half *oh = a.hi + (int64_t)m0 * ds + 2 * w, *ol = a.lo + (int64_t)m0 * ds + 2 * w;
+    RowCodes<LL> cn[kDecU], dn[EVEN ? 1 : kDecU];
+    auto fetch = [&](int64_t r) {
 #pragma unroll
       for (int i = 0; i < kDecU; ++i) {
-        const int64_t r = b * rb + warp * rw + i * lr + lrow;
-        if (on && b < b1 && r < a.rows) row_codes(a.cs, L, a.M, a.v0 + r, m, cn[i]);
+        const int64_t x = r + (int64_t)i * rstep;
+        if (LL > 0 && x < r1) {
+          cn[i].load(a.cs, a.M, a.v0 + x, m);
+          if (!EVEN && second) dn[EVEN ? 0 : i].load(a.cs, a.M, a.v0 + x, m1);
+        }
       }
     };
-#pragma unroll
-    for (int i = 0; i < kDecU; ++i) cn[i][0] = cn[i][1] = cn[i][2] = cn[i][3] = 0;
-    fetch(b0);
-    for (int64_t b = b0; b < b1 && b * rb < a.rows; ++b) {
-      uint32_t c[kDecU][4];
-#pragma unroll
-      for (int i = 0; i < kDecU; ++i)
-#pragma unroll
-        for (int l = 0; l < 4; ++l) c[i][l] = cn[i][l];
-      fetch(b + 1);
-      const int64_t r0 = b * rb + warp * rw;        // first row of this warp
+    fetch(r0 + lrow);
+    for (int64_t r = r0 + lrow; r < r1; r += (int64_t)kDecU * rstep) {
+      RowCodes<LL> c[kDecU], d[EVEN ? 1 : kDecU];
 #pragma unroll
       for (int i = 0; i < kDecU; ++i) {
-        const int x = i * lr + lrow;
-        const int64_t r = r0 + x;
-        if (!on || r >= a.rows) continue;
-        __half *oh = DS == 0 && a.direct ? a.hi + r * a.pitch + (int64_t)m * ds
-                                         : strip + (size_t)x * a.strip + sub * ds;
-        __half *ol = DS == 0 && a.direct ? a.lo + r * a.pitch + (int64_t)m * ds
-                                         : oh + (size_t)rw * a.strip;
-        auto code = [&](int l) {
-          return l == 0 ? c[i][0] : l == 1 ? c[i][1] : l == 2 ? c[i][2] : l == 3 ? c[i][3]
-                                                 : a.cs(a.v0 + r, m * L + l);
-        };
-        if (DS > 0 && DS % 2 == 0) {
-          float2 e[DS > 1 ? DS / 2 : 1];
+        c[i] = cn[i];
+        if (!EVEN) d[EVEN ? 0 : i] = dn[EVEN ? 0 : i];
+      }
+      fetch(r + (int64_t)kDecU * rstep);
 #pragma unroll
-          for (int j = 0; j < DS / 2; ++j) e[j] = make_float2(0.f, 0.f);
-#pragma unroll 2
-          for (int l = 0; l < L; ++l) {
-            const float *w = book + ((size_t)l * K + code(l)) * DS;
-#pragma unroll
-            for (int j = 0; j < DS / 2; ++j) {
-              const float2 y = SMEM ? *reinterpret_cast<const float2 *>(w + 2 * j)
-                                    : make_float2(w[2 * j], w[2 * j + 1]);
-              e[j].x = __fadd_rn(e[j].x, y.x);
-              e[j].y = __fadd_rn(e[j].y, y.y);
+      for (int i = 0; i < kDecU; ++i) {
+        const int64_t x = r + (int64_t)i * rstep;
+        if (x >= r1) break;
+        float e0 = 0.f, e1 = 0.f;
+#pragma unroll(LL > 0 ? LL : 1)
+        for (int l = 0; l < L; ++l) {
+          const uint32_t cl = LL > 0 ? c[i].get(a.cs, m, l) : a.cs(a.v0 + x, m * L + l);
+          const float *p0 = b0 + (int64_t)(l * K + (int)cl) * ds;
+          if (EVEN && SMEM) {
+            const float2 y = *reinterpret_cast<const float2 *>(p0);
+            e0 = __fadd_rn(e0, y.x);
+            e1 = __fadd_rn(e1, y.y);
+          } else {
+            e0 = __fadd_rn(e0, *p0);
+            if (EVEN) {
+              e1 = __fadd_rn(e1, p0[1]);
+            } else if (second) {
+              const uint32_t dl = LL > 0 ? d[EVEN ? 0 : i].get(a.cs, m1, l)
+                                         : a.cs(a.v0 + x, m1 * L + l);
+              e1 = __fadd_rn(e1, b1[(int64_t)(l * K + (int)dl) * ds]);
             }
           }
-#pragma unroll
-          for (int j = 0; j < DS / 2; ++j) {
-            if (!SMEM) e[j] = make_float2(__fmul_rn(e[j].x, se), __fmul_rn(e[j].y, se));
-            const __half2 h = __floats2half2_rn(e[j].x, e[j].y);
-            const float2 f = __half22float2(h);
-            reinterpret_cast<__half2 *>(oh)[j] = h;
-            reinterpret_cast<__half2 *>(ol)[j] =
-                __floats2half2_rn(__fsub_rn(e[j].x, f.x), __fsub_rn(e[j].y, f.y));
-          }
-        } else {
-#pragma unroll(DS > 0 ? DS : 1)
-          for (int j = 0; j < ds; ++j) {
-            float e = 0.f;
-            for (int l = 0; l < L; ++l) e = __fadd_rn(e, book[((size_t)l * K + code(l)) * ds + j]);
-            split_f16(SMEM ? e : __fmul_rn(e, se), oh[j], ol[j]);
-          }
         }
+        if (!SMEM) {
+          e0 = __fmul_rn(e0, se);
+          e1 = __fmul_rn(e1, se);
+        }
+        const __half2 h = __floats2half2_rn(e0, e1);
+        const float2 f = __half22float2(h);
+        const __half2 lw = __floats2half2_rn(__fsub_rn(e0, f.x), __fsub_rn(e1, f.y));
+        // rows are padded to whole vectors, so a pair past D has its place; a
+        // group starts on a pair unless gs ds is odd (one group then)
+        *reinterpret_cast<__half2 *>(oh + x * a.pitch) = h;
+        *reinterpret_cast<__half2 *>(ol + x * a.pitch) = lw;
       }
-      if (DS == 0 && a.direct) continue;
-      __syncwarp();
-      // the strips out, from column m0 ds on
-      if (a.vec && ms == gs) {
-        int q = q0, x = x0;
-        for (int i = lane; i < vecs; i += 32) {
-          if (r0 + x < a.rows) {
-            const int64_t o = (r0 + x) * a.pitch + (int64_t)m0 * ds + q * 8;
-            const uint4 *src = reinterpret_cast<const uint4 *>(strip) + i;
-            *reinterpret_cast<uint4 *>(a.hi + o) = src[0];
-            *reinterpret_cast<uint4 *>(a.lo + o) = src[vecs];
-          }
-          q += dq;
-          x += dx;
-          if (q >= per) {
-            q -= per;
-            ++x;
-          }
-        }
-      } else {
-        const int n = ms * ds, both = 2 * rw * n;
-        for (int i = lane; i < both; i += 32) {
-          const int pl = i / (rw * n), y = i - pl * rw * n, x = y / n, q = y - x * n;
-          if (r0 + x < a.rows)
-            ((pl ? a.lo : a.hi) + (r0 + x) * a.pitch + (int64_t)m0 * ds)[q] =
-                strip[((size_t)pl * rw + x) * a.strip + q];
-        }
-      }
-      __syncwarp();
     }
   }
 }
@@ -577,17 +556,14 @@ cudaError_t launch_loss_widen_h(const void *h, int64_t n, float *out, cudaStream
 }
 
 namespace {
-template <bool SMEM>
-const void *decode_fn(int ds) {
-  switch (ds) {
-    case 2: return reinterpret_cast<const void *>(&loss_decode_kernel<2, SMEM>);
-    case 3: return reinterpret_cast<const void *>(&loss_decode_kernel<3, SMEM>);
-    case 4: return reinterpret_cast<const void *>(&loss_decode_kernel<4, SMEM>);
-    case 5: return reinterpret_cast<const void *>(&loss_decode_kernel<5, SMEM>);
-    case 6: return reinterpret_cast<const void *>(&loss_decode_kernel<6, SMEM>);
-    case 8: return reinterpret_cast<const void *>(&loss_decode_kernel<8, SMEM>);
+template <bool EVEN, bool SMEM>
+const void *decode_fn(int L) {
+  switch (L) {
+    case 1: return reinterpret_cast<const void *>(&loss_decode_kernel<1, EVEN, SMEM>);
+    case 2: return reinterpret_cast<const void *>(&loss_decode_kernel<2, EVEN, SMEM>);
+    case 3: return reinterpret_cast<const void *>(&loss_decode_kernel<3, EVEN, SMEM>);
   }
-  return reinterpret_cast<const void *>(&loss_decode_kernel<0, SMEM>);
+  return reinterpret_cast<const void *>(&loss_decode_kernel<0, EVEN, SMEM>);
 }
 }  // namespace
 
@@ -606,49 +582,48 @@ cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, 
   a.amax = amax;
   a.hi = hi;
   a.lo = lo;
-  const int64_t book = (int64_t)L * cs.K * ds;
-  const auto strips = [&](int g) -> size_t {
-    return ds > 32 ? 0 : (size_t)(kDecThreads / 32) * 2 * kDecU * (32 / g) * ((g * ds + 7) / 8 * 8) * 2;
-  };
-  const bool in_smem = (size_t)book * 4 + strips(1) <= 220 * 1024;
-  // as many subspaces (a power of two up to a warp's lanes) as their
-  // codebooks fit beside the strips
-  int gs = 1;
-  size_t smem = 0;
-  auto bytes_of = [&](int g) {
-    return (in_smem ? ((size_t)g * book * 4 + 15) / 16 * 16 : 0) + strips(g);
-  };
-  while (gs < 32 && gs * 2 <= M && bytes_of(gs * 2) <= 220 * 1024) gs *= 2;
-  smem = bytes_of(gs);
-  if (smem > 225 * 1024) return cudaErrorInvalidValue;
-  a.gs = gs;
-  a.direct = ds > 32;
-  a.groups = (M + gs - 1) / gs;
-  a.book = in_smem ? (int)book : 0;
-  if (!in_smem && book > 0x7fffffff) return cudaErrorInvalidValue;
-  if (!in_smem) a.book = (int)book;
-  a.strip = (gs * ds + 7) / 8 * 8;
-  a.vec = (gs * ds) % 8 == 0;
-  a.quad = (reinterpret_cast<uintptr_t>(C) & 15) == 0 && (gs * book) % 4 == 0;
-  const void *fn = in_smem ? decode_fn<true>(ds) : decode_fn<false>(ds);
+  a.book = (int64_t)L * cs.K * ds;
+  // as many subspaces as their codebooks fit in shared memory, at most a pair
+  // per thread, and a whole number of pairs unless one group has them all
+  const int64_t fit = 220 * 1024 / 4 / a.book;
+  const bool even = ds % 2 == 0;
+  const bool in_smem = fit >= (even || M == 1 ? 1 : 2);
+  int64_t gs = in_smem ? fit : M;
+  if (gs > M) gs = M;
+  if (gs * ds > 2 * kDecThreads) gs = 2 * kDecThreads / ds;
+  if (gs < 1) return cudaErrorInvalidValue;
+  if (!even && gs < M) gs -= gs % 2;
+  if (gs < 1) return cudaErrorInvalidValue;
+  a.gs = (int)gs;
+  a.groups = (M + a.gs - 1) / a.gs;
+  // even groups: fewer leftovers
+  a.gs = (M + a.groups - 1) / a.groups;
+  if (!even && a.gs < M) a.gs += a.gs % 2;
+  a.groups = (M + a.gs - 1) / a.gs;
+  const size_t smem = in_smem ? (size_t)a.gs * a.book * 4 : 0;
+  a.quad = (reinterpret_cast<uintptr_t>(C) & 15) == 0 && a.gs * a.book % 4 == 0;
+  const void *fn = even ? (in_smem ? decode_fn<true, true>(L) : decode_fn<true, false>(L))
+                        : (in_smem ? decode_fn<false, true>(L) : decode_fn<false, false>(L));
   cudaError_t e = ensure_smem_limit(fn, di.device, smem);
   if (e != cudaSuccess) return e;
   const int occ = occupancy_cached(fn, di.device, kDecThreads, smem);
-  const int rb = kDecU * (32 / gs) * (kDecThreads / 32);
-  const int64_t ctas = (int64_t)di.sms * occ, blocks = (rows + rb - 1) / rb;
-  // rows per chunk: the fewest steps of the last CTA, with the load of the
-  // books (about 300 rows' worth) counted per item
+  const int rstep = kDecThreads / ((a.gs * ds + 1) / 2);
+  const int64_t ctas = (int64_t)di.sms * occ;
+  // rows per chunk: the shortest time of the last CTA, an item costing its rows
+  // and the load of its books (as long as about 300 rows of 48 KB books a
+  // subspace, less for smaller ones)
+  const int64_t load = in_smem ? 300 * a.book / (2 * 1024 * 6) + 32 : 32;
   int64_t best = 0, chunk = 1;
-  for (int64_t c = 1; c <= blocks && c * rb <= 4096; ++c) {
-    const int64_t waves = ((blocks + c - 1) / c * a.groups + ctas - 1) / ctas;
-    const int64_t cost = waves * (c * rb + 300);
+  for (int64_t c = rstep; c - rstep < rows && c <= 4096; c += rstep) {
+    const int64_t waves = ((rows + c - 1) / c * a.groups + ctas - 1) / ctas;
+    const int64_t cost = waves * (c + load);
     if (best == 0 || cost < best) {
       best = cost;
       chunk = c;
     }
   }
-  a.chunk = (int)(chunk * rb);
-  const int64_t items = (blocks + chunk - 1) / chunk * a.groups;
+  a.chunk = (int)chunk;
+  const int64_t items = (rows + chunk - 1) / chunk * a.groups;
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
   a.items = (int)items;
   void *args[] = {&a};

@@ -219,27 +219,28 @@ def test_index(K, skew):
     raw = rq.rq_prepare_grad(x.packed, rq.U16, x.d).cpu().numpy()
     up = lambda n, a: (n + a - 1) // a * a  # noqa: E731
     g = 1
-    while g < 32 and K * g < 512:
+    while g < 32 and K * g < 1024:
         g *= 2
     ns = (K * g + 31) // 32
     code_at = up(2 * ns + 2, 16)
     over_at = code_at + up(2 * K, 16)
-    entry_at = up(over_at + 2 * (R // (g * (cap - 1) + 1) + 2), 64)
-    unit = entry_at + up(2 * (R + 32 * cap + (32 * ns if g > 1 else 0)), 64)
+    entry_at = up(over_at + 2 * (R // (g * (cap - 1) + 1) + 2), 128)
+    unit = entry_at + up(2 * (R + 32 * cap + (64 if g > 1 else 32) * ns), 128)
     assert raw.size == 2 * P * unit == rq.rq_grad_index_bytes(x.d)
     codes = codes.cpu().numpy()
     for b, n in ((0, R), (1, 77)):
         for p in range(P):
             u = raw[(b * P + p) * unit:][:unit].view(np.uint16)
             off, code, over = u[:ns + 1].astype(int), u[code_at // 2:][:K], u[over_at // 2:]
-            entry = u[entry_at // 2:]
+            entry = u[entry_at // 2:] // 4
+            assert (u[entry_at // 2:][:64 * off[ns]] % 4 == 0).all()
             assert sorted(code) == list(range(K)) and off[0] == 0
             seen = 0
             for s in range(K):
                 lanes = []
                 for vl in range(s * g, s * g + g):
                     sl = vl // 32
-                    lane = entry[32 * off[sl]:32 * off[sl + 1]].reshape(-1, 32)[:, vl % 32]
+                    lane = entry[64 * off[sl]:64 * off[sl + 1]].reshape(-1, 32, 2)[:, vl % 32].reshape(-1)
                     lanes.append(lane[lane < R])
                     assert (lane[len(lanes[-1]):] == R).all()
                 got = np.full(g * max(map(len, lanes)) if lanes else 0, R)
@@ -247,7 +248,7 @@ def test_index(K, skew):
                     got[i::g][:len(lane)] = lane
                 got = got[got < R]
                 if s < over[0]:
-                    rest = entry[32 * off[ns]:][over[1 + s]:over[2 + s]]
+                    rest = entry[64 * off[ns]:][over[1 + s]:over[2 + s]]
                     got = np.concatenate([got, rest])
                 want = np.nonzero(codes[b * R:b * R + n, p] == code[s])[0]
                 assert np.array_equal(got, want)
