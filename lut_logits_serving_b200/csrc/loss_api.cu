@@ -1,12 +1,13 @@
 // loss_api.cu -- the losses of the C ABI (see include/rqlut.h): argument
 // checks, workspace layout, choice of path and launches.
 //
-// Two paths.  Few tokens: the logits of the serving kernels (one pass over the
-// codes) go to the workspace, and the gradients come from sums of the logits'
-// gradients by code (loss_codebook.cu), so the V x D matrix is formed in
-// neither direction.  More tokens: pieces of the vocabulary are decoded once
-// and multiplied with all tokens on the tensor cores; logits exist one tile at
-// a time, gradients of the logits one piece at a time.
+// Logits come from the serving kernels (a few tokens: one pass over the codes,
+// tables in shared memory) into the workspace, or from the tensor cores:
+// pieces of the vocabulary are decoded once and multiplied with all tokens,
+// and logits exist one tile at a time.  Gradients come from sums of the
+// logits' gradients by code (a few tokens: the V x D matrix is formed in
+// neither direction), or from tensor-core products with the decoded piece and
+// the hidden states, one piece at a time.  choose() picks by estimated time.
 #include "loss_common.cuh"
 
 using namespace rq;
@@ -15,8 +16,8 @@ namespace {
 
 constexpr int64_t kPieceRows = 4 * kGradRows;   // rows of the vocabulary per piece
 constexpr int kTokenChunk = 4096;         // tokens per sweep over the vocabulary
-constexpr int kFewTokens = 64;            // up to here a loss takes the serving kernels' logits
-constexpr int kFewTokensGrad = 16;        // and a gradient the sums by code
+constexpr int kServeTokens = 64;          // most tokens of a call on the serving kernels' logits
+constexpr int kSumTokens = 32;            // and of one on sums by code
 constexpr int kSms = 148;                 // sizes do not depend on the current device
 constexpr int kMaxSplits = 32;            // of the vocabulary in dz E
 constexpr int kChain = 4;                 // blocks of 64 per accumulation chain
@@ -62,16 +63,6 @@ struct Arena {
   }
 };
 
-// A token group's table must fit the table build's shared memory (the rule of
-// rq_logits_from_hidden).
-bool few_ok(const rq_dims &d, int N, int limit) {
-  if (N > limit) return false;
-  const int g = N < kTokenGroup ? N : kTokenGroup;
-  return (size_t)rq_lut_token_stride(g) * (d.D / d.M) * 4 <= 48 * 1024;
-}
-bool few_loss(const rq_dims &d, int N) { return few_ok(d, N, kFewTokens); }
-bool few_grad(const rq_dims &d, int N) { return few_ok(d, N, kFewTokensGrad) && d.D / d.M <= 128; }
-
 int64_t piece_rows(const rq_dims &d) { return d.V < kPieceRows ? d.V : kPieceRows; }
 int64_t pitch16(int64_t n) { return align_up(n, 16); }   // fp16 rows of whole sectors
 
@@ -95,78 +86,150 @@ int dh_splits(const rq_dims &d, int64_t n) {
   return s < 1 ? 1 : (int)s;
 }
 
-struct FewLayout {
-  size_t logits, stat, wide, sid, sq, f, dz, S, dhp, fused, fused_bytes, total;
-  int splits;
+// Where the logits come from and how the gradients are formed.
+struct Choice {
+  bool serve, sums;
 };
 
-FewLayout few_layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
-  FewLayout x{};
-  Arena a;
-  x.logits = a.take((int64_t)N * d.V * 4);
-  x.stat = a.take((int64_t)loss_stat_parts(d.V) * N * 8);
-  x.wide = a.take((int64_t)N * d.D * 4);
-  if (grad) {
-    const int P = d.M * d.L;
-    x.splits = codebook_sum_splits(d.V, d.M, d.L, d.K, N);
-    x.sid = a.take((int64_t)N * k * 4);
-    x.sq = a.take((int64_t)N * k * 4);
-    x.f = a.take((int64_t)N * 4);
-    x.dz = a.take((int64_t)N * pitch16(d.V) * 4);
-    x.S = a.take((int64_t)(N + 1) / 2 * x.splits * P * d.K * 8);
-    x.dhp = a.take((int64_t)P * N * (d.D / d.M) * 4);
-  }
-  x.fused_bytes = rq_fused_workspace_bytes(d, N, fmt, 0);
-  x.fused = a.take((int64_t)x.fused_bytes);
-  x.total = a.at;
-  return x;
+// Estimated microseconds of the ways, from measurements at 256000 rows of 768
+// codes (V P = 197 million) and at heads a few hundred times smaller:
+//   decoding           1070 for 295 million pairs of dims, two levels
+//   a tensor product   V D 128 per token tile at 1.1 PFLOP/s (a third more
+//                      for the first and the last wave of small ones: 12)
+//   serving, B <= 4    116 per token (tables in shared memory)
+//   serving, groups    tables through L2: 0.12 per column and row a thread
+//                      has; decoded groups: 450 (32 tokens, 1024 rows per SM),
+//                      340 (64, 512)
+//   sums by code       1.95 per million codes and pair (of tokens or dims)
+// The serving kernels' fallback for odd layouts walks a row's codes one by one
+// (385 where the tensor cores take 45) and is never chosen.
+double decode_us(const rq_dims &d) {
+  return 8 + (double)d.V * d.D / 2e6 * (2.2 + 0.7 * d.L) * ((d.D / d.M) % 2 ? 1.25 : 1.0);
+}
+double product_us(const rq_dims &d, int N) {
+  return 12 + 3.0 * 2 * 128 * ((N + 127) / 128) * (double)d.V * d.D / 1.1e9;
+}
+double sums_us(const rq_dims &d, int pairs) {
+  return 8 + 1.95 * pairs * (double)d.V * d.M * d.L / 1e6;
 }
 
-struct ManyLayout {
-  size_t amax, hh, hl, wh, wl, stat, y, sid, sq, f, zh, zl, dw, cpart, part, total;
-  int64_t hp, zp;      // row pitches: D and the piece's rows, in elements
+double serve_us(const rq_dims &d, int N, int fmt) {
+  const double never = 1e30;
+  const int P = d.M * d.L;
+  const int g = N < kTokenGroup ? N : kTokenGroup;
+  if (N > kServeTokens || (size_t)rq_lut_token_stride(g) * (d.D / d.M) * 4 > 48 * 1024) return never;
+  DevInfo di{};
+  di.sms = kSms;
+  di.max_smem_optin = 232448;
+  const double codes = (double)d.V * P / 1e6;
+  if (plan_chunk(d.V, P, d.K, N, fmt, di).ok) return 12 + 0.59 * N * codes;
+  const bool fast = fmt == RQ_CODES_U16     ? P % 8 == 0
+                    : fmt == RQ_CODES_SCHED ? P % 32 == 0
+                    : fmt == RQ_CODES_U8    ? P % 16 == 0
+                                            : P % 64 == 0;
+  if (!fast) return never;
+  const bool tc = decode_mma_shape_ok(fmt, d.V, d.D, d.M, d.L, d.K);
+  const int64_t per_sm = (d.V + kSms - 1) / kSms;
+  double us = 8;
+  for (int left = N; left > 0;) {
+    if (tc && left > 32) {
+      us += 340.0 * ((per_sm + 511) / 512) * P / 768 + 40;
+      left -= 64;
+    } else if (tc && left > 16) {
+      us += 450.0 * ((per_sm + 1023) / 1024) * P / 768 + 40;
+      left -= 32;
+    } else {
+      int tok = 4;
+      while (tok < left && tok < 32) tok *= 2;
+      const int64_t grid = d.V / 256 < 4 * kSms ? (d.V + 255) / 256 : 4 * kSms;
+      const int64_t steps = (d.V + grid * (1024 / tok) - 1) / (grid * (1024 / tok));
+      us += 8 + 0.12 * steps * P;
+      left -= tok;
+    }
+  }
+  return us;
+}
+
+Choice choose(const rq_dims &d, int N, int fmt, bool grad) {
+  Choice c;
+  const int ds = d.D / d.M;
+  const double serve = serve_us(d, N, fmt), tensor = decode_us(d) + product_us(d, N);
+  c.serve = serve < tensor;
+  c.sums = false;
+  if (grad) {
+    // the products write and read V D floats besides
+    const double sums = (c.serve ? serve : tensor) + sums_us(d, (N + 1) / 2);
+    const double products = tensor + 2 * product_us(d, N) + (double)d.V * d.D * 4 / 3e6 +
+                            sums_us(d, (ds + 1) / 2);
+    c.sums = N <= kSumTokens && ds <= 128 && sums < products;
+    if (!c.sums) c.serve = false;
+  }
+  return c;
+}
+
+struct Layout {
+  Choice how;
+  size_t amax, hh, hl, wh, wl, stat, y;            // tensor-core logits and products
+  size_t logits, wide, fused, fused_bytes;         // serving logits
+  size_t sid, sq, f;                               // gradients
+  size_t dz, S, dhp;                               // sums by code
+  size_t zh, zl, dw, cpart, part;                  // products
+  size_t total;
+  int64_t hp, zp, vp;  // row pitches: D, the piece's rows, V
   int64_t chunk;       // tokens per sweep
-  int csplits;         // shares of the codebooks' sums
+  int splits;          // shares of the sums by code
 };
 
-ManyLayout many_layout(const rq_dims &d, int N, int k, bool grad) {
-  ManyLayout x{};
+Layout layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
+  Layout x{};
   Arena a;
+  x.how = choose(d, N, fmt, grad);
   const int64_t n = N < kTokenChunk ? N : kTokenChunk, rows = piece_rows(d);
+  const int P = d.M * d.L, ds = d.D / d.M;
   x.chunk = n;
   x.hp = pitch16(d.D);
   x.zp = pitch16(rows);
-  x.amax = a.take(3 * kAmaxBlocks * 4);
-  x.hh = a.take(n * x.hp * 2);
-  x.hl = a.take(n * x.hp * 2);
-  x.wh = a.take(rows * x.hp * 2);
-  x.wl = a.take(rows * x.hp * 2);
-  x.y = a.take(n * k * 4);
+  x.vp = pitch16(d.V);
+  if (!x.how.serve) {
+    x.amax = a.take(3 * kAmaxBlocks * 4);
+    x.hh = a.take(n * x.hp * 2);
+    x.hl = a.take(n * x.hp * 2);
+    x.wh = a.take(rows * x.hp * 2);
+    x.wl = a.take(rows * x.hp * 2);
+    x.y = a.take(n * k * 4);
+  } else {
+    x.logits = a.take((int64_t)N * d.V * 4);
+    x.wide = a.take((int64_t)N * d.D * 4);
+    x.fused_bytes = rq_fused_workspace_bytes(d, N, fmt, 0);
+    x.fused = a.take((int64_t)x.fused_bytes);
+  }
   if (!grad) {
-    x.stat = a.take((int64_t)total_parts(d) * n * 8);
+    x.stat = a.take((int64_t)(x.how.serve ? loss_stat_parts(d.V) : total_parts(d)) * n * 8);
   } else {
     x.sid = a.take(n * k * 4);
     x.sq = a.take(n * k * 4);
     x.f = a.take(n * 4);
-    x.zh = a.take(n * x.zp * 2);
-    x.zl = a.take(n * x.zp * 2);
-    x.dw = a.take((int64_t)d.D * x.zp * 4);
-    x.csplits = codebook_rows_splits(d.V, rows, d.M, d.L, d.K, d.D / d.M);
-    x.cpart = a.take(x.csplits > 1 ? (int64_t)x.csplits * d.M * d.L * d.K * (d.D / d.M) * 4 : 0);
-    // the last sweep may have fewer tokens and with them more splits
-    int64_t part = dh_splits(d, n) * n;
-    const int64_t last = N % n == 0 ? n : N % n;
-    const int64_t p2 = dh_splits(d, last) * last;
-    if (p2 > part) part = p2;
-    x.part = a.take(part * x.hp * 4);
+    if (x.how.sums) {
+      x.splits = codebook_sum_splits(d.V, d.M, d.L, d.K, N);
+      x.dz = a.take((int64_t)N * x.vp * 4);
+      x.S = a.take((int64_t)(N + 1) / 2 * x.splits * P * d.K * 8);
+      x.dhp = a.take((int64_t)P * N * ds * 4);
+    } else {
+      x.zh = a.take(n * x.zp * 2);
+      x.zl = a.take(n * x.zp * 2);
+      x.dw = a.take((int64_t)d.D * x.zp * 4);
+      x.splits = codebook_rows_splits(d.V, rows, d.M, d.L, d.K, ds);
+      x.cpart = a.take(x.splits > 1 ? (int64_t)x.splits * P * d.K * ds * 4 : 0);
+      // the last sweep may have fewer tokens and with them more splits
+      int64_t part = dh_splits(d, n) * n;
+      const int64_t last = N % n == 0 ? n : N % n;
+      const int64_t p2 = dh_splits(d, last) * last;
+      if (p2 > part) part = p2;
+      x.part = a.take(part * x.hp * 4);
+    }
   }
   x.total = a.at;
   return x;
-}
-
-size_t loss_bytes(const rq_dims &d, int N, int fmt, int k, bool grad) {
-  if (grad ? few_grad(d, N) : few_loss(d, N)) return few_layout(d, N, fmt, k, grad).total;
-  return many_layout(d, N, k, grad).total;
 }
 
 #define RQ_TRY(call)                           \
@@ -180,12 +243,13 @@ T *at(void *ws, size_t off) {
   return reinterpret_cast<T *>(static_cast<unsigned char *>(ws) + off);
 }
 
-// Logits [N][V] of a few tokens in the workspace.
-int few_logits(const Problem &q, const FewLayout &x, void *ws, cudaStream_t s, cudaError_t *err) {
+// Logits [N][V] of the serving kernels in the workspace.
+int serve_logits(const Problem &q, const Layout &x, void *ws, cudaStream_t s) {
   const float *h = static_cast<const float *>(q.h);
   if (q.bf16) {
-    *err = launch_loss_widen_h(q.h, (int64_t)q.N * q.d.D, at<float>(ws, x.wide), s);
-    if (*err != cudaSuccess) return RQ_ERR_CUDA;
+    const cudaError_t e =
+        launch_loss_widen_h(q.h, (int64_t)q.N * q.d.D, at<float>(ws, x.wide), s);
+    if (e != cudaSuccess) return rq::note_cuda_error(e);
     h = at<float>(ws, x.wide);
   }
   return rq_logits_from_hidden(h, q.C, q.codes, q.fmt, q.d, q.N, q.cap, at<float>(ws, x.logits),
@@ -216,97 +280,122 @@ GemmArgs gemm_args(const Problem &q, const float *amax, const DevInfo &di) {
   return g;
 }
 
-cudaError_t many_loss(const Problem &q, const ManyLayout &x, float *loss, float *lse, void *ws,
-                      const DevInfo &di, cudaStream_t s) {
-  const rq_dims &d = q.d;
-  const int esz = q.bf16 ? 2 : 4;
-  float *amax = at<float>(ws, x.amax);
-  __half *hh = at<__half>(ws, x.hh), *hl = q.bf16 ? nullptr : at<__half>(ws, x.hl);
-  RQ_TRY(launch_loss_amax(q.h, q.bf16, (int64_t)q.N * d.D, q.C, (int64_t)d.M * d.L * d.K * q.ds(),
-                          nullptr, 0, amax, s));
-  for (int64_t n0 = 0; n0 < q.N; n0 += x.chunk) {
-    const int64_t n = q.N - n0 < x.chunk ? q.N - n0 : x.chunk;
-    const void *h = static_cast<const char *>(q.h) + n0 * d.D * esz;
-    LossTargets t = q.t;
-    t.id += n0 * t.k;
-    if (t.val) t.val += n0 * t.k;
-    RQ_TRY(launch_loss_split_h(h, q.bf16, n, d.D, x.hp, amax, hh, hl, s));
-    RQ_TRY(launch_loss_pick(h, q.bf16, q.src(), q.C, d.D, d.M, d.L, t.id, n, t.k, q.cap,
-                            at<float>(ws, x.y), s));
-    int part0 = 0;
-    for (int64_t v0 = 0; v0 < d.V; v0 += kPieceRows) {
-      const int64_t rows = d.V - v0 < kPieceRows ? d.V - v0 : kPieceRows;
-      RQ_TRY(launch_loss_decode(q.src(), q.C, d.M, d.L, q.ds(), v0, rows, x.hp, amax,
-                                at<__half>(ws, x.wh), at<__half>(ws, x.wl), di, s));
-      GemmArgs g = gemm_args(q, amax, di);
-      g.rows = (int)n;
-      g.cols = (int)rows;
-      g.stat = at<float2>(ws, x.stat);
-      g.stat_ld = (int)x.chunk;
-      g.stat_part0 = part0;
-      RQ_TRY(launch_loss_gemm(kGemmStats, planes(hh, hl, n, d.D, x.hp),
-                              planes(at<void>(ws, x.wh), at<void>(ws, x.wl), rows, d.D, x.hp), g,
-                              di, s));
-      part0 += 2 * (int)((rows + 255) / 256);
-    }
-    RQ_TRY(launch_loss_finish(at<float2>(ws, x.stat), part0, (int)x.chunk, n, d.V, t,
-                              at<float>(ws, x.y), false, loss + n0, lse + n0, di.err, s));
+// The tokens [n0, n0 + n) of a call.
+Problem slice(const Problem &q, int64_t n0, int64_t n) {
+  Problem p = q;
+  p.h = static_cast<const char *>(q.h) + n0 * q.d.D * (q.bf16 ? 2 : 4);
+  p.N = (int)n;
+  p.t.id += n0 * q.t.k;
+  if (p.t.val) p.t.val += n0 * q.t.k;
+  return p;
+}
+
+cudaError_t scales(const Problem &q, const Layout &x, const float *w, void *ws, cudaStream_t s) {
+  return launch_loss_amax(q.h, q.bf16, (int64_t)q.N * q.d.D, q.C,
+                          (int64_t)q.d.M * q.d.L * q.d.K * q.ds(), w, w ? q.N : 0,
+                          at<float>(ws, x.amax), s);
+}
+
+// Piece [v0, v0 + rows) decoded.
+cudaError_t decode(const Problem &q, const Layout &x, int64_t v0, int64_t rows, void *ws,
+                   const DevInfo &di, cudaStream_t s) {
+  return launch_loss_decode(q.src(), q.C, q.d.M, q.d.L, q.ds(), v0, rows, x.hp,
+                            at<float>(ws, x.amax), at<__half>(ws, x.wh), at<__half>(ws, x.wl), di,
+                            s);
+}
+
+// h and the decoded piece, the factors of the logits.
+GemmPlanes h_planes(const Problem &q, const Layout &x, void *ws) {
+  return planes(at<void>(ws, x.hh), q.bf16 ? nullptr : at<void>(ws, x.hl), q.N, q.d.D, x.hp);
+}
+GemmPlanes w_planes(const Problem &q, const Layout &x, int64_t rows, void *ws) {
+  return planes(at<void>(ws, x.wh), at<void>(ws, x.wl), rows, q.d.D, x.hp);
+}
+
+template <typename Each>
+cudaError_t for_pieces(const rq_dims &d, Each &&each) {
+  for (int64_t v0 = 0; v0 < d.V; v0 += kPieceRows) {
+    const cudaError_t e = each(v0, d.V - v0 < kPieceRows ? d.V - v0 : kPieceRows);
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
-cudaError_t many_grad(const Problem &q, const ManyLayout &x, const float *lse, const float *w,
-                      const void *index, void *dh, float *dC, void *ws, const DevInfo &di,
-                      cudaStream_t s) {
-  const rq_dims &d = q.d;
-  const int esz = q.bf16 ? 2 : 4;
+cudaError_t tensor_loss(const Problem &all, const Layout &x, float *loss, float *lse, void *ws,
+                        const DevInfo &di, cudaStream_t s) {
+  float *amax = at<float>(ws, x.amax), *y = at<float>(ws, x.y);
+  RQ_TRY(scales(all, x, nullptr, ws, s));
+  for (int64_t n0 = 0; n0 < all.N; n0 += x.chunk) {
+    const Problem q = slice(all, n0, all.N - n0 < x.chunk ? all.N - n0 : x.chunk);
+    const rq_dims &d = q.d;
+    RQ_TRY(launch_loss_split_h(q.h, q.bf16, q.N, d.D, x.hp, amax, at<__half>(ws, x.hh),
+                               q.bf16 ? nullptr : at<__half>(ws, x.hl), s));
+    RQ_TRY(launch_loss_pick(q.h, q.bf16, q.src(), q.C, d.D, d.M, d.L, q.t.id, q.N, q.t.k, q.cap, y,
+                            s));
+    int part0 = 0;
+    RQ_TRY(for_pieces(d, [&](int64_t v0, int64_t rows) {
+      RQ_TRY(decode(q, x, v0, rows, ws, di, s));
+      GemmArgs g = gemm_args(q, amax, di);
+      g.rows = q.N;
+      g.cols = (int)rows;
+      g.stat = at<float2>(ws, x.stat);
+      g.stat_ld = (int)x.chunk;
+      g.stat_part0 = part0;
+      part0 += 2 * (int)((rows + 255) / 256);
+      return launch_loss_gemm(kGemmStats, h_planes(q, x, ws), w_planes(q, x, rows, ws), g, di, s);
+    }));
+    RQ_TRY(launch_loss_finish(at<float2>(ws, x.stat), part0, (int)x.chunk, q.N, d.V, q.t, y, false,
+                              loss + n0, lse + n0, di.err, s));
+  }
+  return cudaSuccess;
+}
+
+cudaError_t products_grad(const Problem &all, const Layout &x, const float *lse, const float *w,
+                          const void *index, void *dh, float *dC, void *ws, const DevInfo &di,
+                          cudaStream_t s) {
   float *amax = at<float>(ws, x.amax), *f = at<float>(ws, x.f), *y = at<float>(ws, x.y);
-  __half *hh = at<__half>(ws, x.hh), *hl = q.bf16 ? nullptr : at<__half>(ws, x.hl);
   __half *zh = at<__half>(ws, x.zh), *zl = at<__half>(ws, x.zl);
-  __half *wh = at<__half>(ws, x.wh), *wl = at<__half>(ws, x.wl);
   int32_t *sid = at<int32_t>(ws, x.sid);
   float *sq = at<float>(ws, x.sq);
-  RQ_TRY(launch_loss_amax(q.h, q.bf16, (int64_t)q.N * d.D, q.C, (int64_t)d.M * d.L * d.K * q.ds(), w,
-                          q.N, amax, s));
-  for (int64_t n0 = 0; n0 < q.N; n0 += x.chunk) {
-    const int64_t n = q.N - n0 < x.chunk ? q.N - n0 : x.chunk;
-    const void *h = static_cast<const char *>(q.h) + n0 * d.D * esz;
-    LossTargets t = q.t;
-    t.id += n0 * t.k;
-    if (t.val) t.val += n0 * t.k;
-    const int splits = dh_splits(d, n);
-    RQ_TRY(launch_loss_split_h(h, q.bf16, n, d.D, x.hp, amax, hh, hl, s));
-    RQ_TRY(launch_loss_sparse(t, n, d.V, w ? w + n0 : nullptr, sid, sq, f, di.err, s));
-    RQ_TRY(launch_loss_pick(h, q.bf16, q.src(), q.C, d.D, d.M, d.L, sid, n, t.k, q.cap, y, s));
-    for (int64_t v0 = 0; v0 < d.V; v0 += kPieceRows) {
-      const int64_t rows = d.V - v0 < kPieceRows ? d.V - v0 : kPieceRows;
-      RQ_TRY(launch_loss_decode(q.src(), q.C, d.M, d.L, q.ds(), v0, rows, x.hp, amax, wh, wl, di,
-                                s));
+  const int64_t books = (int64_t)all.d.M * all.d.L * all.d.K * all.ds();
+  RQ_TRY(scales(all, x, w, ws, s));
+  for (int64_t n0 = 0; n0 < all.N; n0 += x.chunk) {
+    const Problem q = slice(all, n0, all.N - n0 < x.chunk ? all.N - n0 : x.chunk);
+    const rq_dims &d = q.d;
+    const float *ql = lse + n0;
+    const int splits = dh_splits(d, q.N);
+    RQ_TRY(launch_loss_split_h(q.h, q.bf16, q.N, d.D, x.hp, amax, at<__half>(ws, x.hh),
+                               q.bf16 ? nullptr : at<__half>(ws, x.hl), s));
+    RQ_TRY(launch_loss_sparse(q.t, q.N, d.V, w ? w + n0 : nullptr, sid, sq, f, di.err, s));
+    RQ_TRY(launch_loss_pick(q.h, q.bf16, q.src(), q.C, d.D, d.M, d.L, sid, q.N, q.t.k, q.cap, y, s));
+    RQ_TRY(for_pieces(d, [&](int64_t v0, int64_t rows) {
+      RQ_TRY(decode(q, x, v0, rows, ws, di, s));
       GemmArgs g = gemm_args(q, amax, di);
-      g.rows = (int)n;
+      g.rows = q.N;
       g.cols = (int)rows;
-      g.lse = lse + n0;
+      g.lse = ql;
       g.f = f;
       g.dz_hi = zh;
       g.dz_lo = zl;
       g.dz_pitch = x.zp;
-      RQ_TRY(launch_loss_gemm(kGemmGrad, planes(hh, hl, n, d.D, x.hp),
-                              planes(wh, wl, rows, d.D, x.hp), g, di, s));
-      RQ_TRY(launch_loss_fix_planes(sid, sq, y, t.k, n, v0, rows, lse + n0, f, amax, t.T, t.beta,
+      RQ_TRY(launch_loss_gemm(kGemmGrad, h_planes(q, x, ws), w_planes(q, x, rows, ws), g, di, s));
+      RQ_TRY(launch_loss_fix_planes(sid, sq, y, q.t.k, q.N, v0, rows, ql, f, amax, q.t.T, q.t.beta,
                                     q.cap, zh, zl, x.zp, s));
       if (dh) {
         // a bf16 dh keeps 8 bits: the high planes' 11 on either side are
         // within a sixth of its rounding
         GemmArgs p = gemm_args(q, amax, di);
         p.splits = splits;
-        p.rows = (int)n;
+        p.rows = q.N;
         p.cols = d.D;
         p.out = at<float>(ws, x.part);
         p.out_pitch = x.hp;
-        p.out_split = n * x.hp;
+        p.out_split = q.N * x.hp;
         p.accumulate = v0 > 0;
-        RQ_TRY(launch_loss_gemm(kGemmDh, planes(zh, q.bf16 ? nullptr : zl, n, rows, x.zp),
-                                planes(wh, q.bf16 ? nullptr : wl, rows, d.D, x.hp), p, di, s));
+        RQ_TRY(launch_loss_gemm(
+            kGemmDh, planes(zh, q.bf16 ? nullptr : zl, q.N, rows, x.zp),
+            planes(at<void>(ws, x.wh), q.bf16 ? nullptr : at<void>(ws, x.wl), rows, d.D, x.hp), p,
+            di, s));
       }
       if (dC) {
         GemmArgs p = gemm_args(q, amax, di);
@@ -314,35 +403,58 @@ cudaError_t many_grad(const Problem &q, const ManyLayout &x, const float *lse, c
         p.cols = (int)rows;
         p.out = at<float>(ws, x.dw);
         p.out_pitch = x.zp;
-        RQ_TRY(launch_loss_gemm(kGemmDw, planes(hh, hl, n, d.D, x.hp), planes(zh, zl, n, rows, x.zp),
-                                p, di, s));
+        RQ_TRY(launch_loss_gemm(kGemmDw, h_planes(q, x, ws), planes(zh, zl, q.N, rows, x.zp), p, di,
+                                s));
         RQ_TRY(launch_codebook_rows(at<float>(ws, x.dw), x.zp, v0, rows, index, d.V, d.M, d.L, d.K,
-                                    q.ds(), x.csplits, n0 > 0 || v0 > 0,
-                                    x.csplits > 1 ? at<float>(ws, x.cpart) : dC, di, s));
+                                    q.ds(), x.splits, n0 > 0 || v0 > 0,
+                                    x.splits > 1 ? at<float>(ws, x.cpart) : dC, di, s));
       }
-    }
+      return cudaSuccess;
+    }));
     if (dh)
-      RQ_TRY(launch_loss_dh_sum(at<float>(ws, x.part), splits, n * x.hp, x.hp, n, d.D, q.bf16,
-                                static_cast<char *>(dh) + n0 * d.D * esz, s));
+      RQ_TRY(launch_loss_dh_sum(at<float>(ws, x.part), splits, q.N * x.hp, x.hp, q.N, d.D, q.bf16,
+                                static_cast<char *>(dh) + n0 * d.D * (q.bf16 ? 2 : 4), s));
   }
-  if (dC && x.csplits > 1)
-    RQ_TRY(launch_codebook_join(at<float>(ws, x.cpart), x.csplits,
-                                (int64_t)d.M * d.L * d.K * q.ds(), dC, s));
+  if (dC && x.splits > 1)
+    RQ_TRY(launch_codebook_join(at<float>(ws, x.cpart), x.splits, books, dC, s));
   return cudaSuccess;
 }
 
-cudaError_t few_gradients(const Problem &q, const FewLayout &x, const float *lse, const float *w,
-                          const void *index, void *dh, float *dC, void *ws, const DevInfo &di,
-                          cudaStream_t s) {
+// Gradients from sums by code; the serving logits, where chosen, are there.
+cudaError_t sums_grad(const Problem &q, const Layout &x, const float *lse, const float *w,
+                      const void *index, void *dh, float *dC, void *ws, const DevInfo &di,
+                      cudaStream_t s) {
   const rq_dims &d = q.d;
-  const int64_t pitch = pitch16(d.V);
   int32_t *sid = at<int32_t>(ws, x.sid);
   float *sq = at<float>(ws, x.sq), *f = at<float>(ws, x.f), *dz = at<float>(ws, x.dz);
   float *S = at<float>(ws, x.S), *dhp = dh ? at<float>(ws, x.dhp) : nullptr;
   RQ_TRY(launch_loss_sparse(q.t, q.N, d.V, w, sid, sq, f, di.err, s));
-  RQ_TRY(launch_loss_dz_small(at<float>(ws, x.logits), q.N, d.V, sid, sq, q.t.k, lse, f, q.t.beta,
-                              q.cap, dz, pitch, s));
-  RQ_TRY(launch_codebook_sums(dz, pitch, q.N, index, d.V, d.M, d.L, d.K, S, di, s));
+  const float *y = at<float>(ws, x.logits);
+  if (x.how.serve) {
+    RQ_TRY(launch_loss_dz(y, q.N, d.V, lse, f, q.t.beta, q.cap, dz, x.vp, s));
+  } else {
+    float *amax = at<float>(ws, x.amax), *picks = at<float>(ws, x.y);
+    y = picks;
+    RQ_TRY(scales(q, x, nullptr, ws, s));
+    RQ_TRY(launch_loss_split_h(q.h, q.bf16, q.N, d.D, x.hp, amax, at<__half>(ws, x.hh),
+                               q.bf16 ? nullptr : at<__half>(ws, x.hl), s));
+    RQ_TRY(launch_loss_pick(q.h, q.bf16, q.src(), q.C, d.D, d.M, d.L, sid, q.N, q.t.k, q.cap, picks,
+                            s));
+    RQ_TRY(for_pieces(d, [&](int64_t v0, int64_t rows) {
+      RQ_TRY(decode(q, x, v0, rows, ws, di, s));
+      GemmArgs g = gemm_args(q, amax, di);
+      g.rows = q.N;
+      g.cols = (int)rows;
+      g.lse = lse;
+      g.f = f;
+      g.dz = dz + v0;
+      g.dz_pitch = x.vp;
+      return launch_loss_gemm(kGemmGrad32, h_planes(q, x, ws), w_planes(q, x, rows, ws), g, di, s);
+    }));
+  }
+  RQ_TRY(launch_loss_fix(sid, sq, y, x.how.serve, q.t.k, q.N, d.V, lse, f, q.t.beta, q.cap, dz, x.vp,
+                         s));
+  RQ_TRY(launch_codebook_sums(dz, x.vp, q.N, index, d.V, d.M, d.L, d.K, S, di, s));
   RQ_TRY(launch_codebook_finish(S, x.splits, q.h, q.bf16, q.N, q.C, d.D, d.M, d.L, d.K, dC, dhp, s));
   if (dh) RQ_TRY(launch_codebook_dh(dhp, q.N, d.D, d.M, d.L, q.bf16, dh, s));
   return cudaSuccess;
@@ -370,18 +482,15 @@ int run_loss(const Problem &q, float *loss, float *lse, void *ws, size_t ws_byte
   const int bad = check(q, ws);
   if (bad) return bad;
   if (!aligned(loss, 4) || !aligned(lse, 4)) return RQ_ERR_MISALIGNED;
-  if (!ws || ws_bytes < loss_bytes(q.d, q.N, q.fmt, q.t.k, false)) return RQ_ERR_WORKSPACE_TOO_SMALL;
+  const Layout x = layout(q.d, q.N, q.fmt, q.t.k, false);
+  if (!ws || ws_bytes < x.total) return RQ_ERR_WORKSPACE_TOO_SMALL;
   DevInfo di;
   cudaError_t e = dev_info(&di);
   if (e != cudaSuccess) return status_of(e);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!few_loss(q.d, q.N)) {
-    const ManyLayout x = many_layout(q.d, q.N, q.t.k, false);
-    return status_of(many_loss(q, x, loss, lse, ws, di, s));
-  }
-  const FewLayout x = few_layout(q.d, q.N, q.fmt, q.t.k, false);
-  const int st = few_logits(q, x, ws, s, &e);
-  if (st != RQ_OK) return e != cudaSuccess ? status_of(e) : st;
+  if (!x.how.serve) return status_of(tensor_loss(q, x, loss, lse, ws, di, s));
+  const int st = serve_logits(q, x, ws, s);
+  if (st != RQ_OK) return st;
   e = launch_loss_logit_stats(at<float>(ws, x.logits), q.N, q.d.V, q.t.beta, at<float2>(ws, x.stat),
                               q.N, s);
   if (e == cudaSuccess)
@@ -399,19 +508,18 @@ int run_grad(const Problem &q, const float *lse, const float *w, const void *ind
   if (!aligned(lse, 4) || (w && !aligned(w, 4)) || !aligned(index, 16) ||
       (dh && !aligned(dh, q.bf16 ? 2 : 4)) || (dC && !aligned(dC, 4)))
     return RQ_ERR_MISALIGNED;
-  if (!ws || ws_bytes < loss_bytes(q.d, q.N, q.fmt, q.t.k, true)) return RQ_ERR_WORKSPACE_TOO_SMALL;
+  const Layout x = layout(q.d, q.N, q.fmt, q.t.k, true);
+  if (!ws || ws_bytes < x.total) return RQ_ERR_WORKSPACE_TOO_SMALL;
   DevInfo di;
   cudaError_t e = dev_info(&di);
   if (e != cudaSuccess) return status_of(e);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!few_grad(q.d, q.N)) {
-    const ManyLayout x = many_layout(q.d, q.N, q.t.k, true);
-    return status_of(many_grad(q, x, lse, w, index, dh, dC, ws, di, s));
+  if (!x.how.sums) return status_of(products_grad(q, x, lse, w, index, dh, dC, ws, di, s));
+  if (x.how.serve) {
+    const int st = serve_logits(q, x, ws, s);
+    if (st != RQ_OK) return st;
   }
-  const FewLayout x = few_layout(q.d, q.N, q.fmt, q.t.k, true);
-  const int st = few_logits(q, x, ws, s, &e);
-  if (st != RQ_OK) return e != cudaSuccess ? status_of(e) : st;
-  return status_of(few_gradients(q, x, lse, w, index, dh, dC, ws, di, s));
+  return status_of(sums_grad(q, x, lse, w, index, dh, dC, ws, di, s));
 }
 
 Problem problem(const void *h, int h_bf16, const float *C, const void *codes, int fmt, rq_dims d,
@@ -461,8 +569,8 @@ size_t rq_loss_workspace_bytes(rq_dims d, int N, int fmt, int k, int grad) {
       k > kMaxList || k > d.V)
     return 0;
   if (k < 1) k = 1;
-  const size_t a = loss_bytes(d, N, fmt, k, false);
-  const size_t b = grad ? loss_bytes(d, N, fmt, k, true) : 0;
+  const size_t a = layout(d, N, fmt, k, false).total;
+  const size_t b = grad ? layout(d, N, fmt, k, true).total : 0;
   return a > b ? a : b;
 }
 

@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
   if (tid < 4) vals[tid * kPairPitch + kGradRows] = 0.f;
   __syncthreads();
   // thread 0 keeps the copies a step (units) and a block (values) ahead
-  GatherAhead nu, nv;
+  GatherAhead nu{}, nv{};
   int it = 0, iv = 0;        // copies issued
   auto issue_unit = [&]() {
     if (nu.u >= a.units) return;

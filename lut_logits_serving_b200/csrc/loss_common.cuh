@@ -103,7 +103,8 @@ enum LossGemm {
   kGemmStats = 0,   // y = softcap(h E^T): per (row, 128 columns) max and sum of exp(y / T)
   kGemmGrad = 1,    // y again, gradients of the logits as fp16 hi / lo planes
   kGemmDh = 2,      // dz E, fp32, split over the vocabulary
-  kGemmDw = 3       // (h^T dz), fp32 [D][rows]
+  kGemmDw = 3,      // (h^T dz), fp32 [D][rows]
+  kGemmGrad32 = 4   // kGemmGrad with fp32 gradients, unscaled
 };
 
 struct GemmPlanes {          // row-major fp16 planes; lo may be null
@@ -125,6 +126,7 @@ struct GemmArgs {
   int stat_part0;            // first part of this launch
   const float *lse, *f;      // per row: log-sum-exp, w T (0: no gradient)
   __half *dz_hi, *dz_lo;
+  float *dz;
   int64_t dz_pitch;
   float *out;                // fp32 output
   int64_t out_pitch, out_split;   // row pitch; stride between splits
@@ -176,10 +178,14 @@ cudaError_t launch_loss_fix_planes(const int32_t *sid, const float *sq, const fl
                                    const float *f, const float *amax, float T, float beta,
                                    float cap, __half *hi, __half *lo, int64_t pitch,
                                    cudaStream_t s);
-// logits [N][V] -> their gradients [N][pitch], with the listed ids' corrections
-cudaError_t launch_loss_dz_small(const float *logits, int64_t N, int64_t V, const int32_t *sid,
-                                 const float *sq, int k, const float *lse, const float *f,
-                                 float beta, float cap, float *dz, int64_t pitch, cudaStream_t s);
+// logits [N][V] -> their gradients [N][pitch], dense part
+cudaError_t launch_loss_dz(const float *logits, int64_t N, int64_t V, const float *lse,
+                           const float *f, float beta, float cap, float *dz, int64_t pitch,
+                           cudaStream_t s);
+// dz [N][pitch] at the listed ids; y as for launch_loss_finish
+cudaError_t launch_loss_fix(const int32_t *sid, const float *sq, const float *y, bool y_is_logits,
+                            int k, int64_t N, int64_t V, const float *lse, const float *f,
+                            float beta, float cap, float *dz, int64_t pitch, cudaStream_t s);
 cudaError_t launch_loss_dh_sum(const float *part, int splits, int64_t stride, int64_t pitch,
                                int64_t N, int D, int bf16, void *dh, cudaStream_t s);
 

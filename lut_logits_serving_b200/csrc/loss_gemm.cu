@@ -3,7 +3,8 @@
 //
 //   kGemmStats  y = cap tanh(h E^T / cap); per row and 128 columns the
 //               maximum of y / T and the sum of exp(y / T - max)
-//   kGemmGrad   y again; dz = w T exp(y / T - lse) (1 - (y / cap)^2)
+//   kGemmGrad   y again; dz = w T exp(y / T - lse) (1 - (y / cap)^2), as fp16
+//               planes for the next two, or (kGemmGrad32) in fp32
 //   kGemmDh     dz E       (contraction over the rows of the vocabulary)
 //   kGemmDw     h^T dz     (contraction over the tokens)
 //
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     loss_gemm_kernel(const __grid_constant__ CUtensorMap a_hi, const __grid_constant__ CUtensorMap a_lo,
                      const __grid_constant__ CUtensorMap b_hi, const __grid_constant__ CUtensorMap b_lo,
                      const GemmArgs g) {
+  constexpr bool LOGITS = MODE == kGemmStats || MODE == kGemmGrad || MODE == kGemmGrad32;
   constexpr bool A_MN = MODE == kGemmDw;                        // contraction down the rows of A
   constexpr bool B_MN = MODE == kGemmDh || MODE == kGemmDw;     // and of B
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     };
     const float sh = MODE != kGemmDh ? scale_h(g.amax) : 1.f;
     const float se = MODE != kGemmDw ? scale_e(g.amax, g.L) : 1.f;
-    const float sz = MODE != kGemmStats ? scale_z(g.amax, g.T) : 1.f;
+    const float sz = MODE != kGemmStats && MODE != kGemmGrad32 ? scale_z(g.amax, g.T) : 1.f;
     const float inv = MODE == kGemmDh ? 1.f / (sz * se) : MODE == kGemmDw ? 1.f / (sz * sh)
                                                                           : 1.f / (sh * se);
     float acc[128];
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             acc[j0 + 16 + j] = __fadd_rn(acc[j0 + 16 + j], y[j]);
           }
         }
-        if ((MODE == kGemmStats || MODE == kGemmGrad) && ka + g.chain >= k1) {
+        if (LOGITS && ka + g.chain >= k1) {
           // the tile's sums back into the chain's columns, from where the
           // epilogue takes them 16 at a time (the registers cannot be indexed
           // by a loop, and 128 unrolled tanh and exp would not fit the
@@ -361,6 +363,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                   slope = 1.f - th * th;
                 }
                 const float d = f != 0.f ? expf(y * g.beta - lse) * slope * fs : 0.f;
+                if (MODE == kGemmGrad32) {
+                  x[j] = d;
+                  continue;
+                }
                 __half dh, dl;
                 split_f16(d, dh, dl);
                 if (j & 1) {
@@ -372,7 +378,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
               }
               if (in) {
-                if (col0 + j0 < g.dz_pitch) {      // the pitch is whole sectors
+                if (MODE == kGemmGrad32) {
+                  if (col0 + j0 < g.cols) {        // the rows' pitch is 16 floats
+                    stg32(g.dz + at + j0, reinterpret_cast<const uint32_t *>(x));
+                    stg32(g.dz + at + j0 + 8, reinterpret_cast<const uint32_t *>(x + 8));
+                  }
+                } else if (col0 + j0 < g.dz_pitch) {   // the pitch is whole sectors
                   stg32(g.dz_hi + at + j0, reinterpret_cast<const uint32_t *>(hi));
                   stg32(g.dz_lo + at + j0, reinterpret_cast<const uint32_t *>(lo));
                 }
@@ -465,6 +476,7 @@ cudaError_t launch_loss_gemm(int mode, const GemmPlanes &A, const GemmPlanes &B,
     case kGemmGrad: return launch_gemm<kGemmGrad>(A, B, a, di, s);
     case kGemmDh: return launch_gemm<kGemmDh>(A, B, a, di, s);
     case kGemmDw: return launch_gemm<kGemmDw>(A, B, a, di, s);
+    case kGemmGrad32: return launch_gemm<kGemmGrad32>(A, B, a, di, s);
   }
   return cudaErrorInvalidValue;
 }

@@ -498,26 +498,26 @@ __global__ void __launch_bounds__(256) loss_fix_planes_kernel(
 
 // ------------------------------------------------------------- few tokens
 
-__global__ void __launch_bounds__(256) loss_dz_small_kernel(const float *__restrict__ logits,
-                                                            int64_t V,
-                                                            const float *__restrict__ lse,
-                                                            const float *__restrict__ f, float beta,
-                                                            float cap, float *__restrict__ dz,
-                                                            int64_t pitch) {
+__global__ void __launch_bounds__(256) loss_dz_kernel(const float *__restrict__ logits, int64_t V,
+                                                      const float *__restrict__ lse,
+                                                      const float *__restrict__ f, float beta,
+                                                      float cap, float *__restrict__ dz,
+                                                      int64_t pitch) {
   const int64_t n = blockIdx.y;
   const float l = lse[n], w = f[n];
   for (int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x; v < pitch; v += (int64_t)gridDim.x * 256)
     dz[n * pitch + v] = v < V ? dz_at(logits[n * V + v], 0.f, l, w, beta, cap) : 0.f;
 }
 
-__global__ void __launch_bounds__(256) loss_fix_small_kernel(
-    const int32_t *__restrict__ sid, const float *__restrict__ sq, const float *__restrict__ logits,
-    int k, int64_t count, int64_t V, const float *__restrict__ lse, const float *__restrict__ f,
-    float beta, float cap, float *__restrict__ dz, int64_t pitch) {
+__global__ void __launch_bounds__(256) loss_fix_kernel(
+    const int32_t *__restrict__ sid, const float *__restrict__ sq, const float *__restrict__ y,
+    int y_is_logits, int k, int64_t count, int64_t V, const float *__restrict__ lse,
+    const float *__restrict__ f, float beta, float cap, float *__restrict__ dz, int64_t pitch) {
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= count || sid[i] < 0) return;
   const int64_t n = i / k, v = sid[i];
-  dz[n * pitch + v] = dz_at(logits[n * V + v], sq[i], lse[n], f[n], beta, cap);
+  dz[n * pitch + v] =
+      dz_at(y_is_logits ? y[n * V + v] : y[i], sq[i], lse[n], f[n], beta, cap);
 }
 
 __global__ void __launch_bounds__(256) loss_dh_sum_kernel(const float *__restrict__ part,
@@ -673,15 +673,19 @@ cudaError_t launch_loss_fix_planes(const int32_t *sid, const float *sq, const fl
   return cudaGetLastError();
 }
 
-cudaError_t launch_loss_dz_small(const float *logits, int64_t N, int64_t V, const int32_t *sid,
-                                 const float *sq, int k, const float *lse, const float *f,
-                                 float beta, float cap, float *dz, int64_t pitch, cudaStream_t s) {
-  loss_dz_small_kernel<<<dim3(blocks_of(pitch, 1024), (unsigned)N), 256, 0, s>>>(
-      logits, V, lse, f, beta, cap, dz, pitch);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  loss_fix_small_kernel<<<blocks_of(N * k, 256), 256, 0, s>>>(sid, sq, logits, k, N * k, V, lse, f,
-                                                              beta, cap, dz, pitch);
+cudaError_t launch_loss_dz(const float *logits, int64_t N, int64_t V, const float *lse,
+                           const float *f, float beta, float cap, float *dz, int64_t pitch,
+                           cudaStream_t s) {
+  loss_dz_kernel<<<dim3(blocks_of(pitch, 1024), (unsigned)N), 256, 0, s>>>(logits, V, lse, f, beta,
+                                                                           cap, dz, pitch);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_loss_fix(const int32_t *sid, const float *sq, const float *y, bool y_is_logits,
+                            int k, int64_t N, int64_t V, const float *lse, const float *f,
+                            float beta, float cap, float *dz, int64_t pitch, cudaStream_t s) {
+  loss_fix_kernel<<<blocks_of(N * k, 256), 256, 0, s>>>(sid, sq, y, y_is_logits, k, N * k, V, lse, f,
+                                                        beta, cap, dz, pitch);
   return cudaGetLastError();
 }
 

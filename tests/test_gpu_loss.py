@@ -105,6 +105,9 @@ FEW = [
     (5000, 32, 6, 2, 1024, 16, "f", "sched", 1.0, 30.0),
     (5000, 32, 6, 2, 512, 7, "f", "rot10", 1.5, 30.0),
     (3000, 3, 40, 5, 4096, 2, "f", "u16", 1.0, 10.0),
+    (40000, 67, 8, 3, 64, 4, "b", "u16", 1.5, 30.0),
+    (33000, 21, 8, 1, 500, 20, "f", "packed10", 1.0, 30.0),
+    (1, 1, 1, 1, 1, 3, "f", "u8", 1.0, 30.0),
 ]
 MANY = [
     (4096, 32, 6, 2, 256, 33, "f", "u8", 1.0, 30.0),
