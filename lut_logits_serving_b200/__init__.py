@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -488,73 +489,123 @@ def rq_grad_index_bytes(d: RqDims) -> int:
     return int(lib().rq_grad_index_bytes(d))
 
 
-@contextlib.contextmanager
-def _on(stream, like, *others):
-    """Current device and stream of a call on `like`: every tensor of it lives
-    on one device, and what the call allocates belongs to its stream."""
+@functools.lru_cache(maxsize=256)
+def _loss_sizes(V, D, M, L, K, fmt, N, k, grad):
+    """(codes, codebooks, index, workspace) bytes of a loss call: pure
+    arithmetic, kept because a small call's time is its host side."""
+    d = dims(V, D, M, L, K)
+    return (rq_codes_bytes(d, fmt), _book_bytes(d), rq_grad_index_bytes(d) if grad else 0,
+            rq_loss_workspace_bytes(d, N, fmt, k, grad))
+
+
+class _LossCall:
+    """Checks and pointers of one call of the losses: every tensor on h's
+    device, which is made current with the call's stream for the call's time
+    (what the call allocates then belongs to that stream)."""
+
+    def __init__(self, h, d, fmt, k, grad, stream):
+        torch = _torch()
+        if not isinstance(h, torch.Tensor):
+            raise ValueError("h: expected a torch.Tensor")
+        if h.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"h: dtype {h.dtype}, expected float32 or bfloat16")
+        self.h, self.device, self.N = h, h.device, _tokens(h, d)
+        self.bf16 = int(h.dtype == torch.bfloat16)
+        self.code_dtype = torch.uint16 if fmt in (U16, SCHED) else torch.uint8
+        (self.codes_bytes, self.book_bytes, self.index_bytes,
+         self.ws_bytes) = _loss_sizes(d.V, d.D, d.M, d.L, d.K, fmt, self.N, k, grad)
+        self.stream, self.stack = stream, None
+
+    def __enter__(self):
+        if self.h.is_cuda:
+            torch = _torch()
+            if self.stream is not None or torch.cuda.current_device() != self.device.index:
+                self.stack = contextlib.ExitStack()
+                self.stack.enter_context(torch.cuda.device(self.device))
+                if self.stream is not None:
+                    if self.stream.device != self.device:
+                        raise ValueError(f"stream on {self.stream.device}, h on {self.device}")
+                    self.stack.enter_context(torch.cuda.stream(self.stream))
+        return self
+
+    def __exit__(self, *exc):
+        return self.stack.__exit__(*exc) if self.stack is not None else None
+
+    def ptr(self, t, dtype, name, nbytes):
+        """Address of `t` after the checks of _cuda and of its device."""
+        if not isinstance(t, _torch().Tensor):
+            raise ValueError(f"{name}: expected a torch.Tensor")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+        if t.nbytes < nbytes:
+            raise ValueError(f"{name}: {t.nbytes} bytes, the call needs {nbytes}")
+        if not _on_device(t):
+            raise ValueError(f"{name}: must be a CUDA tensor (no CPU fallback)")
+        if t.device != self.device:
+            raise ValueError(f"{name}: on {t.device}, h on {self.device}")
+        return t.data_ptr()
+
+    def out(self, t, shape, dtype):
+        return self.h.new_empty(shape, dtype=dtype) if t is None else t
+
+    def workspace(self, ws):
+        if ws is None or ws.nbytes < self.ws_bytes:
+            ws = self.h.new_empty((self.ws_bytes,), dtype=_torch().uint8)
+        return ws, self.ptr(ws, ws.dtype, "ws", self.ws_bytes), ws.nbytes
+
+    def head(self, C, codes, fmt, d, softcap):
+        """The arguments every loss call begins with."""
+        return (self.ptr(self.h, self.h.dtype, "h", 0), self.bf16,
+                self.ptr(C, _torch().float32, "C", self.book_bytes),
+                self.ptr(codes, self.code_dtype, "codes", self.codes_bytes), fmt, d, self.N,
+                float(softcap))
+
+
+def _lists(call, val, idx, temperature):
+    """The arguments of a teacher's lists [N, k]."""
     torch = _torch()
-    for t in others:
-        if t is not None and t.device != like.device:
-            raise ValueError(f"tensors on {t.device} and {like.device}: one device expected")
-    if not like.is_cuda:          # a CPU tensor is refused by name below
-        yield stream
-        return
-    with torch.cuda.device(like.device):
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            yield torch.cuda.current_stream()
+    n = call.N * idx.shape[1] * 4
+    return (call.ptr(val, torch.float32, "teacher_val", n),
+            call.ptr(idx, torch.int32, "teacher_idx", n), idx.shape[1], float(temperature))
 
 
-def _hidden(h, d):
-    """(pointer, bf16 flag, N) of hidden states [N, D] float32 or bfloat16."""
-    torch = _torch()
-    if h.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"h: dtype {h.dtype}, expected float32 or bfloat16")
-    N = _tokens(h, d)
-    return _cuda(h, h.dtype, "h"), int(h.dtype == torch.bfloat16), N
-
-
-def _lists(val, idx, N):
-    """k of a teacher's lists [N, k]."""
-    if idx.dim() != 2 or idx.shape[0] != N or tuple(val.shape) != tuple(idx.shape):
-        raise ValueError(f"teacher_val, teacher_idx: [{N}, k] expected")
+def _lists_k(h, val, idx):
+    if idx.dim() != 2 or idx.shape[0] != (h.shape[0] if h.dim() == 2 else 1) or \
+            val.shape != idx.shape:
+        raise ValueError("teacher_val, teacher_idx: [N, k] expected")
     return idx.shape[1]
 
 
-def _run_loss(fn, h, C, codes, fmt, d, extra, k, tensors, softcap, loss, lse, ws, stream):
-    torch = _torch()
-    with _on(stream, h, C, codes, loss, lse, ws, *tensors) as s:
-        hp, hb, N = _hidden(h, d)
-        if loss is None:
-            loss = _empty((N,), torch.float32, h)
-        if lse is None:
-            lse = _empty((N,), torch.float32, h)
-        wp, wn, ws = _workspace(rq_loss_workspace_bytes(d, N, fmt, k), h, ws)
-        _check(fn, getattr(lib(), fn)(
-            hp, hb, _cuda(C, torch.float32, "C", _book_bytes(d)),
-            _cuda(codes, _codes_dtype(fmt), "codes", rq_codes_bytes(d, fmt)), fmt, d, N,
-            float(softcap), *extra(N), _cuda(loss, torch.float32, "loss", N * 4),
-            _cuda(lse, torch.float32, "lse", N * 4), wp, wn, _stream(s)))
+def _run_loss(fn, h, C, codes, fmt, d, k, extra, softcap, loss, lse, ws, stream):
+    f32 = _torch().float32
+    with _LossCall(h, d, fmt, k, False, stream) as c:
+        loss, lse = c.out(loss, (c.N,), f32), c.out(lse, (c.N,), f32)
+        args = c.head(C, codes, fmt, d, softcap) + extra(c)
+        ws, wp, wn = c.workspace(ws)
+        _check(fn, getattr(lib(), fn)(*args, c.ptr(loss, f32, "loss", c.N * 4),
+                                      c.ptr(lse, f32, "lse", c.N * 4), wp, wn, _stream(None)))
     return loss, lse, ws
 
 
-def _run_grad(fn, h, C, codes, fmt, d, extra, k, tensors, lse, index, weight, softcap, want_dh,
-              want_dC, dh, dC, ws, stream):
+def _run_grad(fn, h, C, codes, fmt, d, k, extra, lse, index, weight, softcap, want_dh, want_dC, dh,
+              dC, ws, stream):
     torch = _torch()
-    with _on(stream, h, C, codes, lse, index, weight, dh, dC, ws, *tensors) as s:
-        hp, hb, N = _hidden(h, d)
-        if want_dh and dh is None:
-            dh = _empty((N, d.D), h.dtype, h)
-        if want_dC and dC is None:
-            dC = _empty((d.M, d.L, d.K, d.D // d.M), torch.float32, h)
-        wp, wn, ws = _workspace(rq_loss_workspace_bytes(d, N, fmt, k, True), h, ws)
+    f32 = torch.float32
+    with _LossCall(h, d, fmt, k, True, stream) as c:
+        if want_dh:
+            dh = c.out(dh, (c.N, d.D), h.dtype)
+        if want_dC:
+            dC = c.out(dC, (d.M, d.L, d.K, d.D // d.M), f32)
+        args = c.head(C, codes, fmt, d, softcap) + extra(c)
+        ws, wp, wn = c.workspace(ws)
         _check(fn, getattr(lib(), fn)(
-            hp, hb, _cuda(C, torch.float32, "C", _book_bytes(d)),
-            _cuda(codes, _codes_dtype(fmt), "codes", rq_codes_bytes(d, fmt)), fmt, d, N,
-            float(softcap), *extra(N), _cuda(lse, torch.float32, "lse", N * 4),
-            _ptr_or_null(weight, torch.float32, "weight", N * 4),
-            _cuda(index, torch.uint8, "index", rq_grad_index_bytes(d)),
-            _ptr_or_null(dh, h.dtype, "dh", N * d.D * h.element_size()),
-            _ptr_or_null(dC, torch.float32, "dC", _book_bytes(d)), wp, wn, _stream(s)))
+            *args, c.ptr(lse, f32, "lse", c.N * 4),
+            None if weight is None else c.ptr(weight, f32, "weight", c.N * 4),
+            c.ptr(index, torch.uint8, "index", c.index_bytes),
+            None if dh is None else c.ptr(dh, h.dtype, "dh", c.N * d.D * h.element_size()),
+            None if dC is None else c.ptr(dC, f32, "dC", c.book_bytes), wp, wn, _stream(None)))
     return dh, dC, ws
 
 
@@ -562,13 +613,16 @@ def rq_prepare_grad(codes, fmt: int, d: RqDims, out=None, stream=None):
     """Codes in any layout -> the index uint8 [rq_grad_index_bytes(d)] that
     the gradients of the losses sum the vocabulary's rows by."""
     torch = _torch()
-    with _on(stream, codes, out) as s:
-        nbytes = rq_grad_index_bytes(d)
-        if out is None:
-            out = _empty((nbytes,), torch.uint8, codes)
-        _check("rq_prepare_grad", lib().rq_prepare_grad(
-            _cuda(codes, _codes_dtype(fmt), "codes", rq_codes_bytes(d, fmt)), fmt, d,
-            _cuda(out, torch.uint8, "index", nbytes), _stream(s)))
+    nbytes = rq_grad_index_bytes(d)
+    with torch.cuda.device(codes.device) if codes.is_cuda else contextlib.nullcontext():
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            if out is None:
+                out = _empty((nbytes,), torch.uint8, codes)
+            if out.device != codes.device:
+                raise ValueError(f"out: on {out.device}, codes on {codes.device}")
+            _check("rq_prepare_grad", lib().rq_prepare_grad(
+                _cuda(codes, _codes_dtype(fmt), "codes", rq_codes_bytes(d, fmt)), fmt, d,
+                _cuda(out, torch.uint8, "index", nbytes), _stream(None)))
     return out
 
 
@@ -577,10 +631,10 @@ def rq_xent(h, C, codes, fmt: int, d: RqDims, target, softcap: float = 30.0, los
     """Softmax cross entropy of the head against target ids int32 [N] (below
     0: none, loss 0), h [N, D] float32 or bfloat16.  Returns (loss float32
     [N], lse float32 [N], ws)."""
-    torch = _torch()
-    return _run_loss("rq_xent", h, C, codes, fmt, d,
-                     lambda N: (_cuda(target, torch.int32, "target", N * 4),), 1, (target,),
-                     softcap, loss, lse, ws, stream)
+    i32 = _torch().int32
+    return _run_loss("rq_xent", h, C, codes, fmt, d, 1,
+                     lambda c: (c.ptr(target, i32, "target", c.N * 4),), softcap, loss, lse, ws,
+                     stream)
 
 
 def rq_xent_grad(h, C, codes, fmt: int, d: RqDims, target, lse, index, weight=None,
@@ -589,10 +643,10 @@ def rq_xent_grad(h, C, codes, fmt: int, d: RqDims, target, lse, index, weight=No
     """Gradient of sum_n weight[n] loss[n] of rq_xent (weight float32 [N],
     None: all 1), from its lse and rq_prepare_grad's index.  Returns (dh [N, D]
     in h's type or None, dC float32 [M, L, K, ds] or None, ws)."""
-    torch = _torch()
-    return _run_grad("rq_xent_grad", h, C, codes, fmt, d,
-                     lambda N: (_cuda(target, torch.int32, "target", N * 4),), 1, (target,), lse,
-                     index, weight, softcap, want_dh, want_dC, dh, dC, ws, stream)
+    i32 = _torch().int32
+    return _run_grad("rq_xent_grad", h, C, codes, fmt, d, 1,
+                     lambda c: (c.ptr(target, i32, "target", c.N * 4),), lse, index, weight,
+                     softcap, want_dh, want_dC, dh, dC, ws, stream)
 
 
 def rq_distill(h, C, codes, fmt: int, d: RqDims, teacher_val, teacher_idx,
@@ -601,13 +655,9 @@ def rq_distill(h, C, codes, fmt: int, d: RqDims, teacher_val, teacher_idx,
     """Distillation from a teacher's top logits float32 [N, k] at ids int32
     [N, k] (below 0: none), as rq_topk_sample returns them.  Returns (loss
     float32 [N], lse float32 [N] at the temperature, ws)."""
-    torch = _torch()
-    k = _lists(teacher_val, teacher_idx, _tokens(h, d))
-    return _run_loss("rq_distill", h, C, codes, fmt, d,
-                     lambda N: (_cuda(teacher_val, torch.float32, "teacher_val"),
-                                _cuda(teacher_idx, torch.int32, "teacher_idx"), k,
-                                float(temperature)),
-                     k, (teacher_val, teacher_idx), softcap, loss, lse, ws, stream)
+    return _run_loss("rq_distill", h, C, codes, fmt, d, _lists_k(h, teacher_val, teacher_idx),
+                     lambda c: _lists(c, teacher_val, teacher_idx, temperature), softcap, loss,
+                     lse, ws, stream)
 
 
 def rq_distill_grad(h, C, codes, fmt: int, d: RqDims, teacher_val, teacher_idx, lse, index,
@@ -615,14 +665,10 @@ def rq_distill_grad(h, C, codes, fmt: int, d: RqDims, teacher_val, teacher_idx, 
                     want_dh: bool = True, want_dC: bool = True, dh=None, dC=None, ws=None,
                     stream=None):
     """Gradient of sum_n weight[n] loss[n] of rq_distill; see rq_xent_grad."""
-    torch = _torch()
-    k = _lists(teacher_val, teacher_idx, _tokens(h, d))
     return _run_grad("rq_distill_grad", h, C, codes, fmt, d,
-                     lambda N: (_cuda(teacher_val, torch.float32, "teacher_val"),
-                                _cuda(teacher_idx, torch.int32, "teacher_idx"), k,
-                                float(temperature)),
-                     k, (teacher_val, teacher_idx), lse, index, weight, softcap, want_dh, want_dC,
-                     dh, dC, ws, stream)
+                     _lists_k(h, teacher_val, teacher_idx),
+                     lambda c: _lists(c, teacher_val, teacher_idx, temperature), lse, index,
+                     weight, softcap, want_dh, want_dC, dh, dC, ws, stream)
 
 
 def rq_device_error(clear: bool = True) -> int:

@@ -290,10 +290,24 @@ Problem slice(const Problem &q, int64_t n0, int64_t n) {
   return p;
 }
 
-cudaError_t scales(const Problem &q, const Layout &x, const float *w, void *ws, cudaStream_t s) {
-  return launch_loss_amax(q.h, q.bf16, (int64_t)q.N * q.d.D, q.C,
-                          (int64_t)q.d.M * q.d.L * q.d.K * q.ds(), w, w ? q.N : 0,
-                          at<float>(ws, x.amax), s);
+// Scales of the operands of all tokens (`x` on the tensor cores), and the
+// sparse part of the gradient of the tokens of `part` (null: a loss).
+cudaError_t begin(const Problem &all, const Layout &x, bool amax, const Problem *part,
+                  const float *w, const float *part_w, void *ws, const DevInfo &di,
+                  cudaStream_t s) {
+  const rq_dims &d = all.d;
+  return launch_loss_begin(all.h, all.bf16, (int64_t)all.N * d.D, all.C,
+                           (int64_t)d.M * d.L * d.K * all.ds(), w, w ? all.N : 0,
+                           amax ? at<float>(ws, x.amax) : nullptr, part ? part->t : all.t,
+                           part ? part->N : 0, d.V, part_w, at<int32_t>(ws, x.sid),
+                           at<float>(ws, x.sq), at<float>(ws, x.f), di.err, s);
+}
+
+// h's planes, and the logits at the listed ids.
+cudaError_t pick(const Problem &q, const Layout &x, const int32_t *id, void *ws, cudaStream_t s) {
+  return launch_loss_pick(q.h, q.bf16, q.N, x.hp, at<float>(ws, x.amax), at<__half>(ws, x.hh),
+                          q.bf16 ? nullptr : at<__half>(ws, x.hl), q.src(), q.C, q.d.D, q.d.M,
+                          q.d.L, id, q.t.k, q.cap, at<float>(ws, x.y), s);
 }
 
 // Piece [v0, v0 + rows) decoded.
@@ -324,14 +338,11 @@ cudaError_t for_pieces(const rq_dims &d, Each &&each) {
 cudaError_t tensor_loss(const Problem &all, const Layout &x, float *loss, float *lse, void *ws,
                         const DevInfo &di, cudaStream_t s) {
   float *amax = at<float>(ws, x.amax), *y = at<float>(ws, x.y);
-  RQ_TRY(scales(all, x, nullptr, ws, s));
+  RQ_TRY(begin(all, x, true, nullptr, nullptr, nullptr, ws, di, s));
   for (int64_t n0 = 0; n0 < all.N; n0 += x.chunk) {
     const Problem q = slice(all, n0, all.N - n0 < x.chunk ? all.N - n0 : x.chunk);
     const rq_dims &d = q.d;
-    RQ_TRY(launch_loss_split_h(q.h, q.bf16, q.N, d.D, x.hp, amax, at<__half>(ws, x.hh),
-                               q.bf16 ? nullptr : at<__half>(ws, x.hl), s));
-    RQ_TRY(launch_loss_pick(q.h, q.bf16, q.src(), q.C, d.D, d.M, d.L, q.t.id, q.N, q.t.k, q.cap, y,
-                            s));
+    RQ_TRY(pick(q, x, q.t.id, ws, s));
     int part0 = 0;
     RQ_TRY(for_pieces(d, [&](int64_t v0, int64_t rows) {
       RQ_TRY(decode(q, x, v0, rows, ws, di, s));
@@ -358,16 +369,13 @@ cudaError_t products_grad(const Problem &all, const Layout &x, const float *lse,
   int32_t *sid = at<int32_t>(ws, x.sid);
   float *sq = at<float>(ws, x.sq);
   const int64_t books = (int64_t)all.d.M * all.d.L * all.d.K * all.ds();
-  RQ_TRY(scales(all, x, w, ws, s));
   for (int64_t n0 = 0; n0 < all.N; n0 += x.chunk) {
     const Problem q = slice(all, n0, all.N - n0 < x.chunk ? all.N - n0 : x.chunk);
     const rq_dims &d = q.d;
     const float *ql = lse + n0;
     const int splits = dh_splits(d, q.N);
-    RQ_TRY(launch_loss_split_h(q.h, q.bf16, q.N, d.D, x.hp, amax, at<__half>(ws, x.hh),
-                               q.bf16 ? nullptr : at<__half>(ws, x.hl), s));
-    RQ_TRY(launch_loss_sparse(q.t, q.N, d.V, w ? w + n0 : nullptr, sid, sq, f, di.err, s));
-    RQ_TRY(launch_loss_pick(q.h, q.bf16, q.src(), q.C, d.D, d.M, d.L, sid, q.N, q.t.k, q.cap, y, s));
+    RQ_TRY(begin(all, x, n0 == 0, &q, w, w ? w + n0 : nullptr, ws, di, s));
+    RQ_TRY(pick(q, x, sid, ws, s));
     RQ_TRY(for_pieces(d, [&](int64_t v0, int64_t rows) {
       RQ_TRY(decode(q, x, v0, rows, ws, di, s));
       GemmArgs g = gemm_args(q, amax, di);
@@ -428,18 +436,14 @@ cudaError_t sums_grad(const Problem &q, const Layout &x, const float *lse, const
   int32_t *sid = at<int32_t>(ws, x.sid);
   float *sq = at<float>(ws, x.sq), *f = at<float>(ws, x.f), *dz = at<float>(ws, x.dz);
   float *S = at<float>(ws, x.S), *dhp = dh ? at<float>(ws, x.dhp) : nullptr;
-  RQ_TRY(launch_loss_sparse(q.t, q.N, d.V, w, sid, sq, f, di.err, s));
+  RQ_TRY(begin(q, x, !x.how.serve, &q, nullptr, w, ws, di, s));
   const float *y = at<float>(ws, x.logits);
   if (x.how.serve) {
     RQ_TRY(launch_loss_dz(y, q.N, d.V, lse, f, q.t.beta, q.cap, dz, x.vp, s));
   } else {
-    float *amax = at<float>(ws, x.amax), *picks = at<float>(ws, x.y);
-    y = picks;
-    RQ_TRY(scales(q, x, nullptr, ws, s));
-    RQ_TRY(launch_loss_split_h(q.h, q.bf16, q.N, d.D, x.hp, amax, at<__half>(ws, x.hh),
-                               q.bf16 ? nullptr : at<__half>(ws, x.hl), s));
-    RQ_TRY(launch_loss_pick(q.h, q.bf16, q.src(), q.C, d.D, d.M, d.L, sid, q.N, q.t.k, q.cap, picks,
-                            s));
+    const float *amax = at<float>(ws, x.amax);
+    y = at<float>(ws, x.y);
+    RQ_TRY(pick(q, x, sid, ws, s));
     RQ_TRY(for_pieces(d, [&](int64_t v0, int64_t rows) {
       RQ_TRY(decode(q, x, v0, rows, ws, di, s));
       GemmArgs g = gemm_args(q, amax, di);

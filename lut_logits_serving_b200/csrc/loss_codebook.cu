@@ -281,7 +281,9 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
     abort_flag = 0;
   }
   if (tid < 4) vals[tid * kPairPitch + kGradRows] = 0.f;
+  griddep_launch_dependents();
   __syncthreads();
+  griddep_wait();
   // thread 0 keeps the copies a step (units) and a block (values) ahead
   GatherAhead nu{}, nv{};
   int it = 0, iv = 0;        // copies issued
@@ -449,6 +451,8 @@ out:
 __global__ void __launch_bounds__(256) codebook_join_kernel(const float *__restrict__ part,
                                                             int splits, int64_t n,
                                                             float *__restrict__ out) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   float s = part[i];
@@ -465,6 +469,8 @@ constexpr int kFinTokens = 4;        // tokens whose sums a thread holds at once
 __global__ void __launch_bounds__(kFinThreads) codebook_finish_kernel(
     const float *__restrict__ S, int splits, const void *h, int bf16, int nt,
     const float *__restrict__ C, int D, int L, int K, int P, int ds, float *dC, float *dhp) {
+  griddep_launch_dependents();
+  griddep_wait();
   extern __shared__ float fin[];     // [nt][ds] hidden slices, [8][kFinTokens][ds] partials
   const int p = blockIdx.x, m = p / L, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float *part = fin + nt * ds;
@@ -538,6 +544,8 @@ __global__ void __launch_bounds__(kFinThreads) codebook_finish_kernel(
 __global__ void __launch_bounds__(256) codebook_dh_kernel(const float *__restrict__ dhp, int nt,
                                                           int D, int L, int ds, int bf16,
                                                           void *dh) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= (int64_t)nt * D) return;
   const int t = (int)(i / D), c = (int)(i % D), m = c / ds, j = c % ds;
@@ -613,7 +621,7 @@ cudaError_t launch_gather(GatherArgs a, const GatherPlan &p, const DevInfo &di, 
   if (e != cudaSuccess) return e;
   void *args[] = {&a};
   return launch_maybe_pdl(fn, dim3((unsigned)(p.units < di.sms ? p.units : di.sms)),
-                          dim3(kGatherThreads), p.smem, s, args, false);
+                          dim3(kGatherThreads), p.smem, s, args, true);
 }
 
 int blocks_of(int64_t rows) { return (int)((rows + kGradRows - 1) / kGradRows); }
@@ -654,8 +662,7 @@ cudaError_t launch_codebook_rows(const float *dwt, int64_t pitch, int64_t v0, in
 
 cudaError_t launch_codebook_join(const float *part, int splits, int64_t n, float *dC,
                                  cudaStream_t s) {
-  codebook_join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(part, splits, n, dC);
-  return cudaGetLastError();
+  return pdl_launch(codebook_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), (size_t)0, s, part, splits, n, dC);
 }
 
 int codebook_sum_splits(int64_t V, int M, int L, int K, int N) {
@@ -688,16 +695,13 @@ cudaError_t launch_codebook_finish(const float *S, int splits, const void *h, in
                                    float *dhp, cudaStream_t s) {
   const int ds = D / M, P = M * L;
   const size_t smem = (size_t)(N + kFinThreads / 32 * kFinTokens) * ds * 4;
-  codebook_finish_kernel<<<P, kFinThreads, smem, s>>>(S, splits, h, bf16, N, C, D, L, K, P, ds, dC,
-                                                      dhp);
-  return cudaGetLastError();
+  return pdl_launch(codebook_finish_kernel, dim3(P), dim3(kFinThreads), smem, s, S, splits, h, bf16, N, C, D, L, K, P, ds, dC, dhp);
 }
 
 cudaError_t launch_codebook_dh(const float *dhp, int N, int D, int M, int L, int bf16, void *dh,
                                cudaStream_t s) {
   const int64_t n = (int64_t)N * D;
-  codebook_dh_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(dhp, N, D, L, D / M, bf16, dh);
-  return cudaGetLastError();
+  return pdl_launch(codebook_dh_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), (size_t)0, s, dhp, N, D, L, D / M, bf16, dh);
 }
 
 }  // namespace rq

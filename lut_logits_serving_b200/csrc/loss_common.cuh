@@ -47,9 +47,9 @@ struct CodeSrc {
 // largest element.  a b = a_hi b_hi + a_lo b_hi + a_hi b_lo + (dropped
 // a_lo b_lo, 2^-22 |a b|).
 
-// Largest magnitudes found by loss_amax_kernel: kAmaxBlocks partial maxima
+// Largest magnitudes found by loss_begin_kernel: kAmaxBlocks partial maxima
 // each of |h|, of |C| and of |weight|.
-constexpr int kAmaxBlocks = 64;
+constexpr int kAmaxBlocks = 128;
 enum { kAmaxH = 0, kAmaxC = 1, kAmaxW = 2 };
 
 // Largest power of two s (clamped to 2^-60 .. 2^60) with bound s < 2^14; 1 for
@@ -139,18 +139,10 @@ cudaError_t launch_loss_gemm(int mode, const GemmPlanes &A, const GemmPlanes &B,
 
 // Rows of a piece decoded into fp16 hi / lo planes and the other row-wise
 // kernels (loss_rows.cu).
-cudaError_t launch_loss_amax(const void *h, int bf16, int64_t nh, const float *C, int64_t nc,
-                             const float *w, int64_t nw, float *amax, cudaStream_t s);
-cudaError_t launch_loss_split_h(const void *h, int bf16, int64_t N, int D, int64_t pitch,
-                                const float *amax, __half *hi, __half *lo, cudaStream_t s);
 cudaError_t launch_loss_widen_h(const void *h, int64_t n, float *out, cudaStream_t s);
 cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, int ds, int64_t v0,
                                int64_t rows, int64_t pitch, const float *amax, __half *hi,
                                __half *lo, const DevInfo &di, cudaStream_t s);
-// y[n][j] = softcapped logit of id[n][j] (0 where id < 0 or >= V)
-cudaError_t launch_loss_pick(const void *h, int bf16, const CodeSrc &cs, const float *C, int D,
-                             int M, int L, const int32_t *id, int64_t N, int k, float cap,
-                             float *y, cudaStream_t s);
 // (max, sum) parts of logits [N][V] at 1 / T = beta
 int loss_stat_parts(int64_t V);
 cudaError_t launch_loss_logit_stats(const float *logits, int64_t N, int64_t V, float beta,
@@ -164,14 +156,22 @@ struct LossTargets {
   int k;
   float T, beta;
 };
+// The first launch: scales (amax null: none) and the gradient's sparse part of
+// `rows` rows: q, merged ids and f = weight T (0 for rows without a target)
+cudaError_t launch_loss_begin(const void *h, int bf16, int64_t nh, const float *C, int64_t nc,
+                              const float *w, int64_t nw, float *amax, const LossTargets &t,
+                              int64_t rows, int64_t V, const float *weight, int32_t *sid, float *sq,
+                              float *f, unsigned *err, cudaStream_t s);
+// fp16 planes of h, and y[n][j] = softcapped logit of id[n][j] (0 where the id
+// is < 0 or >= V)
+cudaError_t launch_loss_pick(const void *h, int bf16, int64_t N, int64_t pitch, const float *amax,
+                             __half *hi, __half *lo, const CodeSrc &cs, const float *C, int D, int M,
+                             int L, const int32_t *id, int k, float cap, float *y, cudaStream_t s);
 // lse and loss from the parts and the picked logits: y[n * k + j], or, with
 // y_is_logits, y[n * V + id].
 cudaError_t launch_loss_finish(const float2 *stat, int parts, int stat_ld, int64_t N, int64_t V,
                                const LossTargets &t, const float *y, bool y_is_logits, float *loss,
                                float *lse, unsigned *err, cudaStream_t s);
-// q, merged ids and f = w T (0 for rows without a target)
-cudaError_t launch_loss_sparse(const LossTargets &t, int64_t N, int64_t V, const float *w,
-                               int32_t *sid, float *sq, float *f, unsigned *err, cudaStream_t s);
 // dz planes at the listed ids of rows [v0, v0 + rows)
 cudaError_t launch_loss_fix_planes(const int32_t *sid, const float *sq, const float *y, int k,
                                    int64_t N, int64_t v0, int64_t rows, const float *lse,

@@ -149,9 +149,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                  "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  griddep_launch_dependents();
   tc_before();
   __syncthreads();
   tc_after();
+  griddep_wait();
   const uint32_t tmem = tmem_slot;
 
   const int mn = g.m_tiles * g.n_tiles, total = mn * g.splits;
@@ -464,7 +466,7 @@ cudaError_t launch_gemm(const GemmPlanes &A, const GemmPlanes &B, GemmArgs a, co
   if (total < 1 || total > 0x7fffffff) return cudaErrorInvalidValue;
   const int grid = (int)(total < di.sms ? total : di.sms);
   void *args[] = {&ah, &al, &bh, &bl, &a};
-  return launch_maybe_pdl(fn, dim3(grid), dim3(kGemmThreads), smem, s, args, false);
+  return launch_maybe_pdl(fn, dim3(grid), dim3(kGemmThreads), smem, s, args, true);
 }
 
 }  // namespace

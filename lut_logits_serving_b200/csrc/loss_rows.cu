@@ -33,48 +33,76 @@ __device__ __forceinline__ float block_max(float m, float *red) {
   return m;
 }
 
-// Blocks [0, 64): |h|, [64, 128): |C|, [128, 192): |w| (1 without weights).
-__global__ void __launch_bounds__(512) loss_amax_kernel(const void *h, int bf16, int64_t nh,
-                                                        const float *__restrict__ C, int64_t nc,
-                                                        const float *__restrict__ w, int64_t nw,
-                                                        float *__restrict__ amax) {
-  __shared__ float red[32];
-  const int kind = blockIdx.x / kAmaxBlocks, b = blockIdx.x % kAmaxBlocks;
+__device__ __forceinline__ float abs_max(const float *x, int64_t n, int b) {
   const int64_t stride = (int64_t)kAmaxBlocks * blockDim.x;
   const int64_t i0 = (int64_t)b * blockDim.x + threadIdx.x;
   float m = 0.f;
-  if (kind == kAmaxH) {
-#pragma unroll 8
-    for (int64_t i = i0; i < nh; i += stride) m = fmaxf(m, fabsf(load_h(h, bf16, i)));
-  } else if (kind == kAmaxC) {
-#pragma unroll 8
-    for (int64_t i = i0; i < nc; i += stride) m = fmaxf(m, fabsf(C[i]));
-  } else if (w != nullptr) {
-    for (int64_t i = i0; i < nw; i += stride) m = fmaxf(m, fabsf(w[i]));
-  } else {
-    m = 1.f;
+  int64_t done = 0;
+  if ((reinterpret_cast<uintptr_t>(x) & 15) == 0) {
+    done = n / 4 * 4;
+#pragma unroll 4
+    for (int64_t i = i0; i < n / 4; i += stride) {
+      const float4 v = __ldg(reinterpret_cast<const float4 *>(x) + i);
+      m = fmaxf(fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+    }
   }
-  m = block_max(m, red);
-  if (threadIdx.x == 0) amax[blockIdx.x] = m;
+  for (int64_t i = done + i0; i < n; i += stride) m = fmaxf(m, fabsf(x[i]));
+  return m;
 }
 
-__global__ void __launch_bounds__(256) loss_split_h_kernel(const void *h, int bf16, int64_t N,
-                                                           int D, int64_t pitch,
-                                                           const float *__restrict__ amax,
-                                                           __half *__restrict__ hi,
-                                                           __half *__restrict__ lo) {
-  const float s = scale_h(amax);
-  const int64_t n = blockIdx.x;
-  for (int i = threadIdx.x; i < D; i += blockDim.x) {
-    __half a, b;
-    split_f16(__fmul_rn(load_h(h, bf16, n * D + i), s), a, b);
-    hi[n * pitch + i] = a;
-    if (lo) lo[n * pitch + i] = b;
+// The first kernel of a call.  Blocks [0, amax_blocks): partial maxima of |h|,
+// |C| and |w| (1 without weights), kAmaxBlocks each; the blocks after those: a
+// row each of the gradient's sparse part (sparse_row).
+struct BeginArgs {
+  int amax_blocks;
+  const void *h;
+  int bf16;
+  int64_t nh;
+  const float *C;
+  int64_t nc;
+  const float *w;
+  int64_t nw;
+  float *amax;
+  LossTargets t;
+  int64_t V;
+  const float *weight;     // of the rows of the sparse part
+  int32_t *sid;
+  float *sq, *f;
+  unsigned *err;
+};
+
+__device__ void sparse_row(const BeginArgs &a, int64_t n, float *lists);
+
+__global__ void __launch_bounds__(256) loss_begin_kernel(const BeginArgs a) {
+  extern __shared__ float lists[];
+  __shared__ float red[32];
+  griddep_launch_dependents();
+  griddep_wait();
+  if ((int)blockIdx.x >= a.amax_blocks) {
+    sparse_row(a, (int)blockIdx.x - a.amax_blocks, lists);
+    return;
   }
+  const int kind = blockIdx.x / kAmaxBlocks, b = blockIdx.x % kAmaxBlocks;
+  float m = 0.f;
+  if (kind == kAmaxH && a.bf16) {
+    for (int64_t i = (int64_t)b * blockDim.x + threadIdx.x; i < a.nh;
+         i += (int64_t)kAmaxBlocks * blockDim.x)
+      m = fmaxf(m, fabsf(load_h(a.h, 1, i)));
+  } else if (kind == kAmaxH) {
+    m = abs_max(static_cast<const float *>(a.h), a.nh, b);
+  } else if (kind == kAmaxC) {
+    m = abs_max(a.C, a.nc, b);
+  } else {
+    m = a.w ? abs_max(a.w, a.nw, b) : 1.f;
+  }
+  m = block_max(m, red);
+  if (threadIdx.x == 0) a.amax[blockIdx.x] = m;
 }
 
 __global__ void __launch_bounds__(256) loss_widen_h_kernel(const __nv_bfloat16 *__restrict__ h,
                                                            int64_t n, float *__restrict__ out) {
+  griddep_launch_dependents();
+  griddep_wait();
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
        i += (int64_t)gridDim.x * blockDim.x)
     out[i] = __bfloat162float(h[i]);
@@ -154,6 +182,8 @@ struct RowCodes {
 template <int LL, bool EVEN, bool SMEM>
 __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeArgs a) {
   extern __shared__ __align__(16) float books[];
+  griddep_launch_dependents();
+  griddep_wait();
   const int ds = a.ds, L = LL > 0 ? LL : a.L, K = a.cs.K, tid = threadIdx.x;
   const float se = scale_e(a.amax, a.L);
   const int words = (a.gs * ds + 1) / 2;            // pairs of a row's group
@@ -254,40 +284,64 @@ __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeAr
 
 // ------------------------------------------------------------- picked logits
 
-// One warp per (token, list entry): <h_n, E_id> in fp32.
-__global__ void __launch_bounds__(256) loss_pick_kernel(const void *h, int bf16, const CodeSrc cs,
-                                                        const float *__restrict__ C, int D, int M,
-                                                        int L, const int32_t *__restrict__ id,
-                                                        int64_t count, int k, float cap,
-                                                        float *__restrict__ y) {
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31, ds = D / M;
-  if (i >= count) return;
-  const int32_t v = id[i];
+// Blocks [0, N): the fp16 planes of a hidden state.  After those, one warp per
+// (token, list entry): <h_n, E_id> in fp32.
+struct PickArgs {
+  const void *h;
+  int bf16;
+  int64_t N, pitch;
+  const float *amax;
+  __half *hi, *lo;
+  CodeSrc cs;
+  const float *C;
+  int D, M, L, k;
+  const int32_t *id;
+  float cap;
+  float *y;
+};
+
+__global__ void __launch_bounds__(256) loss_pick_kernel(const PickArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  if (blockIdx.x < a.N) {
+    const float s = scale_h(a.amax);
+    const int64_t n = blockIdx.x;
+    for (int i = threadIdx.x; i < a.D; i += blockDim.x) {
+      __half x, r;
+      split_f16(__fmul_rn(load_h(a.h, a.bf16, n * a.D + i), s), x, r);
+      a.hi[n * a.pitch + i] = x;
+      if (a.lo) a.lo[n * a.pitch + i] = r;
+    }
+    return;
+  }
+  const int64_t i = (int64_t)(blockIdx.x - a.N) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, ds = a.D / a.M, L = a.L, K = a.cs.K;
+  if (i >= a.N * a.k) return;
+  const int32_t v = a.id[i];
   float z = 0.f;
-  if (v >= 0 && v < cs.V) {
-    const int64_t n = i / k;
-    for (int m = lane; m < M; m += 32) {
-      const int64_t hm = n * D + (int64_t)m * ds;
+  if (v >= 0 && v < a.cs.V) {
+    const int64_t n = i / a.k;
+    for (int m = lane; m < a.M; m += 32) {
+      const int64_t hm = n * a.D + (int64_t)m * ds;
       if (ds == 6 && L == 2) {
-        const float *w0 = C + ((size_t)(2 * m) * cs.K + cs(v, 2 * m)) * 6;
-        const float *w1 = C + ((size_t)(2 * m + 1) * cs.K + cs(v, 2 * m + 1)) * 6;
+        const float *w0 = a.C + ((size_t)(2 * m) * K + a.cs(v, 2 * m)) * 6;
+        const float *w1 = a.C + ((size_t)(2 * m + 1) * K + a.cs(v, 2 * m + 1)) * 6;
 #pragma unroll
         for (int j = 0; j < 6; ++j)
-          z = fmaf(load_h(h, bf16, hm + j), __fadd_rn(__ldg(w0 + j), __ldg(w1 + j)), z);
+          z = fmaf(load_h(a.h, a.bf16, hm + j), __fadd_rn(__ldg(w0 + j), __ldg(w1 + j)), z);
       } else {
         for (int j = 0; j < ds; ++j) {
           float e = 0.f;
           for (int l = 0; l < L; ++l)
-            e = __fadd_rn(e, __ldg(C + ((size_t)(m * L + l) * cs.K + cs(v, m * L + l)) * ds + j));
-          z = fmaf(load_h(h, bf16, hm + j), e, z);
+            e = __fadd_rn(e, __ldg(a.C + ((size_t)(m * L + l) * K + a.cs(v, m * L + l)) * ds + j));
+          z = fmaf(load_h(a.h, a.bf16, hm + j), e, z);
         }
       }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   }
-  if (lane == 0) y[i] = softcap_f(z, cap);
+  if (lane == 0) a.y[i] = softcap_f(z, a.cap);
 }
 
 // ------------------------------------------------------------- statistics
@@ -304,6 +358,8 @@ __global__ void __launch_bounds__(256) loss_logit_stats_kernel(const float *__re
                                                                int64_t V, float beta,
                                                                float2 *__restrict__ stat,
                                                                int stat_ld) {
+  griddep_launch_dependents();
+  griddep_wait();
   __shared__ float2 red[8];
   const int64_t n = blockIdx.y, c0 = (int64_t)blockIdx.x * kStatCols;
   float x[kStatCols / 256], m = -INFINITY, s = 0.f;
@@ -353,6 +409,8 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const float2 *__restr
                                                            int y_is_logits,
                                                            float *__restrict__ loss,
                                                            float *__restrict__ lse, unsigned *err) {
+  griddep_launch_dependents();
+  griddep_wait();
   __shared__ float2 red[32][33];
   const int r = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * 32 + r;
@@ -411,24 +469,19 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const float2 *__restr
 
 // One block per row: q_j of the listed ids, an id listed twice merged into its
 // first place (so each id is corrected once, by one thread), and f = w T.
-__global__ void __launch_bounds__(128) loss_sparse_kernel(const LossTargets t, int64_t V,
-                                                          const float *__restrict__ w,
-                                                          int32_t *__restrict__ sid,
-                                                          float *__restrict__ sq,
-                                                          float *__restrict__ f, unsigned *err) {
-  extern __shared__ float lists[];                 // [k] q, [k] id
-  __shared__ float red[4], red2[4];
-  const int64_t n = blockIdx.x;
-  const int tid = threadIdx.x, k = t.k;
+__device__ void sparse_row(const BeginArgs &a, int64_t n, float *lists) {
+  __shared__ float red[8], red2[8];       // lists: [k] q, [k] id
+  const LossTargets &t = a.t;
+  const int tid = threadIdx.x, k = t.k, nt = blockDim.x, warps = nt / 32;
   float *q = lists;
   int *ids = reinterpret_cast<int *>(lists + k);
   const int32_t *id = t.id + n * k;
   float m = -INFINITY;
-  for (int j = tid; j < k; j += 128) {
+  for (int j = tid; j < k; j += nt) {
     int32_t v = id[j];
     float x = t.val ? t.val[n * k + j] * t.beta : 0.f;
-    if (v >= V) atomicOr(err, RQ_DEVERR_BAD_ID);
-    if (!listed(v, V)) {
+    if (v >= a.V) atomicOr(a.err, RQ_DEVERR_BAD_ID);
+    if (!listed(v, a.V)) {
       v = -1;
       x = -INFINITY;
     }
@@ -439,10 +492,12 @@ __global__ void __launch_bounds__(128) loss_sparse_kernel(const LossTargets t, i
   m = warp_max(m);
   if ((tid & 31) == 0) red[tid >> 5] = m;
   __syncthreads();
-  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  m = red[0];
+  for (int i = 1; i < warps; ++i) m = fmaxf(m, red[i]);
+  const bool some = m > -INFINITY;
   float z = 0.f;
-  if (m > -INFINITY)
-    for (int j = tid; j < k; j += 128) {
+  if (some)
+    for (int j = tid; j < k; j += nt) {
       const float e = ids[j] >= 0 ? expf(q[j] - m) : 0.f;
       q[j] = e;
       z += e;
@@ -450,9 +505,9 @@ __global__ void __launch_bounds__(128) loss_sparse_kernel(const LossTargets t, i
   z = warp_sum(z);
   if ((tid & 31) == 0) red2[tid >> 5] = z;
   __syncthreads();
-  z = (red2[0] + red2[1]) + (red2[2] + red2[3]);
-  const bool some = m > -INFINITY;
-  for (int j = tid; j < k; j += 128) {
+  z = red2[0];
+  for (int i = 1; i < warps; ++i) z += red2[i];
+  for (int j = tid; j < k; j += nt) {
     int v = some ? ids[j] : -1;
     float s = 0.f;
     if (v >= 0) {
@@ -467,10 +522,10 @@ __global__ void __launch_bounds__(128) loss_sparse_kernel(const LossTargets t, i
           if (ids[i] == v) s += q[i];
       }
     }
-    sid[n * k + j] = v;
-    sq[n * k + j] = v >= 0 ? s / z : 0.f;
+    a.sid[n * k + j] = v;
+    a.sq[n * k + j] = v >= 0 ? s / z : 0.f;
   }
-  if (tid == 0) f[n] = some ? (w ? w[n] : 1.f) * t.T : 0.f;
+  if (tid == 0) a.f[n] = some ? (a.weight ? a.weight[n] : 1.f) * t.T : 0.f;
 }
 
 __device__ __forceinline__ float dz_at(float y, float q, float lse, float f, float beta,
@@ -484,6 +539,8 @@ __global__ void __launch_bounds__(256) loss_fix_planes_kernel(
     int k, int64_t count, int64_t v0, int64_t rows, const float *__restrict__ lse,
     const float *__restrict__ f, const float *__restrict__ amax, float T, float beta, float cap,
     __half *__restrict__ hi, __half *__restrict__ lo, int64_t pitch) {
+  griddep_launch_dependents();
+  griddep_wait();
   const float sz = scale_z(amax, T);
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= count) return;
@@ -503,6 +560,8 @@ __global__ void __launch_bounds__(256) loss_dz_kernel(const float *__restrict__ 
                                                       const float *__restrict__ f, float beta,
                                                       float cap, float *__restrict__ dz,
                                                       int64_t pitch) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t n = blockIdx.y;
   const float l = lse[n], w = f[n];
   for (int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x; v < pitch; v += (int64_t)gridDim.x * 256)
@@ -513,6 +572,8 @@ __global__ void __launch_bounds__(256) loss_fix_kernel(
     const int32_t *__restrict__ sid, const float *__restrict__ sq, const float *__restrict__ y,
     int y_is_logits, int k, int64_t count, int64_t V, const float *__restrict__ lse,
     const float *__restrict__ f, float beta, float cap, float *__restrict__ dz, int64_t pitch) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= count || sid[i] < 0) return;
   const int64_t n = i / k, v = sid[i];
@@ -524,6 +585,8 @@ __global__ void __launch_bounds__(256) loss_dh_sum_kernel(const float *__restric
                                                           int splits, int64_t stride,
                                                           int64_t pitch, int64_t N, int D,
                                                           int bf16, void *__restrict__ dh) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= N * D) return;
   const int64_t n = i / D, c = i - n * D;
@@ -537,22 +600,34 @@ unsigned blocks_of(int64_t n, int per) { return (unsigned)((n + per - 1) / per);
 
 }  // namespace
 
-cudaError_t launch_loss_amax(const void *h, int bf16, int64_t nh, const float *C, int64_t nc,
-                             const float *w, int64_t nw, float *amax, cudaStream_t s) {
-  loss_amax_kernel<<<3 * kAmaxBlocks, 512, 0, s>>>(h, bf16, nh, C, nc, w, nw, amax);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_loss_split_h(const void *h, int bf16, int64_t N, int D, int64_t pitch,
-                                const float *amax, __half *hi, __half *lo, cudaStream_t s) {
-  loss_split_h_kernel<<<(unsigned)N, 256, 0, s>>>(h, bf16, N, D, pitch, amax, hi, lo);
-  return cudaGetLastError();
+cudaError_t launch_loss_begin(const void *h, int bf16, int64_t nh, const float *C, int64_t nc,
+                              const float *w, int64_t nw, float *amax, const LossTargets &t,
+                              int64_t rows, int64_t V, const float *weight, int32_t *sid, float *sq,
+                              float *f, unsigned *err, cudaStream_t s) {
+  BeginArgs a;
+  a.amax_blocks = amax ? 3 * kAmaxBlocks : 0;
+  a.h = h;
+  a.bf16 = bf16;
+  a.nh = nh;
+  a.C = C;
+  a.nc = nc;
+  a.w = w;
+  a.nw = nw;
+  a.amax = amax;
+  a.t = t;
+  a.V = V;
+  a.weight = weight;
+  a.sid = sid;
+  a.sq = sq;
+  a.f = f;
+  a.err = err;
+  return pdl_launch(loss_begin_kernel, dim3((unsigned)(a.amax_blocks + rows)), dim3(256),
+                    rows > 0 ? (size_t)t.k * 8 : 0, s, a);
 }
 
 cudaError_t launch_loss_widen_h(const void *h, int64_t n, float *out, cudaStream_t s) {
-  loss_widen_h_kernel<<<blocks_of(n, 1024), 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(h), n,
-                                                         out);
-  return cudaGetLastError();
+  return pdl_launch(loss_widen_h_kernel, dim3(blocks_of(n, 1024)), dim3(256), 0, s,
+                    static_cast<const __nv_bfloat16 *>(h), n, out);
 }
 
 namespace {
@@ -628,38 +703,43 @@ cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, 
   a.items = (int)items;
   void *args[] = {&a};
   return launch_maybe_pdl(fn, dim3((unsigned)(items < ctas ? items : ctas)), dim3(kDecThreads), smem,
-                          s, args, false);
+                          s, args, true);
 }
 
-cudaError_t launch_loss_pick(const void *h, int bf16, const CodeSrc &cs, const float *C, int D,
-                             int M, int L, const int32_t *id, int64_t N, int k, float cap,
-                             float *y, cudaStream_t s) {
-  loss_pick_kernel<<<blocks_of(N * k, 8), 256, 0, s>>>(h, bf16, cs, C, D, M, L, id, N * k, k, cap,
-                                                       y);
-  return cudaGetLastError();
+cudaError_t launch_loss_pick(const void *h, int bf16, int64_t N, int64_t pitch, const float *amax,
+                             __half *hi, __half *lo, const CodeSrc &cs, const float *C, int D, int M,
+                             int L, const int32_t *id, int k, float cap, float *y, cudaStream_t s) {
+  PickArgs a;
+  a.h = h;
+  a.bf16 = bf16;
+  a.N = N;
+  a.pitch = pitch;
+  a.amax = amax;
+  a.hi = hi;
+  a.lo = lo;
+  a.cs = cs;
+  a.C = C;
+  a.D = D;
+  a.M = M;
+  a.L = L;
+  a.k = k;
+  a.id = id;
+  a.cap = cap;
+  a.y = y;
+  return pdl_launch(loss_pick_kernel, dim3((unsigned)N + blocks_of(N * k, 8)), dim3(256), 0, s, a);
 }
 
 int loss_stat_parts(int64_t V) { return (int)((V + kStatCols - 1) / kStatCols); }
 
 cudaError_t launch_loss_logit_stats(const float *logits, int64_t N, int64_t V, float beta,
                                     float2 *stat, int stat_ld, cudaStream_t s) {
-  loss_logit_stats_kernel<<<dim3(loss_stat_parts(V), (unsigned)N), 256, 0, s>>>(logits, V, beta,
-                                                                               stat, stat_ld);
-  return cudaGetLastError();
+  return pdl_launch(loss_logit_stats_kernel, dim3(loss_stat_parts(V), (unsigned)N), dim3(256), (size_t)0, s, logits, V, beta, stat, stat_ld);
 }
 
 cudaError_t launch_loss_finish(const float2 *stat, int parts, int stat_ld, int64_t N, int64_t V,
                                const LossTargets &t, const float *y, bool y_is_logits, float *loss,
                                float *lse, unsigned *err, cudaStream_t s) {
-  loss_finish_kernel<<<blocks_of(N, 32), 1024, 0, s>>>(stat, parts, stat_ld, N, V, t, y,
-                                                       y_is_logits, loss, lse, err);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_loss_sparse(const LossTargets &t, int64_t N, int64_t V, const float *w,
-                               int32_t *sid, float *sq, float *f, unsigned *err, cudaStream_t s) {
-  loss_sparse_kernel<<<(unsigned)N, 128, (size_t)t.k * 8, s>>>(t, V, w, sid, sq, f, err);
-  return cudaGetLastError();
+  return pdl_launch(loss_finish_kernel, dim3(blocks_of(N, 32)), dim3(1024), (size_t)0, s, stat, parts, stat_ld, N, V, t, y, y_is_logits, loss, lse, err);
 }
 
 cudaError_t launch_loss_fix_planes(const int32_t *sid, const float *sq, const float *y, int k,
@@ -667,33 +747,24 @@ cudaError_t launch_loss_fix_planes(const int32_t *sid, const float *sq, const fl
                                    const float *f, const float *amax, float T, float beta,
                                    float cap, __half *hi, __half *lo, int64_t pitch,
                                    cudaStream_t s) {
-  loss_fix_planes_kernel<<<blocks_of(N * k, 256), 256, 0, s>>>(sid, sq, y, k, N * k, v0, rows, lse,
-                                                               f, amax, T, beta, cap, hi, lo,
-                                                               pitch);
-  return cudaGetLastError();
+  return pdl_launch(loss_fix_planes_kernel, dim3(blocks_of(N * k, 256)), dim3(256), (size_t)0, s, sid, sq, y, k, N * k, v0, rows, lse, f, amax, T, beta, cap, hi, lo, pitch);
 }
 
 cudaError_t launch_loss_dz(const float *logits, int64_t N, int64_t V, const float *lse,
                            const float *f, float beta, float cap, float *dz, int64_t pitch,
                            cudaStream_t s) {
-  loss_dz_kernel<<<dim3(blocks_of(pitch, 1024), (unsigned)N), 256, 0, s>>>(logits, V, lse, f, beta,
-                                                                           cap, dz, pitch);
-  return cudaGetLastError();
+  return pdl_launch(loss_dz_kernel, dim3(blocks_of(pitch, 1024), (unsigned)N), dim3(256), (size_t)0, s, logits, V, lse, f, beta, cap, dz, pitch);
 }
 
 cudaError_t launch_loss_fix(const int32_t *sid, const float *sq, const float *y, bool y_is_logits,
                             int k, int64_t N, int64_t V, const float *lse, const float *f,
                             float beta, float cap, float *dz, int64_t pitch, cudaStream_t s) {
-  loss_fix_kernel<<<blocks_of(N * k, 256), 256, 0, s>>>(sid, sq, y, y_is_logits, k, N * k, V, lse, f,
-                                                        beta, cap, dz, pitch);
-  return cudaGetLastError();
+  return pdl_launch(loss_fix_kernel, dim3(blocks_of(N * k, 256)), dim3(256), (size_t)0, s, sid, sq, y, y_is_logits, k, N * k, V, lse, f, beta, cap, dz, pitch);
 }
 
 cudaError_t launch_loss_dh_sum(const float *part, int splits, int64_t stride, int64_t pitch,
                                int64_t N, int D, int bf16, void *dh, cudaStream_t s) {
-  loss_dh_sum_kernel<<<blocks_of(N * D, 256), 256, 0, s>>>(part, splits, stride, pitch, N, D, bf16,
-                                                           dh);
-  return cudaGetLastError();
+  return pdl_launch(loss_dh_sum_kernel, dim3(blocks_of(N * D, 256)), dim3(256), (size_t)0, s, part, splits, stride, pitch, N, D, bf16, dh);
 }
 
 }  // namespace rq
