@@ -20,7 +20,6 @@ constexpr int kServeTokens = 64;          // most tokens of a call on the servin
 constexpr int kSumTokens = 32;            // and of one on sums by code
 constexpr int kSms = 148;                 // sizes do not depend on the current device
 constexpr int kMaxSplits = 32;            // of the vocabulary in dz E
-constexpr int kChain = 4;                 // blocks of 64 per accumulation chain
 constexpr int kMaxList = 1024;            // a teacher's entries per token
 constexpr int kMaxGradK = 4096;           // codewords per codebook, gradients
 
@@ -66,11 +65,11 @@ struct Arena {
 int64_t piece_rows(const rq_dims &d) { return d.V < kPieceRows ? d.V : kPieceRows; }
 int64_t pitch16(int64_t n) { return align_up(n, 16); }   // fp16 rows of whole sectors
 
-int total_parts(const rq_dims &d) {
+int total_parts(const rq_dims &d, int64_t tokens) {
   int n = 0;
   for (int64_t v0 = 0; v0 < d.V; v0 += kPieceRows) {
     const int64_t r = d.V - v0 < kPieceRows ? d.V - v0 : kPieceRows;
-    n += 2 * (int)((r + 255) / 256);
+    n += loss_stats_parts(tokens, r);
   }
   return n;
 }
@@ -186,6 +185,7 @@ Layout layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
   x.how = choose(d, N, fmt, grad);
   const int64_t n = N < kTokenChunk ? N : kTokenChunk, rows = piece_rows(d);
   const int P = d.M * d.L, ds = d.D / d.M;
+  const int64_t last = N % n == 0 ? n : N % n;     // tokens of the last sweep
   x.chunk = n;
   x.hp = pitch16(d.D);
   x.zp = pitch16(rows);
@@ -204,7 +204,12 @@ Layout layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
     x.fused = a.take((int64_t)x.fused_bytes);
   }
   if (!grad) {
-    x.stat = a.take((int64_t)(x.how.serve ? loss_stat_parts(d.V) : total_parts(d)) * n * 8);
+    int parts = loss_stat_parts(d.V);
+    if (!x.how.serve) {
+      parts = total_parts(d, n);
+      if (total_parts(d, last) > parts) parts = total_parts(d, last);
+    }
+    x.stat = a.take((int64_t)parts * n * 8);
   } else {
     x.sid = a.take(n * k * 4);
     x.sq = a.take(n * k * 4);
@@ -220,9 +225,8 @@ Layout layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
       x.dw = a.take((int64_t)d.D * x.zp * 4);
       x.splits = codebook_rows_splits(d.V, rows, d.M, d.L, d.K, ds);
       x.cpart = a.take(x.splits > 1 ? (int64_t)x.splits * P * d.K * ds * 4 : 0);
-      // the last sweep may have fewer tokens and with them more splits
+      // with fewer tokens there are more shares
       int64_t part = dh_splits(d, n) * n;
-      const int64_t last = N % n == 0 ? n : N % n;
       const int64_t p2 = dh_splits(d, last) * last;
       if (p2 > part) part = p2;
       x.part = a.take(part * x.hp * 4);
@@ -269,7 +273,6 @@ GemmPlanes planes(const void *hi, const void *lo, int64_t rows, int64_t cols, in
 GemmArgs gemm_args(const Problem &q, const float *amax, const DevInfo &di) {
   GemmArgs g{};
   g.splits = 1;
-  g.chain = kChain;
   g.amax = amax;
   g.L = q.d.L;
   g.cap = q.cap;
@@ -352,7 +355,7 @@ cudaError_t tensor_loss(const Problem &all, const Layout &x, float *loss, float 
       g.stat = at<float2>(ws, x.stat);
       g.stat_ld = (int)x.chunk;
       g.stat_part0 = part0;
-      part0 += 2 * (int)((rows + 255) / 256);
+      part0 += loss_stats_parts(q.N, rows);
       return launch_loss_gemm(kGemmStats, h_planes(q, x, ws), w_planes(q, x, rows, ws), g, di, s);
     }));
     RQ_TRY(launch_loss_finish(at<float2>(ws, x.stat), part0, (int)x.chunk, q.N, d.V, q.t, y, false,

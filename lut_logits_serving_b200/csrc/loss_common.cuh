@@ -17,6 +17,9 @@ namespace rq {
 // fit half an SM's shared memory.
 constexpr int kGradRows = 8192;
 
+// Exponentials are formed in base 2: exp(x - m) = exp2(x log2 e - m log2 e).
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
 // Code p of row v in any layout, safe for codes >= K (see CodeFix).
 struct CodeSrc {
   const void *codes;
@@ -100,7 +103,7 @@ __device__ __forceinline__ float load_h(const void *h, int bf16, int64_t i) {
 
 // Tensor-core products of the loss kernels (loss_gemm.cu).
 enum LossGemm {
-  kGemmStats = 0,   // y = softcap(h E^T): per (row, 128 columns) max and sum of exp(y / T)
+  kGemmStats = 0,   // y = softcap(h E^T): per row and part max and sum of exp(y / T)
   kGemmGrad = 1,    // y again, gradients of the logits as fp16 hi / lo planes
   kGemmDh = 2,      // dz E, fp32, split over the vocabulary
   kGemmDw = 3,      // (h^T dz), fp32 [D][rows]
@@ -121,7 +124,7 @@ struct GemmArgs {
   int L;
   // epilogues
   float inv_cap, cap, beta, T;
-  float2 *stat;              // [parts][stat_ld] (max, sum)
+  float2 *stat;              // [parts][stat_ld] (max, sum), base 2
   int stat_ld;
   int stat_part0;            // first part of this launch
   const float *lse, *f;      // per row: log-sum-exp, w T (0: no gradient)
@@ -134,7 +137,9 @@ struct GemmArgs {
   unsigned *err;
 };
 
-cudaError_t launch_loss_gemm(int mode, const GemmPlanes &A, const GemmPlanes &B, GemmArgs a,
+// parts of a row that kGemmStats writes for `rows` rows of the vocabulary
+int loss_stats_parts(int64_t tokens, int64_t rows);
+cudaError_t launch_loss_gemm(int mode, const GemmPlanes &A, const GemmPlanes &B, const GemmArgs &a,
                              const DevInfo &di, cudaStream_t s);
 
 // Rows of a piece decoded into fp16 hi / lo planes and the other row-wise

@@ -1,8 +1,8 @@
 // loss_gemm.cu -- the tensor-core products of the loss kernels, each fused
 // with what it feeds:
 //
-//   kGemmStats  y = cap tanh(h E^T / cap); per row and 128 columns the
-//               maximum of y / T and the sum of exp(y / T - max)
+//   kGemmStats  y = cap tanh(h E^T / cap); per row and half a tile's columns
+//               the maximum m of y / T and the sum of exp(y / T - m), base 2
 //   kGemmGrad   y again; dz = w T exp(y / T - lse) (1 - (y / cap)^2), as fp16
 //               planes for the next two, or (kGemmGrad32) in fp32
 //   kGemmDh     dz E       (contraction over the rows of the vocabulary)
@@ -13,31 +13,40 @@
 // tensor-core products, a_hi b_hi + a_lo b_hi + a_hi b_lo (two where one
 // operand is bf16, which a scaled fp16 plane holds exactly).  The tensor
 // core's fp32 accumulator does not round to nearest and its error grows with
-// the chain of MMAs, so a chain covers `chain` blocks of 64 of the
-// contraction; a finished chain is added to fp32 registers, round to nearest,
+// the chain of MMAs, so a chain has 48 of them; a finished chain is added to fp32 registers, round to nearest,
 // while the next one runs into the other half of tensor memory.
 //
 // One persistent CTA per SM: a copy warp (TMA tiles of 64 contraction
-// elements, 128-byte swizzle), an MMA warp (128 x 256 x 16 tcgen05.mma, both
-// operands in shared memory), eight warps that own the accumulators (a thread
-// has one row and 128 columns) and run the epilogue.  Operands whose
+// elements, 128-byte swizzle), an MMA warp (tcgen05.mma, both operands in
+// shared memory), eight warps that own the accumulators (a thread has one row
+// and half the tile's columns) and run the epilogue.  Operands whose
 // contraction runs down the rows of a row-major matrix are read as they lie
-// (MN-major tiles), so nothing is stored twice.  Every wait is bounded; one
-// that runs out raises RQ_DEVERR_TIMEOUT, lets copies and MMAs in flight
-// land, frees tensor memory and ends the CTA.
+// (MN-major tiles), so nothing is stored twice.
+//
+// Tiles.  A CTA pair shares a 256 x 256 tile (cta_group::2: each SM holds its
+// 128 rows of A and half of B): one SM alone on 128 x 256 would read
+// (128 + 256) x 32 bytes of shared memory per MMA of 128 cycles and take in 64
+// bytes a cycle of new tiles on top, more than the 128 bytes a cycle there
+// are; a pair needs two thirds of that.  A single SM takes 128 x 256 where the
+// rows fill no pair, and 128 x 64 where wider tiles would leave most SMs
+// without one.
+//
+// Every wait is bounded; one that runs out raises RQ_DEVERR_TIMEOUT, lets
+// copies and MMAs in flight land, frees tensor memory and ends the CTA.
 #include "loss_common.cuh"
 
 namespace rq {
 
 namespace {
 
-constexpr int kTM = 128, kTN = 256, kTK = 64;
+constexpr int kTM = 128, kTK = 64;               // rows of a CTA, contraction block
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = (kEpiWarps + 2) * 32;
-constexpr int kMaxStages = 6;
-constexpr int kABytes = kTM * kTK * 2, kBBytes = kTN * kTK * 2;
-constexpr size_t kGemmSmemMax = 225 * 1024;   // 227 KB less the static part
-constexpr size_t kGemmSmemTail = 1024 + 256;   // alignment slack, barriers
+constexpr int kMaxStages = 8;
+constexpr int kABytes = kTM * kTK * 2;
+constexpr int kChainMmas = 48;                   // MMAs of one accumulation chain
+constexpr size_t kGemmSmemMax = 225 * 1024;      // 227 KB less the static part
+constexpr size_t kGemmSmemTail = 1024 + 256;     // alignment slack, barriers
 
 // Shared-memory matrix descriptor: 128-byte swizzle (layout type 2), version
 // 1.  K-major tiles are rows of 64 elements (128 bytes), 8-row groups 1024
@@ -49,18 +58,69 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lead) {
          ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+template <int CG>
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                            uint32_t accum) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accum));
+  if (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum));
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum));
 }
 
+// MMAs issued so far done: arrive at `bar`, in both CTAs of a pair.
+template <int CG>
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   bar)
-               : "memory");
+  if (CG == 1)
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// 2-D tiled load into this CTA's shared memory; of a pair, completing on the
+// first CTA's barrier (the shared-window address with the rank bit cleared).
+template <int CG>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                          uint32_t bar, uint64_t pol) {
+  if (CG == 1)
+    tma_load_2d(dst, map, x, y, bar, pol);
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+        "bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar & 0xFEFFFFFFu), "l"(pol)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync_all() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// Arrive at the barrier of the pair's first CTA.
+__device__ __forceinline__ void arrive_first(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}\n" ::"r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ void tc_after() {
@@ -84,15 +144,6 @@ __device__ __forceinline__ void ld16(uint32_t t, float (&r)[16]) {
       : "r"(t));
 }
 
-__device__ __forceinline__ void st16(uint32_t t, const float *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16};" ::"r"(t),
-      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]),
-      "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]),
-      "f"(r[15]));
-}
-
 // 32 bytes, a whole sector, at once
 __device__ __forceinline__ void stg32(void *p, const uint32_t *v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
@@ -103,13 +154,9 @@ __device__ __forceinline__ void stg32(void *p, const uint32_t *v) {
 __device__ __forceinline__ void wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
 }  // namespace
 
-template <int MODE>
+template <int MODE, int CG, int TN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     loss_gemm_kernel(const __grid_constant__ CUtensorMap a_hi, const __grid_constant__ CUtensorMap a_lo,
                      const __grid_constant__ CUtensorMap b_hi, const __grid_constant__ CUtensorMap b_lo,
@@ -117,9 +164,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   constexpr bool LOGITS = MODE == kGemmStats || MODE == kGemmGrad || MODE == kGemmGrad32;
   constexpr bool A_MN = MODE == kGemmDw;                        // contraction down the rows of A
   constexpr bool B_MN = MODE == kGemmDh || MODE == kGemmDw;     // and of B
+  constexpr int BN = TN / CG;                    // columns of B in this CTA's shared memory
+  constexpr int HALF = TN / 2;                   // columns of an accumulator thread
+  constexpr int B_BYTES = BN * kTK * 2;
+  constexpr uint32_t TMEM_COLS = 2 * TN;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t stage_bytes = (uint32_t)(g.a_planes * kABytes + g.b_planes * kBBytes);
+  const uint32_t stage_bytes = (uint32_t)(g.a_planes * kABytes + g.b_planes * B_BYTES);
   const uint32_t bars = base + (uint32_t)g.stages * stage_bytes;
   auto full = [&](int i) { return bars + 8u * i; };
   auto empty = [&](int i) { return bars + 8u * (kMaxStages + i); };
@@ -129,6 +180,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   __shared__ volatile int abort_flag;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = CG == 2 ? (int)cta_rank() : 0;
   if (tid == 0) {
     prefetch_tmap(&a_hi);
     prefetch_tmap(&b_hi);
@@ -138,24 +190,35 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull(i), 1);
-      mbar_init(tempty(i), kEpiWarps);
+      mbar_init(tempty(i), kEpiWarps * CG);
     }
     fence_mbar_init();
     abort_flag = 0;
   }
+  if (CG == 2) cluster_sync_all();               // the pair's barriers exist
   if (warp == kEpiWarps + 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(&tmem_slot)),
-                 "r"(512));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if (CG == 1) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_addr(&tmem_slot)),
+                   "r"(TMEM_COLS));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_addr(&tmem_slot)),
+                   "r"(TMEM_COLS));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
   }
   griddep_launch_dependents();
   tc_before();
   __syncthreads();
+  if (CG == 2) cluster_sync_all();               // and its tensor memory
   tc_after();
   griddep_wait();
   const uint32_t tmem = tmem_slot;
 
+  // CTA (or pair) `unit` of `units` takes every units-th tile
+  const int unit = blockIdx.x / CG, units = gridDim.x / CG;
   const int mn = g.m_tiles * g.n_tiles, total = mn * g.splits;
   bool to = false;
   auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -171,62 +234,67 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_last();
       int it = 0;
-      for (int t = blockIdx.x; t < total && !abort_flag; t += gridDim.x) {
-        const int sp = t / mn, r = t % mn, n0 = r / g.m_tiles * kTN, m0 = r % g.m_tiles * kTM;
+      for (int t = unit; t < total && !abort_flag; t += units) {
+        const int sp = t / mn, r = t % mn;
+        const int n0 = r / g.m_tiles * TN + rank * BN;
+        const int m0 = (r % g.m_tiles * CG + rank) * kTM;
         const int k0 = (int)((int64_t)g.kblocks * sp / g.splits);
         const int k1 = (int)((int64_t)g.kblocks * (sp + 1) / g.splits);
         for (int k = k0; k < k1; ++k, ++it) {
           const int st = it % g.stages;
           if (!wait(empty(st), ((uint32_t)(it / g.stages) & 1u) ^ 1u)) break;
-          mbar_arrive_expect_tx(full(st), stage_bytes);
+          // a pair's first CTA expects both CTAs' bytes
+          if (rank == 0) mbar_arrive_expect_tx(full(st), stage_bytes * CG);
           uint32_t dst = base + (uint32_t)st * stage_bytes;
           for (int p = 0; p < g.a_planes; ++p, dst += kABytes) {
             const CUtensorMap *map = p ? &a_lo : &a_hi;
             if (A_MN) {
+#pragma unroll
               for (int i = 0; i < kTM / 64; ++i)
-                tma_load_2d(dst + i * 8192, map, m0 + i * 64, k * kTK, full(st), pol);
+                load_tile<CG>(dst + i * 8192, map, m0 + i * 64, k * kTK, full(st), pol);
             } else {
-              tma_load_2d(dst, map, k * kTK, m0, full(st), pol);
+              load_tile<CG>(dst, map, k * kTK, m0, full(st), pol);
             }
           }
-          for (int p = 0; p < g.b_planes; ++p, dst += kBBytes) {
+          for (int p = 0; p < g.b_planes; ++p, dst += B_BYTES) {
             const CUtensorMap *map = p ? &b_lo : &b_hi;
             if (B_MN) {
-              for (int i = 0; i < kTN / 64; ++i)
-                tma_load_2d(dst + i * 8192, map, n0 + i * 64, k * kTK, full(st), pol);
+#pragma unroll
+              for (int i = 0; i < BN / 64; ++i)
+                load_tile<CG>(dst + i * 8192, map, n0 + i * 64, k * kTK, full(st), pol);
             } else {
-              tma_load_2d(dst, map, k * kTK, n0, full(st), pol);
+              load_tile<CG>(dst, map, k * kTK, n0, full(st), pol);
             }
           }
         }
         if (to) break;
       }
       if (abort_flag) {
-        // the last copy into each stage lands before the shared memory goes
-        for (int st = 0; st < g.stages; ++st) {
-          const int last = it - 1 - ((it - 1 - st) % g.stages + g.stages) % g.stages;
-          if (it > 0 && last >= 0) mbar_wait_bounded(full(st), (uint32_t)(last / g.stages) & 1u);
+        // the copies in flight land before the shared memory goes: a
+        // millisecond, as a pair's second CTA has no barrier to wait on
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000) {
         }
         atomicOr(g.err, RQ_DEVERR_TIMEOUT);
       }
     }
   } else if (warp == kEpiWarps + 1) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       const uint32_t idesc = (1u << 4) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
-                             ((uint32_t)(kTN >> 3) << 17) | ((uint32_t)(kTM >> 4) << 24);
+                             ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(kTM * CG >> 4) << 24);
       // 16 contraction elements further: 32 bytes along a K-major row, 16
       // rows of 128 bytes in an MN-major tile (in descriptor units of 16 B)
       constexpr uint32_t a_step = A_MN ? 2048 / 16 : 32 / 16, b_step = B_MN ? 2048 / 16 : 32 / 16;
       int it = 0, c = 0;
-      for (int t = blockIdx.x; t < total && !abort_flag; t += gridDim.x) {
+      for (int t = unit; t < total && !abort_flag; t += units) {
         const int sp = t / mn;
         const int k0 = (int)((int64_t)g.kblocks * sp / g.splits);
         const int k1 = (int)((int64_t)g.kblocks * (sp + 1) / g.splits);
         for (int ka = k0; ka < k1; ka += g.chain, ++c) {
           if (!wait(tempty(c & 1), ((uint32_t)(c >> 1) & 1u) ^ 1u)) break;
           tc_after();
-          const uint32_t d = tmem + (uint32_t)(c & 1) * kTN;
+          const uint32_t d = tmem + (uint32_t)(c & 1) * TN;
           const int kb = ka + g.chain < k1 ? ka + g.chain : k1;
           for (int k = ka; k < kb; ++k, ++it) {
             const int st = it % g.stages;
@@ -236,24 +304,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const uint32_t sb = sa + (uint32_t)g.a_planes * kABytes;
             const uint64_t ah = sw128_desc(sa, A_MN ? 8192 : 16);
             const uint64_t bh = sw128_desc(sb, B_MN ? 8192 : 16);
-            const uint64_t al = ah + kABytes / 16, bl = bh + kBBytes / 16;
+            const uint64_t al = ah + kABytes / 16, bl = bh + B_BYTES / 16;
 #pragma unroll
             for (int j = 0; j < kTK / 16; ++j)
-              mma_f16_ss(d, ah + j * a_step, bh + j * b_step, idesc, k > ka || j > 0);
+              mma_f16_ss<CG>(d, ah + j * a_step, bh + j * b_step, idesc, k > ka || j > 0);
             if (g.a_planes > 1) {
 #pragma unroll
               for (int j = 0; j < kTK / 16; ++j)
-                mma_f16_ss(d, al + j * a_step, bh + j * b_step, idesc, 1u);
+                mma_f16_ss<CG>(d, al + j * a_step, bh + j * b_step, idesc, 1u);
             }
             if (g.b_planes > 1) {
 #pragma unroll
               for (int j = 0; j < kTK / 16; ++j)
-                mma_f16_ss(d, ah + j * a_step, bl + j * b_step, idesc, 1u);
+                mma_f16_ss<CG>(d, ah + j * a_step, bl + j * b_step, idesc, 1u);
             }
-            tc_commit(empty(st));
+            tc_commit<CG>(empty(st));
           }
           if (to) break;
-          tc_commit(tfull(c & 1));
+          tc_commit<CG>(tfull(c & 1));
         }
         if (to) break;
       }
@@ -267,7 +335,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   } else {
     // ------------------------------------------------------------ accumulators
     const int q = warp & 3, half = warp >> 2;
-    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)half * 128;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * HALF);
     auto wait_all = [&](uint32_t bar, uint32_t parity) {
       bool ok = to || mbar_try_wait(bar, parity) || mbar_wait_bounded(bar, parity);
       ok = __all_sync(0xffffffffu, ok);
@@ -282,126 +350,111 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const float sz = MODE != kGemmStats && MODE != kGemmGrad32 ? scale_z(g.amax, g.T) : 1.f;
     const float inv = MODE == kGemmDh ? 1.f / (sz * se) : MODE == kGemmDw ? 1.f / (sz * sh)
                                                                           : 1.f / (sh * se);
-    float acc[128];
+    const float cap = g.cap, icap = g.inv_cap, beta2 = g.beta * kLog2e;
+    float acc[HALF];
     int c = 0;
-    for (int t = blockIdx.x; t < total && !to; t += gridDim.x) {
+    for (int t = unit; t < total && !to; t += units) {
       const int sp = t / mn, r = t % mn, nt = r / g.m_tiles;
-      const int col0 = nt * kTN + half * 128, row = r % g.m_tiles * kTM + q * 32 + lane;
+      const int col0 = nt * TN + half * HALF;
+      const int row = (r % g.m_tiles * CG + rank) * kTM + q * 32 + lane;
       const int k0 = (int)((int64_t)g.kblocks * sp / g.splits);
       const int k1 = (int)((int64_t)g.kblocks * (sp + 1) / g.splits);
 #pragma unroll
-      for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+      for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
       for (int ka = k0; ka < k1; ka += g.chain, ++c) {
         if (!wait_all(tfull(c & 1), (uint32_t)(c >> 1) & 1u)) break;
         tc_after();
-        const uint32_t src = lanes + (uint32_t)(c & 1) * kTN;
+        const uint32_t src = lanes + (uint32_t)(c & 1) * TN;
 #pragma unroll
-        for (int j0 = 0; j0 < 128; j0 += 32) {
-          float x[16], y[16];
+        for (int j0 = 0; j0 < HALF; j0 += 16) {
+          float x[16];
           ld16(src + j0, x);
-          ld16(src + j0 + 16, y);
           wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            acc[j0 + j] = __fadd_rn(acc[j0 + j], x[j]);
-            acc[j0 + 16 + j] = __fadd_rn(acc[j0 + 16 + j], y[j]);
-          }
-        }
-        if (LOGITS && ka + g.chain >= k1) {
-          // the tile's sums back into the chain's columns, from where the
-          // epilogue takes them 16 at a time (the registers cannot be indexed
-          // by a loop, and 128 unrolled tanh and exp would not fit the
-          // instruction cache)
-#pragma unroll
-          for (int j0 = 0; j0 < 128; j0 += 16) st16(src + j0, acc + j0);
-          wait_st();
-          const float cap = g.cap, icap = g.inv_cap;
-          if (MODE == kGemmStats) {
-            float mx = -INFINITY, sum = 0.f;
-#pragma unroll 1
-            for (int j0 = 0; j0 < 128; j0 += 16) {
-              float x[16];
-              ld16(src + j0, x);
-              wait_ld();
-              float cm = -INFINITY;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float z = x[j] * inv;
-                const float y = cap > 0.f ? cap * tanhf(z * icap) : z;
-                x[j] = col0 + j0 + j < g.cols ? y * g.beta : -INFINITY;
-                cm = fmaxf(cm, x[j]);
-              }
-              const float nm = fmaxf(mx, cm);
-              if (nm > -INFINITY) {
-                sum *= expf(mx - nm);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) sum += expf(x[j] - nm);
-              } else {      // no column, or NaN in all of them
-#pragma unroll
-                for (int j = 0; j < 16; ++j) sum += x[j] != x[j] ? x[j] : 0.f;
-              }
-              mx = nm;
-            }
-            if (row < g.rows)
-              g.stat[(int64_t)(g.stat_part0 + nt * 2 + half) * g.stat_ld + row] =
-                  make_float2(mx, sum);
-          } else {
-            const bool in = row < g.rows;
-            const float f = in ? g.f[row] : 0.f, lse = in ? g.lse[row] : 0.f, fs = f * sz;
-            const int64_t at = (int64_t)row * g.dz_pitch + col0;
-#pragma unroll 1
-            for (int j0 = 0; j0 < 128; j0 += 16) {
-              float x[16];
-              ld16(src + j0, x);
-              wait_ld();
-              __half2 hi[8], lo[8];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float z = x[j] * inv;
-                float y = z, slope = 1.f;
-                if (cap > 0.f) {
-                  const float th = tanhf(z * icap);
-                  y = cap * th;
-                  slope = 1.f - th * th;
-                }
-                const float d = f != 0.f ? expf(y * g.beta - lse) * slope * fs : 0.f;
-                if (MODE == kGemmGrad32) {
-                  x[j] = d;
-                  continue;
-                }
-                __half dh, dl;
-                split_f16(d, dh, dl);
-                if (j & 1) {
-                  hi[j / 2].y = dh;
-                  lo[j / 2].y = dl;
-                } else {
-                  hi[j / 2].x = dh;
-                  lo[j / 2].x = dl;
-                }
-              }
-              if (in) {
-                if (MODE == kGemmGrad32) {
-                  if (col0 + j0 < g.cols) {        // the rows' pitch is 16 floats
-                    stg32(g.dz + at + j0, reinterpret_cast<const uint32_t *>(x));
-                    stg32(g.dz + at + j0 + 8, reinterpret_cast<const uint32_t *>(x + 8));
-                  }
-                } else if (col0 + j0 < g.dz_pitch) {   // the pitch is whole sectors
-                  stg32(g.dz_hi + at + j0, reinterpret_cast<const uint32_t *>(hi));
-                  stg32(g.dz_lo + at + j0, reinterpret_cast<const uint32_t *>(lo));
-                }
-              }
-            }
-          }
+          for (int j = 0; j < 16; ++j) acc[j0 + j] = __fadd_rn(acc[j0 + j], x[j]);
         }
         tc_before();
         __syncwarp();
-        if (lane == 0) arrive(tempty(c & 1));
+        if (lane == 0) {
+          if (CG == 2) arrive_first(tempty(c & 1));
+          else arrive(tempty(c & 1));
+        }
       }
       if (to) break;
-      if ((MODE == kGemmDh || MODE == kGemmDw) && row < g.rows) {
+      if (MODE == kGemmStats) {
+        // The epilogues take 16 columns at a time from the front of the sums,
+        // which then move up: registers cannot be indexed by a loop, and 128
+        // unrolled tanh and exp would not fit the instruction cache.
+        float mx = -INFINITY, sum = 0.f;
+#pragma unroll 1
+        for (int j0 = 0; j0 < HALF; j0 += 16) {
+          float cm = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float z = acc[j] * inv;
+            const float y = cap > 0.f ? cap * tanhf(z * icap) : z;
+            acc[j] = col0 + j0 + j < g.cols ? y * beta2 : -INFINITY;
+            cm = fmaxf(cm, acc[j]);
+          }
+          const float nm = fmaxf(mx, cm);
+          if (nm > -INFINITY) {
+            sum *= exp2f(mx - nm);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum += exp2f(acc[j] - nm);
+          } else {      // no column, or NaN in all of them
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum += acc[j] != acc[j] ? acc[j] : 0.f;
+          }
+          mx = nm;
+#pragma unroll
+          for (int j = 0; j + 16 < HALF; ++j) acc[j] = acc[j + 16];
+        }
+        if (row < g.rows)
+          g.stat[(int64_t)(g.stat_part0 + nt * 2 + half) * g.stat_ld + row] = make_float2(mx, sum);
+      } else if (LOGITS) {
+        const bool in = row < g.rows;
+        const float f = in ? g.f[row] : 0.f, lse2 = in ? g.lse[row] * kLog2e : 0.f, fs = f * sz;
+        const int64_t at = (int64_t)row * g.dz_pitch + col0;
+#pragma unroll 1
+        for (int j0 = 0; j0 < HALF; j0 += 16) {
+          float x[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float z = acc[j] * inv;
+            float y = z, slope = 1.f;
+            if (cap > 0.f) {
+              const float th = tanhf(z * icap);
+              y = cap * th;
+              slope = 1.f - th * th;
+            }
+            x[j] = f != 0.f ? exp2f(y * beta2 - lse2) * slope * fs : 0.f;
+          }
+          if (MODE == kGemmGrad32) {
+            if (in && col0 + j0 < g.cols) {          // the rows' pitch is 16 floats
+              stg32(g.dz + at + j0, reinterpret_cast<const uint32_t *>(x));
+              stg32(g.dz + at + j0 + 8, reinterpret_cast<const uint32_t *>(x + 8));
+            }
+          } else if (in && col0 + j0 < g.dz_pitch) {   // the pitch is whole sectors
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const __half2 h = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+              const float2 y = __half22float2(h);
+              const __half2 l =
+                  __floats2half2_rn(__fsub_rn(x[2 * j], y.x), __fsub_rn(x[2 * j + 1], y.y));
+              hi[j] = *reinterpret_cast<const uint32_t *>(&h);
+              lo[j] = *reinterpret_cast<const uint32_t *>(&l);
+            }
+            stg32(g.dz_hi + at + j0, hi);
+            stg32(g.dz_lo + at + j0, lo);
+          }
+#pragma unroll
+          for (int j = 0; j + 16 < HALF; ++j) acc[j] = acc[j + 16];
+        }
+      } else if (row < g.rows) {
         float *o = g.out + (int64_t)sp * g.out_split + (int64_t)row * g.out_pitch + col0;
 #pragma unroll
-        for (int j = 0; j < 128; j += 8) {
+        for (int j = 0; j < HALF; j += 8) {
           if (col0 + j < g.out_pitch) {
             float v[8];
 #pragma unroll
@@ -425,53 +478,109 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   tc_before();
   __syncthreads();
+  if (CG == 2) cluster_sync_all();      // nothing of the pair still on its way here
   if (warp == kEpiWarps + 1) {
     __syncwarp();
     tc_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    if (CG == 1)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(TMEM_COLS));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(TMEM_COLS));
   }
 }
 
 namespace {
+
+// Tile of a product with `m` rows, `n` columns and `splits` shares of the
+// contraction; see the comment at the top of the file.  Measured, the logits'
+// statistics of 256000 rows of 2304: pairs PAIR_US us for 2048 bf16 tokens,
+// single SMs SINGLE_US.
+struct Tile {
+  int cg, tn;
+};
+
+Tile tile_of(int64_t m, int64_t n, int splits) {
+  const int64_t mt = (m + kTM - 1) / kTM, nt = (n + 255) / 256;
+  if (mt * nt * splits < 74) return {1, 64};
+  // a pair's last tile may be half empty: worth it from 7 row tiles on
+  if (mt % 2 == 0 || mt >= 7) return {2, 256};
+  return {1, 256};
+}
 
 bool plane_map(CUtensorMap *m, const void *p, const GemmPlanes &x, bool mn, int tile) {
   return encode_tmap_2d_u16(m, p, (uint64_t)x.cols, (uint64_t)x.rows, (uint64_t)x.pitch * 2, 64,
                             mn ? 64 : (uint32_t)tile, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int MODE>
-cudaError_t launch_gemm(const GemmPlanes &A, const GemmPlanes &B, GemmArgs a, const DevInfo &di,
+template <int MODE, int CG, int TN>
+cudaError_t launch_tile(const GemmPlanes &A, const GemmPlanes &B, GemmArgs a, const DevInfo &di,
                         cudaStream_t s) {
   constexpr bool A_MN = MODE == kGemmDw, B_MN = MODE == kGemmDh || MODE == kGemmDw;
+  constexpr int BN = TN / CG;
   CUtensorMap ah, al, bh, bl;
-  if (!plane_map(&ah, A.hi, A, A_MN, kTM) || !plane_map(&al, A.lo ? A.lo : A.hi, A, A_MN, kTM) ||
-      !plane_map(&bh, B.hi, B, B_MN, kTN) || !plane_map(&bl, B.lo ? B.lo : B.hi, B, B_MN, kTN))
+  if (!plane_map(&ah, A.hi, A, A_MN, kTM) || !plane_map(&bh, B.hi, B, B_MN, BN))
+    return cudaErrorInvalidValue;
+  al = ah;
+  bl = bh;
+  if ((A.lo && !plane_map(&al, A.lo, A, A_MN, kTM)) || (B.lo && !plane_map(&bl, B.lo, B, B_MN, BN)))
     return cudaErrorInvalidValue;
   const int64_t k = A_MN ? A.rows : A.cols;
   a.a_planes = A.lo ? 2 : 1;
   a.b_planes = B.lo ? 2 : 1;
-  a.m_tiles = (int)(((A_MN ? A.cols : A.rows) + kTM - 1) / kTM);
-  a.n_tiles = (int)(((B_MN ? B.cols : B.rows) + kTN - 1) / kTN);
+  a.chain = kChainMmas / (kTK / 16 * (a.a_planes + a.b_planes - 1));
+  a.m_tiles = (int)(((A_MN ? A.cols : A.rows) + kTM * CG - 1) / (kTM * CG));
+  a.n_tiles = (int)(((B_MN ? B.cols : B.rows) + TN - 1) / TN);
   a.kblocks = (int)((k + kTK - 1) / kTK);
-  if (a.splits < 1) a.splits = 1;
   if (a.splits > a.kblocks) a.splits = a.kblocks;
-  const size_t stage = (size_t)a.a_planes * kABytes + (size_t)a.b_planes * kBBytes;
+  const size_t stage = (size_t)a.a_planes * kABytes + (size_t)a.b_planes * (BN * kTK * 2);
   int st = (int)((kGemmSmemMax - kGemmSmemTail) / stage);
   a.stages = st > kMaxStages ? kMaxStages : st;
   const size_t smem = kGemmSmemTail + a.stages * stage;
-  const void *fn = reinterpret_cast<const void *>(&loss_gemm_kernel<MODE>);
+  const void *fn = reinterpret_cast<const void *>(&loss_gemm_kernel<MODE, CG, TN>);
   cudaError_t e = ensure_smem_limit(fn, di.device, smem);
   if (e != cudaSuccess) return e;
   const int64_t total = (int64_t)a.m_tiles * a.n_tiles * a.splits;
   if (total < 1 || total > 0x7fffffff) return cudaErrorInvalidValue;
-  const int grid = (int)(total < di.sms ? total : di.sms);
+  const int units = di.sms / CG;
   void *args[] = {&ah, &al, &bh, &bl, &a};
-  return launch_maybe_pdl(fn, dim3(grid), dim3(kGemmThreads), smem, s, args, true);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((total < units ? total : units) * CG));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+template <int MODE>
+cudaError_t launch_gemm(const GemmPlanes &A, const GemmPlanes &B, GemmArgs a, const DevInfo &di,
+                        cudaStream_t s) {
+  constexpr bool A_MN = MODE == kGemmDw, B_MN = MODE == kGemmDh || MODE == kGemmDw;
+  if (a.splits < 1) a.splits = 1;
+  const Tile t = tile_of(A_MN ? A.cols : A.rows, B_MN ? B.cols : B.rows, a.splits);
+  if (t.cg == 2) return launch_tile<MODE, 2, 256>(A, B, a, di, s);
+  if (t.tn == 64) return launch_tile<MODE, 1, 64>(A, B, a, di, s);
+  return launch_tile<MODE, 1, 256>(A, B, a, di, s);
 }
 
 }  // namespace
 
-cudaError_t launch_loss_gemm(int mode, const GemmPlanes &A, const GemmPlanes &B, GemmArgs a,
+int loss_stats_parts(int64_t tokens, int64_t rows) {
+  const int tn = tile_of(tokens, rows, 1).tn;
+  return 2 * (int)((rows + tn - 1) / tn);
+}
+
+cudaError_t launch_loss_gemm(int mode, const GemmPlanes &A, const GemmPlanes &B, const GemmArgs &a,
                              const DevInfo &di, cudaStream_t s) {
   switch (mode) {
     case kGemmStats: return launch_gemm<kGemmStats>(A, B, a, di, s);

@@ -9,8 +9,8 @@
 //                  loss_n = T^2 sum_j q_j (log q_j - y[n, id_j] / T + lse_n)
 //   dy[n,v] = w_n T (exp(y[n,v] / T - lse_n) - q_n[v])
 //
-// The statistics are kept in fp32 as (maximum, sum of exp) parts that are
-// joined in a fixed order, so every result is the same from run to run.
+// The statistics are kept in fp32 as (maximum, sum of exp) parts, base 2, that
+// are joined in a fixed order, so every result is the same from run to run.
 #include "loss_common.cuh"
 
 namespace rq {
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(256) loss_pick_kernel(const PickArgs a) {
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
   const float m = fmaxf(a.x, b.x);
   if (!(m > -INFINITY)) return make_float2(m, a.y + b.y);
-  return make_float2(m, a.y * expf(a.x - m) + b.y * expf(b.x - m));
+  return make_float2(m, a.y * exp2f(a.x - m) + b.y * exp2f(b.x - m));
 }
 
 constexpr int kStatCols = 2048;   // logits one block folds into a part
@@ -366,12 +366,12 @@ __global__ void __launch_bounds__(256) loss_logit_stats_kernel(const float *__re
 #pragma unroll
   for (int i = 0; i < kStatCols / 256; ++i) {
     const int64_t c = c0 + i * 256 + threadIdx.x;
-    x[i] = c < V ? logits[n * V + c] * beta : -INFINITY;
+    x[i] = c < V ? logits[n * V + c] * (beta * kLog2e) : -INFINITY;
     m = fmaxf(m, x[i]);
   }
 #pragma unroll
   for (int i = 0; i < kStatCols / 256; ++i)
-    s += m > -INFINITY ? expf(x[i] - m) : (x[i] != x[i] ? x[i] : 0.f);
+    s += m > -INFINITY ? exp2f(x[i] - m) : (x[i] != x[i] ? x[i] : 0.f);
   float2 p = make_float2(m, s);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const float2 *__restr
   for (int o = 16; o > 0; o >>= 1)
     p = join(p, make_float2(__shfl_xor_sync(0xffffffffu, p.x, o),
                             __shfl_xor_sync(0xffffffffu, p.y, o)));
-  const float l = p.x + logf(p.y);
+  const float l = (p.x + log2f(p.y)) * kLn2;
   const int32_t *id = t.id + n * t.k;
   auto logit = [&](int j) { return y_is_logits ? y[n * V + id[j]] : y[n * t.k + j]; };
   float out = 0.f;
