@@ -14,7 +14,7 @@ using namespace rq;
 
 namespace {
 
-constexpr int64_t kPieceRows = 4 * kGradRows;   // rows of the vocabulary per piece
+constexpr int64_t kPieceRows = 8 * kGradRows;   // most rows of the vocabulary per piece
 constexpr int kTokenChunk = 4096;         // tokens per sweep over the vocabulary
 constexpr int kServeTokens = 64;          // most tokens of a call on the serving kernels' logits
 constexpr int kSumTokens = 32;            // and of one on sums by code

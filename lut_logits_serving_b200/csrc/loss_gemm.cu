@@ -13,7 +13,7 @@
 // tensor-core products, a_hi b_hi + a_lo b_hi + a_hi b_lo (two where one
 // operand is bf16, which a scaled fp16 plane holds exactly).  The tensor
 // core's fp32 accumulator does not round to nearest and its error grows with
-// the chain of MMAs, so a chain has 48 of them; a finished chain is added to fp32 registers, round to nearest,
+// the chain of MMAs, so a chain has 24 to 36 of them; a finished chain is added to fp32 registers, round to nearest,
 // while the next one runs into the other half of tensor memory.
 //
 // One persistent CTA per SM: a copy warp (TMA tiles of 64 contraction
@@ -44,7 +44,11 @@ constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = (kEpiWarps + 2) * 32;
 constexpr int kMaxStages = 8;
 constexpr int kABytes = kTM * kTK * 2;
-constexpr int kChainMmas = 48;                   // MMAs of one accumulation chain
+// MMAs of one accumulation chain.  Errors of dC and dh against 64 bits (500
+// fp32 tokens, 256000 rows): chains of 48 1.4e-6 and 1.4e-6, of 24 7.8e-7 and
+// 8.0e-7, for 5 to 8 % of a step's time; an fp32 library product leaves 8.4e-7
+// and 1.6e-6.  So the sums that only pass through one product get longer ones.
+constexpr int kChainMmas = 36, kChainMmasDw = 24;
 constexpr size_t kGemmSmemMax = 225 * 1024;      // 227 KB less the static part
 constexpr size_t kGemmSmemTail = 1024 + 256;     // alignment slack, barriers
 
@@ -366,12 +370,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tc_after();
         const uint32_t src = lanes + (uint32_t)(c & 1) * TN;
 #pragma unroll
-        for (int j0 = 0; j0 < HALF; j0 += 16) {
-          float x[16];
+        for (int j0 = 0; j0 < HALF; j0 += 32) {
+          float x[16], y[16];
           ld16(src + j0, x);
+          ld16(src + j0 + 16, y);
           wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[j0 + j] = __fadd_rn(acc[j0 + j], x[j]);
+          for (int j = 0; j < 16; ++j) {
+            acc[j0 + j] = __fadd_rn(acc[j0 + j], x[j]);
+            acc[j0 + 16 + j] = __fadd_rn(acc[j0 + 16 + j], y[j]);
+          }
         }
         tc_before();
         __syncwarp();
@@ -494,9 +502,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 namespace {
 
 // Tile of a product with `m` rows, `n` columns and `splits` shares of the
-// contraction; see the comment at the top of the file.  Measured, the logits'
-// statistics of 256000 rows of 2304: pairs PAIR_US us for 2048 bf16 tokens,
-// single SMs SINGLE_US.
+// contraction; see the comment at the top of the file.  Measured, 256000 rows
+// of 2304: a training step of 2048 bf16 tokens 21.9 ms on single SMs, 18.1 ms
+// on pairs; 4096 rows of 192, 33 tokens: the gradients of the logits 23 us with
+// 256 columns a tile, 11 us with 64.
 struct Tile {
   int cg, tn;
 };
@@ -529,7 +538,8 @@ cudaError_t launch_tile(const GemmPlanes &A, const GemmPlanes &B, GemmArgs a, co
   const int64_t k = A_MN ? A.rows : A.cols;
   a.a_planes = A.lo ? 2 : 1;
   a.b_planes = B.lo ? 2 : 1;
-  a.chain = kChainMmas / (kTK / 16 * (a.a_planes + a.b_planes - 1));
+  a.chain = (MODE == kGemmDw ? kChainMmasDw : kChainMmas) /
+            (kTK / 16 * (a.a_planes + a.b_planes - 1));
   a.m_tiles = (int)(((A_MN ? A.cols : A.rows) + kTM * CG - 1) / (kTM * CG));
   a.n_tiles = (int)(((B_MN ? B.cols : B.rows) + TN - 1) / TN);
   a.kblocks = (int)((k + kTK - 1) / kTK);

@@ -323,19 +323,19 @@ __global__ void __launch_bounds__(256) loss_pick_kernel(const PickArgs a) {
     const int64_t n = i / a.k;
     for (int m = lane; m < a.M; m += 32) {
       const int64_t hm = n * a.D + (int64_t)m * ds;
-      if (ds == 6 && L == 2) {
-        const float *w0 = a.C + ((size_t)(2 * m) * K + a.cs(v, 2 * m)) * 6;
-        const float *w1 = a.C + ((size_t)(2 * m + 1) * K + a.cs(v, 2 * m + 1)) * 6;
+      const float *book = a.C + (size_t)m * L * K * ds;
+      uint32_t c[4];
 #pragma unroll
-        for (int j = 0; j < 6; ++j)
-          z = fmaf(load_h(a.h, a.bf16, hm + j), __fadd_rn(__ldg(w0 + j), __ldg(w1 + j)), z);
-      } else {
-        for (int j = 0; j < ds; ++j) {
-          float e = 0.f;
-          for (int l = 0; l < L; ++l)
-            e = __fadd_rn(e, __ldg(a.C + ((size_t)(m * L + l) * K + a.cs(v, m * L + l)) * ds + j));
-          z = fmaf(load_h(a.h, a.bf16, hm + j), e, z);
-        }
+      for (int l = 0; l < 4; ++l) c[l] = l < L ? a.cs(v, m * L + l) : 0u;
+#pragma unroll 6
+      for (int j = 0; j < ds; ++j) {
+        float e = 0.f;
+#pragma unroll
+        for (int l = 0; l < 4; ++l)
+          if (l < L) e = __fadd_rn(e, __ldg(book + ((size_t)l * K + c[l]) * ds + j));
+        for (int l = 4; l < L; ++l)
+          e = __fadd_rn(e, __ldg(book + ((size_t)l * K + a.cs(v, m * L + l)) * ds + j));
+        z = fmaf(load_h(a.h, a.bf16, hm + j), e, z);
       }
     }
 #pragma unroll
