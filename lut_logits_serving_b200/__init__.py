@@ -509,7 +509,7 @@ class _LossCall:
             raise ValueError("h: expected a torch.Tensor")
         if h.dtype not in (torch.float32, torch.bfloat16):
             raise ValueError(f"h: dtype {h.dtype}, expected float32 or bfloat16")
-        self.h, self.device, self.N = h, h.device, _tokens(h, d)
+        self.tensor, self.h, self.device, self.N = torch.Tensor, h, h.device, _tokens(h, d)
         self.bf16 = int(h.dtype == torch.bfloat16)
         self.code_dtype = torch.uint16 if fmt in (U16, SCHED) else torch.uint8
         (self.codes_bytes, self.book_bytes, self.index_bytes,
@@ -532,8 +532,12 @@ class _LossCall:
         return self.stack.__exit__(*exc) if self.stack is not None else None
 
     def ptr(self, t, dtype, name, nbytes):
-        """Address of `t` after the checks of _cuda and of its device."""
-        if not isinstance(t, _torch().Tensor):
+        """Address of `t` after the checks of _cuda and of its device (at once,
+        then one by one to name what is wrong)."""
+        if isinstance(t, self.tensor) and t.dtype is dtype and t.device == self.device and \
+                t.nbytes >= nbytes and t.is_contiguous() and _on_device(t):
+            return t.data_ptr()
+        if not isinstance(t, self.tensor):
             raise ValueError(f"{name}: expected a torch.Tensor")
         if t.dtype is not dtype:
             raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -543,9 +547,7 @@ class _LossCall:
             raise ValueError(f"{name}: {t.nbytes} bytes, the call needs {nbytes}")
         if not _on_device(t):
             raise ValueError(f"{name}: must be a CUDA tensor (no CPU fallback)")
-        if t.device != self.device:
-            raise ValueError(f"{name}: on {t.device}, h on {self.device}")
-        return t.data_ptr()
+        raise ValueError(f"{name}: on {t.device}, h on {self.device}")
 
     def out(self, t, shape, dtype):
         return self.h.new_empty(shape, dtype=dtype) if t is None else t

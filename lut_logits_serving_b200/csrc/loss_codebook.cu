@@ -70,9 +70,15 @@ __host__ __device__ inline IndexShape index_shape(int64_t V, int P, int K) {
 
 // One block takes `cols` adjacent columns of a block of rows, staged column by
 // column in shared memory; a warp per column.  Rows go in ascending order, 32
-// at a time; the lanes with one code take consecutive places (match_any), so
-// no order of arrival enters.
+// at a time; lanes with one code take consecutive places, so no order of
+// arrival enters.
 constexpr int kStagePitch = kGradRows + 8;   // columns 4 banks apart
+
+// A warp's counters: rows per code, slots, buckets, starts of the slices, and
+// the lane that last wrote a code's mark.
+__host__ __device__ __forceinline__ int prep_words(const IndexShape &x) {
+  return 2 * x.K + kCap + 2 + x.slices + 1 + (x.K + 1) / 2;
+}
 
 __global__ void __launch_bounds__(256) prepare_grad_kernel(const CodeSrc cs, const IndexShape x,
                                                            int cols, unsigned char *index) {
@@ -83,16 +89,30 @@ __global__ void __launch_bounds__(256) prepare_grad_kernel(const CodeSrc cs, con
   const int nc = x.P - p0 < cols ? x.P - p0 : cols;
   const int64_t v0 = (int64_t)block * kGradRows;
   const int rows = (int)(x.V - v0 < kGradRows ? x.V - v0 : kGradRows);
-  for (int i = threadIdx.x; i < rows * cols; i += blockDim.x) {
-    const int r = i / cols, c = i - r * cols;
-    if (c < nc) sm[c * kStagePitch + r] = (uint16_t)cs(v0 + r, p0 + c);
+  // eight codes of a thread on their way at a time
+  const int csh = __ffs(cols) - 1, c = threadIdx.x & (cols - 1);
+  if (c < nc) {
+    for (int r0 = threadIdx.x >> csh; r0 < rows; r0 += 8 * (blockDim.x >> csh)) {
+      uint32_t x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + i * (blockDim.x >> csh);
+        if (r < rows) x[i] = cs.raw(v0 + r, p0 + c);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + i * (blockDim.x >> csh);
+        if (r < rows) sm[c * kStagePitch + r] = (uint16_t)cs.fix(x[i]);
+      }
+    }
   }
   __syncthreads();
   if (warp >= nc) return;
-  const int p = p0 + warp, g = x.lanes;
+  const int p = p0 + warp, g = x.lanes, gsh = __ffs(g) - 1;
   const uint16_t *col = sm + warp * kStagePitch;
-  uint16_t *cnt = sm + cols * kStagePitch + (size_t)warp * (2 * x.K + kCap + 32);
-  uint16_t *slot = cnt + x.K, *bucket = slot + x.K;
+  uint16_t *cnt = sm + cols * kStagePitch + (size_t)warp * prep_words(x);
+  uint16_t *slot = cnt + x.K, *bucket = slot + x.K, *start = bucket + kCap + 2;
+  unsigned char *mark = reinterpret_cast<unsigned char *>(start + x.slices + 1);
   const unsigned below = (1u << lane) - 1u;
   unsigned char *unit = index + ((size_t)block * x.P + p) * x.unit;
   uint16_t *off = reinterpret_cast<uint16_t *>(unit);
@@ -105,9 +125,20 @@ __global__ void __launch_bounds__(256) prepare_grad_kernel(const CodeSrc cs, con
   auto sweep = [&](auto &&each) {
     for (int r0 = 0; r0 < rows; r0 += 32) {
       const int r = r0 + lane;
-      const uint32_t c = r < rows ? col[r] : 0xFFFFFFFFu;
-      const unsigned same = __match_any_sync(0xffffffffu, c);
-      if (r < rows) each((int)c, r, same);
+      const int c = r < rows ? col[r] : -1;
+      // lanes with this lane's code: mostly itself alone.  Each marks its code;
+      // who finds another's mark shares it, and only those are looked up
+      // (match_any takes several times as long on 32 different codes)
+      if (c >= 0) mark[c] = (unsigned char)lane;
+      __syncwarp();
+      unsigned lost = __ballot_sync(0xffffffffu, c >= 0 && mark[c] != lane), same = 1u << lane;
+      while (lost) {
+        const unsigned m =
+            __ballot_sync(0xffffffffu, c == __shfl_sync(0xffffffffu, c, __ffs(lost) - 1));
+        if (m >> lane & 1u) same = m;
+        lost &= ~m;
+      }
+      if (c >= 0) each(c, r, same);
       __syncwarp();
     }
   };
@@ -116,7 +147,7 @@ __global__ void __launch_bounds__(256) prepare_grad_kernel(const CodeSrc cs, con
   });
   // codes by falling number of rounds: bucket starts, then places in code order
   auto key = [&](int c) {
-    const int n = (cnt[c] + g - 1) / g;
+    const int n = (cnt[c] + g - 1) >> gsh;
     return kCap - (n < kCap ? n : kCap);
   };
   for (int c0 = 0; c0 < x.K; c0 += 32) {
@@ -161,8 +192,8 @@ __global__ void __launch_bounds__(256) prepare_grad_kernel(const CodeSrc cs, con
   }
   __threadfence_block();
   __syncwarp();
-  const int total = scan(x.slices, [&](int s) { return (kCap - key(code[s * 32 / g]) + 1) / 2; },
-                         [&](int s, int at) { off[s] = (uint16_t)at; });
+  const int total = scan(x.slices, [&](int s) { return (kCap - key(code[s * 32 >> gsh]) + 1) >> 1; },
+                         [&](int s, int at) { off[s] = start[s] = (uint16_t)at; });
   if (lane == 0) off[x.slices] = (uint16_t)total;
   const int more = scan(full,
                         [&](int s) {
@@ -183,8 +214,8 @@ __global__ void __launch_bounds__(256) prepare_grad_kernel(const CodeSrc cs, con
     __syncwarp(same);
     int at;
     if (e < g * kCap) {
-      const int vl = s * g + e % g, i = e / g;
-      at = ((off[vl >> 5] + i / 2) * 32 + (vl & 31)) * 2 + (i & 1);
+      const int vl = (s << gsh) + (e & (g - 1)), i = e >> gsh;
+      at = ((start[vl >> 5] + (i >> 1)) * 32 + (vl & 31)) * 2 + (i & 1);
     } else {
       at = total * 64 + over[1 + s] + e - g * kCap;
     }
@@ -567,7 +598,7 @@ cudaError_t launch_prepare_grad(const CodeSrc &cs, void *index, const DevInfo &d
   // as many columns a block as their counters leave room for
   int cols = 8;
   auto bytes = [&](int n) {
-    return (size_t)n * (kStagePitch + 2 * cs.K + kCap + 32) * 2;
+    return (size_t)n * (kStagePitch + prep_words(x)) * 2;
   };
   while (cols > 1 && bytes(cols) > 220 * 1024) cols /= 2;
   const void *fn = reinterpret_cast<const void *>(&prepare_grad_kernel);

@@ -27,18 +27,17 @@ struct CodeSrc {
   int64_t V;
   int P, K;
   CodeFix fix;
-  __device__ __forceinline__ uint32_t operator()(int64_t v, int p) const {
-    uint32_t c;
-    if (fmt == RQ_CODES_U16) c = __ldg(static_cast<const uint16_t *>(codes) + v * P + p);
-    else if (fmt == RQ_CODES_U8) c = __ldg(static_cast<const uint8_t *>(codes) + v * P + p);
-    else if (fmt == RQ_CODES_SCHED)
-      c = sched_code(static_cast<const uint16_t *>(codes), V, v, p, sched_shift(K));
-    else if (fmt == RQ_CODES_PACKED10_ROT)
-      c = rot10_code(static_cast<const uint8_t *>(codes), V, P, v, p);
-    else
-      c = packed10_code(static_cast<const uint8_t *>(codes) + v * ((10LL * P + 7) / 8), p);
-    return fix(c);
+  // as stored (not yet safe as an index)
+  __device__ __forceinline__ uint32_t raw(int64_t v, int p) const {
+    if (fmt == RQ_CODES_U16) return __ldg(static_cast<const uint16_t *>(codes) + v * P + p);
+    if (fmt == RQ_CODES_U8) return __ldg(static_cast<const uint8_t *>(codes) + v * P + p);
+    if (fmt == RQ_CODES_SCHED)
+      return sched_code(static_cast<const uint16_t *>(codes), V, v, p, sched_shift(K));
+    if (fmt == RQ_CODES_PACKED10_ROT)
+      return rot10_code(static_cast<const uint8_t *>(codes), V, P, v, p);
+    return packed10_code(static_cast<const uint8_t *>(codes) + v * ((10LL * P + 7) / 8), p);
   }
+  __device__ __forceinline__ uint32_t operator()(int64_t v, int p) const { return fix(raw(v, p)); }
 };
 
 // ------------------------------------------------------------- fp16 splits
