@@ -74,15 +74,24 @@ int total_parts(const rq_dims &d, int64_t tokens) {
   return n;
 }
 
-// Splits of dz E over the vocabulary: enough that its 128 x 256 tiles fill the
-// SMs.
+// Shares of the vocabulary in dz E: its tiles are few (tokens by dims), so the
+// contraction is split until whole waves of them fill the SMs.  A share costs
+// its block products (0.85 us for 64 rows) and a pass over its sums.
 int dh_splits(const rq_dims &d, int64_t n) {
-  const int64_t tiles = (n + 127) / 128 * ((d.D + 255) / 256);
-  int64_t s = kSms / tiles;
-  const int64_t kb = (piece_rows(d) + 63) / 64;
-  if (s > kb) s = kb;
-  if (s > kMaxSplits) s = kMaxSplits;
-  return s < 1 ? 1 : (int)s;
+  const int64_t mt = (n + 127) / 128, nt = (d.D + 255) / 256, kb = (piece_rows(d) + 63) / 64;
+  const bool pairs = mt % 2 == 0 || mt >= 7;
+  const int64_t tiles = pairs ? (mt + 1) / 2 * nt : mt * nt, units = pairs ? kSms / 2 : kSms;
+  int best = 1;
+  double least = 1e30;
+  for (int s = 1; s <= kMaxSplits && s <= kb; ++s) {
+    const double us = (double)((tiles * s + units - 1) / units) * (double)((kb + s - 1) / s) * 0.85 +
+                      (double)s * (double)n * d.D * 8 / 5e6;
+    if (us < least) {
+      least = us;
+      best = s;
+    }
+  }
+  return best;
 }
 
 // Where the logits come from and how the gradients are formed.
@@ -306,11 +315,27 @@ cudaError_t begin(const Problem &all, const Layout &x, bool amax, const Problem 
                            at<float>(ws, x.sq), at<float>(ws, x.f), di.err, s);
 }
 
-// h's planes, and the logits at the listed ids.
-cudaError_t pick(const Problem &q, const Layout &x, const int32_t *id, void *ws, cudaStream_t s) {
-  return launch_loss_pick(q.h, q.bf16, q.N, x.hp, at<float>(ws, x.amax), at<__half>(ws, x.hh),
-                          q.bf16 ? nullptr : at<__half>(ws, x.hl), q.src(), q.C, q.d.D, q.d.M,
-                          q.d.L, id, q.t.k, q.cap, at<float>(ws, x.y), s);
+cudaError_t split(const Problem &q, const Layout &x, void *ws, cudaStream_t s) {
+  return launch_loss_split(q.h, q.bf16, q.N, q.d.D, x.hp, at<float>(ws, x.amax),
+                           at<__half>(ws, x.hh), q.bf16 ? nullptr : at<__half>(ws, x.hl), s);
+}
+
+// The listed ids of a decoded piece; for a loss as it is, for gradients the
+// caller adds where they go.
+EntryCall entries(const Problem &q, const Layout &x, int64_t v0, int64_t rows, void *ws) {
+  EntryCall c = {};
+  c.h = q.h;
+  c.bf16 = q.bf16;
+  c.D = q.d.D;
+  c.L = q.d.L;
+  c.amax = at<float>(ws, x.amax);
+  c.wh = at<__half>(ws, x.wh);
+  c.wl = at<__half>(ws, x.wl);
+  c.pitch = x.hp;
+  c.v0 = v0;
+  c.rows = rows;
+  c.cap = q.cap;
+  return c;
 }
 
 // Piece [v0, v0 + rows) decoded.
@@ -345,10 +370,11 @@ cudaError_t tensor_loss(const Problem &all, const Layout &x, float *loss, float 
   for (int64_t n0 = 0; n0 < all.N; n0 += x.chunk) {
     const Problem q = slice(all, n0, all.N - n0 < x.chunk ? all.N - n0 : x.chunk);
     const rq_dims &d = q.d;
-    RQ_TRY(pick(q, x, q.t.id, ws, s));
+    RQ_TRY(split(q, x, ws, s));
     int part0 = 0;
     RQ_TRY(for_pieces(d, [&](int64_t v0, int64_t rows) {
       RQ_TRY(decode(q, x, v0, rows, ws, di, s));
+      RQ_TRY(launch_loss_entries(entries(q, x, v0, rows, ws), q.t, q.t.id, q.N, y, s));
       GemmArgs g = gemm_args(q, amax, di);
       g.rows = q.N;
       g.cols = (int)rows;
@@ -367,7 +393,7 @@ cudaError_t tensor_loss(const Problem &all, const Layout &x, float *loss, float 
 cudaError_t products_grad(const Problem &all, const Layout &x, const float *lse, const float *w,
                           const void *index, void *dh, float *dC, void *ws, const DevInfo &di,
                           cudaStream_t s) {
-  float *amax = at<float>(ws, x.amax), *f = at<float>(ws, x.f), *y = at<float>(ws, x.y);
+  float *amax = at<float>(ws, x.amax), *f = at<float>(ws, x.f);
   __half *zh = at<__half>(ws, x.zh), *zl = at<__half>(ws, x.zl);
   int32_t *sid = at<int32_t>(ws, x.sid);
   float *sq = at<float>(ws, x.sq);
@@ -378,7 +404,7 @@ cudaError_t products_grad(const Problem &all, const Layout &x, const float *lse,
     const float *ql = lse + n0;
     const int splits = dh_splits(d, q.N);
     RQ_TRY(begin(all, x, n0 == 0, &q, w, w ? w + n0 : nullptr, ws, di, s));
-    RQ_TRY(pick(q, x, sid, ws, s));
+    RQ_TRY(split(q, x, ws, s));
     RQ_TRY(for_pieces(d, [&](int64_t v0, int64_t rows) {
       RQ_TRY(decode(q, x, v0, rows, ws, di, s));
       GemmArgs g = gemm_args(q, amax, di);
@@ -390,8 +416,14 @@ cudaError_t products_grad(const Problem &all, const Layout &x, const float *lse,
       g.dz_lo = zl;
       g.dz_pitch = x.zp;
       RQ_TRY(launch_loss_gemm(kGemmGrad, h_planes(q, x, ws), w_planes(q, x, rows, ws), g, di, s));
-      RQ_TRY(launch_loss_fix_planes(sid, sq, y, q.t.k, q.N, v0, rows, ql, f, amax, q.t.T, q.t.beta,
-                                    q.cap, zh, zl, x.zp, s));
+      EntryCall c = entries(q, x, v0, rows, ws);
+      c.sq = sq;
+      c.lse = ql;
+      c.f = f;
+      c.zh = zh;
+      c.zl = zl;
+      c.zpitch = x.zp;
+      RQ_TRY(launch_loss_entries(c, q.t, sid, q.N, nullptr, s));
       if (dh) {
         // a bf16 dh keeps 8 bits: the high planes' 11 on either side are
         // within a sixth of its rounding
@@ -440,13 +472,13 @@ cudaError_t sums_grad(const Problem &q, const Layout &x, const float *lse, const
   float *sq = at<float>(ws, x.sq), *f = at<float>(ws, x.f), *dz = at<float>(ws, x.dz);
   float *S = at<float>(ws, x.S), *dhp = dh ? at<float>(ws, x.dhp) : nullptr;
   RQ_TRY(begin(q, x, !x.how.serve, &q, nullptr, w, ws, di, s));
-  const float *y = at<float>(ws, x.logits);
   if (x.how.serve) {
+    const float *y = at<float>(ws, x.logits);
     RQ_TRY(launch_loss_dz(y, q.N, d.V, lse, f, q.t.beta, q.cap, dz, x.vp, s));
+    RQ_TRY(launch_loss_fix(sid, sq, y, q.t.k, q.N, d.V, lse, f, q.t.beta, q.cap, dz, x.vp, s));
   } else {
     const float *amax = at<float>(ws, x.amax);
-    y = at<float>(ws, x.y);
-    RQ_TRY(pick(q, x, sid, ws, s));
+    RQ_TRY(split(q, x, ws, s));
     RQ_TRY(for_pieces(d, [&](int64_t v0, int64_t rows) {
       RQ_TRY(decode(q, x, v0, rows, ws, di, s));
       GemmArgs g = gemm_args(q, amax, di);
@@ -456,11 +488,16 @@ cudaError_t sums_grad(const Problem &q, const Layout &x, const float *lse, const
       g.f = f;
       g.dz = dz + v0;
       g.dz_pitch = x.vp;
-      return launch_loss_gemm(kGemmGrad32, h_planes(q, x, ws), w_planes(q, x, rows, ws), g, di, s);
+      RQ_TRY(launch_loss_gemm(kGemmGrad32, h_planes(q, x, ws), w_planes(q, x, rows, ws), g, di, s));
+      EntryCall c = entries(q, x, v0, rows, ws);
+      c.sq = sq;
+      c.lse = lse;
+      c.f = f;
+      c.dz = dz;
+      c.zpitch = x.vp;
+      return launch_loss_entries(c, q.t, sid, q.N, nullptr, s);
     }));
   }
-  RQ_TRY(launch_loss_fix(sid, sq, y, x.how.serve, q.t.k, q.N, d.V, lse, f, q.t.beta, q.cap, dz, x.vp,
-                         s));
   RQ_TRY(launch_codebook_sums(dz, x.vp, q.N, index, d.V, d.M, d.L, d.K, S, di, s));
   RQ_TRY(launch_codebook_finish(S, x.splits, q.h, q.bf16, q.N, q.C, d.D, d.M, d.L, d.K, dC, dhp, s));
   if (dh) RQ_TRY(launch_codebook_dh(dhp, q.N, d.D, d.M, d.L, q.bf16, dh, s));

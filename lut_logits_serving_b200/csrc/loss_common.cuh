@@ -166,30 +166,37 @@ cudaError_t launch_loss_begin(const void *h, int bf16, int64_t nh, const float *
                               const float *w, int64_t nw, float *amax, const LossTargets &t,
                               int64_t rows, int64_t V, const float *weight, int32_t *sid, float *sq,
                               float *f, unsigned *err, cudaStream_t s);
-// fp16 planes of h, and y[n][j] = softcapped logit of id[n][j] (0 where the id
-// is < 0 or >= V)
-cudaError_t launch_loss_pick(const void *h, int bf16, int64_t N, int64_t pitch, const float *amax,
-                             __half *hi, __half *lo, const CodeSrc &cs, const float *C, int D, int M,
-                             int L, const int32_t *id, int k, float cap, float *y, cudaStream_t s);
-// lse and loss from the parts and the picked logits: y[n * k + j], or, with
+cudaError_t launch_loss_split(const void *h, int bf16, int64_t N, int D, int64_t pitch,
+                              const float *amax, __half *hi, __half *lo, cudaStream_t s);
+// lse and loss from the parts and the listed ids' logits: y[n * k + j], or, with
 // y_is_logits, y[n * V + id].
 cudaError_t launch_loss_finish(const float2 *stat, int parts, int stat_ld, int64_t N, int64_t V,
                                const LossTargets &t, const float *y, bool y_is_logits, float *loss,
                                float *lse, unsigned *err, cudaStream_t s);
-// dz planes at the listed ids of rows [v0, v0 + rows)
-cudaError_t launch_loss_fix_planes(const int32_t *sid, const float *sq, const float *y, int k,
-                                   int64_t N, int64_t v0, int64_t rows, const float *lse,
-                                   const float *f, const float *amax, float T, float beta,
-                                   float cap, __half *hi, __half *lo, int64_t pitch,
-                                   cudaStream_t s);
+// The listed ids in a decoded piece: their logits y[n][j] (sq null), or their
+// gradients, in the piece's planes zh, zl or (dz set) in fp32 [N][zpitch].
+struct EntryCall {
+  const void *h;
+  int bf16, D, L;
+  const float *amax;
+  const __half *wh, *wl;     // the piece, rows v0 .. v0 + rows
+  int64_t pitch, v0, rows;
+  float cap;
+  const float *sq, *lse, *f;
+  __half *zh, *zl;
+  float *dz;
+  int64_t zpitch;
+};
+cudaError_t launch_loss_entries(const EntryCall &c, const LossTargets &t, const int32_t *id,
+                                int64_t N, float *y, cudaStream_t s);
 // logits [N][V] -> their gradients [N][pitch], dense part
 cudaError_t launch_loss_dz(const float *logits, int64_t N, int64_t V, const float *lse,
                            const float *f, float beta, float cap, float *dz, int64_t pitch,
                            cudaStream_t s);
-// dz [N][pitch] at the listed ids; y as for launch_loss_finish
-cudaError_t launch_loss_fix(const int32_t *sid, const float *sq, const float *y, bool y_is_logits,
-                            int k, int64_t N, int64_t V, const float *lse, const float *f,
-                            float beta, float cap, float *dz, int64_t pitch, cudaStream_t s);
+// dz [N][pitch] at the listed ids, from the logits
+cudaError_t launch_loss_fix(const int32_t *sid, const float *sq, const float *logits, int k,
+                            int64_t N, int64_t V, const float *lse, const float *f, float beta,
+                            float cap, float *dz, int64_t pitch, cudaStream_t s);
 cudaError_t launch_loss_dh_sum(const float *part, int splits, int64_t stride, int64_t pitch,
                                int64_t N, int D, int bf16, void *dh, cudaStream_t s);
 

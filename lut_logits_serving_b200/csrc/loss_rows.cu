@@ -1,7 +1,7 @@
 // loss_rows.cu -- the row-wise kernels of the losses on the RQ-coded head:
 // operand scales and fp16 splits, decoding a piece of the vocabulary for the
-// tensor cores, the logits at the listed ids, log-sum-exp and losses, and the
-// sparse part of the logits' gradient.
+// tensor cores, log-sum-exp and losses, and the listed ids' part of the logits
+// and their gradient.
 //
 //   lse_n = log sum_v exp(y[n,v] / T)
 //   cross entropy  loss_n = lse_n - y[n, t_n]
@@ -282,66 +282,23 @@ __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeAr
   }
 }
 
-// ------------------------------------------------------------- picked logits
+// ------------------------------------------------------------- hidden planes
 
-// Blocks [0, N): the fp16 planes of a hidden state.  After those, one warp per
-// (token, list entry): <h_n, E_id> in fp32.
-struct PickArgs {
-  const void *h;
-  int bf16;
-  int64_t N, pitch;
-  const float *amax;
-  __half *hi, *lo;
-  CodeSrc cs;
-  const float *C;
-  int D, M, L, k;
-  const int32_t *id;
-  float cap;
-  float *y;
-};
-
-__global__ void __launch_bounds__(256) loss_pick_kernel(const PickArgs a) {
+__global__ void __launch_bounds__(256) loss_split_kernel(const void *h, int bf16, int D,
+                                                         int64_t pitch,
+                                                         const float *__restrict__ amax,
+                                                         __half *__restrict__ hi,
+                                                         __half *__restrict__ lo) {
   griddep_launch_dependents();
   griddep_wait();
-  if (blockIdx.x < a.N) {
-    const float s = scale_h(a.amax);
-    const int64_t n = blockIdx.x;
-    for (int i = threadIdx.x; i < a.D; i += blockDim.x) {
-      __half x, r;
-      split_f16(__fmul_rn(load_h(a.h, a.bf16, n * a.D + i), s), x, r);
-      a.hi[n * a.pitch + i] = x;
-      if (a.lo) a.lo[n * a.pitch + i] = r;
-    }
-    return;
+  const float s = scale_h(amax);
+  const int64_t n = blockIdx.x;
+  for (int i = threadIdx.x; i < D; i += blockDim.x) {
+    __half x, r;
+    split_f16(__fmul_rn(load_h(h, bf16, n * D + i), s), x, r);
+    hi[n * pitch + i] = x;
+    if (lo) lo[n * pitch + i] = r;
   }
-  const int64_t i = (int64_t)(blockIdx.x - a.N) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31, ds = a.D / a.M, L = a.L, K = a.cs.K;
-  if (i >= a.N * a.k) return;
-  const int32_t v = a.id[i];
-  float z = 0.f;
-  if (v >= 0 && v < a.cs.V) {
-    const int64_t n = i / a.k;
-    for (int m = lane; m < a.M; m += 32) {
-      const int64_t hm = n * a.D + (int64_t)m * ds;
-      const float *book = a.C + (size_t)m * L * K * ds;
-      uint32_t c[4];
-#pragma unroll
-      for (int l = 0; l < 4; ++l) c[l] = l < L ? a.cs(v, m * L + l) : 0u;
-#pragma unroll 6
-      for (int j = 0; j < ds; ++j) {
-        float e = 0.f;
-#pragma unroll
-        for (int l = 0; l < 4; ++l)
-          if (l < L) e = __fadd_rn(e, __ldg(book + ((size_t)l * K + c[l]) * ds + j));
-        for (int l = 4; l < L; ++l)
-          e = __fadd_rn(e, __ldg(book + ((size_t)l * K + a.cs(v, m * L + l)) * ds + j));
-        z = fmaf(load_h(a.h, a.bf16, hm + j), e, z);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  }
-  if (lane == 0) a.y[i] = softcap_f(z, a.cap);
 }
 
 // ------------------------------------------------------------- statistics
@@ -534,26 +491,86 @@ __device__ __forceinline__ float dz_at(float y, float q, float lse, float f, flo
   return f != 0.f ? (expf(y * beta - lse) - q) * (1.f - th * th) * f : 0.f;
 }
 
-__global__ void __launch_bounds__(256) loss_fix_planes_kernel(
-    const int32_t *__restrict__ sid, const float *__restrict__ sq, const float *__restrict__ y,
-    int k, int64_t count, int64_t v0, int64_t rows, const float *__restrict__ lse,
-    const float *__restrict__ f, const float *__restrict__ amax, float T, float beta, float cap,
-    __half *__restrict__ hi, __half *__restrict__ lo, int64_t pitch) {
+// The listed ids that lie in a decoded piece, one warp each: the logit from the
+// row's planes in fp32 (9 KB side by side for 2304 dims; rebuilding the row
+// from its codes gathers 384 codewords all over the codebooks, 95 us against
+// 30 for 12800 entries), then what it is for: y itself, or the corrected
+// gradient in the piece's planes or in fp32.
+struct EntryArgs {
+  const void *h;
+  int bf16, vec;         // vec: h and D allow 16-byte vectors
+  int D, k, L;
+  int64_t count, v0, rows, pitch;
+  const __half *wh, *wl;
+  const float *amax;
+  const int32_t *id;
+  float cap, beta, T;
+  float *y;              // [count]
+  const float *sq, *lse, *f;
+  __half *zh, *zl;       // [N][zpitch]
+  float *dz;             // [N][zpitch], of the whole vocabulary
+  int64_t zpitch;
+};
+
+__global__ void __launch_bounds__(256) loss_entry_kernel(const EntryArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  const float sz = scale_z(amax, T);
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= count) return;
-  const int64_t v = (int64_t)sid[i] - v0;
-  if (sid[i] < 0 || v < 0 || v >= rows) return;
-  const int64_t n = i / k;
-  __half a, b;
-  split_f16(dz_at(y[i], sq[i], lse[n], f[n] * sz, beta, cap), a, b);
-  hi[n * pitch + v] = a;
-  lo[n * pitch + v] = b;
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (i >= a.count) return;
+  const int64_t v = (int64_t)a.id[i] - a.v0;
+  if (v < 0 || v >= a.rows) return;       // (an id below 0 too: v0 >= 0)
+  const int64_t n = i / a.k, hn = n * a.D;
+  const __half *wh = a.wh + v * a.pitch, *wl = a.wl + v * a.pitch;
+  float z = 0.f;
+  if (a.vec) {
+    for (int c = lane * 8; c < a.D; c += 256) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4 *>(wh + c));
+      const uint4 y = __ldg(reinterpret_cast<const uint4 *>(wl + c));
+      float h[8];
+      if (a.bf16) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(
+            static_cast<const __nv_bfloat16 *>(a.h) + hn + c));
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          h[2 * j] = __uint_as_float(u[j] << 16);
+          h[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+        }
+      } else {
+        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.h) + hn + c);
+        const float4 u = __ldg(p), w = __ldg(p + 1);
+        h[0] = u.x, h[1] = u.y, h[2] = u.z, h[3] = u.w;
+        h[4] = w.x, h[5] = w.y, h[6] = w.z, h[7] = w.w;
+      }
+      const __half2 *xh = reinterpret_cast<const __half2 *>(&x);
+      const __half2 *xl = reinterpret_cast<const __half2 *>(&y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 p = __half22float2(xh[j]), q = __half22float2(xl[j]);
+        z = fmaf(h[2 * j], __fadd_rn(p.x, q.x), z);
+        z = fmaf(h[2 * j + 1], __fadd_rn(p.y, q.y), z);
+      }
+    }
+  } else {
+    for (int c = lane; c < a.D; c += 32)
+      z = fmaf(load_h(a.h, a.bf16, hn + c),
+               __fadd_rn(__half2float(wh[c]), __half2float(wl[c])), z);
+  }
+  z = warp_sum(z) / scale_e(a.amax, a.L);
+  const float y = softcap_f(z, a.cap);
+  if (a.sq == nullptr) {
+    if (lane == 0) a.y[i] = y;
+    return;
+  }
+  const float d = dz_at(y, a.sq[i], a.lse[n], a.f[n], a.beta, a.cap);
+  if (a.dz != nullptr) {
+    if (lane == 0) a.dz[n * a.zpitch + a.v0 + v] = d;
+    return;
+  }
+  const float sz = scale_z(a.amax, a.T);
+  if (lane == 0) split_f16(d * sz, a.zh[n * a.zpitch + v], a.zl[n * a.zpitch + v]);
 }
-
-// ------------------------------------------------------------- few tokens
 
 __global__ void __launch_bounds__(256) loss_dz_kernel(const float *__restrict__ logits, int64_t V,
                                                       const float *__restrict__ lse,
@@ -569,16 +586,15 @@ __global__ void __launch_bounds__(256) loss_dz_kernel(const float *__restrict__ 
 }
 
 __global__ void __launch_bounds__(256) loss_fix_kernel(
-    const int32_t *__restrict__ sid, const float *__restrict__ sq, const float *__restrict__ y,
-    int y_is_logits, int k, int64_t count, int64_t V, const float *__restrict__ lse,
-    const float *__restrict__ f, float beta, float cap, float *__restrict__ dz, int64_t pitch) {
+    const int32_t *__restrict__ sid, const float *__restrict__ sq, const float *__restrict__ logits,
+    int k, int64_t count, int64_t V, const float *__restrict__ lse, const float *__restrict__ f,
+    float beta, float cap, float *__restrict__ dz, int64_t pitch) {
   griddep_launch_dependents();
   griddep_wait();
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= count || sid[i] < 0) return;
   const int64_t n = i / k, v = sid[i];
-  dz[n * pitch + v] =
-      dz_at(y_is_logits ? y[n * V + v] : y[i], sq[i], lse[n], f[n], beta, cap);
+  dz[n * pitch + v] = dz_at(logits[n * V + v], sq[i], lse[n], f[n], beta, cap);
 }
 
 __global__ void __launch_bounds__(256) loss_dh_sum_kernel(const float *__restrict__ part,
@@ -706,27 +722,41 @@ cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, 
                           s, args, true);
 }
 
-cudaError_t launch_loss_pick(const void *h, int bf16, int64_t N, int64_t pitch, const float *amax,
-                             __half *hi, __half *lo, const CodeSrc &cs, const float *C, int D, int M,
-                             int L, const int32_t *id, int k, float cap, float *y, cudaStream_t s) {
-  PickArgs a;
-  a.h = h;
-  a.bf16 = bf16;
-  a.N = N;
-  a.pitch = pitch;
-  a.amax = amax;
-  a.hi = hi;
-  a.lo = lo;
-  a.cs = cs;
-  a.C = C;
-  a.D = D;
-  a.M = M;
-  a.L = L;
-  a.k = k;
+cudaError_t launch_loss_split(const void *h, int bf16, int64_t N, int D, int64_t pitch,
+                              const float *amax, __half *hi, __half *lo, cudaStream_t s) {
+  return pdl_launch(loss_split_kernel, dim3((unsigned)N), dim3(256), (size_t)0, s, h, bf16, D, pitch,
+                    amax, hi, lo);
+}
+
+cudaError_t launch_loss_entries(const EntryCall &c, const LossTargets &t, const int32_t *id,
+                                int64_t N, float *y, cudaStream_t s) {
+  EntryArgs a = {};
+  a.h = c.h;
+  a.bf16 = c.bf16;
+  a.vec = c.D % 8 == 0 && (reinterpret_cast<uintptr_t>(c.h) & 15) == 0;
+  a.D = c.D;
+  a.k = t.k;
+  a.L = c.L;
+  a.count = N * t.k;
+  a.v0 = c.v0;
+  a.rows = c.rows;
+  a.pitch = c.pitch;
+  a.wh = c.wh;
+  a.wl = c.wl;
+  a.amax = c.amax;
   a.id = id;
-  a.cap = cap;
+  a.cap = c.cap;
+  a.beta = t.beta;
+  a.T = t.T;
   a.y = y;
-  return pdl_launch(loss_pick_kernel, dim3((unsigned)N + blocks_of(N * k, 8)), dim3(256), 0, s, a);
+  a.sq = c.sq;
+  a.lse = c.lse;
+  a.f = c.f;
+  a.zh = c.zh;
+  a.zl = c.zl;
+  a.dz = c.dz;
+  a.zpitch = c.zpitch;
+  return pdl_launch(loss_entry_kernel, dim3(blocks_of(N * t.k, 8)), dim3(256), (size_t)0, s, a);
 }
 
 int loss_stat_parts(int64_t V) { return (int)((V + kStatCols - 1) / kStatCols); }
@@ -742,24 +772,17 @@ cudaError_t launch_loss_finish(const float2 *stat, int parts, int stat_ld, int64
   return pdl_launch(loss_finish_kernel, dim3(blocks_of(N, 32)), dim3(1024), (size_t)0, s, stat, parts, stat_ld, N, V, t, y, y_is_logits, loss, lse, err);
 }
 
-cudaError_t launch_loss_fix_planes(const int32_t *sid, const float *sq, const float *y, int k,
-                                   int64_t N, int64_t v0, int64_t rows, const float *lse,
-                                   const float *f, const float *amax, float T, float beta,
-                                   float cap, __half *hi, __half *lo, int64_t pitch,
-                                   cudaStream_t s) {
-  return pdl_launch(loss_fix_planes_kernel, dim3(blocks_of(N * k, 256)), dim3(256), (size_t)0, s, sid, sq, y, k, N * k, v0, rows, lse, f, amax, T, beta, cap, hi, lo, pitch);
-}
-
 cudaError_t launch_loss_dz(const float *logits, int64_t N, int64_t V, const float *lse,
                            const float *f, float beta, float cap, float *dz, int64_t pitch,
                            cudaStream_t s) {
   return pdl_launch(loss_dz_kernel, dim3(blocks_of(pitch, 1024), (unsigned)N), dim3(256), (size_t)0, s, logits, V, lse, f, beta, cap, dz, pitch);
 }
 
-cudaError_t launch_loss_fix(const int32_t *sid, const float *sq, const float *y, bool y_is_logits,
-                            int k, int64_t N, int64_t V, const float *lse, const float *f,
-                            float beta, float cap, float *dz, int64_t pitch, cudaStream_t s) {
-  return pdl_launch(loss_fix_kernel, dim3(blocks_of(N * k, 256)), dim3(256), (size_t)0, s, sid, sq, y, y_is_logits, k, N * k, V, lse, f, beta, cap, dz, pitch);
+cudaError_t launch_loss_fix(const int32_t *sid, const float *sq, const float *logits, int k,
+                            int64_t N, int64_t V, const float *lse, const float *f, float beta,
+                            float cap, float *dz, int64_t pitch, cudaStream_t s) {
+  return pdl_launch(loss_fix_kernel, dim3(blocks_of(N * k, 256)), dim3(256), (size_t)0, s, sid, sq,
+                    logits, k, N * k, V, lse, f, beta, cap, dz, pitch);
 }
 
 cudaError_t launch_loss_dh_sum(const float *part, int splits, int64_t stride, int64_t pitch,
