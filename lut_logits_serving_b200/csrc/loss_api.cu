@@ -14,7 +14,6 @@ using namespace rq;
 
 namespace {
 
-constexpr int64_t kPieceRows = 8 * kGradRows;   // most rows of the vocabulary per piece
 constexpr int kTokenChunk = 4096;         // tokens per sweep over the vocabulary
 constexpr int kServeTokens = 64;          // most tokens of a call on the serving kernels' logits
 constexpr int kSumTokens = 32;            // and of one on sums by code
@@ -62,23 +61,29 @@ struct Arena {
   }
 };
 
-int64_t piece_rows(const rq_dims &d) { return d.V < kPieceRows ? d.V : kPieceRows; }
+// Rows of the vocabulary per piece, whole index blocks: 65536, or more where
+// rows are short, up to what 600 MB of planes hold (8 blocks measured fastest
+// for rows of 2304 and 256 to 2048 tokens: 9.9 ms where 4 take 10.3, 2 take
+// 10.9, 1 takes 12.0; fewer launches and ends of waves).
+int64_t piece_rows(const rq_dims &d, int64_t tokens) {
+  const int64_t fit = 600000000 / (8 * (int64_t)d.D + 4 * tokens) / kGradRows;
+  const int64_t rows = (fit < 8 ? 8 : fit) * kGradRows;
+  return d.V < rows ? d.V : rows;
+}
 int64_t pitch16(int64_t n) { return align_up(n, 16); }   // fp16 rows of whole sectors
 
-int total_parts(const rq_dims &d, int64_t tokens) {
+int total_parts(const rq_dims &d, int64_t tokens, int64_t piece) {
   int n = 0;
-  for (int64_t v0 = 0; v0 < d.V; v0 += kPieceRows) {
-    const int64_t r = d.V - v0 < kPieceRows ? d.V - v0 : kPieceRows;
-    n += loss_stats_parts(tokens, r);
-  }
+  for (int64_t v0 = 0; v0 < d.V; v0 += piece)
+    n += loss_stats_parts(tokens, d.V - v0 < piece ? d.V - v0 : piece);
   return n;
 }
 
 // Shares of the vocabulary in dz E: its tiles are few (tokens by dims), so the
 // contraction is split until whole waves of them fill the SMs.  A share costs
 // its block products (0.85 us for 64 rows) and a pass over its sums.
-int dh_splits(const rq_dims &d, int64_t n) {
-  const int64_t mt = (n + 127) / 128, nt = (d.D + 255) / 256, kb = (piece_rows(d) + 63) / 64;
+int dh_splits(const rq_dims &d, int64_t n, int64_t piece) {
+  const int64_t mt = (n + 127) / 128, nt = (d.D + 255) / 256, kb = (piece + 63) / 64;
   const bool pairs = mt % 2 == 0 || mt >= 7;
   const int64_t tiles = pairs ? (mt + 1) / 2 * nt : mt * nt, units = pairs ? kSms / 2 : kSms;
   int best = 1;
@@ -105,9 +110,10 @@ struct Choice {
 //   a tensor product   V D 128 per token tile at 1.1 PFLOP/s (a third more
 //                      for the first and the last wave of small ones: 12)
 //   serving, B <= 4    116 per token (tables in shared memory)
-//   serving, groups    tables through L2: 0.12 per column and row a thread
-//                      has; decoded groups: 450 (32 tokens, 1024 rows per SM),
-//                      340 (64, 512)
+//   serving, groups    tables through L2: 14 TB/s, and at least 0.09 (10 bits
+//                      0.13, bytes 0.24) per column and row a thread has;
+//                      decoded groups: 450 (32 tokens, 1024 rows per SM), 340
+//                      (64, 512)
 //   sums by code       1.95 per million codes and pair (of tokens or dims)
 // The serving kernels' fallback for odd layouts walks a row's codes one by one
 // (385 where the tensor cores take 45) and is never chosen.
@@ -151,7 +157,9 @@ double serve_us(const rq_dims &d, int N, int fmt) {
       while (tok < left && tok < 32) tok *= 2;
       const int64_t grid = d.V / 256 < 4 * kSms ? (d.V + 255) / 256 : 4 * kSms;
       const int64_t steps = (d.V + grid * (1024 / tok) - 1) / (grid * (1024 / tok));
-      us += 8 + 0.12 * steps * P;
+      const double wait = (fmt == RQ_CODES_U8 ? 0.24 : fmt == RQ_CODES_U16 ? 0.09 : 0.13) * steps * P;
+      const double move = codes * tok * 4 / 14;
+      us += 10 + (wait > move ? wait : move);
       left -= tok;
     }
   }
@@ -185,6 +193,7 @@ struct Layout {
   size_t total;
   int64_t hp, zp, vp;  // row pitches: D, the piece's rows, V
   int64_t chunk;       // tokens per sweep
+  int64_t piece;       // rows of the vocabulary per piece
   int splits;          // shares of the sums by code
 };
 
@@ -192,10 +201,11 @@ Layout layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
   Layout x{};
   Arena a;
   x.how = choose(d, N, fmt, grad);
-  const int64_t n = N < kTokenChunk ? N : kTokenChunk, rows = piece_rows(d);
+  const int64_t n = N < kTokenChunk ? N : kTokenChunk, rows = piece_rows(d, n);
   const int P = d.M * d.L, ds = d.D / d.M;
   const int64_t last = N % n == 0 ? n : N % n;     // tokens of the last sweep
   x.chunk = n;
+  x.piece = rows;
   x.hp = pitch16(d.D);
   x.zp = pitch16(rows);
   x.vp = pitch16(d.V);
@@ -215,8 +225,8 @@ Layout layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
   if (!grad) {
     int parts = loss_stat_parts(d.V);
     if (!x.how.serve) {
-      parts = total_parts(d, n);
-      if (total_parts(d, last) > parts) parts = total_parts(d, last);
+      parts = total_parts(d, n, rows);
+      if (total_parts(d, last, rows) > parts) parts = total_parts(d, last, rows);
     }
     x.stat = a.take((int64_t)parts * n * 8);
   } else {
@@ -235,8 +245,8 @@ Layout layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
       x.splits = codebook_rows_splits(d.V, rows, d.M, d.L, d.K, ds);
       x.cpart = a.take(x.splits > 1 ? (int64_t)x.splits * P * d.K * ds * 4 : 0);
       // with fewer tokens there are more shares
-      int64_t part = dh_splits(d, n) * n;
-      const int64_t p2 = dh_splits(d, last) * last;
+      int64_t part = dh_splits(d, n, rows) * n;
+      const int64_t p2 = dh_splits(d, last, rows) * last;
       if (p2 > part) part = p2;
       x.part = a.take(part * x.hp * 4);
     }
@@ -355,9 +365,9 @@ GemmPlanes w_planes(const Problem &q, const Layout &x, int64_t rows, void *ws) {
 }
 
 template <typename Each>
-cudaError_t for_pieces(const rq_dims &d, Each &&each) {
-  for (int64_t v0 = 0; v0 < d.V; v0 += kPieceRows) {
-    const cudaError_t e = each(v0, d.V - v0 < kPieceRows ? d.V - v0 : kPieceRows);
+cudaError_t for_pieces(const rq_dims &d, const Layout &x, Each &&each) {
+  for (int64_t v0 = 0; v0 < d.V; v0 += x.piece) {
+    const cudaError_t e = each(v0, d.V - v0 < x.piece ? d.V - v0 : x.piece);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -372,7 +382,7 @@ cudaError_t tensor_loss(const Problem &all, const Layout &x, float *loss, float 
     const rq_dims &d = q.d;
     RQ_TRY(split(q, x, ws, s));
     int part0 = 0;
-    RQ_TRY(for_pieces(d, [&](int64_t v0, int64_t rows) {
+    RQ_TRY(for_pieces(d, x, [&](int64_t v0, int64_t rows) {
       RQ_TRY(decode(q, x, v0, rows, ws, di, s));
       RQ_TRY(launch_loss_entries(entries(q, x, v0, rows, ws), q.t, q.t.id, q.N, y, s));
       GemmArgs g = gemm_args(q, amax, di);
@@ -402,10 +412,10 @@ cudaError_t products_grad(const Problem &all, const Layout &x, const float *lse,
     const Problem q = slice(all, n0, all.N - n0 < x.chunk ? all.N - n0 : x.chunk);
     const rq_dims &d = q.d;
     const float *ql = lse + n0;
-    const int splits = dh_splits(d, q.N);
+    const int splits = dh_splits(d, q.N, x.piece);
     RQ_TRY(begin(all, x, n0 == 0, &q, w, w ? w + n0 : nullptr, ws, di, s));
     RQ_TRY(split(q, x, ws, s));
-    RQ_TRY(for_pieces(d, [&](int64_t v0, int64_t rows) {
+    RQ_TRY(for_pieces(d, x, [&](int64_t v0, int64_t rows) {
       RQ_TRY(decode(q, x, v0, rows, ws, di, s));
       GemmArgs g = gemm_args(q, amax, di);
       g.rows = q.N;
@@ -479,7 +489,7 @@ cudaError_t sums_grad(const Problem &q, const Layout &x, const float *lse, const
   } else {
     const float *amax = at<float>(ws, x.amax);
     RQ_TRY(split(q, x, ws, s));
-    RQ_TRY(for_pieces(d, [&](int64_t v0, int64_t rows) {
+    RQ_TRY(for_pieces(d, x, [&](int64_t v0, int64_t rows) {
       RQ_TRY(decode(q, x, v0, rows, ws, di, s));
       GemmArgs g = gemm_args(q, amax, di);
       g.rows = q.N;

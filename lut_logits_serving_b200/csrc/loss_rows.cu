@@ -137,40 +137,62 @@ struct DecodeArgs {
 };
 
 constexpr int kDecThreads = 1024;
-constexpr int kDecU = 4;           // rows a thread has in flight
+constexpr int kDecU = 3;           // rows a thread has in flight
 
-// The codes of subspace m of a row, fetched ahead: load() only issues loads
+// Where the codes of subspace m start in a chunk's first row, and the bytes
+// from one row to the next (uint16, bytes, and 10 bits at two levels; the other
+// layouts go through CodeSrc).
+struct CodeRow {
+  const uint8_t *at;
+  int step, shift;
+  __device__ __forceinline__ CodeRow(const CodeSrc &cs, int64_t v, int m, int L) {
+    const uint8_t *b = static_cast<const uint8_t *>(cs.codes);
+    shift = 0;
+    if (cs.fmt == RQ_CODES_U16) {
+      step = cs.P * 2;
+      at = b + v * step + m * L * 2;
+    } else if (cs.fmt == RQ_CODES_U8) {
+      step = cs.P;
+      at = b + v * step + m * L;
+    } else {      // bits [20 m, 20 m + 20) of the row, in three bytes
+      step = (10 * cs.P + 7) / 8;
+      at = b + v * step + (20 * m >> 3);
+      shift = (m & 1) * 4;
+    }
+  }
+};
+
+// The codes of a subspace of a row, fetched ahead: load() only issues loads
 // (an instruction on what they bring would wait for it), get() makes codes of
 // them.  LL = 0 (many levels): nothing is kept, codes are fetched when used.
 template <int LL>
 struct RowCodes {
   uint32_t raw[LL == 0 ? 1 : LL == 2 ? 3 : LL];
-  __device__ __forceinline__ void load(const CodeSrc &cs, int M, int64_t v, int m) {
+  // row x of the chunk, row v of the vocabulary
+  __device__ __forceinline__ void load(const CodeSrc &cs, const CodeRow &c, int x, int64_t v,
+                                       int m) {
+    const uint8_t *p = c.at + (int64_t)x * c.step;
     if (LL == 2 && cs.fmt == RQ_CODES_U16) {
-      raw[0] = __ldg(static_cast<const uint32_t *>(cs.codes) + v * M + m);
+      raw[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
     } else if (LL == 2 && cs.fmt == RQ_CODES_PACKED10) {
-      // bits [20 m, 20 m + 20) of the row, in three bytes
-      const uint8_t *b =
-          static_cast<const uint8_t *>(cs.codes) + v * ((20LL * M + 7) / 8) + (20 * m >> 3);
 #pragma unroll
-      for (int i = 0; i < (LL == 2 ? 3 : 0); ++i) raw[i] = __ldg(b + i);
+      for (int i = 0; i < (LL == 2 ? 3 : 0); ++i) raw[i] = __ldg(p + i);
     } else if (cs.fmt == RQ_CODES_U16) {
 #pragma unroll
-      for (int l = 0; l < LL; ++l)
-        raw[l] = __ldg(static_cast<const uint16_t *>(cs.codes) + v * cs.P + m * LL + l);
+      for (int l = 0; l < LL; ++l) raw[l] = __ldg(reinterpret_cast<const uint16_t *>(p) + l);
     } else if (cs.fmt == RQ_CODES_U8) {
 #pragma unroll
-      for (int l = 0; l < LL; ++l)
-        raw[l] = __ldg(static_cast<const uint8_t *>(cs.codes) + v * cs.P + m * LL + l);
+      for (int l = 0; l < LL; ++l) raw[l] = __ldg(p + l);
     } else {
 #pragma unroll
       for (int l = 0; l < LL; ++l) raw[l] = cs(v, m * LL + l);
     }
   }
-  __device__ __forceinline__ uint32_t get(const CodeSrc &cs, int m, int l) const {
+  __device__ __forceinline__ uint32_t get(const CodeSrc &cs, const CodeRow &c, int l) const {
     if (LL == 2 && cs.fmt == RQ_CODES_U16) return cs.fix(l == 0 ? raw[0] & 0xFFFFu : raw[0] >> 16);
     if (LL == 2 && cs.fmt == RQ_CODES_PACKED10) {
-      const uint32_t w = (raw[0] | raw[LL == 2 ? 1 : 0] << 8 | raw[LL == 2 ? 2 : 0] << 16) >> ((m & 1) * 4);
+      const uint32_t w =
+          (raw[0] | raw[LL == 2 ? 1 : 0] << 8 | raw[LL == 2 ? 2 : 0] << 16) >> c.shift;
       return cs.fix(w >> (10 * l) & 1023u);
     }
     return cs.fix(raw[LL > 0 ? l : 0]);
@@ -221,35 +243,39 @@ __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeAr
     const float *b0 = (SMEM ? books + sub * a.book : a.C + (m0 + sub) * a.book) + j;
     const float *b1 = (SMEM ? books + sub1 * a.book : a.C + (m0 + sub1) * a.book) + j1;
     const int m = m0 + sub, m1 = m0 + sub1;
-    __half *oh = a.hi + (int64_t)m0 * ds + 2 * w, *ol = a.lo + (int64_t)m0 * ds + 2 * w;
+    const int64_t vc = a.v0 + r0;
+    const int n = (int)(r1 - r0), pitch = (int)a.pitch;
+    const CodeRow ca(a.cs, vc, m, L), cb(a.cs, vc, EVEN ? m : m1, L);
+    __half *oh = a.hi + r0 * a.pitch + (int64_t)m0 * ds + 2 * w;
+    __half *ol = a.lo + r0 * a.pitch + (int64_t)m0 * ds + 2 * w;
     RowCodes<LL> cn[kDecU], dn[EVEN ? 1 : kDecU];
-    auto fetch = [&](int64_t r) {
+    auto fetch = [&](int r) {
 #pragma unroll
       for (int i = 0; i < kDecU; ++i) {
-        const int64_t x = r + (int64_t)i * rstep;
-        if (LL > 0 && x < r1) {
-          cn[i].load(a.cs, a.M, a.v0 + x, m);
-          if (!EVEN && second) dn[EVEN ? 0 : i].load(a.cs, a.M, a.v0 + x, m1);
+        const int x = r + i * rstep;
+        if (LL > 0 && x < n) {
+          cn[i].load(a.cs, ca, x, vc + x, m);
+          if (!EVEN && second) dn[EVEN ? 0 : i].load(a.cs, cb, x, vc + x, m1);
         }
       }
     };
-    fetch(r0 + lrow);
-    for (int64_t r = r0 + lrow; r < r1; r += (int64_t)kDecU * rstep) {
+    fetch(lrow);
+    for (int r = lrow; r < n; r += kDecU * rstep) {
       RowCodes<LL> c[kDecU], d[EVEN ? 1 : kDecU];
 #pragma unroll
       for (int i = 0; i < kDecU; ++i) {
         c[i] = cn[i];
         if (!EVEN) d[EVEN ? 0 : i] = dn[EVEN ? 0 : i];
       }
-      fetch(r + (int64_t)kDecU * rstep);
+      fetch(r + kDecU * rstep);
 #pragma unroll
       for (int i = 0; i < kDecU; ++i) {
-        const int64_t x = r + (int64_t)i * rstep;
-        if (x >= r1) break;
+        const int x = r + i * rstep;
+        if (x >= n) break;
         float e0 = 0.f, e1 = 0.f;
 #pragma unroll(LL > 0 ? LL : 1)
         for (int l = 0; l < L; ++l) {
-          const uint32_t cl = LL > 0 ? c[i].get(a.cs, m, l) : a.cs(a.v0 + x, m * L + l);
+          const uint32_t cl = LL > 0 ? c[i].get(a.cs, ca, l) : a.cs(vc + x, m * L + l);
           const float *p0 = b0 + (int64_t)(l * K + (int)cl) * ds;
           if (EVEN && SMEM) {
             const float2 y = *reinterpret_cast<const float2 *>(p0);
@@ -260,8 +286,8 @@ __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeAr
             if (EVEN) {
               e1 = __fadd_rn(e1, p0[1]);
             } else if (second) {
-              const uint32_t dl = LL > 0 ? d[EVEN ? 0 : i].get(a.cs, m1, l)
-                                         : a.cs(a.v0 + x, m1 * L + l);
+              const uint32_t dl = LL > 0 ? d[EVEN ? 0 : i].get(a.cs, cb, l)
+                                         : a.cs(vc + x, m1 * L + l);
               e1 = __fadd_rn(e1, b1[(int64_t)(l * K + (int)dl) * ds]);
             }
           }
@@ -275,8 +301,8 @@ __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeAr
         const __half2 lw = __floats2half2_rn(__fsub_rn(e0, f.x), __fsub_rn(e1, f.y));
         // rows are padded to whole vectors, so a pair past D has its place; a
         // group starts on a pair unless gs ds is odd (one group then)
-        *reinterpret_cast<__half2 *>(oh + x * a.pitch) = h;
-        *reinterpret_cast<__half2 *>(ol + x * a.pitch) = lw;
+        *reinterpret_cast<__half2 *>(oh + (int64_t)x * pitch) = h;
+        *reinterpret_cast<__half2 *>(ol + (int64_t)x * pitch) = lw;
       }
     }
   }
