@@ -49,7 +49,8 @@ constexpr int kABytes = kTM * kTK * 2;
 // 8.0e-7, for 5 to 8 % of a step's time; an fp32 library product leaves 8.4e-7
 // and 1.6e-6.  So the sums that only pass through one product get longer ones.
 constexpr int kChainMmas = 36, kChainMmasDw = 24;
-constexpr size_t kGemmSmemMax = 225 * 1024;      // 227 KB less the static part
+constexpr size_t kGemmSmemMax = 226 * 1024;      // 227 KB less the static part
+constexpr int kStoreBytes = 16384;               // a warpgroup's outgoing 128 rows x 128 bytes
 constexpr size_t kGemmSmemTail = 1024 + 256;     // alignment slack, barriers
 
 // Shared-memory matrix descriptor: 128-byte swizzle (layout type 2), version
@@ -155,6 +156,37 @@ __device__ __forceinline__ void stg32(void *p, const uint32_t *v) {
                : "memory");
 }
 
+// Outgoing tiles leave through shared memory as TMA stores: a thread has a row,
+// and stored directly a warp's words go to 32 rows, a sector each, which keeps
+// the threads from the next tile's sums (h^T dz of 500 tokens: 396 us, 261
+// without any store).
+__device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+__device__ __forceinline__ void store_tile(const CUtensorMap *map, uint32_t src, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(src)
+      : "memory");
+}
+__device__ __forceinline__ void store_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void store_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ void async_fence() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void group_sync(int id) {     // the 128 threads of a warpgroup
+  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+}
+
 __device__ __forceinline__ void wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -164,7 +196,9 @@ template <int MODE, int CG, int TN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     loss_gemm_kernel(const __grid_constant__ CUtensorMap a_hi, const __grid_constant__ CUtensorMap a_lo,
                      const __grid_constant__ CUtensorMap b_hi, const __grid_constant__ CUtensorMap b_lo,
+                     const __grid_constant__ CUtensorMap o_hi, const __grid_constant__ CUtensorMap o_lo,
                      const GemmArgs g) {
+  constexpr bool STAGED = MODE == kGemmGrad || MODE == kGemmDw;   // output through TMA
   constexpr bool LOGITS = MODE == kGemmStats || MODE == kGemmGrad || MODE == kGemmGrad32;
   constexpr bool A_MN = MODE == kGemmDw;                        // contraction down the rows of A
   constexpr bool B_MN = MODE == kGemmDh || MODE == kGemmDw;     // and of B
@@ -175,7 +209,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t stage_bytes = (uint32_t)(g.a_planes * kABytes + g.b_planes * B_BYTES);
-  const uint32_t bars = base + (uint32_t)g.stages * stage_bytes;
+  const uint32_t staging = base + (uint32_t)g.stages * stage_bytes;
+  const uint32_t bars = staging + (STAGED ? 2 * kStoreBytes : 0);
   auto full = [&](int i) { return bars + 8u * i; };
   auto empty = [&](int i) { return bars + 8u * (kMaxStages + i); };
   auto tfull = [&](int i) { return bars + 8u * (2 * kMaxStages + i); };
@@ -424,40 +459,88 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const float f = in ? g.f[row] : 0.f, lse2 = in ? g.lse[row] * kLog2e : 0.f, fs = f * sz;
         const int64_t at = (int64_t)row * g.dz_pitch + col0;
 #pragma unroll 1
-        for (int j0 = 0; j0 < HALF; j0 += 16) {
-          float x[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float z = acc[j] * inv;
-            float y = z, slope = 1.f;
-            if (cap > 0.f) {
-              const float th = tanhf(z * icap);
-              y = cap * th;
-              slope = 1.f - th * th;
-            }
-            x[j] = f != 0.f ? exp2f(y * beta2 - lse2) * slope * fs : 0.f;
-          }
-          if (MODE == kGemmGrad32) {
-            if (in && col0 + j0 < g.cols) {          // the rows' pitch is 16 floats
-              stg32(g.dz + at + j0, reinterpret_cast<const uint32_t *>(x));
-              stg32(g.dz + at + j0 + 8, reinterpret_cast<const uint32_t *>(x + 8));
-            }
-          } else if (in && col0 + j0 < g.dz_pitch) {   // the pitch is whole sectors
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const __half2 h = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
-              const float2 y = __half22float2(h);
-              const __half2 l =
-                  __floats2half2_rn(__fsub_rn(x[2 * j], y.x), __fsub_rn(x[2 * j + 1], y.y));
-              hi[j] = *reinterpret_cast<const uint32_t *>(&h);
-              lo[j] = *reinterpret_cast<const uint32_t *>(&l);
-            }
-            stg32(g.dz_hi + at + j0, hi);
-            stg32(g.dz_lo + at + j0, lo);
+        for (int j0 = 0; j0 < HALF; j0 += 32) {
+          if (STAGED) {
+            if (q == 0 && lane == 0) store_wait_read();   // the last chunk is read out
+            group_sync(1 + half);
           }
 #pragma unroll
-          for (int j = 0; j + 16 < HALF; ++j) acc[j] = acc[j + 16];
+          for (int k = 0; k < 2; ++k) {
+            float x[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float z = acc[16 * k + j] * inv;
+              float y = z, slope = 1.f;
+              if (cap > 0.f) {
+                const float th = tanhf(z * icap);
+                y = cap * th;
+                slope = 1.f - th * th;
+              }
+              x[j] = f != 0.f ? exp2f(y * beta2 - lse2) * slope * fs : 0.f;
+            }
+            if (MODE == kGemmGrad32) {
+              if (in && col0 + j0 + 16 * k < g.cols) {          // the rows' pitch is 16 floats
+                stg32(g.dz + at + j0 + 16 * k, reinterpret_cast<const uint32_t *>(x));
+                stg32(g.dz + at + j0 + 16 * k + 8, reinterpret_cast<const uint32_t *>(x + 8));
+              }
+            } else {
+              uint32_t hi[8], lo[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const __half2 h = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+                const float2 y = __half22float2(h);
+                const __half2 l =
+                    __floats2half2_rn(__fsub_rn(x[2 * j], y.x), __fsub_rn(x[2 * j + 1], y.y));
+                hi[j] = *reinterpret_cast<const uint32_t *>(&h);
+                lo[j] = *reinterpret_cast<const uint32_t *>(&l);
+              }
+              // rows of 64 bytes, 16-byte pieces swizzled by row / 2
+              const uint32_t r = staging + (uint32_t)(half * kStoreBytes + (q * 32 + lane) * 64);
+              const uint32_t sw = (uint32_t)(lane >> 1) & 3u;
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                const uint32_t o = r + (((uint32_t)(2 * k + p) ^ sw) << 4);
+                sts16(o, hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
+                sts16(o + kStoreBytes / 2, lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
+              }
+            }
+          }
+          if (STAGED) {
+            async_fence();
+            group_sync(1 + half);
+            if (q == 0 && lane == 0) {
+              const int x = col0 + j0, y = row;           // (row of the group's first thread)
+              if (x < g.cols && y < g.rows) {
+                store_tile(&o_hi, staging + half * kStoreBytes, x, y);
+                store_tile(&o_lo, staging + half * kStoreBytes + kStoreBytes / 2, x, y);
+              }
+              store_commit();
+            }
+          }
+#pragma unroll
+          for (int j = 0; j + 32 < HALF; ++j) acc[j] = acc[j + 32];
+        }
+      } else if (MODE == kGemmDw) {
+#pragma unroll
+        for (int j0 = 0; j0 < HALF; j0 += 32) {
+          if (q == 0 && lane == 0) store_wait_read();
+          group_sync(1 + half);
+          // rows of 128 bytes, 16-byte pieces swizzled by row
+          const uint32_t r = staging + (uint32_t)(half * kStoreBytes + (q * 32 + lane) * 128);
+#pragma unroll
+          for (int p = 0; p < 8; ++p)
+            sts16(r + (((uint32_t)p ^ ((uint32_t)lane & 7u)) << 4),
+                  __float_as_uint(acc[j0 + 4 * p] * inv), __float_as_uint(acc[j0 + 4 * p + 1] * inv),
+                  __float_as_uint(acc[j0 + 4 * p + 2] * inv),
+                  __float_as_uint(acc[j0 + 4 * p + 3] * inv));
+          async_fence();
+          group_sync(1 + half);
+          if (q == 0 && lane == 0) {
+            // 32-bit elements as pairs of 16
+            if (col0 + j0 < g.cols && row < g.rows)
+              store_tile(&o_hi, staging + half * kStoreBytes, 2 * (col0 + j0), row);
+            store_commit();
+          }
         }
       } else if (row < g.rows) {
         float *o = g.out + (int64_t)sp * g.out_split + (int64_t)row * g.out_pitch + col0;
@@ -467,7 +550,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             float v[8];
 #pragma unroll
             for (int x = 0; x < 8; ++x) v[x] = acc[j + x] * inv;
-            if (MODE == kGemmDh && g.accumulate) {
+            if (g.accumulate) {
 #pragma unroll
               for (int x = 0; x < 8; x += 4) {
                 const float4 w = *reinterpret_cast<const float4 *>(o + j + x);
@@ -482,6 +565,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
     }
+    if (STAGED && q == 0 && lane == 0) store_wait_all();
     if (to && lane == 0) atomicOr(g.err, RQ_DEVERR_TIMEOUT);
   }
   tc_before();
@@ -544,17 +628,29 @@ cudaError_t launch_tile(const GemmPlanes &A, const GemmPlanes &B, GemmArgs a, co
   a.n_tiles = (int)(((B_MN ? B.cols : B.rows) + TN - 1) / TN);
   a.kblocks = (int)((k + kTK - 1) / kTK);
   if (a.splits > a.kblocks) a.splits = a.kblocks;
+  CUtensorMap oh = ah, ol = ah;
+  if (MODE == kGemmGrad &&
+      (!encode_tmap_2d_u16(&oh, a.dz_hi, (uint64_t)a.cols, (uint64_t)a.rows,
+                           (uint64_t)a.dz_pitch * 2, 32, kTM, CU_TENSOR_MAP_SWIZZLE_64B) ||
+       !encode_tmap_2d_u16(&ol, a.dz_lo, (uint64_t)a.cols, (uint64_t)a.rows,
+                           (uint64_t)a.dz_pitch * 2, 32, kTM, CU_TENSOR_MAP_SWIZZLE_64B)))
+    return cudaErrorInvalidValue;
+  if (MODE == kGemmDw &&
+      !encode_tmap_2d_u16(&oh, a.out, (uint64_t)a.cols * 2, (uint64_t)a.rows,
+                          (uint64_t)a.out_pitch * 4, 64, kTM, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
   const size_t stage = (size_t)a.a_planes * kABytes + (size_t)a.b_planes * (BN * kTK * 2);
-  int st = (int)((kGemmSmemMax - kGemmSmemTail) / stage);
+  const size_t tail = kGemmSmemTail + (MODE == kGemmGrad || MODE == kGemmDw ? 2 * kStoreBytes : 0);
+  int st = (int)((kGemmSmemMax - tail) / stage);
   a.stages = st > kMaxStages ? kMaxStages : st;
-  const size_t smem = kGemmSmemTail + a.stages * stage;
+  const size_t smem = tail + a.stages * stage;
   const void *fn = reinterpret_cast<const void *>(&loss_gemm_kernel<MODE, CG, TN>);
   cudaError_t e = ensure_smem_limit(fn, di.device, smem);
   if (e != cudaSuccess) return e;
   const int64_t total = (int64_t)a.m_tiles * a.n_tiles * a.splits;
   if (total < 1 || total > 0x7fffffff) return cudaErrorInvalidValue;
   const int units = di.sms / CG;
-  void *args[] = {&ah, &al, &bh, &bl, &a};
+  void *args[] = {&ah, &al, &bh, &bl, &oh, &ol, &a};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((total < units ? total : units) * CG));
   cfg.blockDim = dim3(kGemmThreads);
