@@ -255,8 +255,23 @@ struct GatherArgs {
   int64_t out_p, out_k, out_split;   // strides: column, code, share
   int64_t out_pair;                  // pair (0: its two columns lie at 2 pair)
   int accumulate;
+  int buffers;              // for units: 2, or 3 (see the kernel)
   unsigned *err;
 };
+
+// Shared memory by 32-bit address, an immediate offset apart.
+template <int OFF>
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float x;
+  asm volatile("ld.shared.f32 %0, [%1+%2];" : "=f"(x) : "r"(a), "n"(OFF));
+  return x;
+}
+template <int OFF>
+__device__ __forceinline__ uint32_t lds_b32(uint32_t a) {
+  uint32_t x;
+  asm volatile("ld.shared.b32 %0, [%1+%2];" : "=r"(x) : "r"(a), "n"(OFF));
+  return x;
+}
 
 struct GatherUnit {         // subspace, pair, levels, share of the blocks
   int m, j, l0, l1, b0, b1, share;
@@ -299,15 +314,20 @@ struct GatherAhead {
 
 __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(const GatherArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int kWarps = kGatherThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int K = a.x.K, g = a.x.lanes, gsh = __ffs(g) - 1;
-  unsigned char *units = smem;                                     // [2] units
-  float *vals = reinterpret_cast<float *>(smem + 2 * a.x.unit);    // [2][2][kPairPitch]
+  const int K = a.x.K, g = a.x.lanes, gsh = __ffs(g) - 1, nb = a.buffers;
+  unsigned char *units = smem;                                     // [nb] units
+  float *vals = reinterpret_cast<float *>(smem + nb * a.x.unit);   // [2][2][kPairPitch]
   float2 *stage = reinterpret_cast<float2 *>(vals + 4 * kPairPitch);   // [levels][K]
-  __shared__ uint64_t bars[4];                                     // units, values
+  __shared__ uint64_t bars[3 + 2 + 2];        // units, values, steps done (all warps)
   __shared__ volatile int abort_flag;
+  auto ubar = [&](int i) { return smem_addr(&bars[i]); };
+  auto vbar = [&](int i) { return smem_addr(&bars[3 + i]); };
+  auto dbar = [&](int i) { return smem_addr(&bars[5 + i]); };
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(smem_addr(&bars[i]), 1);
+    for (int i = 0; i < 5; ++i) mbar_init(smem_addr(&bars[i]), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(dbar(i), kWarps);
     fence_mbar_init();
     abort_flag = 0;
   }
@@ -315,17 +335,23 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
   griddep_launch_dependents();
   __syncthreads();
   griddep_wait();
-  // thread 0 keeps the copies a step (units) and a block (values) ahead
+  // The last warp, whose lists are the shortest, issues the copies: a step
+  // (units) and a block (values) ahead.  With three unit buffers the warps may
+  // be a step apart (`lag` 2: a step starts when all have finished the last but
+  // one), so that nobody waits for the longest list of every step.
+  const int lag = nb - 1;
+  const uint32_t vals_at = smem_addr(vals);
+  const bool issuer = tid == kGatherThreads - 32;
   GatherAhead nu{}, nv{};
   int it = 0, iv = 0;        // copies issued
   auto issue_unit = [&]() {
     if (nu.u >= a.units) return;
-    const uint32_t b = smem_addr(&bars[it & 1]);
-    mbar_arrive_expect_tx(b, (uint32_t)a.x.unit);
-    bulk_g2s(smem_addr(units + (it & 1) * a.x.unit),
+    const int i = it % nb;
+    mbar_arrive_expect_tx(ubar(i), (uint32_t)a.x.unit);
+    bulk_g2s(smem_addr(units + i * a.x.unit),
              static_cast<const unsigned char *>(a.index) +
                  ((size_t)(a.block0 + nu.b) * a.x.P + nu.q.m * a.L + nu.l) * a.x.unit,
-             (uint32_t)a.x.unit, b);
+             (uint32_t)a.x.unit, ubar(i));
     ++it;
     nu.step(a);
   };
@@ -333,27 +359,26 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
     if (nv.u >= a.units) return;
     const int64_t r0 = (int64_t)nv.b * kGradRows, left = a.rows - r0;
     const uint32_t bytes = (uint32_t)align_up(left < kGradRows ? left : kGradRows, 4) * 4;
-    const int w = a.ds - nv.q.j < 2 ? 1 : 2;
-    const uint32_t b = smem_addr(&bars[2 + (iv & 1)]);
-    mbar_arrive_expect_tx(b, bytes * w);
-    for (int i = 0; i < w; ++i)
-      bulk_g2s(smem_addr(vals + ((iv & 1) * 2 + i) * kPairPitch),
-               a.vals + (int64_t)((a.per_subspace ? nv.q.m * a.ds : 0) + nv.q.j + i) * a.pitch + r0,
-               bytes, b);
+    const int w = a.ds - nv.q.j < 2 ? 1 : 2, i = iv & 1;
+    mbar_arrive_expect_tx(vbar(i), bytes * w);
+    for (int k = 0; k < w; ++k)
+      bulk_g2s(smem_addr(vals + (i * 2 + k) * kPairPitch),
+               a.vals + (int64_t)((a.per_subspace ? nv.q.m * a.ds : 0) + nv.q.j + k) * a.pitch + r0,
+               bytes, vbar(i));
     ++iv;
     nv.block(a);
   };
-  if (tid == 0) {
+  if (issuer) {
     nu.unit(a, blockIdx.x);
     nv = nu;
     issue_unit();
     issue_vals();
   }
-  int t = 0, vt = 0;         // steps and blocks done
+  int t = 0, vt = 0, ub = 0;     // steps and blocks so far; the step's unit buffer
+  uint32_t uphase = 0;           // and its phase
   bool ok = true;
-  auto wait = [&](int i, int n) {
-    const uint32_t b = smem_addr(&bars[i]), parity = (uint32_t)(n >> 1) & 1u;
-    if (ok && !mbar_try_wait(b, parity) && !mbar_wait_bounded(b, parity)) {
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (ok && !mbar_try_wait(bar, parity) && !mbar_wait_bounded(bar, parity)) {
       ok = false;
       abort_flag = 1;
     }
@@ -364,52 +389,57 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
     const bool two = a.ds - q.j > 1;
     for (int b = q.b0; b < q.b1; ++b, ++vt) {
       for (int l = q.l0; l < q.l1; ++l, ++t) {
-        // the next copies go into the buffers that the last step (block) left
-        if (tid == 0) {
+        if (abort_flag) ok = false;      // (the loops go on, without work, to meet at their ends)
+        // everyone has finished step t - lag: its unit buffer takes the next
+        // unit, its lists' sums are in the stage, and, a step into a block (at
+        // lag 1 at once), nobody reads the last block's values any more
+        if (t >= lag) wait(dbar((t - lag) & 1), (uint32_t)((t - lag) >> 1) & 1u);
+        if (issuer && ok) {
           issue_unit();
-          if (l == q.l0) issue_vals();
+          if (l == q.l0 + (lag > 1 ? 1 : 0)) issue_vals();
         }
-        wait(t & 1, t);
-        if (l == q.l0) wait(2 + (vt & 1), vt);
-        const unsigned char *ub = units + (t & 1) * a.x.unit;
-        const uint16_t *off = reinterpret_cast<const uint16_t *>(ub);
-        const uint16_t *code = reinterpret_cast<const uint16_t *>(ub + a.x.code_at);
-        const uint16_t *over = reinterpret_cast<const uint16_t *>(ub + a.x.over_at);
-        const uint32_t *entry = reinterpret_cast<const uint32_t *>(ub + a.x.entry_at) + lane;
-        const unsigned char *v0 =
-            reinterpret_cast<const unsigned char *>(vals + (vt & 1) * 2 * kPairPitch);
-        float2 *st = stage + (size_t)(l - q.l0) * K;
-        // one word of entries: two rows of either value row
-        auto add = [&](uint32_t w, float &s0, float &s1) {
-          const unsigned char *p = v0 + (w & 0xFFFFu), *r = v0 + (w >> 16);
-          s0 += *reinterpret_cast<const float *>(p);
-          s1 += *reinterpret_cast<const float *>(p + 4 * kPairPitch);
-          s0 += *reinterpret_cast<const float *>(r);
-          s1 += *reinterpret_cast<const float *>(r + 4 * kPairPitch);
-        };
-        int full = 0;
+        wait(ubar(ub), uphase);
+        if (l == q.l0) wait(vbar(vt & 1), (uint32_t)(vt >> 1) & 1u);
         if (ok) {
-          full = over[0];
-          for (int sl = warp; sl < a.x.slices; sl += kGatherThreads / 32) {
+          const unsigned char *un = units + ub * a.x.unit;
+          const uint16_t *off = reinterpret_cast<const uint16_t *>(un);
+          const uint16_t *code = reinterpret_cast<const uint16_t *>(un + a.x.code_at);
+          const uint16_t *over = reinterpret_cast<const uint16_t *>(un + a.x.over_at);
+          const uint32_t entry = smem_addr(un) + (uint32_t)a.x.entry_at + (uint32_t)lane * 4;
+          const uint32_t v0 = vals_at + (uint32_t)(vt & 1) * (2 * kPairPitch * 4);
+          float2 *st = stage + (size_t)(l - q.l0) * K;
+          // one word of entries: two rows of either value row
+          auto add = [&](uint32_t w, float &s0, float &s1) {
+            const uint32_t p = v0 + (w & 0xFFFFu), r = v0 + (w >> 16);
+            const float x0 = lds_f32<0>(p), x1 = lds_f32<4 * kPairPitch>(p);
+            const float y0 = lds_f32<0>(r), y1 = lds_f32<4 * kPairPitch>(r);
+            s0 += x0;
+            s1 += x1;
+            s0 += y0;
+            s1 += y1;
+          };
+          const int full = over[0];
+          for (int sl = warp; sl < a.x.slices; sl += kWarps) {
             const int e0 = off[sl], n = off[sl + 1] - e0;
-            const uint32_t *e = entry + e0 * 32;
+            uint32_t e = entry + (uint32_t)e0 * 128;
             const int s = (sl * 32 + lane) >> gsh;
             float s0 = 0.f, s1 = 0.f;
             int i = 0;
-            for (; i + 4 <= n; i += 4, e += 128) {
-              const uint32_t w0 = e[0], w1 = e[32], w2 = e[64], w3 = e[96];
+            for (; i + 4 <= n; i += 4, e += 512) {
+              const uint32_t w0 = lds_b32<0>(e), w1 = lds_b32<128>(e), w2 = lds_b32<256>(e),
+                             w3 = lds_b32<384>(e);
               add(w0, s0, s1);
               add(w1, s0, s1);
               add(w2, s0, s1);
               add(w3, s0, s1);
             }
             if (i + 2 <= n) {
-              const uint32_t w0 = e[0], w1 = e[32];
+              const uint32_t w0 = lds_b32<0>(e), w1 = lds_b32<128>(e);
               add(w0, s0, s1);
               add(w1, s0, s1);
-              e += 64;
+              e += 256;
             }
-            if (n & 1) add(e[0], s0, s1);
+            if (n & 1) add(lds_b32<0>(e), s0, s1);
             for (int o = g >> 1; o > 0; o >>= 1) {
               s0 += __shfl_xor_sync(0xffffffffu, s0, o);
               s1 += __shfl_xor_sync(0xffffffffu, s1, o);
@@ -423,34 +453,40 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
               }
               st[c] = make_float2(s0, s1);
             }
-          }
-          if (full > 0) {      // uniform: every thread reads the same unit
-            __syncthreads();
-            const uint16_t *rest =
-                reinterpret_cast<const uint16_t *>(ub + a.x.entry_at) + off[a.x.slices] * 64;
-            for (int s = warp; s < full; s += kGatherThreads / 32) {
-              float s0 = 0.f, s1 = 0.f;
-              for (int i = over[1 + s] + lane; i < over[2 + s]; i += 32) {
-                const unsigned char *p = v0 + rest[i];
-                s0 += *reinterpret_cast<const float *>(p);
-                s1 += *reinterpret_cast<const float *>(p + 4 * kPairPitch);
+            // what this slice's codes have beyond their lanes' kCap entries
+            const int f1 = (sl + 1) * 32 >> gsh;
+            for (int f = sl * 32 >> gsh; f < f1 && f < full; ++f) {
+              __syncwarp();
+              const uint16_t *rest =
+                  reinterpret_cast<const uint16_t *>(un + a.x.entry_at) + off[a.x.slices] * 64;
+              float r0 = 0.f, r1 = 0.f;
+              for (int k = over[1 + f] + lane; k < over[2 + f]; k += 32) {
+                const uint32_t p = v0 + rest[k];
+                r0 += lds_f32<0>(p);
+                r1 += lds_f32<4 * kPairPitch>(p);
               }
 #pragma unroll
               for (int o = 16; o > 0; o >>= 1) {
-                s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-                s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+                r0 += __shfl_xor_sync(0xffffffffu, r0, o);
+                r1 += __shfl_xor_sync(0xffffffffu, r1, o);
               }
               if (lane == 0) {
-                const float2 d = st[code[s]];
-                st[code[s]] = make_float2(d.x + s0, d.y + s1);
+                const float2 d = st[code[f]];
+                st[code[f]] = make_float2(d.x + r0, d.y + r1);
               }
             }
           }
         }
-        __syncthreads();
-        if (abort_flag) goto out;
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(dbar(t & 1)) : "memory");
+        if (++ub == nb) {
+          ub = 0;
+          uphase ^= 1u;
+        }
       }
     }
+    __syncthreads();
     // the unit's sums out, in code order
     const int w = two ? 2 : 1;
     for (int l = q.l0; l < q.l1; ++l) {
@@ -466,14 +502,12 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
     }
     __syncthreads();
   }
-out:
-  if (abort_flag && tid == 0) {
+  if (issuer && abort_flag) {
     // the copies in flight land before the shared memory goes
-    for (int i = 1; i <= 2; ++i) {
-      if (it >= i) mbar_wait_bounded(smem_addr(&bars[(it - i) & 1]), (uint32_t)((it - i) >> 1) & 1u);
-      if (iv >= i)
-        mbar_wait_bounded(smem_addr(&bars[2 + ((iv - i) & 1)]), (uint32_t)((iv - i) >> 1) & 1u);
-    }
+    for (int i = 1; i <= nb; ++i)
+      if (it >= i) mbar_wait_bounded(ubar((it - i) % nb), (uint32_t)((it - i) / nb) & 1u);
+    for (int i = 1; i <= 2; ++i)
+      if (iv >= i) mbar_wait_bounded(vbar((iv - i) & 1), (uint32_t)((iv - i) >> 1) & 1u);
     atomicOr(a.err, RQ_DEVERR_TIMEOUT);
   }
 }
@@ -618,20 +652,24 @@ namespace {
 // shares of the blocks.
 struct GatherPlan {
   bool by_level;
-  int splits;
+  int splits, buffers;
   int64_t units;
   size_t smem;
 };
 
 GatherPlan gather_plan(const IndexShape &x, int blocks, int sources, int pairs, int L) {
   GatherPlan p;
-  const auto bytes = [&](int levels) {
-    return 2 * x.unit + (size_t)4 * kPairPitch * 4 + (size_t)levels * x.K * 8;
+  const auto bytes = [&](int levels, int buffers = 2) {
+    return buffers * x.unit + (size_t)4 * kPairPitch * 4 + (size_t)levels * x.K * 8;
   };
   p.units = (int64_t)sources * pairs;
-  p.by_level = L > 1 && (bytes(L) > 224 * 1024 || p.units < 148);
+  p.by_level = L > 1 && (bytes(L) > 225 * 1024 || p.units < 148);
   if (p.by_level) p.units *= L;
-  p.smem = bytes(p.by_level ? 1 : L);
+  // warps a step apart need a third unit buffer, and two levels: a step's sums
+  // and values are then not those of the step before
+  const int levels = p.by_level ? 1 : L;
+  p.buffers = levels > 1 && bytes(levels, 3) <= 226 * 1024 ? 3 : 2;
+  p.smem = bytes(levels, p.buffers);
   p.splits = 1;
   if (p.units < 148) {
     const int64_t n = 148 / p.units;
@@ -645,6 +683,7 @@ cudaError_t launch_gather(GatherArgs a, const GatherPlan &p, const DevInfo &di, 
   if (p.units > 0x7fffffff || p.smem > 226 * 1024) return cudaErrorInvalidValue;
   a.by_level = p.by_level ? 1 : 0;
   a.splits = p.splits;
+  a.buffers = p.buffers;
   a.units = (int)p.units;
   a.err = di.err;
   const void *fn = reinterpret_cast<const void *>(&codebook_gather_kernel);
