@@ -187,7 +187,7 @@ struct Layout {
   Choice how;
   size_t amax, hh, hl, wh, wl, stat, y;            // tensor-core logits and products
   size_t logits, wide, fused, fused_bytes;         // serving logits
-  size_t sid, sq, f;                               // gradients
+  size_t sid, sj, sq, f;                           // sorted lists; gradients
   size_t dz, S, dhp;                               // sums by code
   size_t zh, zl, dw, cpart, part;                  // products
   size_t total;
@@ -229,6 +229,10 @@ Layout layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
       if (total_parts(d, last, rows) > parts) parts = total_parts(d, last, rows);
     }
     x.stat = a.take((int64_t)parts * n * 8);
+    if (!x.how.serve) {
+      x.sid = a.take(n * k * 4);
+      x.sj = a.take(n * k * 4);
+    }
   } else {
     x.sid = a.take(n * k * 4);
     x.sq = a.take(n * k * 4);
@@ -289,6 +293,7 @@ GemmPlanes planes(const void *hi, const void *lo, int64_t rows, int64_t cols, in
   return p;
 }
 
+// The products' common arguments; those of the logits add their own.
 GemmArgs gemm_args(const Problem &q, const float *amax, const DevInfo &di) {
   GemmArgs g{};
   g.splits = 1;
@@ -312,40 +317,22 @@ Problem slice(const Problem &q, int64_t n0, int64_t n) {
   return p;
 }
 
-// Scales of the operands of all tokens (`x` on the tensor cores), and the
-// sparse part of the gradient of the tokens of `part` (null: a loss).
-cudaError_t begin(const Problem &all, const Layout &x, bool amax, const Problem *part,
+// Scales of the operands of all tokens (amax), and the sorted lists of the
+// tokens of `part`; of a gradient with their probabilities and weights.
+cudaError_t begin(const Problem &all, const Layout &x, bool amax, const Problem &part, bool grad,
                   const float *w, const float *part_w, void *ws, const DevInfo &di,
                   cudaStream_t s) {
   const rq_dims &d = all.d;
   return launch_loss_begin(all.h, all.bf16, (int64_t)all.N * d.D, all.C,
                            (int64_t)d.M * d.L * d.K * all.ds(), w, w ? all.N : 0,
-                           amax ? at<float>(ws, x.amax) : nullptr, part ? part->t : all.t,
-                           part ? part->N : 0, d.V, part_w, at<int32_t>(ws, x.sid),
-                           at<float>(ws, x.sq), at<float>(ws, x.f), di.err, s);
+                           amax ? at<float>(ws, x.amax) : nullptr, part.t, part.N, d.V, part_w,
+                           at<int32_t>(ws, x.sid), grad ? nullptr : at<int32_t>(ws, x.sj),
+                           grad ? at<float>(ws, x.sq) : nullptr, at<float>(ws, x.f), di.err, s);
 }
 
 cudaError_t split(const Problem &q, const Layout &x, void *ws, cudaStream_t s) {
   return launch_loss_split(q.h, q.bf16, q.N, q.d.D, x.hp, at<float>(ws, x.amax),
                            at<__half>(ws, x.hh), q.bf16 ? nullptr : at<__half>(ws, x.hl), s);
-}
-
-// The listed ids of a decoded piece; for a loss as it is, for gradients the
-// caller adds where they go.
-EntryCall entries(const Problem &q, const Layout &x, int64_t v0, int64_t rows, void *ws) {
-  EntryCall c = {};
-  c.h = q.h;
-  c.bf16 = q.bf16;
-  c.D = q.d.D;
-  c.L = q.d.L;
-  c.amax = at<float>(ws, x.amax);
-  c.wh = at<__half>(ws, x.wh);
-  c.wl = at<__half>(ws, x.wl);
-  c.pitch = x.hp;
-  c.v0 = v0;
-  c.rows = rows;
-  c.cap = q.cap;
-  return c;
 }
 
 // Piece [v0, v0 + rows) decoded.
@@ -376,18 +363,22 @@ cudaError_t for_pieces(const rq_dims &d, const Layout &x, Each &&each) {
 cudaError_t tensor_loss(const Problem &all, const Layout &x, float *loss, float *lse, void *ws,
                         const DevInfo &di, cudaStream_t s) {
   float *amax = at<float>(ws, x.amax), *y = at<float>(ws, x.y);
-  RQ_TRY(begin(all, x, true, nullptr, nullptr, nullptr, ws, di, s));
   for (int64_t n0 = 0; n0 < all.N; n0 += x.chunk) {
     const Problem q = slice(all, n0, all.N - n0 < x.chunk ? all.N - n0 : x.chunk);
     const rq_dims &d = q.d;
+    RQ_TRY(begin(all, x, n0 == 0, q, false, nullptr, nullptr, ws, di, s));
     RQ_TRY(split(q, x, ws, s));
     int part0 = 0;
     RQ_TRY(for_pieces(d, x, [&](int64_t v0, int64_t rows) {
       RQ_TRY(decode(q, x, v0, rows, ws, di, s));
-      RQ_TRY(launch_loss_entries(entries(q, x, v0, rows, ws), q.t, q.t.id, q.N, y, s));
       GemmArgs g = gemm_args(q, amax, di);
       g.rows = q.N;
       g.cols = (int)rows;
+      g.sid = at<int32_t>(ws, x.sid);
+      g.k = q.t.k;
+      g.v0 = (int)v0;
+      g.sj = at<int32_t>(ws, x.sj);
+      g.y = y;
       g.stat = at<float2>(ws, x.stat);
       g.stat_ld = (int)x.chunk;
       g.stat_part0 = part0;
@@ -413,27 +404,23 @@ cudaError_t products_grad(const Problem &all, const Layout &x, const float *lse,
     const rq_dims &d = q.d;
     const float *ql = lse + n0;
     const int splits = dh_splits(d, q.N, x.piece);
-    RQ_TRY(begin(all, x, n0 == 0, &q, w, w ? w + n0 : nullptr, ws, di, s));
+    RQ_TRY(begin(all, x, n0 == 0, q, true, w, w ? w + n0 : nullptr, ws, di, s));
     RQ_TRY(split(q, x, ws, s));
     RQ_TRY(for_pieces(d, x, [&](int64_t v0, int64_t rows) {
       RQ_TRY(decode(q, x, v0, rows, ws, di, s));
       GemmArgs g = gemm_args(q, amax, di);
       g.rows = q.N;
       g.cols = (int)rows;
+      g.sid = at<int32_t>(ws, x.sid);
+      g.k = q.t.k;
+      g.v0 = (int)v0;
+      g.sq = sq;
       g.lse = ql;
       g.f = f;
       g.dz_hi = zh;
       g.dz_lo = zl;
       g.dz_pitch = x.zp;
       RQ_TRY(launch_loss_gemm(kGemmGrad, h_planes(q, x, ws), w_planes(q, x, rows, ws), g, di, s));
-      EntryCall c = entries(q, x, v0, rows, ws);
-      c.sq = sq;
-      c.lse = ql;
-      c.f = f;
-      c.zh = zh;
-      c.zl = zl;
-      c.zpitch = x.zp;
-      RQ_TRY(launch_loss_entries(c, q.t, sid, q.N, nullptr, s));
       if (dh) {
         // a bf16 dh keeps 8 bits: the high planes' 11 on either side are
         // within a sixth of its rounding
@@ -481,7 +468,7 @@ cudaError_t sums_grad(const Problem &q, const Layout &x, const float *lse, const
   int32_t *sid = at<int32_t>(ws, x.sid);
   float *sq = at<float>(ws, x.sq), *f = at<float>(ws, x.f), *dz = at<float>(ws, x.dz);
   float *S = at<float>(ws, x.S), *dhp = dh ? at<float>(ws, x.dhp) : nullptr;
-  RQ_TRY(begin(q, x, !x.how.serve, &q, nullptr, w, ws, di, s));
+  RQ_TRY(begin(q, x, !x.how.serve, q, true, nullptr, w, ws, di, s));
   if (x.how.serve) {
     const float *y = at<float>(ws, x.logits);
     RQ_TRY(launch_loss_dz(y, q.N, d.V, lse, f, q.t.beta, q.cap, dz, x.vp, s));
@@ -494,18 +481,15 @@ cudaError_t sums_grad(const Problem &q, const Layout &x, const float *lse, const
       GemmArgs g = gemm_args(q, amax, di);
       g.rows = q.N;
       g.cols = (int)rows;
+      g.sid = at<int32_t>(ws, x.sid);
+      g.k = q.t.k;
+      g.v0 = (int)v0;
+      g.sq = sq;
       g.lse = lse;
       g.f = f;
       g.dz = dz + v0;
       g.dz_pitch = x.vp;
-      RQ_TRY(launch_loss_gemm(kGemmGrad32, h_planes(q, x, ws), w_planes(q, x, rows, ws), g, di, s));
-      EntryCall c = entries(q, x, v0, rows, ws);
-      c.sq = sq;
-      c.lse = lse;
-      c.f = f;
-      c.dz = dz;
-      c.zpitch = x.vp;
-      return launch_loss_entries(c, q.t, sid, q.N, nullptr, s);
+      return launch_loss_gemm(kGemmGrad32, h_planes(q, x, ws), w_planes(q, x, rows, ws), g, di, s);
     }));
   }
   RQ_TRY(launch_codebook_sums(dz, x.vp, q.N, index, d.V, d.M, d.L, d.K, S, di, s));

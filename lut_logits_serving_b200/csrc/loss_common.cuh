@@ -17,8 +17,10 @@ namespace rq {
 // fit half an SM's shared memory.
 constexpr int kGradRows = 8192;
 
-// Exponentials are formed in base 2: exp(x - m) = exp2(x log2 e - m log2 e).
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// Place of no id, after all others in a sorted list.
+constexpr int32_t kNoId = 0x7fffffff;
 
 // Code p of row v in any layout, safe for codes >= K (see CodeFix).
 struct CodeSrc {
@@ -130,6 +132,11 @@ struct GemmArgs {
   __half *dz_hi, *dz_lo;
   float *dz;
   int64_t dz_pitch;
+  // listed ids, ascending per row; columns are rows v0 .. of the vocabulary
+  const int32_t *sid, *sj;   // [rows][k], places in y's rows (a loss)
+  const float *sq;           // [rows][k] (gradients)
+  float *y;                  // [rows][k], their logits (a loss)
+  int k, v0;
   float *out;                // fp32 output
   int64_t out_pitch, out_split;   // row pitch; stride between splits
   int accumulate;
@@ -160,12 +167,13 @@ struct LossTargets {
   int k;
   float T, beta;
 };
-// The first launch: scales (amax null: none) and the gradient's sparse part of
-// `rows` rows: q, merged ids and f = weight T (0 for rows without a target)
+// The first launch: scales (amax null: none) and the sorted lists of `rows`
+// rows; for a gradient (sq set) merged, with q and f = weight T (0 for rows
+// without a target), for a loss with their places sj
 cudaError_t launch_loss_begin(const void *h, int bf16, int64_t nh, const float *C, int64_t nc,
                               const float *w, int64_t nw, float *amax, const LossTargets &t,
-                              int64_t rows, int64_t V, const float *weight, int32_t *sid, float *sq,
-                              float *f, unsigned *err, cudaStream_t s);
+                              int64_t rows, int64_t V, const float *weight, int32_t *sid, int32_t *sj,
+                              float *sq, float *f, unsigned *err, cudaStream_t s);
 cudaError_t launch_loss_split(const void *h, int bf16, int64_t N, int D, int64_t pitch,
                               const float *amax, __half *hi, __half *lo, cudaStream_t s);
 // lse and loss from the parts and the listed ids' logits: y[n * k + j], or, with
@@ -173,22 +181,6 @@ cudaError_t launch_loss_split(const void *h, int bf16, int64_t N, int D, int64_t
 cudaError_t launch_loss_finish(const float2 *stat, int parts, int stat_ld, int64_t N, int64_t V,
                                const LossTargets &t, const float *y, bool y_is_logits, float *loss,
                                float *lse, unsigned *err, cudaStream_t s);
-// The listed ids in a decoded piece: their logits y[n][j] (sq null), or their
-// gradients, in the piece's planes zh, zl or (dz set) in fp32 [N][zpitch].
-struct EntryCall {
-  const void *h;
-  int bf16, D, L;
-  const float *amax;
-  const __half *wh, *wl;     // the piece, rows v0 .. v0 + rows
-  int64_t pitch, v0, rows;
-  float cap;
-  const float *sq, *lse, *f;
-  __half *zh, *zl;
-  float *dz;
-  int64_t zpitch;
-};
-cudaError_t launch_loss_entries(const EntryCall &c, const LossTargets &t, const int32_t *id,
-                                int64_t N, float *y, cudaStream_t s);
 // logits [N][V] -> their gradients [N][pitch], dense part
 cudaError_t launch_loss_dz(const float *logits, int64_t N, int64_t V, const float *lse,
                            const float *f, float beta, float cap, float *dz, int64_t pitch,

@@ -2,7 +2,7 @@
 // with what it feeds:
 //
 //   kGemmStats  y = cap tanh(h E^T / cap); per row and half a tile's columns
-//               the maximum m of y / T and the sum of exp(y / T - m), base 2
+//               the maximum m of y / T and the sum of exp(y / T - m)
 //   kGemmGrad   y again; dz = w T exp(y / T - lse) (1 - (y / cap)^2), as fp16
 //               planes for the next two, or (kGemmGrad32) in fp32
 //   kGemmDh     dz E       (contraction over the rows of the vocabulary)
@@ -15,6 +15,13 @@
 // core's fp32 accumulator does not round to nearest and its error grows with
 // the chain of MMAs, so a chain has 24 to 36 of them; a finished chain is added to fp32 registers, round to nearest,
 // while the next one runs into the other half of tensor memory.
+//
+// Listed ids (targets, a teacher's lists) are served where their logits are: a
+// tile's threads find those of their row and columns by bisection in the row's
+// sorted list, write their logits (a loss) or subtract their probabilities.  A
+// logit formed anew elsewhere would differ in its last bits from the one in
+// the log-sum-exp, and 1 - p of a confident row with it (a loss of 61 such rows
+// 1.6e-6 off instead of 3e-7, its gradients 8e-6).
 //
 // One persistent CTA per SM: a copy warp (TMA tiles of 64 contraction
 // elements, 128-byte swizzle), an MMA warp (tcgen05.mma, both operands in
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const float sz = MODE != kGemmStats && MODE != kGemmGrad32 ? scale_z(g.amax, g.T) : 1.f;
     const float inv = MODE == kGemmDh ? 1.f / (sz * se) : MODE == kGemmDw ? 1.f / (sz * sh)
                                                                           : 1.f / (sh * se);
-    const float cap = g.cap, icap = g.inv_cap, beta2 = g.beta * kLog2e;
+    const float cap = g.cap, icap = g.inv_cap, beta = g.beta;
     float acc[HALF];
     int c = 0;
     for (int t = unit; t < total && !to; t += units) {
@@ -398,6 +405,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int row = (r % g.m_tiles * CG + rank) * kTM + q * 32 + lane;
       const int k0 = (int)((int64_t)g.kblocks * sp / g.splits);
       const int k1 = (int)((int64_t)g.kblocks * (sp + 1) / g.splits);
+      // the row's next listed id, as a column (looked up while the MMAs run)
+      int li = 0, next = kNoId;
+      const int32_t *list = g.sid + (int64_t)row * g.k;
+      if (LOGITS && row < g.rows) {
+        const int want = g.v0 + col0;
+        for (int hi = g.k; li < hi;) {
+          const int mid = (li + hi) >> 1;
+          if (__ldg(list + mid) < want) li = mid + 1;
+          else hi = mid;
+        }
+        if (li < g.k) next = __ldg(list + li) - g.v0;
+      }
+      auto step = [&]() { next = ++li < g.k ? __ldg(list + li) - g.v0 : kNoId; };
 #pragma unroll
       for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
       for (int ka = k0; ka < k1; ka += g.chain, ++c) {
@@ -435,15 +455,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float z = acc[j] * inv;
-            const float y = cap > 0.f ? cap * tanhf(z * icap) : z;
-            acc[j] = col0 + j0 + j < g.cols ? y * beta2 : -INFINITY;
+            acc[j] = cap > 0.f ? cap * tanhf(z * icap) : z;
+          }
+          for (; next < col0 + j0 + 16; step()) {      // listed here
+            float y = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y = col0 + j0 + j == next ? acc[j] : y;
+            const int64_t at = (int64_t)row * g.k;
+            g.y[at + __ldg(g.sj + at + li)] = y;
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            acc[j] = col0 + j0 + j < g.cols ? __fmul_rn(acc[j], beta) : -INFINITY;
             cm = fmaxf(cm, acc[j]);
           }
           const float nm = fmaxf(mx, cm);
           if (nm > -INFINITY) {
-            sum *= exp2f(mx - nm);
+            sum *= exp2f((mx - nm) * kLog2e);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sum += exp2f(acc[j] - nm);
+            for (int j = 0; j < 16; ++j) sum += exp2f((acc[j] - nm) * kLog2e);
           } else {      // no column, or NaN in all of them
 #pragma unroll
             for (int j = 0; j < 16; ++j) sum += acc[j] != acc[j] ? acc[j] : 0.f;
@@ -456,7 +486,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           g.stat[(int64_t)(g.stat_part0 + nt * 2 + half) * g.stat_ld + row] = make_float2(mx, sum);
       } else if (LOGITS) {
         const bool in = row < g.rows;
-        const float f = in ? g.f[row] : 0.f, lse2 = in ? g.lse[row] * kLog2e : 0.f, fs = f * sz;
+        const float f = in ? g.f[row] : 0.f, lse = in ? g.lse[row] : 0.f, fs = f * sz;
         const int64_t at = (int64_t)row * g.dz_pitch + col0;
 #pragma unroll 1
         for (int j0 = 0; j0 < HALF; j0 += 32) {
@@ -476,7 +506,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 y = cap * th;
                 slope = 1.f - th * th;
               }
-              x[j] = f != 0.f ? exp2f(y * beta2 - lse2) * slope * fs : 0.f;
+              x[j] = f != 0.f ? exp2f(fmaf(y, beta, -lse) * kLog2e) * slope * fs : 0.f;
+            }
+            for (; next < col0 + j0 + 16 * k + 16; step()) {      // listed here
+              float z = 0.f;
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                z = col0 + j0 + 16 * k + j == next ? acc[16 * k + j] * inv : z;
+              const float th = cap > 0.f ? tanhf(z * icap) : 0.f;
+              const float y = cap > 0.f ? cap * th : z;
+              const float p = exp2f(fmaf(y, beta, -lse) * kLog2e);
+              const float d =
+                  f != 0.f ? (p - __ldg(g.sq + (int64_t)row * g.k + li)) * (1.f - th * th) * fs : 0.f;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j] = col0 + j0 + 16 * k + j == next ? d : x[j];
             }
             if (MODE == kGemmGrad32) {
               if (in && col0 + j0 + 16 * k < g.cols) {          // the rows' pitch is 16 floats

@@ -1,7 +1,6 @@
 // loss_rows.cu -- the row-wise kernels of the losses on the RQ-coded head:
 // operand scales and fp16 splits, decoding a piece of the vocabulary for the
-// tensor cores, log-sum-exp and losses, and the listed ids' part of the logits
-// and their gradient.
+// tensor cores, log-sum-exp and losses, and the listed ids.
 //
 //   lse_n = log sum_v exp(y[n,v] / T)
 //   cross entropy  loss_n = lse_n - y[n, t_n]
@@ -9,8 +8,8 @@
 //                  loss_n = T^2 sum_j q_j (log q_j - y[n, id_j] / T + lse_n)
 //   dy[n,v] = w_n T (exp(y[n,v] / T - lse_n) - q_n[v])
 //
-// The statistics are kept in fp32 as (maximum, sum of exp) parts, base 2, that
-// are joined in a fixed order, so every result is the same from run to run.
+// The statistics are kept in fp32 as (maximum, sum of exp) parts that are
+// joined in a fixed order, so every result is the same from run to run.
 #include "loss_common.cuh"
 
 namespace rq {
@@ -52,7 +51,7 @@ __device__ __forceinline__ float abs_max(const float *x, int64_t n, int b) {
 
 // The first kernel of a call.  Blocks [0, amax_blocks): partial maxima of |h|,
 // |C| and |w| (1 without weights), kAmaxBlocks each; the blocks after those: a
-// row each of the gradient's sparse part (sparse_row).
+// row's lists each (sparse_row).
 struct BeginArgs {
   int amax_blocks;
   const void *h;
@@ -65,8 +64,8 @@ struct BeginArgs {
   float *amax;
   LossTargets t;
   int64_t V;
-  const float *weight;     // of the rows of the sparse part
-  int32_t *sid;
+  const float *weight;     // of the listed rows
+  int32_t *sid, *sj;
   float *sq, *f;
   unsigned *err;
 };
@@ -332,7 +331,7 @@ __global__ void __launch_bounds__(256) loss_split_kernel(const void *h, int bf16
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
   const float m = fmaxf(a.x, b.x);
   if (!(m > -INFINITY)) return make_float2(m, a.y + b.y);
-  return make_float2(m, a.y * exp2f(a.x - m) + b.y * exp2f(b.x - m));
+  return make_float2(m, a.y * expf(a.x - m) + b.y * expf(b.x - m));
 }
 
 constexpr int kStatCols = 2048;   // logits one block folds into a part
@@ -349,12 +348,12 @@ __global__ void __launch_bounds__(256) loss_logit_stats_kernel(const float *__re
 #pragma unroll
   for (int i = 0; i < kStatCols / 256; ++i) {
     const int64_t c = c0 + i * 256 + threadIdx.x;
-    x[i] = c < V ? logits[n * V + c] * (beta * kLog2e) : -INFINITY;
+    x[i] = c < V ? __fmul_rn(logits[n * V + c], beta) : -INFINITY;
     m = fmaxf(m, x[i]);
   }
 #pragma unroll
   for (int i = 0; i < kStatCols / 256; ++i)
-    s += m > -INFINITY ? exp2f(x[i] - m) : (x[i] != x[i] ? x[i] : 0.f);
+    s += m > -INFINITY ? expf(x[i] - m) : (x[i] != x[i] ? x[i] : 0.f);
   float2 p = make_float2(m, s);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
@@ -411,14 +410,17 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const float2 *__restr
   for (int o = 16; o > 0; o >>= 1)
     p = join(p, make_float2(__shfl_xor_sync(0xffffffffu, p.x, o),
                             __shfl_xor_sync(0xffffffffu, p.y, o)));
-  const float l = (p.x + log2f(p.y)) * kLn2;
+  // lse = p.x + ls.  A loss takes p.x - y first: where a listed logit is the
+  // maximum that is exactly 0, and a confident row's small loss keeps its bits
+  // (the listed logits are those that the statistics were made of).
+  const float ls = logf(p.y), l = p.x + ls;
   const int32_t *id = t.id + n * t.k;
   auto logit = [&](int j) { return y_is_logits ? y[n * V + id[j]] : y[n * t.k + j]; };
   float out = 0.f;
   if (t.val == nullptr) {
     if (r == 0) {
       if (id[0] >= V) atomicOr(err, RQ_DEVERR_BAD_ID);
-      if (listed(id[0], V)) out = l - logit(0);
+      if (listed(id[0], V)) out = (p.x - __fmul_rn(logit(0), t.beta)) + ls;
     }
   } else {
     const float *val = t.val + n * t.k;
@@ -437,7 +439,8 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const float2 *__restr
       for (int j = r; j < t.k; j += 32) {
         if (!listed(id[j], V)) continue;
         const float d = val[j] * t.beta - m, e = expf(d);
-        if (e > 0.f || e != e) a = fmaf(e, (d - logz) - logit(j) * t.beta + l, a);
+        if (e > 0.f || e != e)
+          a = fmaf(e, (d - logz) + ((p.x - __fmul_rn(logit(j), t.beta)) + ls), a);
       }
       out = warp_sum(a) / z * t.T * t.T;
     }
@@ -450,152 +453,90 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const float2 *__restr
 
 // ------------------------------------------------------------- gradient, sparse part
 
-// One block per row: q_j of the listed ids, an id listed twice merged into its
-// first place (so each id is corrected once, by one thread), and f = w T.
+// One block per row: its listed ids in ascending order (kNoId after them), so
+// that a tile of columns finds its own by bisection.  For a loss (sq null) sj
+// keeps their places in the list; for a gradient an id listed twice is merged
+// into one, with q_j, and f = w T.
 __device__ void sparse_row(const BeginArgs &a, int64_t n, float *lists) {
-  __shared__ float red[8], red2[8];       // lists: [k] q, [k] id
+  __shared__ float red[8], red2[8];       // lists: [k] q, [k] id, [k] counts
   const LossTargets &t = a.t;
   const int tid = threadIdx.x, k = t.k, nt = blockDim.x, warps = nt / 32;
   float *q = lists;
   int *ids = reinterpret_cast<int *>(lists + k);
   const int32_t *id = t.id + n * k;
+  const bool grad = a.sq != nullptr;
   float m = -INFINITY;
   for (int j = tid; j < k; j += nt) {
     int32_t v = id[j];
     float x = t.val ? t.val[n * k + j] * t.beta : 0.f;
-    if (v >= a.V) atomicOr(a.err, RQ_DEVERR_BAD_ID);
+    if (grad && v >= a.V) atomicOr(a.err, RQ_DEVERR_BAD_ID);
     if (!listed(v, a.V)) {
-      v = -1;
+      v = kNoId;
       x = -INFINITY;
     }
     ids[j] = v;
     q[j] = x;
     m = fmaxf(m, x);
   }
-  m = warp_max(m);
-  if ((tid & 31) == 0) red[tid >> 5] = m;
-  __syncthreads();
-  m = red[0];
-  for (int i = 1; i < warps; ++i) m = fmaxf(m, red[i]);
-  const bool some = m > -INFINITY;
+  bool some = true;
   float z = 0.f;
-  if (some)
-    for (int j = tid; j < k; j += nt) {
-      const float e = ids[j] >= 0 ? expf(q[j] - m) : 0.f;
-      q[j] = e;
-      z += e;
-    }
-  z = warp_sum(z);
-  if ((tid & 31) == 0) red2[tid >> 5] = z;
-  __syncthreads();
-  z = red2[0];
-  for (int i = 1; i < warps; ++i) z += red2[i];
-  for (int j = tid; j < k; j += nt) {
-    int v = some ? ids[j] : -1;
-    float s = 0.f;
-    if (v >= 0) {
-      for (int i = 0; i < j; ++i)
-        if (ids[i] == v) {
-          v = -1;
-          break;
-        }
-      if (v >= 0) {
-        s = q[j];
-        for (int i = j + 1; i < k; ++i)
-          if (ids[i] == v) s += q[i];
+  if (grad) {
+    m = warp_max(m);
+    if ((tid & 31) == 0) red[tid >> 5] = m;
+    __syncthreads();
+    m = red[0];
+    for (int i = 1; i < warps; ++i) m = fmaxf(m, red[i]);
+    some = m > -INFINITY;
+    if (some)
+      for (int j = tid; j < k; j += nt) {
+        const float e = ids[j] != kNoId ? expf(q[j] - m) : 0.f;
+        q[j] = e;
+        z += e;
       }
-    }
-    a.sid[n * k + j] = v;
-    a.sq[n * k + j] = v >= 0 ? s / z : 0.f;
+    z = warp_sum(z);
+    if ((tid & 31) == 0) red2[tid >> 5] = z;
+    __syncthreads();
+    z = red2[0];
+    for (int i = 1; i < warps; ++i) z += red2[i];
+  } else {
+    __syncthreads();
   }
-  if (tid == 0) a.f[n] = some ? (a.weight ? a.weight[n] : 1.f) * t.T : 0.f;
+  // an entry counts if it is valid and, of a gradient, the first of its id
+  int *counts = ids + k;
+  int total = 0;
+  for (int j0 = 0; j0 < k; j0 += nt) {
+    const int j = j0 + tid, v = j < k && some ? ids[j] : kNoId;
+    bool c = v != kNoId;
+    if (grad)
+      for (int i = 0; i < j && c; ++i) c = ids[i] != v;
+    if (j < k) counts[j] = c;
+    total += __syncthreads_count(c);
+  }
+  for (int j = tid; j < k; j += nt) {
+    if (!counts[j]) continue;
+    const int v = ids[j];
+    int at = 0;
+    float s = 0.f;
+    for (int i = 0; i < k; ++i) {
+      const int w = ids[i];
+      at += counts[i] && (w < v || (w == v && i < j));
+      if (grad && w == v) s += q[i];
+    }
+    a.sid[n * k + at] = v;
+    if (grad) a.sq[n * k + at] = s / z;
+    else a.sj[n * k + at] = j;
+  }
+  for (int j = total + tid; j < k; j += nt) {
+    a.sid[n * k + j] = kNoId;
+    if (grad) a.sq[n * k + j] = 0.f;
+  }
+  if (grad && tid == 0) a.f[n] = some ? (a.weight ? a.weight[n] : 1.f) * t.T : 0.f;
 }
 
 __device__ __forceinline__ float dz_at(float y, float q, float lse, float f, float beta,
                                        float cap) {
   const float th = cap > 0.f ? y / cap : 0.f;
-  return f != 0.f ? (expf(y * beta - lse) - q) * (1.f - th * th) * f : 0.f;
-}
-
-// The listed ids that lie in a decoded piece, one warp each: the logit from the
-// row's planes in fp32 (9 KB side by side for 2304 dims; rebuilding the row
-// from its codes gathers 384 codewords all over the codebooks, 95 us against
-// 30 for 12800 entries), then what it is for: y itself, or the corrected
-// gradient in the piece's planes or in fp32.
-struct EntryArgs {
-  const void *h;
-  int bf16, vec;         // vec: h and D allow 16-byte vectors
-  int D, k, L;
-  int64_t count, v0, rows, pitch;
-  const __half *wh, *wl;
-  const float *amax;
-  const int32_t *id;
-  float cap, beta, T;
-  float *y;              // [count]
-  const float *sq, *lse, *f;
-  __half *zh, *zl;       // [N][zpitch]
-  float *dz;             // [N][zpitch], of the whole vocabulary
-  int64_t zpitch;
-};
-
-__global__ void __launch_bounds__(256) loss_entry_kernel(const EntryArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (i >= a.count) return;
-  const int64_t v = (int64_t)a.id[i] - a.v0;
-  if (v < 0 || v >= a.rows) return;       // (an id below 0 too: v0 >= 0)
-  const int64_t n = i / a.k, hn = n * a.D;
-  const __half *wh = a.wh + v * a.pitch, *wl = a.wl + v * a.pitch;
-  float z = 0.f;
-  if (a.vec) {
-    for (int c = lane * 8; c < a.D; c += 256) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4 *>(wh + c));
-      const uint4 y = __ldg(reinterpret_cast<const uint4 *>(wl + c));
-      float h[8];
-      if (a.bf16) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(
-            static_cast<const __nv_bfloat16 *>(a.h) + hn + c));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          h[2 * j] = __uint_as_float(u[j] << 16);
-          h[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-        }
-      } else {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.h) + hn + c);
-        const float4 u = __ldg(p), w = __ldg(p + 1);
-        h[0] = u.x, h[1] = u.y, h[2] = u.z, h[3] = u.w;
-        h[4] = w.x, h[5] = w.y, h[6] = w.z, h[7] = w.w;
-      }
-      const __half2 *xh = reinterpret_cast<const __half2 *>(&x);
-      const __half2 *xl = reinterpret_cast<const __half2 *>(&y);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 p = __half22float2(xh[j]), q = __half22float2(xl[j]);
-        z = fmaf(h[2 * j], __fadd_rn(p.x, q.x), z);
-        z = fmaf(h[2 * j + 1], __fadd_rn(p.y, q.y), z);
-      }
-    }
-  } else {
-    for (int c = lane; c < a.D; c += 32)
-      z = fmaf(load_h(a.h, a.bf16, hn + c),
-               __fadd_rn(__half2float(wh[c]), __half2float(wl[c])), z);
-  }
-  z = warp_sum(z) / scale_e(a.amax, a.L);
-  const float y = softcap_f(z, a.cap);
-  if (a.sq == nullptr) {
-    if (lane == 0) a.y[i] = y;
-    return;
-  }
-  const float d = dz_at(y, a.sq[i], a.lse[n], a.f[n], a.beta, a.cap);
-  if (a.dz != nullptr) {
-    if (lane == 0) a.dz[n * a.zpitch + a.v0 + v] = d;
-    return;
-  }
-  const float sz = scale_z(a.amax, a.T);
-  if (lane == 0) split_f16(d * sz, a.zh[n * a.zpitch + v], a.zl[n * a.zpitch + v]);
+  return f != 0.f ? (expf(fmaf(y, beta, -lse)) - q) * (1.f - th * th) * f : 0.f;
 }
 
 __global__ void __launch_bounds__(256) loss_dz_kernel(const float *__restrict__ logits, int64_t V,
@@ -618,7 +559,7 @@ __global__ void __launch_bounds__(256) loss_fix_kernel(
   griddep_launch_dependents();
   griddep_wait();
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= count || sid[i] < 0) return;
+  if (i >= count || sid[i] == kNoId) return;
   const int64_t n = i / k, v = sid[i];
   dz[n * pitch + v] = dz_at(logits[n * V + v], sq[i], lse[n], f[n], beta, cap);
 }
@@ -644,8 +585,8 @@ unsigned blocks_of(int64_t n, int per) { return (unsigned)((n + per - 1) / per);
 
 cudaError_t launch_loss_begin(const void *h, int bf16, int64_t nh, const float *C, int64_t nc,
                               const float *w, int64_t nw, float *amax, const LossTargets &t,
-                              int64_t rows, int64_t V, const float *weight, int32_t *sid, float *sq,
-                              float *f, unsigned *err, cudaStream_t s) {
+                              int64_t rows, int64_t V, const float *weight, int32_t *sid, int32_t *sj,
+                              float *sq, float *f, unsigned *err, cudaStream_t s) {
   BeginArgs a;
   a.amax_blocks = amax ? 3 * kAmaxBlocks : 0;
   a.h = h;
@@ -660,11 +601,12 @@ cudaError_t launch_loss_begin(const void *h, int bf16, int64_t nh, const float *
   a.V = V;
   a.weight = weight;
   a.sid = sid;
+  a.sj = sj;
   a.sq = sq;
   a.f = f;
   a.err = err;
   return pdl_launch(loss_begin_kernel, dim3((unsigned)(a.amax_blocks + rows)), dim3(256),
-                    rows > 0 ? (size_t)t.k * 8 : 0, s, a);
+                    rows > 0 ? (size_t)t.k * 12 : 0, s, a);
 }
 
 cudaError_t launch_loss_widen_h(const void *h, int64_t n, float *out, cudaStream_t s) {
@@ -752,37 +694,6 @@ cudaError_t launch_loss_split(const void *h, int bf16, int64_t N, int D, int64_t
                               const float *amax, __half *hi, __half *lo, cudaStream_t s) {
   return pdl_launch(loss_split_kernel, dim3((unsigned)N), dim3(256), (size_t)0, s, h, bf16, D, pitch,
                     amax, hi, lo);
-}
-
-cudaError_t launch_loss_entries(const EntryCall &c, const LossTargets &t, const int32_t *id,
-                                int64_t N, float *y, cudaStream_t s) {
-  EntryArgs a = {};
-  a.h = c.h;
-  a.bf16 = c.bf16;
-  a.vec = c.D % 8 == 0 && (reinterpret_cast<uintptr_t>(c.h) & 15) == 0;
-  a.D = c.D;
-  a.k = t.k;
-  a.L = c.L;
-  a.count = N * t.k;
-  a.v0 = c.v0;
-  a.rows = c.rows;
-  a.pitch = c.pitch;
-  a.wh = c.wh;
-  a.wl = c.wl;
-  a.amax = c.amax;
-  a.id = id;
-  a.cap = c.cap;
-  a.beta = t.beta;
-  a.T = t.T;
-  a.y = y;
-  a.sq = c.sq;
-  a.lse = c.lse;
-  a.f = c.f;
-  a.zh = c.zh;
-  a.zl = c.zl;
-  a.dz = c.dz;
-  a.zpitch = c.zpitch;
-  return pdl_launch(loss_entry_kernel, dim3(blocks_of(N * t.k, 8)), dim3(256), (size_t)0, s, a);
 }
 
 int loss_stat_parts(int64_t V) { return (int)((V + kStatCols - 1) / kStatCols); }
