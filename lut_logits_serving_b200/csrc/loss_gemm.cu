@@ -48,7 +48,7 @@ namespace {
 
 constexpr int kTM = 128, kTK = 64;               // rows of a CTA, contraction block
 constexpr int kEpiWarps = 8;
-constexpr int kGemmThreads = (kEpiWarps + 2) * 32;
+constexpr int kGemmThreads = (kEpiWarps + 4) * 32;   // + copy, MMA, two idle: whole warpgroups
 constexpr int kMaxStages = 8;
 constexpr int kABytes = kTM * kTK * 2;
 // MMAs of one accumulation chain.  Errors of dC and dh against 64 bits (500
@@ -275,6 +275,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     return !to;
   };
 
+  // the accumulating warpgroups take over registers that the third does not
+  // need: 8 x 232 + 4 x 40 = 12 x 168, the launch's total
+  if (warp >= kEpiWarps) {
+    if (TN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
   if (warp == kEpiWarps) {
     // ------------------------------------------------------------ copies
     if (lane == 0) {
@@ -378,8 +382,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         atomicOr(g.err, RQ_DEVERR_TIMEOUT);
       }
     }
+  }
   } else {
     // ------------------------------------------------------------ accumulators
+    if (TN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int q = warp & 3, half = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * HALF);
     auto wait_all = [&](uint32_t bar, uint32_t parity) {
@@ -405,19 +411,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int row = (r % g.m_tiles * CG + rank) * kTM + q * 32 + lane;
       const int k0 = (int)((int64_t)g.kblocks * sp / g.splits);
       const int k1 = (int)((int64_t)g.kblocks * (sp + 1) / g.splits);
-      // the row's next listed id, as a column (looked up while the MMAs run)
+      // what the epilogue needs of the row, on its way while the MMAs run: the
+      // next listed id at or after col0, its weight and log-sum-exp
+      const bool in = row < g.rows;
       int li = 0, next = kNoId;
-      const int32_t *list = g.sid + (int64_t)row * g.k;
-      if (LOGITS && row < g.rows) {
+      float f = 0.f, lse = 0.f;
+      if (LOGITS && in) {
+        const int32_t *list = g.sid + (int64_t)row * g.k;
         const int want = g.v0 + col0;
-        for (int hi = g.k; li < hi;) {
-          const int mid = (li + hi) >> 1;
-          if (__ldg(list + mid) < want) li = mid + 1;
-          else hi = mid;
+        if (g.k > 1) {
+          for (int hi = g.k; li < hi;) {
+            const int mid = (li + hi) >> 1;
+            if (__ldg(list + mid) < want) li = mid + 1;
+            else hi = mid;
+          }
         }
-        if (li < g.k) next = __ldg(list + li) - g.v0;
+        if (li < g.k) next = __ldg(list + li);
+        if (MODE != kGemmStats) {
+          f = g.f[row];
+          lse = g.lse[row];
+        }
       }
-      auto step = [&]() { next = ++li < g.k ? __ldg(list + li) - g.v0 : kNoId; };
+      auto step = [&]() {
+        next = ++li < g.k ? __ldg(g.sid + (int64_t)row * g.k + li) - g.v0 : kNoId;
+      };
 #pragma unroll
       for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
       for (int ka = k0; ka < k1; ka += g.chain, ++c) {
@@ -444,6 +461,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
       if (to) break;
+      if (LOGITS && next != kNoId) {       // as a column (a single one may lie before col0)
+        next -= g.v0;
+        if (next < col0) next = kNoId;
+      }
       if (MODE == kGemmStats) {
         // The epilogues take 16 columns at a time from the front of the sums,
         // which then move up: registers cannot be indexed by a loop, and 128
@@ -452,21 +473,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll 1
         for (int j0 = 0; j0 < HALF; j0 += 16) {
           float cm = -INFINITY;
+          for (; next < col0 + j0 + 16; step()) {      // listed here
+            float z = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) z = col0 + j0 + j == next ? acc[j] : z;
+            z *= inv;
+            const int64_t at = (int64_t)row * g.k;
+            g.y[at + __ldg(g.sj + at + li)] = cap > 0.f ? cap * tanhf(z * icap) : z;
+          }
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float z = acc[j] * inv;
-            acc[j] = cap > 0.f ? cap * tanhf(z * icap) : z;
-          }
-          for (; next < col0 + j0 + 16; step()) {      // listed here
-            float y = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) y = col0 + j0 + j == next ? acc[j] : y;
-            const int64_t at = (int64_t)row * g.k;
-            g.y[at + __ldg(g.sj + at + li)] = y;
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            acc[j] = col0 + j0 + j < g.cols ? __fmul_rn(acc[j], beta) : -INFINITY;
+            const float y = cap > 0.f ? cap * tanhf(z * icap) : z;
+            acc[j] = col0 + j0 + j < g.cols ? __fmul_rn(y, beta) : -INFINITY;
             cm = fmaxf(cm, acc[j]);
           }
           const float nm = fmaxf(mx, cm);
@@ -482,11 +501,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
           for (int j = 0; j + 16 < HALF; ++j) acc[j] = acc[j + 16];
         }
-        if (row < g.rows)
+        if (in)
           g.stat[(int64_t)(g.stat_part0 + nt * 2 + half) * g.stat_ld + row] = make_float2(mx, sum);
       } else if (LOGITS) {
-        const bool in = row < g.rows;
-        const float f = in ? g.f[row] : 0.f, lse = in ? g.lse[row] : 0.f, fs = f * sz;
+        const float fs = f * sz;
         const int64_t at = (int64_t)row * g.dz_pitch + col0;
 #pragma unroll 1
         for (int j0 = 0; j0 < HALF; j0 += 32) {
@@ -507,19 +525,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 slope = 1.f - th * th;
               }
               x[j] = f != 0.f ? exp2f(fmaf(y, beta, -lse) * kLog2e) * slope * fs : 0.f;
-            }
-            for (; next < col0 + j0 + 16 * k + 16; step()) {      // listed here
-              float z = 0.f;
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                z = col0 + j0 + 16 * k + j == next ? acc[16 * k + j] * inv : z;
-              const float th = cap > 0.f ? tanhf(z * icap) : 0.f;
-              const float y = cap > 0.f ? cap * th : z;
-              const float p = exp2f(fmaf(y, beta, -lse) * kLog2e);
-              const float d =
-                  f != 0.f ? (p - __ldg(g.sq + (int64_t)row * g.k + li)) * (1.f - th * th) * fs : 0.f;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) x[j] = col0 + j0 + 16 * k + j == next ? d : x[j];
             }
             if (MODE == kGemmGrad32) {
               if (in && col0 + j0 + 16 * k < g.cols) {          // the rows' pitch is 16 floats
@@ -546,6 +551,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 sts16(o, hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
                 sts16(o + kStoreBytes / 2, lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
               }
+            }
+          }
+          for (; next < col0 + j0 + 32; step()) {      // listed here: p - q instead
+            const int c = next - col0 - j0;
+            float z = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z = c == j ? acc[j] : z;
+            z *= inv;
+            const float th = cap > 0.f ? tanhf(z * icap) : 0.f;
+            const float p = exp2f(fmaf(cap > 0.f ? cap * th : z, beta, -lse) * kLog2e);
+            const float d =
+                f != 0.f ? (p - __ldg(g.sq + (int64_t)row * g.k + li)) * (1.f - th * th) * fs : 0.f;
+            if (MODE == kGemmGrad32) {
+              g.dz[at + j0 + c] = d;
+            } else {
+              __half dh, dl;
+              split_f16(d, dh, dl);
+              const uint32_t o = staging + (uint32_t)(half * kStoreBytes + (q * 32 + lane) * 64) +
+                                 ((((uint32_t)c >> 3) ^ ((uint32_t)(lane >> 1) & 3u)) << 4) +
+                                 ((uint32_t)c & 7u) * 2;
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(o), "h"(__half_as_ushort(dh)) : "memory");
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(o + kStoreBytes / 2),
+                           "h"(__half_as_ushort(dl))
+                           : "memory");
             }
           }
           if (STAGED) {
@@ -585,7 +614,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             store_commit();
           }
         }
-      } else if (row < g.rows) {
+      } else if (in) {
         float *o = g.out + (int64_t)sp * g.out_split + (int64_t)row * g.out_pitch + col0;
 #pragma unroll
         for (int j = 0; j < HALF; j += 8) {
