@@ -13,8 +13,9 @@
 // tensor-core products, a_hi b_hi + a_lo b_hi + a_hi b_lo (two where one
 // operand is bf16, which a scaled fp16 plane holds exactly).  The tensor
 // core's fp32 accumulator does not round to nearest and its error grows with
-// the chain of MMAs, so a chain has 24 to 36 of them; a finished chain is added to fp32 registers, round to nearest,
-// while the next one runs into the other half of tensor memory.
+// the chain of MMAs, so a chain has 12 to 36 of them; a finished chain is
+// added to fp32 registers, round to nearest, while the next one runs into the
+// other half of tensor memory.
 //
 // Listed ids (targets, a teacher's lists) are served where their logits are: a
 // tile's threads find those of their row and columns by bisection in the row's
@@ -54,8 +55,10 @@ constexpr int kABytes = kTM * kTK * 2;
 // MMAs of one accumulation chain.  Errors of dC and dh against 64 bits (500
 // fp32 tokens, 256000 rows): chains of 48 1.4e-6 and 1.4e-6, of 24 7.8e-7 and
 // 8.0e-7, for 5 to 8 % of a step's time; an fp32 library product leaves 8.4e-7
-// and 1.6e-6.  So the sums that only pass through one product get longer ones.
-constexpr int kChainMmas = 36, kChainMmasDw = 24;
+// and 1.6e-6.  So the sums that only pass through one product get longer ones,
+// and short contractions (up to 4 blocks, where nothing is left to overlap)
+// the shortest.
+constexpr int kChainMmas = 36, kChainMmasDw = 24, kChainMmasShort = 12;
 constexpr size_t kGemmSmemMax = 226 * 1024;      // 227 KB less the static part
 constexpr int kStoreBytes = 16384;               // a warpgroup's outgoing 128 rows x 128 bytes
 constexpr size_t kGemmSmemTail = 1024 + 256;     // alignment slack, barriers
@@ -193,6 +196,16 @@ __device__ __forceinline__ void async_fence() {
 __device__ __forceinline__ void group_sync(int id) {     // the 128 threads of a warpgroup
   asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
 }
+__device__ __forceinline__ bool group_any(int id, bool x) {   // of them, whether any has x
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id)
+      : "memory");
+  return r != 0;
+}
 
 __device__ __forceinline__ void wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
@@ -279,110 +292,110 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   // need: 8 x 232 + 4 x 40 = 12 x 168, the launch's total
   if (warp >= kEpiWarps) {
     if (TN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-  if (warp == kEpiWarps) {
-    // ------------------------------------------------------------ copies
-    if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_last();
-      int it = 0;
-      for (int t = unit; t < total && !abort_flag; t += units) {
-        const int sp = t / mn, r = t % mn;
-        const int n0 = r / g.m_tiles * TN + rank * BN;
-        const int m0 = (r % g.m_tiles * CG + rank) * kTM;
-        const int k0 = (int)((int64_t)g.kblocks * sp / g.splits);
-        const int k1 = (int)((int64_t)g.kblocks * (sp + 1) / g.splits);
-        for (int k = k0; k < k1; ++k, ++it) {
-          const int st = it % g.stages;
-          if (!wait(empty(st), ((uint32_t)(it / g.stages) & 1u) ^ 1u)) break;
-          // a pair's first CTA expects both CTAs' bytes
-          if (rank == 0) mbar_arrive_expect_tx(full(st), stage_bytes * CG);
-          uint32_t dst = base + (uint32_t)st * stage_bytes;
-          for (int p = 0; p < g.a_planes; ++p, dst += kABytes) {
-            const CUtensorMap *map = p ? &a_lo : &a_hi;
-            if (A_MN) {
-#pragma unroll
-              for (int i = 0; i < kTM / 64; ++i)
-                load_tile<CG>(dst + i * 8192, map, m0 + i * 64, k * kTK, full(st), pol);
-            } else {
-              load_tile<CG>(dst, map, k * kTK, m0, full(st), pol);
-            }
-          }
-          for (int p = 0; p < g.b_planes; ++p, dst += B_BYTES) {
-            const CUtensorMap *map = p ? &b_lo : &b_hi;
-            if (B_MN) {
-#pragma unroll
-              for (int i = 0; i < BN / 64; ++i)
-                load_tile<CG>(dst + i * 8192, map, n0 + i * 64, k * kTK, full(st), pol);
-            } else {
-              load_tile<CG>(dst, map, k * kTK, n0, full(st), pol);
-            }
-          }
-        }
-        if (to) break;
-      }
-      if (abort_flag) {
-        // the copies in flight land before the shared memory goes: a
-        // millisecond, as a pair's second CTA has no barrier to wait on
-        const long long t0 = clock64();
-        while (clock64() - t0 < 2000000) {
-        }
-        atomicOr(g.err, RQ_DEVERR_TIMEOUT);
-      }
-    }
-  } else if (warp == kEpiWarps + 1) {
-    // ------------------------------------------------------------ MMA issue
-    if (lane == 0 && rank == 0) {
-      const uint32_t idesc = (1u << 4) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
-                             ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(kTM * CG >> 4) << 24);
-      // 16 contraction elements further: 32 bytes along a K-major row, 16
-      // rows of 128 bytes in an MN-major tile (in descriptor units of 16 B)
-      constexpr uint32_t a_step = A_MN ? 2048 / 16 : 32 / 16, b_step = B_MN ? 2048 / 16 : 32 / 16;
-      int it = 0, c = 0;
-      for (int t = unit; t < total && !abort_flag; t += units) {
-        const int sp = t / mn;
-        const int k0 = (int)((int64_t)g.kblocks * sp / g.splits);
-        const int k1 = (int)((int64_t)g.kblocks * (sp + 1) / g.splits);
-        for (int ka = k0; ka < k1; ka += g.chain, ++c) {
-          if (!wait(tempty(c & 1), ((uint32_t)(c >> 1) & 1u) ^ 1u)) break;
-          tc_after();
-          const uint32_t d = tmem + (uint32_t)(c & 1) * TN;
-          const int kb = ka + g.chain < k1 ? ka + g.chain : k1;
-          for (int k = ka; k < kb; ++k, ++it) {
+    if (warp == kEpiWarps) {
+      // ------------------------------------------------------------ copies
+      if (lane == 0) {
+        const uint64_t pol = l2_policy_evict_last();
+        int it = 0;
+        for (int t = unit; t < total && !abort_flag; t += units) {
+          const int sp = t / mn, r = t % mn;
+          const int n0 = r / g.m_tiles * TN + rank * BN;
+          const int m0 = (r % g.m_tiles * CG + rank) * kTM;
+          const int k0 = (int)((int64_t)g.kblocks * sp / g.splits);
+          const int k1 = (int)((int64_t)g.kblocks * (sp + 1) / g.splits);
+          for (int k = k0; k < k1; ++k, ++it) {
             const int st = it % g.stages;
-            if (!wait(full(st), (uint32_t)(it / g.stages) & 1u)) break;
-            tc_after();
-            const uint32_t sa = base + (uint32_t)st * stage_bytes;
-            const uint32_t sb = sa + (uint32_t)g.a_planes * kABytes;
-            const uint64_t ah = sw128_desc(sa, A_MN ? 8192 : 16);
-            const uint64_t bh = sw128_desc(sb, B_MN ? 8192 : 16);
-            const uint64_t al = ah + kABytes / 16, bl = bh + B_BYTES / 16;
+            if (!wait(empty(st), ((uint32_t)(it / g.stages) & 1u) ^ 1u)) break;
+            // a pair's first CTA expects both CTAs' bytes
+            if (rank == 0) mbar_arrive_expect_tx(full(st), stage_bytes * CG);
+            uint32_t dst = base + (uint32_t)st * stage_bytes;
+            for (int p = 0; p < g.a_planes; ++p, dst += kABytes) {
+              const CUtensorMap *map = p ? &a_lo : &a_hi;
+              if (A_MN) {
 #pragma unroll
-            for (int j = 0; j < kTK / 16; ++j)
-              mma_f16_ss<CG>(d, ah + j * a_step, bh + j * b_step, idesc, k > ka || j > 0);
-            if (g.a_planes > 1) {
-#pragma unroll
-              for (int j = 0; j < kTK / 16; ++j)
-                mma_f16_ss<CG>(d, al + j * a_step, bh + j * b_step, idesc, 1u);
+                for (int i = 0; i < kTM / 64; ++i)
+                  load_tile<CG>(dst + i * 8192, map, m0 + i * 64, k * kTK, full(st), pol);
+              } else {
+                load_tile<CG>(dst, map, k * kTK, m0, full(st), pol);
+              }
             }
-            if (g.b_planes > 1) {
+            for (int p = 0; p < g.b_planes; ++p, dst += B_BYTES) {
+              const CUtensorMap *map = p ? &b_lo : &b_hi;
+              if (B_MN) {
 #pragma unroll
-              for (int j = 0; j < kTK / 16; ++j)
-                mma_f16_ss<CG>(d, ah + j * a_step, bl + j * b_step, idesc, 1u);
+                for (int i = 0; i < BN / 64; ++i)
+                  load_tile<CG>(dst + i * 8192, map, n0 + i * 64, k * kTK, full(st), pol);
+              } else {
+                load_tile<CG>(dst, map, k * kTK, n0, full(st), pol);
+              }
             }
-            tc_commit<CG>(empty(st));
           }
           if (to) break;
-          tc_commit<CG>(tfull(c & 1));
         }
-        if (to) break;
+        if (abort_flag) {
+          // the copies in flight land before the shared memory goes: a
+          // millisecond, as a pair's second CTA has no barrier to wait on
+          const long long t0 = clock64();
+          while (clock64() - t0 < 2000000) {
+          }
+          atomicOr(g.err, RQ_DEVERR_TIMEOUT);
+        }
       }
-      if (abort_flag) {
-        // the MMAs in flight end before the tensor memory goes
-        if (it > 0)
-          mbar_wait_bounded(empty((it - 1) % g.stages), (uint32_t)((it - 1) / g.stages) & 1u);
-        atomicOr(g.err, RQ_DEVERR_TIMEOUT);
+    } else if (warp == kEpiWarps + 1) {
+      // ------------------------------------------------------------ MMA issue
+      if (lane == 0 && rank == 0) {
+        const uint32_t idesc = (1u << 4) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
+                               ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(kTM * CG >> 4) << 24);
+        // 16 contraction elements further: 32 bytes along a K-major row, 16
+        // rows of 128 bytes in an MN-major tile (in descriptor units of 16 B)
+        constexpr uint32_t a_step = A_MN ? 2048 / 16 : 32 / 16, b_step = B_MN ? 2048 / 16 : 32 / 16;
+        int it = 0, c = 0;
+        for (int t = unit; t < total && !abort_flag; t += units) {
+          const int sp = t / mn;
+          const int k0 = (int)((int64_t)g.kblocks * sp / g.splits);
+          const int k1 = (int)((int64_t)g.kblocks * (sp + 1) / g.splits);
+          for (int ka = k0; ka < k1; ka += g.chain, ++c) {
+            if (!wait(tempty(c & 1), ((uint32_t)(c >> 1) & 1u) ^ 1u)) break;
+            tc_after();
+            const uint32_t d = tmem + (uint32_t)(c & 1) * TN;
+            const int kb = ka + g.chain < k1 ? ka + g.chain : k1;
+            for (int k = ka; k < kb; ++k, ++it) {
+              const int st = it % g.stages;
+              if (!wait(full(st), (uint32_t)(it / g.stages) & 1u)) break;
+              tc_after();
+              const uint32_t sa = base + (uint32_t)st * stage_bytes;
+              const uint32_t sb = sa + (uint32_t)g.a_planes * kABytes;
+              const uint64_t ah = sw128_desc(sa, A_MN ? 8192 : 16);
+              const uint64_t bh = sw128_desc(sb, B_MN ? 8192 : 16);
+              const uint64_t al = ah + kABytes / 16, bl = bh + B_BYTES / 16;
+#pragma unroll
+              for (int j = 0; j < kTK / 16; ++j)
+                mma_f16_ss<CG>(d, ah + j * a_step, bh + j * b_step, idesc, k > ka || j > 0);
+              if (g.a_planes > 1) {
+#pragma unroll
+                for (int j = 0; j < kTK / 16; ++j)
+                  mma_f16_ss<CG>(d, al + j * a_step, bh + j * b_step, idesc, 1u);
+              }
+              if (g.b_planes > 1) {
+#pragma unroll
+                for (int j = 0; j < kTK / 16; ++j)
+                  mma_f16_ss<CG>(d, ah + j * a_step, bl + j * b_step, idesc, 1u);
+              }
+              tc_commit<CG>(empty(st));
+            }
+            if (to) break;
+            tc_commit<CG>(tfull(c & 1));
+          }
+          if (to) break;
+        }
+        if (abort_flag) {
+          // the MMAs in flight end before the tensor memory goes
+          if (it > 0)
+            mbar_wait_bounded(empty((it - 1) % g.stages), (uint32_t)((it - 1) / g.stages) & 1u);
+          atomicOr(g.err, RQ_DEVERR_TIMEOUT);
+        }
       }
     }
-  }
   } else {
     // ------------------------------------------------------------ accumulators
     if (TN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
@@ -460,6 +473,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           else arrive(tempty(c & 1));
         }
       }
+      // a warp that gave up would leave the others waiting at the group's barriers
+      if (STAGED) to = group_any(1 + half, to);
       if (to) break;
       if (LOGITS && next != kNoId) {       // as a column (a single one may lie before col0)
         next -= g.v0;
@@ -694,11 +709,11 @@ cudaError_t launch_tile(const GemmPlanes &A, const GemmPlanes &B, GemmArgs a, co
   const int64_t k = A_MN ? A.rows : A.cols;
   a.a_planes = A.lo ? 2 : 1;
   a.b_planes = B.lo ? 2 : 1;
-  a.chain = (MODE == kGemmDw ? kChainMmasDw : kChainMmas) /
-            (kTK / 16 * (a.a_planes + a.b_planes - 1));
   a.m_tiles = (int)(((A_MN ? A.cols : A.rows) + kTM * CG - 1) / (kTM * CG));
   a.n_tiles = (int)(((B_MN ? B.cols : B.rows) + TN - 1) / TN);
   a.kblocks = (int)((k + kTK - 1) / kTK);
+  const int mmas = a.kblocks <= 4 ? kChainMmasShort : MODE == kGemmDw ? kChainMmasDw : kChainMmas;
+  a.chain = mmas / (kTK / 16 * (a.a_planes + a.b_planes - 1));
   if (a.splits > a.kblocks) a.splits = a.kblocks;
   CUtensorMap oh = ah, ol = ah;
   if (MODE == kGemmGrad &&
