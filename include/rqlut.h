@@ -431,9 +431,10 @@ RQ_API int rq_prepare_rot10(const uint16_t *codes_u16, rq_dims d, uint8_t *out,
  * may be listed twice).  An id below 0 stands for none (padding, masked
  * tokens, short lists), so does a teacher's logit of -inf; an id >= V is
  * taken for none and sets RQ_DEVERR_BAD_ID.  A row with no entry left has
- * loss 0 and no gradient; its lse is written all the same.  Hidden states,
- * codebooks, weights and teacher's logits are finite otherwise (a NaN gives
- * NaN in the rows it reaches).
+ * loss 0 and no gradient; its lse is written all the same, and whatever its
+ * hidden state, weight and lse hold reaches no other row, dh or dC.  Hidden
+ * states, codebooks, weights and teacher's logits are finite otherwise (a NaN
+ * gives NaN in the rows it reaches, and in dC).
  *   h       (device) [N][D]: float, or bf16 bit patterns with h_bf16 = 1
  *   C, codes, fmt, d, softcap: as for rq_logits_from_hidden, every layout
  *   target  (device) int32 [N]; teacher_val (device) float [N][k] and
@@ -450,9 +451,9 @@ RQ_API int rq_prepare_rot10(const uint16_t *codes_u16, rq_dims d, uint8_t *out,
  *           cross entropy; grad = 1: enough for the gradient and the loss)
  * Precision: losses, statistics and sums are fp32; for more than a few tokens
  * the products run on the tensor cores on fp16 hi / lo splits with
- * power-of-two scales (about 2^-22 per product).  dC and, for float h, dh
- * carry fp32 accuracy; a bf16 dh is rounded once.  Sums run in a fixed order:
- * the same call gives the same bits.
+ * power-of-two scales, a token's its own (about 2^-22 per product).  dC and,
+ * for float h, dh carry fp32 accuracy; a bf16 dh is rounded once.  Sums run in
+ * a fixed order: the same call gives the same bits.
  * Errors: RQ_ERR_INVALID_ARGUMENT (null pointer, N < 1, k, T or h_bf16 out of
  * range, bad dims or format), RQ_ERR_UNSUPPORTED (the format cannot hold the
  * shape, k > 1024; gradients: K > 4096), RQ_ERR_MISALIGNED,

@@ -185,11 +185,11 @@ Choice choose(const rq_dims &d, int N, int fmt, bool grad) {
 
 struct Layout {
   Choice how;
-  size_t amax, hh, hl, wh, wl, stat, y;            // tensor-core logits and products
+  size_t amax, sh, hh, hl, wh, wl, stat, y;        // tensor-core logits and products
   size_t logits, wide, fused, fused_bytes;         // serving logits
   size_t sid, sj, sq, f;                           // sorted lists; gradients
   size_t dz, S, dhp;                               // sums by code
-  size_t zh, zl, dw, cpart, part;                  // products
+  size_t hw, gh, gl, zh, zl, dw, cpart, part;      // products
   size_t total;
   int64_t hp, zp, vp;  // row pitches: D, the piece's rows, V
   int64_t chunk;       // tokens per sweep
@@ -210,7 +210,8 @@ Layout layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
   x.zp = pitch16(rows);
   x.vp = pitch16(d.V);
   if (!x.how.serve) {
-    x.amax = a.take(3 * kAmaxBlocks * 4);
+    x.amax = a.take((kAmaxBlocks + 1) * 4);
+    x.sh = a.take(n * 4);
     x.hh = a.take(n * x.hp * 2);
     x.hl = a.take(n * x.hp * 2);
     x.wh = a.take(rows * x.hp * 2);
@@ -243,6 +244,9 @@ Layout layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
       x.S = a.take((int64_t)(N + 1) / 2 * x.splits * P * d.K * 8);
       x.dhp = a.take((int64_t)P * N * ds * 4);
     } else {
+      x.hw = a.take(n * 4);
+      x.gh = a.take(n * x.hp * 2);
+      x.gl = a.take(n * x.hp * 2);
       x.zh = a.take(n * x.zp * 2);
       x.zl = a.take(n * x.zp * 2);
       x.dw = a.take((int64_t)d.D * x.zp * 4);
@@ -294,15 +298,15 @@ GemmPlanes planes(const void *hi, const void *lo, int64_t rows, int64_t cols, in
 }
 
 // The products' common arguments; those of the logits add their own.
-GemmArgs gemm_args(const Problem &q, const float *amax, const DevInfo &di) {
+GemmArgs gemm_args(const Problem &q, const Layout &x, void *ws, const DevInfo &di) {
   GemmArgs g{};
   g.splits = 1;
-  g.amax = amax;
+  g.amax = at<float>(ws, x.amax);
+  g.sh = at<float>(ws, x.sh);
   g.L = q.d.L;
   g.cap = q.cap;
   g.inv_cap = q.cap > 0.f ? 1.f / q.cap : 0.f;
   g.beta = q.t.beta;
-  g.T = q.t.T;
   g.err = di.err;
   return g;
 }
@@ -317,22 +321,51 @@ Problem slice(const Problem &q, int64_t n0, int64_t n) {
   return p;
 }
 
-// Scales of the operands of all tokens (amax), and the sorted lists of the
-// tokens of `part`; of a gradient with their probabilities and weights.
-cudaError_t begin(const Problem &all, const Layout &x, bool amax, const Problem &part, bool grad,
-                  const float *w, const float *part_w, void *ws, const DevInfo &di,
-                  cudaStream_t s) {
-  const rq_dims &d = all.d;
-  return launch_loss_begin(all.h, all.bf16, (int64_t)all.N * d.D, all.C,
-                           (int64_t)d.M * d.L * d.K * all.ds(), w, w ? all.N : 0,
-                           amax ? at<float>(ws, x.amax) : nullptr, part.t, part.N, d.V, part_w,
-                           at<int32_t>(ws, x.sid), grad ? nullptr : at<int32_t>(ws, x.sj),
-                           grad ? at<float>(ws, x.sq) : nullptr, at<float>(ws, x.f), di.err, s);
+// The sorted lists of a sweep's tokens, of a gradient with their probabilities
+// and weights, and (`scales`) the scales of the tensor cores' operands; those of
+// the codebooks with the first sweep.
+cudaError_t begin(const Problem &q, const Layout &x, bool scales, bool first, bool grad,
+                  const float *w, void *ws, const DevInfo &di, cudaStream_t s) {
+  BeginArgs a{};
+  a.C = q.C;
+  a.nc = (int64_t)q.d.M * q.d.L * q.d.K * q.ds();
+  a.amax = scales && first ? at<float>(ws, x.amax) : nullptr;
+  a.h = q.h;
+  a.bf16 = q.bf16;
+  a.D = q.d.D;
+  a.sh = scales ? at<float>(ws, x.sh) : nullptr;
+  a.hw = grad && !x.how.sums ? at<float>(ws, x.hw) : nullptr;
+  a.t = q.t;
+  a.rows = q.N;
+  a.V = q.d.V;
+  a.weight = w;
+  a.sid = at<int32_t>(ws, x.sid);
+  a.sj = grad ? nullptr : at<int32_t>(ws, x.sj);
+  a.sq = grad ? at<float>(ws, x.sq) : nullptr;
+  a.f = grad ? at<float>(ws, x.f) : nullptr;
+  a.err = di.err;
+  return launch_loss_begin(a, s);
 }
 
-cudaError_t split(const Problem &q, const Layout &x, void *ws, cudaStream_t s) {
-  return launch_loss_split(q.h, q.bf16, q.N, q.d.D, x.hp, at<float>(ws, x.amax),
-                           at<__half>(ws, x.hh), q.bf16 ? nullptr : at<__half>(ws, x.hl), s);
+// The hidden states as planes, with `dw` also as h^T dz takes them.
+cudaError_t split(const Problem &q, const Layout &x, bool dw, void *ws, cudaStream_t s) {
+  SplitArgs a{};
+  a.h = q.h;
+  a.bf16 = q.bf16;
+  a.N = q.N;
+  a.D = q.d.D;
+  a.pitch = x.hp;
+  a.sh = at<float>(ws, x.sh);
+  a.hi = at<__half>(ws, x.hh);
+  a.lo = q.bf16 ? nullptr : at<__half>(ws, x.hl);
+  if (dw) {
+    a.hw = at<float>(ws, x.hw);
+    a.f = at<float>(ws, x.f);
+    a.sdw = at<float>(ws, x.amax) + kAmaxBlocks;
+    a.dhi = at<__half>(ws, x.gh);
+    a.dlo = q.bf16 ? nullptr : at<__half>(ws, x.gl);
+  }
+  return launch_loss_split(a, s);
 }
 
 // Piece [v0, v0 + rows) decoded.
@@ -362,16 +395,16 @@ cudaError_t for_pieces(const rq_dims &d, const Layout &x, Each &&each) {
 
 cudaError_t tensor_loss(const Problem &all, const Layout &x, float *loss, float *lse, void *ws,
                         const DevInfo &di, cudaStream_t s) {
-  float *amax = at<float>(ws, x.amax), *y = at<float>(ws, x.y);
+  float *y = at<float>(ws, x.y);
   for (int64_t n0 = 0; n0 < all.N; n0 += x.chunk) {
     const Problem q = slice(all, n0, all.N - n0 < x.chunk ? all.N - n0 : x.chunk);
     const rq_dims &d = q.d;
-    RQ_TRY(begin(all, x, n0 == 0, q, false, nullptr, nullptr, ws, di, s));
-    RQ_TRY(split(q, x, ws, s));
+    RQ_TRY(begin(q, x, true, n0 == 0, false, nullptr, ws, di, s));
+    RQ_TRY(split(q, x, false, ws, s));
     int part0 = 0;
     RQ_TRY(for_pieces(d, x, [&](int64_t v0, int64_t rows) {
       RQ_TRY(decode(q, x, v0, rows, ws, di, s));
-      GemmArgs g = gemm_args(q, amax, di);
+      GemmArgs g = gemm_args(q, x, ws, di);
       g.rows = q.N;
       g.cols = (int)rows;
       g.sid = at<int32_t>(ws, x.sid);
@@ -394,7 +427,7 @@ cudaError_t tensor_loss(const Problem &all, const Layout &x, float *loss, float 
 cudaError_t products_grad(const Problem &all, const Layout &x, const float *lse, const float *w,
                           const void *index, void *dh, float *dC, void *ws, const DevInfo &di,
                           cudaStream_t s) {
-  float *amax = at<float>(ws, x.amax), *f = at<float>(ws, x.f);
+  float *f = at<float>(ws, x.f);
   __half *zh = at<__half>(ws, x.zh), *zl = at<__half>(ws, x.zl);
   int32_t *sid = at<int32_t>(ws, x.sid);
   float *sq = at<float>(ws, x.sq);
@@ -404,11 +437,11 @@ cudaError_t products_grad(const Problem &all, const Layout &x, const float *lse,
     const rq_dims &d = q.d;
     const float *ql = lse + n0;
     const int splits = dh_splits(d, q.N, x.piece);
-    RQ_TRY(begin(all, x, n0 == 0, q, true, w, w ? w + n0 : nullptr, ws, di, s));
-    RQ_TRY(split(q, x, ws, s));
+    RQ_TRY(begin(q, x, true, n0 == 0, true, w ? w + n0 : nullptr, ws, di, s));
+    RQ_TRY(split(q, x, dC != nullptr, ws, s));
     RQ_TRY(for_pieces(d, x, [&](int64_t v0, int64_t rows) {
       RQ_TRY(decode(q, x, v0, rows, ws, di, s));
-      GemmArgs g = gemm_args(q, amax, di);
+      GemmArgs g = gemm_args(q, x, ws, di);
       g.rows = q.N;
       g.cols = (int)rows;
       g.sid = at<int32_t>(ws, x.sid);
@@ -424,10 +457,11 @@ cudaError_t products_grad(const Problem &all, const Layout &x, const float *lse,
       if (dh) {
         // a bf16 dh keeps 8 bits: the high planes' 11 on either side are
         // within a sixth of its rounding
-        GemmArgs p = gemm_args(q, amax, di);
+        GemmArgs p = gemm_args(q, x, ws, di);
         p.splits = splits;
         p.rows = q.N;
         p.cols = d.D;
+        p.f = f;
         p.out = at<float>(ws, x.part);
         p.out_pitch = x.hp;
         p.out_split = q.N * x.hp;
@@ -438,13 +472,15 @@ cudaError_t products_grad(const Problem &all, const Layout &x, const float *lse,
             di, s));
       }
       if (dC) {
-        GemmArgs p = gemm_args(q, amax, di);
+        GemmArgs p = gemm_args(q, x, ws, di);
         p.rows = d.D;
         p.cols = (int)rows;
         p.out = at<float>(ws, x.dw);
         p.out_pitch = x.zp;
-        RQ_TRY(launch_loss_gemm(kGemmDw, h_planes(q, x, ws), planes(zh, zl, q.N, rows, x.zp), p, di,
-                                s));
+        RQ_TRY(launch_loss_gemm(
+            kGemmDw,
+            planes(at<void>(ws, x.gh), q.bf16 ? nullptr : at<void>(ws, x.gl), q.N, d.D, x.hp),
+            planes(zh, zl, q.N, rows, x.zp), p, di, s));
         RQ_TRY(launch_codebook_rows(at<float>(ws, x.dw), x.zp, v0, rows, index, d.V, d.M, d.L, d.K,
                                     q.ds(), x.splits, n0 > 0 || v0 > 0,
                                     x.splits > 1 ? at<float>(ws, x.cpart) : dC, di, s));
@@ -468,17 +504,16 @@ cudaError_t sums_grad(const Problem &q, const Layout &x, const float *lse, const
   int32_t *sid = at<int32_t>(ws, x.sid);
   float *sq = at<float>(ws, x.sq), *f = at<float>(ws, x.f), *dz = at<float>(ws, x.dz);
   float *S = at<float>(ws, x.S), *dhp = dh ? at<float>(ws, x.dhp) : nullptr;
-  RQ_TRY(begin(q, x, !x.how.serve, q, true, nullptr, w, ws, di, s));
+  RQ_TRY(begin(q, x, !x.how.serve, true, true, w, ws, di, s));
   if (x.how.serve) {
     const float *y = at<float>(ws, x.logits);
     RQ_TRY(launch_loss_dz(y, q.N, d.V, lse, f, q.t.beta, q.cap, dz, x.vp, s));
     RQ_TRY(launch_loss_fix(sid, sq, y, q.t.k, q.N, d.V, lse, f, q.t.beta, q.cap, dz, x.vp, s));
   } else {
-    const float *amax = at<float>(ws, x.amax);
-    RQ_TRY(split(q, x, ws, s));
+    RQ_TRY(split(q, x, false, ws, s));
     RQ_TRY(for_pieces(d, x, [&](int64_t v0, int64_t rows) {
       RQ_TRY(decode(q, x, v0, rows, ws, di, s));
-      GemmArgs g = gemm_args(q, amax, di);
+      GemmArgs g = gemm_args(q, x, ws, di);
       g.rows = q.N;
       g.cols = (int)rows;
       g.sid = at<int32_t>(ws, x.sid);
@@ -493,7 +528,7 @@ cudaError_t sums_grad(const Problem &q, const Layout &x, const float *lse, const
     }));
   }
   RQ_TRY(launch_codebook_sums(dz, x.vp, q.N, index, d.V, d.M, d.L, d.K, S, di, s));
-  RQ_TRY(launch_codebook_finish(S, x.splits, q.h, q.bf16, q.N, q.C, d.D, d.M, d.L, d.K, dC, dhp, s));
+  RQ_TRY(launch_codebook_finish(S, x.splits, q.h, q.bf16, q.N, f, q.C, d.D, d.M, d.L, d.K, dC, dhp, s));
   if (dh) RQ_TRY(launch_codebook_dh(dhp, q.N, d.D, d.M, d.L, q.bf16, dh, s));
   return cudaSuccess;
 }

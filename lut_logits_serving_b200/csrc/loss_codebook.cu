@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
       ok = false;
       abort_flag = 1;
     }
+    ok = __all_sync(0xffffffffu, ok);      // a warp works as a whole or not at all
   };
   for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
     GatherUnit q;
@@ -533,14 +534,15 @@ constexpr int kFinTokens = 4;        // tokens whose sums a thread holds at once
 
 __global__ void __launch_bounds__(kFinThreads) codebook_finish_kernel(
     const float *__restrict__ S, int splits, const void *h, int bf16, int nt,
-    const float *__restrict__ C, int D, int L, int K, int P, int ds, float *dC, float *dhp) {
+    const float *__restrict__ f, const float *__restrict__ C, int D, int L, int K, int P, int ds, float *dC, float *dhp) {
   griddep_launch_dependents();
   griddep_wait();
   extern __shared__ float fin[];     // [nt][ds] hidden slices, [8][kFinTokens][ds] partials
   const int p = blockIdx.x, m = p / L, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float *part = fin + nt * ds;
-  for (int i = tid; i < nt * ds; i += kFinThreads)
-    fin[i] = load_h(h, bf16, (int64_t)(i / ds) * D + (int64_t)m * ds + i % ds);
+  for (int i = tid; i < nt * ds; i += kFinThreads)      // (padding may hold anything)
+    fin[i] = f[i / ds] != 0.f ? load_h(h, bf16, (int64_t)(i / ds) * D + (int64_t)m * ds + i % ds)
+                              : 0.f;
   __syncthreads();
   const int64_t pair = (int64_t)splits * P * K * 2;
   for (int t0 = 0; t0 < nt; t0 += kFinTokens) {
@@ -761,11 +763,12 @@ cudaError_t launch_codebook_sums(const float *dz, int64_t pitch, int N, const vo
 }
 
 cudaError_t launch_codebook_finish(const float *S, int splits, const void *h, int bf16, int N,
-                                   const float *C, int D, int M, int L, int K, float *dC,
-                                   float *dhp, cudaStream_t s) {
+                                   const float *f, const float *C, int D, int M, int L, int K,
+                                   float *dC, float *dhp, cudaStream_t s) {
   const int ds = D / M, P = M * L;
   const size_t smem = (size_t)(N + kFinThreads / 32 * kFinTokens) * ds * 4;
-  return pdl_launch(codebook_finish_kernel, dim3(P), dim3(kFinThreads), smem, s, S, splits, h, bf16, N, C, D, L, K, P, ds, dC, dhp);
+  return pdl_launch(codebook_finish_kernel, dim3(P), dim3(kFinThreads), smem, s, S,
+                    splits, h, bf16, N, f, C, D, L, K, P, ds, dC, dhp);
 }
 
 cudaError_t launch_codebook_dh(const float *dhp, int N, int D, int M, int L, int bf16, void *dh,

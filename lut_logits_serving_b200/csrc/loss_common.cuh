@@ -51,10 +51,16 @@ struct CodeSrc {
 // largest element.  a b = a_hi b_hi + a_lo b_hi + a_hi b_lo + (dropped
 // a_lo b_lo, 2^-22 |a b|).
 
-// Largest magnitudes found by loss_begin_kernel: kAmaxBlocks partial maxima
-// each of |h|, of |C| and of |weight|.
+// Scales.  Every row of h has its own, and so has every row of the logits'
+// gradients, bounded by |w| T: a row's scale divides out where its sums leave,
+// so that neither a row of large values nor what padding holds costs the other
+// rows their bits.  h^T dz sums over the rows; there h_n goes in as
+// h_n sdw / scale_z(f_n) with one sdw for all rows (zero where the row has no
+// gradient), and the sums leave divided by sdw.  E has one scale.
+//
+// loss_begin_kernel leaves kAmaxBlocks partial maxima of |C|; behind them
+// loss_split_kernel writes sdw.
 constexpr int kAmaxBlocks = 128;
-enum { kAmaxH = 0, kAmaxC = 1, kAmaxW = 2 };
 
 // Largest power of two s (clamped to 2^-60 .. 2^60) with bound s < 2^14; 1 for
 // a bound that is zero, infinite or NaN.
@@ -67,28 +73,18 @@ __device__ __forceinline__ float pow2_scale(float bound) {
   return ldexpf(1.f, k);
 }
 
-// Maximum of the kAmaxBlocks partials of kind `which`; a whole warp calls it.
-__device__ __forceinline__ float warp_amax(const float *amax, int which) {
+// The scale of decoded rows (sums of L codewords); a whole warp calls it.
+__device__ __forceinline__ float scale_e(const float *amax, int L) {
   const int lane = threadIdx.x & 31;
   float m = 0.f;
-  for (int i = lane; i < kAmaxBlocks; i += 32) m = fmaxf(m, amax[which * kAmaxBlocks + i]);
+  for (int i = lane; i < kAmaxBlocks; i += 32) m = fmaxf(m, amax[i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
+  return pow2_scale(m * (float)L);
 }
-
-// The scales of the three operands: hidden states, decoded rows (a sum of L
-// codewords), gradients of the logits (|w| T times a difference of two
-// probabilities).
-__device__ __forceinline__ float scale_h(const float *amax) {
-  return pow2_scale(warp_amax(amax, kAmaxH));
-}
-__device__ __forceinline__ float scale_e(const float *amax, int L) {
-  return pow2_scale(warp_amax(amax, kAmaxC) * (float)L);
-}
-__device__ __forceinline__ float scale_z(const float *amax, float T) {
-  return pow2_scale(warp_amax(amax, kAmaxW) * T);
-}
+// Of a row of the logits' gradients, f = w T times a difference of two
+// probabilities each.
+__device__ __forceinline__ float scale_z(float f) { return pow2_scale(fabsf(f)); }
 
 __device__ __forceinline__ void split_f16(float x, __half &hi, __half &lo) {
   hi = __float2half_rn(x);
@@ -120,11 +116,11 @@ struct GemmArgs {
   int m_tiles, n_tiles, splits, kblocks;
   int a_planes, b_planes, chain, stages;
   int rows, cols;            // output extents
-  // scales
-  const float *amax;
+  // scales: partial maxima of |C| and sdw, and of h's rows (the logits)
+  const float *amax, *sh;
   int L;
   // epilogues
-  float inv_cap, cap, beta, T;
+  float inv_cap, cap, beta;
   float2 *stat;              // [parts][stat_ld] (max, sum), base 2
   int stat_ld;
   int stat_part0;            // first part of this launch
@@ -167,15 +163,35 @@ struct LossTargets {
   int k;
   float T, beta;
 };
-// The first launch: scales (amax null: none) and the sorted lists of `rows`
-// rows; for a gradient (sq set) merged, with q and f = weight T (0 for rows
-// without a target), for a loss with their places sj
-cudaError_t launch_loss_begin(const void *h, int bf16, int64_t nh, const float *C, int64_t nc,
-                              const float *w, int64_t nw, float *amax, const LossTargets &t,
-                              int64_t rows, int64_t V, const float *weight, int32_t *sid, int32_t *sj,
-                              float *sq, float *f, unsigned *err, cudaStream_t s);
-cudaError_t launch_loss_split(const void *h, int bf16, int64_t N, int D, int64_t pitch,
-                              const float *amax, __half *hi, __half *lo, cudaStream_t s);
+// The first launch: maxima of |C| (amax null: none); the scales sh of h's rows
+// (null: none); the sorted lists, for a gradient (sq set) merged, with q and
+// f = weight T (0 for rows without a target) and, with sh, hw = the rows'
+// largest |h| / scale_z(f), for a loss with their places sj
+struct BeginArgs {
+  const float *C;
+  int64_t nc;
+  float *amax;
+  const void *h;
+  int bf16, D;
+  float *sh, *hw;
+  LossTargets t;
+  int64_t rows, V;
+  const float *weight;
+  int32_t *sid, *sj;
+  float *sq, *f;
+  unsigned *err;
+};
+cudaError_t launch_loss_begin(const BeginArgs &a, cudaStream_t s);
+// h as planes; for a gradient (dhi set) also as h^T dz takes it, and *sdw
+struct SplitArgs {
+  const void *h;
+  int bf16, N, D;
+  int64_t pitch;
+  const float *sh, *hw, *f;
+  float *sdw;
+  __half *hi, *lo, *dhi, *dlo;   // lo and dlo null: bf16 h, which one plane holds
+};
+cudaError_t launch_loss_split(const SplitArgs &a, cudaStream_t s);
 // lse and loss from the parts and the listed ids' logits: y[n * k + j], or, with
 // y_is_logits, y[n * V + id].
 cudaError_t launch_loss_finish(const float2 *stat, int parts, int stat_ld, int64_t N, int64_t V,
@@ -212,8 +228,8 @@ cudaError_t launch_codebook_sums(const float *dz, int64_t pitch, int N, const vo
                                  int M, int L, int K, float *S, const DevInfo &di, cudaStream_t s);
 // from S: dC = S h, dhp[p][t][ds] = S C; dh from dhp
 cudaError_t launch_codebook_finish(const float *S, int splits, const void *h, int bf16, int N,
-                                   const float *C, int D, int M, int L, int K, float *dC,
-                                   float *dhp, cudaStream_t s);
+                                   const float *f, const float *C, int D, int M, int L, int K,
+                                   float *dC, float *dhp, cudaStream_t s);
 cudaError_t launch_codebook_dh(const float *dhp, int N, int D, int M, int L, int bf16, void *dh,
                                cudaStream_t s);
 

@@ -410,11 +410,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       return !to;
     };
-    const float sh = MODE != kGemmDh ? scale_h(g.amax) : 1.f;
     const float se = MODE != kGemmDw ? scale_e(g.amax, g.L) : 1.f;
-    const float sz = MODE != kGemmStats && MODE != kGemmGrad32 ? scale_z(g.amax, g.T) : 1.f;
-    const float inv = MODE == kGemmDh ? 1.f / (sz * se) : MODE == kGemmDw ? 1.f / (sz * sh)
-                                                                          : 1.f / (sh * se);
     const float cap = g.cap, icap = g.inv_cap, beta = g.beta;
     float acc[HALF];
     int c = 0;
@@ -428,7 +424,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       // next listed id at or after col0, its weight and log-sum-exp
       const bool in = row < g.rows;
       int li = 0, next = kNoId;
-      float f = 0.f, lse = 0.f;
+      float f = 0.f, lse = 0.f, inv = 1.f;
+      if (MODE == kGemmDw) inv = 1.f / __ldg(g.amax + kAmaxBlocks);
+      if (MODE == kGemmDh && in) inv = 1.f / (scale_z(g.f[row]) * se);
+      if (LOGITS && in) inv = 1.f / (g.sh[row] * se);
       if (LOGITS && in) {
         const int32_t *list = g.sid + (int64_t)row * g.k;
         const int want = g.v0 + col0;
@@ -519,7 +518,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (in)
           g.stat[(int64_t)(g.stat_part0 + nt * 2 + half) * g.stat_ld + row] = make_float2(mx, sum);
       } else if (LOGITS) {
-        const float fs = f * sz;
+        const float fs = MODE == kGemmGrad ? f * scale_z(f) : f;
         const int64_t at = (int64_t)row * g.dz_pitch + col0;
 #pragma unroll 1
         for (int j0 = 0; j0 < HALF; j0 += 32) {

@@ -32,8 +32,9 @@ __device__ __forceinline__ float block_max(float m, float *red) {
   return m;
 }
 
-__device__ __forceinline__ float abs_max(const float *x, int64_t n, int b) {
-  const int64_t stride = (int64_t)kAmaxBlocks * blockDim.x;
+// This thread's share of the largest |x[0 .. n)|: block b of `blocks`.
+__device__ __forceinline__ float abs_max(const float *x, int64_t n, int b, int blocks) {
+  const int64_t stride = (int64_t)blocks * blockDim.x;
   const int64_t i0 = (int64_t)b * blockDim.x + threadIdx.x;
   float m = 0.f;
   int64_t done = 0;
@@ -49,53 +50,37 @@ __device__ __forceinline__ float abs_max(const float *x, int64_t n, int b) {
   return m;
 }
 
-// The first kernel of a call.  Blocks [0, amax_blocks): partial maxima of |h|,
-// |C| and |w| (1 without weights), kAmaxBlocks each; the blocks after those: a
-// row's lists each (sparse_row).
-struct BeginArgs {
-  int amax_blocks;
-  const void *h;
-  int bf16;
-  int64_t nh;
-  const float *C;
-  int64_t nc;
-  const float *w;
-  int64_t nw;
-  float *amax;
-  LossTargets t;
-  int64_t V;
-  const float *weight;     // of the listed rows
-  int32_t *sid, *sj;
-  float *sq, *f;
-  unsigned *err;
-};
+__device__ float sparse_row(const BeginArgs &a, int64_t n, float *lists);
 
-__device__ void sparse_row(const BeginArgs &a, int64_t n, float *lists);
-
+// The first kernel of a call.  With a.amax, blocks [0, kAmaxBlocks) take the
+// partial maxima of |C|; the blocks after those a row each: its lists and the
+// scale of its hidden state.
 __global__ void __launch_bounds__(256) loss_begin_kernel(const BeginArgs a) {
   extern __shared__ float lists[];
   __shared__ float red[32];
   griddep_launch_dependents();
   griddep_wait();
-  if ((int)blockIdx.x >= a.amax_blocks) {
-    sparse_row(a, (int)blockIdx.x - a.amax_blocks, lists);
+  const int c_blocks = a.amax ? kAmaxBlocks : 0;
+  if ((int)blockIdx.x < c_blocks) {
+    const float m = block_max(abs_max(a.C, a.nc, blockIdx.x, kAmaxBlocks), red);
+    if (threadIdx.x == 0) a.amax[blockIdx.x] = m;
     return;
   }
-  const int kind = blockIdx.x / kAmaxBlocks, b = blockIdx.x % kAmaxBlocks;
+  const int64_t n = (int)blockIdx.x - c_blocks;
   float m = 0.f;
-  if (kind == kAmaxH && a.bf16) {
-    for (int64_t i = (int64_t)b * blockDim.x + threadIdx.x; i < a.nh;
-         i += (int64_t)kAmaxBlocks * blockDim.x)
-      m = fmaxf(m, fabsf(load_h(a.h, 1, i)));
-  } else if (kind == kAmaxH) {
-    m = abs_max(static_cast<const float *>(a.h), a.nh, b);
-  } else if (kind == kAmaxC) {
-    m = abs_max(a.C, a.nc, b);
-  } else {
-    m = a.w ? abs_max(a.w, a.nw, b) : 1.f;
+  if (a.sh && a.bf16) {
+    for (int i = threadIdx.x; i < a.D; i += blockDim.x)
+      m = fmaxf(m, fabsf(load_h(a.h, 1, n * a.D + i)));
+  } else if (a.sh) {
+    m = abs_max(static_cast<const float *>(a.h) + n * a.D, a.D, 0, 1);
   }
+  const float f = sparse_row(a, n, lists);
+  if (!a.sh) return;
   m = block_max(m, red);
-  if (threadIdx.x == 0) a.amax[blockIdx.x] = m;
+  if (threadIdx.x == 0) {
+    a.sh[n] = pow2_scale(m);
+    if (a.hw) a.hw[n] = f != 0.f ? m / scale_z(f) : 0.f;
+  }
 }
 
 __global__ void __launch_bounds__(256) loss_widen_h_kernel(const __nv_bfloat16 *__restrict__ h,
@@ -309,20 +294,35 @@ __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeAr
 
 // ------------------------------------------------------------- hidden planes
 
-__global__ void __launch_bounds__(256) loss_split_kernel(const void *h, int bf16, int D,
-                                                         int64_t pitch,
-                                                         const float *__restrict__ amax,
-                                                         __half *__restrict__ hi,
-                                                         __half *__restrict__ lo) {
+__global__ void __launch_bounds__(256) loss_split_kernel(const SplitArgs a) {
+  __shared__ float red[32];
   griddep_launch_dependents();
   griddep_wait();
-  const float s = scale_h(amax);
   const int64_t n = blockIdx.x;
-  for (int i = threadIdx.x; i < D; i += blockDim.x) {
+  const float s = a.sh[n];
+  float sd = 0.f;          // of h^T dz
+  if (a.dhi) {
+    float m = 0.f;
+    for (int i = threadIdx.x; i < a.N; i += blockDim.x) m = fmaxf(m, a.hw[i]);
+    m = block_max(m, red);
+    if (threadIdx.x == 0) red[0] = m;
+    __syncthreads();
+    const float sdw = pow2_scale(red[0]), f = a.f[n];
+    if (f != 0.f) sd = sdw / scale_z(f);
+    if (n == 0 && threadIdx.x == 0) *a.sdw = sdw;
+  }
+  for (int i = threadIdx.x; i < a.D; i += blockDim.x) {
+    const float y = load_h(a.h, a.bf16, n * a.D + i);
+    const int64_t at = n * a.pitch + i;
     __half x, r;
-    split_f16(__fmul_rn(load_h(h, bf16, n * D + i), s), x, r);
-    hi[n * pitch + i] = x;
-    if (lo) lo[n * pitch + i] = r;
+    split_f16(__fmul_rn(y, s), x, r);
+    a.hi[at] = x;
+    if (a.lo) a.lo[at] = r;
+    if (a.dhi) {
+      split_f16(sd != 0.f ? __fmul_rn(y, sd) : 0.f, x, r);
+      a.dhi[at] = x;
+      if (a.dlo) a.dlo[at] = r;
+    }
   }
 }
 
@@ -456,8 +456,8 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const float2 *__restr
 // One block per row: its listed ids in ascending order (kNoId after them), so
 // that a tile of columns finds its own by bisection.  For a loss (sq null) sj
 // keeps their places in the list; for a gradient an id listed twice is merged
-// into one, with q_j, and f = w T.
-__device__ void sparse_row(const BeginArgs &a, int64_t n, float *lists) {
+// into one, with q_j, and f = w T, which is returned.
+__device__ float sparse_row(const BeginArgs &a, int64_t n, float *lists) {
   __shared__ float red[8], red2[8];       // lists: [k] q, [k] id, [k] counts
   const LossTargets &t = a.t;
   const int tid = threadIdx.x, k = t.k, nt = blockDim.x, warps = nt / 32;
@@ -530,7 +530,10 @@ __device__ void sparse_row(const BeginArgs &a, int64_t n, float *lists) {
     a.sid[n * k + j] = kNoId;
     if (grad) a.sq[n * k + j] = 0.f;
   }
-  if (grad && tid == 0) a.f[n] = some ? (a.weight ? a.weight[n] : 1.f) * t.T : 0.f;
+  if (!grad) return 0.f;
+  const float f = some ? (a.weight ? a.weight[n] : 1.f) * t.T : 0.f;
+  if (tid == 0) a.f[n] = f;
+  return f;
 }
 
 __device__ __forceinline__ float dz_at(float y, float q, float lse, float f, float beta,
@@ -583,30 +586,9 @@ unsigned blocks_of(int64_t n, int per) { return (unsigned)((n + per - 1) / per);
 
 }  // namespace
 
-cudaError_t launch_loss_begin(const void *h, int bf16, int64_t nh, const float *C, int64_t nc,
-                              const float *w, int64_t nw, float *amax, const LossTargets &t,
-                              int64_t rows, int64_t V, const float *weight, int32_t *sid, int32_t *sj,
-                              float *sq, float *f, unsigned *err, cudaStream_t s) {
-  BeginArgs a;
-  a.amax_blocks = amax ? 3 * kAmaxBlocks : 0;
-  a.h = h;
-  a.bf16 = bf16;
-  a.nh = nh;
-  a.C = C;
-  a.nc = nc;
-  a.w = w;
-  a.nw = nw;
-  a.amax = amax;
-  a.t = t;
-  a.V = V;
-  a.weight = weight;
-  a.sid = sid;
-  a.sj = sj;
-  a.sq = sq;
-  a.f = f;
-  a.err = err;
-  return pdl_launch(loss_begin_kernel, dim3((unsigned)(a.amax_blocks + rows)), dim3(256),
-                    rows > 0 ? (size_t)t.k * 12 : 0, s, a);
+cudaError_t launch_loss_begin(const BeginArgs &a, cudaStream_t s) {
+  return pdl_launch(loss_begin_kernel, dim3((unsigned)(a.rows + (a.amax ? kAmaxBlocks : 0))),
+                    dim3(256), (size_t)a.t.k * 12, s, a);
 }
 
 cudaError_t launch_loss_widen_h(const void *h, int64_t n, float *out, cudaStream_t s) {
@@ -690,10 +672,8 @@ cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, 
                           s, args, true);
 }
 
-cudaError_t launch_loss_split(const void *h, int bf16, int64_t N, int D, int64_t pitch,
-                              const float *amax, __half *hi, __half *lo, cudaStream_t s) {
-  return pdl_launch(loss_split_kernel, dim3((unsigned)N), dim3(256), (size_t)0, s, h, bf16, D, pitch,
-                    amax, hi, lo);
+cudaError_t launch_loss_split(const SplitArgs &a, cudaStream_t s) {
+  return pdl_launch(loss_split_kernel, dim3((unsigned)a.N), dim3(256), (size_t)0, s, a);
 }
 
 int loss_stat_parts(int64_t V) { return (int)((V + kStatCols - 1) / kStatCols); }

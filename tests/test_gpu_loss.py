@@ -377,3 +377,87 @@ def test_calls_in_a_row():
     assert abs(moved - want) <= 0.1 * abs(want) + 1e-4
     y, am, _ = rq.rq_logits_from_hidden(h, C, codes, rq.U16, d, 30.0, want_argmax=True)
     assert torch.allclose(torch.logsumexp(y.double(), 1), lse.double(), atol=1e-4)
+
+
+JUNK = (float("nan"), float("inf"), -3e38, 1e30, -float("inf"))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N", [3, 20, 100])
+def test_padding_may_hold_anything(N, dtype):
+    """Rows without a target: their hidden states, weights and lse, finite or
+    not, reach no other row and no gradient."""
+    x = Head(3000, 16, 6, 2, 100, N, dtype, seed=11)
+    pad = torch.arange(N, device="cuda") % 5 != 2
+    pad[0] = True
+    junk = torch.tensor(JUNK, device="cuda")[torch.arange(N, device="cuda") % 5]
+    clean = x.h.masked_fill(pad[:, None], 0)
+    x.h = torch.where(pad[:, None], junk[:, None].to(dtype), x.h)
+    x.h[::2, 1::3] = clean[::2, 1::3]
+    x.weight[pad] = junk[pad]
+    for k in (0, 6):
+        if k:
+            x.teacher(k)
+            x.idx[pad] = -1
+            x.val[pad] = junk[pad, None]
+        else:
+            x.target[pad] = -1
+        got = x.run(1.3 if k else 1.0, weight=x.weight)
+        w = x.weight.masked_fill(pad, 1)
+        ids, val = (x.idx, x.val.masked_fill(pad[:, None], 0)) if k else (x.target, None)
+        ref = loss_ref.losses(clean, x.C, x.codes, ids, val, 1.3 if k else 1.0, 30.0, w)
+        assert (got["loss"][pad] == 0).all() and (got["dh"][pad] == 0).all()
+        got["lse"] = torch.where(pad, ref["lse"].float(), got["lse"])
+        compare(got, ref, dtype == torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N", [4, 24, 130])
+def test_rows_keep_their_own_precision(N, dtype):
+    """Rows and weights twelve orders of magnitude apart: each row's loss, lse
+    and dh within the bounds of that row alone."""
+    x = Head(2500, 16, 6, 2, 64, N, dtype, seed=12)
+    n = torch.arange(N, device="cuda")
+    x.h = (x.h.float() * 10.0 ** (3 * (n % 5) - 6.0)[:, None]).to(dtype)
+    x.weight = 10.0 ** (3 * (n // 5 % 5) - 8.0)
+    got = x.run(weight=x.weight)
+    for i in range(N):
+        s = slice(i, i + 1)
+        ref = loss_ref.losses(x.h[s], x.C, x.codes, x.target[s], None, 1.0, 30.0, x.weight[s])
+        compare({m: got[m][s] for m in ("loss", "lse", "dh")}, ref, dtype == torch.bfloat16)
+    ref = loss_ref.losses(x.h, x.C, x.codes, x.target, None, 1.0, 30.0, x.weight)
+    compare({"dC": got["dC"]}, ref, dtype == torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N", [4099, 8192])
+def test_several_sweeps_of_tokens(N, dtype):
+    """More tokens than one sweep over the vocabulary takes; a short last one."""
+    x = Head(500, 4, 6, 2, 32, N, dtype, seed=13)
+    x.target[::7] = -1
+    x.check(weight=x.weight)
+    x.teacher(3).check(2.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N", [3, 77])
+def test_unaligned_tensors(N, dtype):
+    """Every float tensor an element past a 16-byte boundary: the same bits."""
+    x = Head(2100, 8, 6, 2, 64, N, dtype, seed=14)
+    x.teacher(5)
+    want = x.run(weight=x.weight)
+
+    def off(t):
+        b = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        b[1:] = t.reshape(-1)
+        return b[1:].view(t.shape)
+
+    for name in ("h", "C", "weight", "val", "idx"):
+        setattr(x, name, off(getattr(x, name)))
+    got = x.run(weight=x.weight)
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
+    dh, dC = off(want["dh"]), off(want["dC"])
+    rq.rq_distill_grad(*x.args(), x.val, x.idx, off(want["lse"]), x.index, temperature=1.0,
+                       weight=x.weight, dh=dh, dC=dC)
+    assert torch.equal(dh, want["dh"]) and torch.equal(dC, want["dC"])
