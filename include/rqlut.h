@@ -124,7 +124,7 @@ enum rq_status {
 
 /* Bits of the device error word. */
 #define RQ_DEVERR_TIMEOUT 0x1u  /* a bounded wait inside a kernel expired */
-#define RQ_DEVERR_BAD_ID  0x2u  /* rq_decode_rows saw an id outside [0,V) */
+#define RQ_DEVERR_BAD_ID  0x2u  /* rq_decode_rows saw an id outside [0,V), a loss one >= V */
 
 /* Human-readable name of a status code (static string, never NULL). */
 RQ_API const char *rq_status_string(int status);
@@ -444,7 +444,7 @@ RQ_API int rq_prepare_rot10(const uint16_t *codes_u16, rq_dims d, uint8_t *out,
  *           call wrote for the same inputs
  *   dh      (device) [N][D] in h's type, or NULL; dC (device) float
  *           [M][L][K][ds], or NULL; at least one of the two.  Both are
- *           overwritten and must not overlap an input.
+ *           overwritten.
  *   index   (device) as written by rq_prepare_grad for the codes
  *   ws      (device) >= rq_loss_workspace_bytes(d, N, fmt, k, grad) bytes,
  *           256-byte aligned, contents need no initialisation (k = 1 for
@@ -455,7 +455,8 @@ RQ_API int rq_prepare_rot10(const uint16_t *codes_u16, rq_dims d, uint8_t *out,
  * for float h, dh carry fp32 accuracy; a bf16 dh is rounded once.  Sums run in
  * a fixed order: the same call gives the same bits.
  * Errors: RQ_ERR_INVALID_ARGUMENT (null pointer, N < 1, k, T or h_bf16 out of
- * range, bad dims or format), RQ_ERR_UNSUPPORTED (the format cannot hold the
+ * range, bad dims or format, an output or ws that overlaps another argument),
+ * RQ_ERR_UNSUPPORTED (the format cannot hold the
  * shape, k > 1024; gradients: K > 4096), RQ_ERR_MISALIGNED,
  * RQ_ERR_WORKSPACE_TOO_SMALL, RQ_ERR_CUDA.
  */

@@ -550,6 +550,35 @@ int check(const Problem &q, const void *ws) {
   return RQ_OK;
 }
 
+// What a call reads and writes; a written range may meet no other.
+struct Ranges {
+  struct One {
+    uintptr_t at;
+    size_t bytes;
+    bool out;
+  } r[16];
+  int n = 0;
+  void add(const void *p, size_t bytes, bool out) {
+    if (p) r[n++] = {reinterpret_cast<uintptr_t>(p), bytes, out};
+  }
+  void add_inputs(const Problem &q) {
+    const size_t N = (size_t)q.N;
+    add(q.h, N * q.d.D * (q.bf16 ? 2 : 4), false);
+    add(q.C, (size_t)q.d.M * q.d.L * q.d.K * q.ds() * 4, false);
+    add(q.codes, rq_codes_bytes(q.d, q.fmt), false);
+    add(q.t.id, N * q.t.k * 4, false);
+    add(q.t.val, N * q.t.k * 4, false);
+  }
+  bool meet() const {
+    for (int i = 0; i < n; ++i)
+      for (int j = 0; j < i; ++j)
+        if ((r[i].out || r[j].out) && r[i].at < r[j].at + r[j].bytes &&
+            r[j].at < r[i].at + r[i].bytes)
+          return true;
+    return false;
+  }
+};
+
 int run_loss(const Problem &q, float *loss, float *lse, void *ws, size_t ws_bytes, void *stream) {
   if (!loss || !lse) return RQ_ERR_INVALID_ARGUMENT;
   const int bad = check(q, ws);
@@ -557,6 +586,12 @@ int run_loss(const Problem &q, float *loss, float *lse, void *ws, size_t ws_byte
   if (!aligned(loss, 4) || !aligned(lse, 4)) return RQ_ERR_MISALIGNED;
   const Layout x = layout(q.d, q.N, q.fmt, q.t.k, false);
   if (!ws || ws_bytes < x.total) return RQ_ERR_WORKSPACE_TOO_SMALL;
+  Ranges all;
+  all.add_inputs(q);
+  all.add(loss, (size_t)q.N * 4, true);
+  all.add(lse, (size_t)q.N * 4, true);
+  all.add(ws, x.total, true);
+  if (all.meet()) return RQ_ERR_INVALID_ARGUMENT;
   DevInfo di;
   cudaError_t e = dev_info(&di);
   if (e != cudaSuccess) return status_of(e);
@@ -583,6 +618,15 @@ int run_grad(const Problem &q, const float *lse, const float *w, const void *ind
     return RQ_ERR_MISALIGNED;
   const Layout x = layout(q.d, q.N, q.fmt, q.t.k, true);
   if (!ws || ws_bytes < x.total) return RQ_ERR_WORKSPACE_TOO_SMALL;
+  Ranges all;
+  all.add_inputs(q);
+  all.add(lse, (size_t)q.N * 4, false);
+  all.add(w, (size_t)q.N * 4, false);
+  all.add(index, rq_grad_index_bytes(q.d), false);
+  all.add(dh, (size_t)q.N * q.d.D * (q.bf16 ? 2 : 4), true);
+  all.add(dC, (size_t)q.d.M * q.d.L * q.d.K * q.ds() * 4, true);
+  all.add(ws, x.total, true);
+  if (all.meet()) return RQ_ERR_INVALID_ARGUMENT;
   DevInfo di;
   cudaError_t e = dev_info(&di);
   if (e != cudaSuccess) return status_of(e);

@@ -445,7 +445,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
       auto step = [&]() {
-        next = ++li < g.k ? __ldg(g.sid + (int64_t)row * g.k + li) - g.v0 : kNoId;
+        next = ++li < g.k ? __ldg(g.sid + (int64_t)row * g.k + li) : kNoId;
+        if (next != kNoId) next -= g.v0;
       };
 #pragma unroll
       for (int j = 0; j < HALF; ++j) acc[j] = 0.f;

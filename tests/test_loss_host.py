@@ -78,6 +78,25 @@ def test_alignment():
         assert xent_grad(**{name: _p(0x100000 + off)}) == MIS, name
 
 
+def _apart(**kw):
+    """Arguments 64 GB apart, so that none meets another."""
+    return {n: _p((i + 1) << 36) for i, n in enumerate(kw)} | {n: v for n, v in kw.items() if v}
+
+
+def test_outputs_meet_nothing():
+    """Before any launch: an output or the workspace on an input or on another output."""
+    f = dict.fromkeys(("h", "C", "codes", "target", "loss", "lse", "ws"))
+    a = _apart(**f)
+    for x, y, off in (("loss", "lse", 28), ("loss", "target", -28), ("lse", "h", 64), ("ws", "C", 256),
+                      ("C", "ws", 256), ("loss", "ws", 1024), ("codes", "lse", -16)):
+        assert xent(**_apart(**f | {x: _p(a[y].value + off)})) == INV, (x, y)
+    f = dict.fromkeys(("h", "C", "codes", "target", "lse", "w", "index", "dh", "dC", "ws"))
+    a = _apart(**f)
+    for x, y in (("dh", "h"), ("dC", "C"), ("dC", "dh"), ("dh", "index"), ("dC", "ws"), ("dh", "w"),
+                 ("ws", "codes"), ("dC", "lse")):
+        assert xent_grad(**_apart(**f | {x: a[y]})) == INV, (x, y)
+
+
 @pytest.mark.parametrize("d", [G2, TINY, rq.dims(1, 1, 1, 1, 1), rq.dims(50021, 640, 128, 3, 200)])
 @pytest.mark.parametrize("N", [1, 4, 20, 64, 65, 5000])
 def test_workspace(d, N):
