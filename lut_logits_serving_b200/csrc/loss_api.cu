@@ -214,8 +214,8 @@ Layout layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
     x.sh = a.take(n * 4);
     x.hh = a.take(n * x.hp * 2);
     x.hl = a.take(n * x.hp * 2);
-    x.wh = a.take(rows * x.hp * 2);
-    x.wl = a.take(rows * x.hp * 2);
+    x.wh = a.take((d.D + 7) / 8 * x.zp * 16);        // columns of 8 dims
+    x.wl = a.take((d.D + 7) / 8 * x.zp * 16);
     x.y = a.take(n * k * 4);
   } else {
     x.logits = a.take((int64_t)N * d.V * 4);
@@ -371,7 +371,7 @@ cudaError_t split(const Problem &q, const Layout &x, bool dw, void *ws, cudaStre
 // Piece [v0, v0 + rows) decoded.
 cudaError_t decode(const Problem &q, const Layout &x, int64_t v0, int64_t rows, void *ws,
                    const DevInfo &di, cudaStream_t s) {
-  return launch_loss_decode(q.src(), q.C, q.d.M, q.d.L, q.ds(), v0, rows, x.hp,
+  return launch_loss_decode(q.src(), q.C, q.d.M, q.d.L, q.ds(), v0, rows, x.zp,
                             at<float>(ws, x.amax), at<__half>(ws, x.wh), at<__half>(ws, x.wl), di,
                             s);
 }
@@ -381,7 +381,7 @@ GemmPlanes h_planes(const Problem &q, const Layout &x, void *ws) {
   return planes(at<void>(ws, x.hh), q.bf16 ? nullptr : at<void>(ws, x.hl), q.N, q.d.D, x.hp);
 }
 GemmPlanes w_planes(const Problem &q, const Layout &x, int64_t rows, void *ws) {
-  return planes(at<void>(ws, x.wh), at<void>(ws, x.wl), rows, q.d.D, x.hp);
+  return planes(at<void>(ws, x.wh), at<void>(ws, x.wl), rows, q.d.D, x.zp);
 }
 
 template <typename Each>
@@ -468,7 +468,7 @@ cudaError_t products_grad(const Problem &all, const Layout &x, const float *lse,
         p.accumulate = v0 > 0;
         RQ_TRY(launch_loss_gemm(
             kGemmDh, planes(zh, q.bf16 ? nullptr : zl, q.N, rows, x.zp),
-            planes(at<void>(ws, x.wh), q.bf16 ? nullptr : at<void>(ws, x.wl), rows, d.D, x.hp), p,
+            planes(at<void>(ws, x.wh), q.bf16 ? nullptr : at<void>(ws, x.wl), rows, d.D, x.zp), p,
             di, s));
       }
       if (dC) {

@@ -107,9 +107,11 @@ enum LossGemm {
   kGemmGrad32 = 4   // kGemmGrad with fp32 gradients, unscaled
 };
 
-struct GemmPlanes {          // row-major fp16 planes; lo may be null
+// fp16 planes; lo may be null.  Row-major, rows `pitch` elements apart, but for
+// the decoded rows, whose columns of 8 dims are `pitch` rows apart (loss_rows.cu).
+struct GemmPlanes {
   const void *hi, *lo;
-  int64_t rows, cols, pitch; // extents and row pitch in elements (pitch % 8 == 0)
+  int64_t rows, cols, pitch; // pitch % 8 == 0
 };
 
 struct GemmArgs {

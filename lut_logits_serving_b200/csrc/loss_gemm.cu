@@ -28,8 +28,9 @@
 // elements, 128-byte swizzle), an MMA warp (tcgen05.mma, both operands in
 // shared memory), eight warps that own the accumulators (a thread has one row
 // and half the tile's columns) and run the epilogue.  Operands whose
-// contraction runs down the rows of a row-major matrix are read as they lie
-// (MN-major tiles), so nothing is stored twice.
+// contraction runs down the rows of their matrix are read as they lie (MN-major
+// tiles), so nothing is stored twice; the decoded rows come in blocks of 8 x 8
+// that serve either way without a swizzle.
 //
 // Tiles.  A CTA pair shares a 256 x 256 tile (cta_group::2: each SM holds its
 // 128 rows of A and half of B): one SM alone on 128 x 256 would read
@@ -41,6 +42,8 @@
 //
 // Every wait is bounded; one that runs out raises RQ_DEVERR_TIMEOUT, lets
 // copies and MMAs in flight land, frees tensor memory and ends the CTA.
+#include <cudaTypedefs.h>
+
 #include "loss_common.cuh"
 
 namespace rq {
@@ -71,6 +74,14 @@ constexpr size_t kGemmSmemTail = 1024 + 256;     // alignment slack, barriers
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lead) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) |
          ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Descriptor of a tile without a swizzle, of blocks of 8 rows x 16 bytes that
+// are 128 bytes in one piece.  `lead`: from one block to the next along the
+// contraction; `stride`: along the other extent.
+__device__ __forceinline__ uint64_t block_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) |
+         ((uint64_t)(stride >> 4) << 32) | (1ull << 46);
 }
 
 template <int CG>
@@ -115,6 +126,25 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, 
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
         "bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar & 0xFEFFFFFFu), "l"(pol)
+        : "memory");
+}
+
+// The same of a tile of 8 x 8 blocks: block row y, column of blocks z.
+template <int CG>
+__device__ __forceinline__ void load_blocks(uint32_t dst, const CUtensorMap *map, int y, int z,
+                                            uint32_t bar, uint64_t pol) {
+  if (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar), "l"(pol)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+        "bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar & 0xFEFFFFFFu),
+        "l"(pol)
         : "memory");
 }
 
@@ -250,6 +280,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   constexpr bool LOGITS = MODE == kGemmStats || MODE == kGemmGrad || MODE == kGemmGrad32;
   constexpr bool A_MN = MODE == kGemmDw;                        // contraction down the rows of A
   constexpr bool B_MN = MODE == kGemmDh || MODE == kGemmDw;     // and of B
+  constexpr bool B_ROWS = MODE != kGemmDw;       // B is decoded rows, 8 x 8 blocks
   constexpr int BN = TN / CG;                    // columns of B in this CTA's shared memory
   constexpr int HALF = TN / 2;                   // columns of an accumulator thread
   constexpr int B_BYTES = BN * kTK * 2;
@@ -349,12 +380,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
             for (int p = 0; p < g.b_planes; ++p, dst += B_BYTES) {
               const CUtensorMap *map = p ? &b_lo : &b_hi;
-              if (B_MN) {
+              if (B_ROWS) {
+                if (B_MN) load_blocks<CG>(dst, map, k * (kTK / 8), n0 / 8, full(st), pol);
+                else load_blocks<CG>(dst, map, n0 / 8, k * (kTK / 8), full(st), pol);
+              } else {
 #pragma unroll
                 for (int i = 0; i < BN / 64; ++i)
                   load_tile<CG>(dst + i * 8192, map, n0 + i * 64, k * kTK, full(st), pol);
-              } else {
-                load_tile<CG>(dst, map, k * kTK, n0, full(st), pol);
               }
             }
           }
@@ -376,7 +408,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(kTM * CG >> 4) << 24);
         // 16 contraction elements further: 32 bytes along a K-major row, 16
         // rows of 128 bytes in an MN-major tile (in descriptor units of 16 B)
-        constexpr uint32_t a_step = A_MN ? 2048 / 16 : 32 / 16, b_step = B_MN ? 2048 / 16 : 32 / 16;
+        // (and two blocks of 8 x 8)
+        constexpr uint32_t a_step = A_MN ? 2048 / 16 : 32 / 16;
+        constexpr uint32_t b_step = !B_ROWS ? 2048 / 16 : B_MN ? 256 / 16 : BN * 32 / 16;
         int it = 0, c = 0;
         for (int t = unit; t < total && !abort_flag; t += units) {
           const int sp = t / mn;
@@ -394,7 +428,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               const uint32_t sa = base + (uint32_t)st * stage_bytes;
               const uint32_t sb = sa + (uint32_t)g.a_planes * kABytes;
               const uint64_t ah = sw128_desc(sa, A_MN ? 8192 : 16);
-              const uint64_t bh = sw128_desc(sb, B_MN ? 8192 : 16);
+              const uint64_t bh = !B_ROWS ? sw128_desc(sb, 8192)
+                                  : B_MN  ? block_desc(sb, 128, 1024)
+                                          : block_desc(sb, BN * 16, 128);
               const uint64_t al = ah + kABytes / 16, bl = bh + B_BYTES / 16;
 #pragma unroll
               for (int j = 0; j < kTK / 16; ++j)
@@ -722,17 +758,41 @@ bool plane_map(CUtensorMap *m, const void *p, const GemmPlanes &x, bool mn, int 
                             mn ? 64 : (uint32_t)tile, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Decoded rows: boxes of `brows` x `bcols` blocks of 8 x 8.
+bool rows_map(CUtensorMap *m, const void *p, const GemmPlanes &x, int brows, int bcols) {
+  static const PFN_cuTensorMapEncodeTiled encode = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<PFN_cuTensorMapEncodeTiled>(f)
+               : nullptr;
+  }();
+  if (!encode) return false;
+  const cuuint64_t dim[3] = {64, (cuuint64_t)(x.rows + 7) / 8, (cuuint64_t)(x.cols + 7) / 8};
+  const cuuint64_t stride[2] = {128, (cuuint64_t)x.pitch * 16};
+  const cuuint32_t box[3] = {64, (cuuint32_t)brows, (cuuint32_t)bcols}, one[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(p), dim, stride, box, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int MODE, int CG, int TN>
 cudaError_t launch_tile(const GemmPlanes &A, const GemmPlanes &B, GemmArgs a, const DevInfo &di,
                         cudaStream_t s) {
   constexpr bool A_MN = MODE == kGemmDw, B_MN = MODE == kGemmDh || MODE == kGemmDw;
   constexpr int BN = TN / CG;
   CUtensorMap ah, al, bh, bl;
-  if (!plane_map(&ah, A.hi, A, A_MN, kTM) || !plane_map(&bh, B.hi, B, B_MN, BN))
-    return cudaErrorInvalidValue;
+  auto b_map = [&](CUtensorMap *m, const void *p) {
+    return MODE == kGemmDw ? plane_map(m, p, B, true, BN)
+           : B_MN          ? rows_map(m, p, B, kTK / 8, BN / 8)
+                           : rows_map(m, p, B, BN / 8, kTK / 8);
+  };
+  if (!plane_map(&ah, A.hi, A, A_MN, kTM) || !b_map(&bh, B.hi)) return cudaErrorInvalidValue;
   al = ah;
   bl = bh;
-  if ((A.lo && !plane_map(&al, A.lo, A, A_MN, kTM)) || (B.lo && !plane_map(&bl, B.lo, B, B_MN, BN)))
+  if ((A.lo && !plane_map(&al, A.lo, A, A_MN, kTM)) || (B.lo && !b_map(&bl, B.lo)))
     return cudaErrorInvalidValue;
   const int64_t k = A_MN ? A.rows : A.cols;
   a.a_planes = A.lo ? 2 : 1;

@@ -93,21 +93,31 @@ __global__ void __launch_bounds__(256) loss_widen_h_kernel(const __nv_bfloat16 *
 }
 
 // ------------------------------------------------------------- row decode
+
+// (x, y) as a word of the high plane and one of the low.
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t &hi, uint32_t &lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(__fsub_rn(x, f.x), __fsub_rn(y, f.y));
+  hi = *reinterpret_cast<const uint32_t *>(&h);
+  lo = *reinterpret_cast<const uint32_t *>(&l);
+}
 //
-// Rows v0 .. v0 + rows of E as scaled fp16 hi / lo planes.  A CTA keeps the
-// (scaled) codebooks of a group of gs subspaces in shared memory while it walks
-// a chunk of rows.  A thread has one pair of dims of the group, the same for
-// all its rows: it fetches the row's L codes (a few rows ahead), gathers and
-// adds the pair's L codeword parts, splits the sums and stores one word to
-// each plane.  Neighbouring lanes read neighbouring words of a codeword (three
-// lanes for ds = 6), which spreads a warp's words over the banks better than a
-// lane per codeword, and their stores join; nothing is passed between threads.
-// The items go chunk by chunk, all groups of a chunk at about the same time: a
-// group writes 2 gs ds bytes of a row, and the L2 joins them to whole sectors
-// and lines only if the row's other groups follow before it evicts them
-// (groups at unrelated rows: 474 us for 32768 rows of 2304, of which 320 were
-// the scattered writes; a lane per codeword, results through a strip of shared
-// memory: 185 us).  Bound by the random shared-memory gathers.
+// Rows v0 .. v0 + rows of E as scaled fp16 hi / lo planes, in columns of 8 dims:
+// element (row, dim) at ((dim / 8) pitch + row) 8 + dim % 8, zeros up to whole
+// columns and to 8 rows.  Eight rows of a column are 128 bytes, the unit that
+// the tensor cores take without a swizzle as either operand's rows, and a
+// warp that decodes 32 rows stores whole lines.
+//
+// Two kernels.  loss_decode_rows_kernel (below) takes the sizes that it is
+// compiled for; this one the others (many levels, odd or long subspaces, large
+// codebooks): a CTA keeps the (scaled) codebooks of a group of gs subspaces in
+// shared memory, if one fits, while it walks a chunk of rows.  A thread has one
+// pair of dims of the group, the same for all its rows: it fetches the row's L
+// codes (a few rows ahead), gathers and adds the pair's L codeword parts and
+// stores one word to each plane; neighbouring lanes read neighbouring words of
+// a codeword.  The items go chunk by chunk, all groups of a chunk at about the
+// same time, so that the L2 joins their stores and codes.
 struct DecodeArgs {
   CodeSrc cs;
   const float *C;
@@ -228,10 +238,11 @@ __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeAr
     const float *b1 = (SMEM ? books + sub1 * a.book : a.C + (m0 + sub1) * a.book) + j1;
     const int m = m0 + sub, m1 = m0 + sub1;
     const int64_t vc = a.v0 + r0;
-    const int n = (int)(r1 - r0), pitch = (int)a.pitch;
+    const int n = (int)(r1 - r0);
     const CodeRow ca(a.cs, vc, m, L), cb(a.cs, vc, EVEN ? m : m1, L);
-    __half *oh = a.hi + r0 * a.pitch + (int64_t)m0 * ds + 2 * w;
-    __half *ol = a.lo + r0 * a.pitch + (int64_t)m0 * ds + 2 * w;
+    const int dim = m0 * ds + 2 * w;
+    __half *oh = a.hi + ((dim >> 3) * a.pitch + r0) * 8 + (dim & 7);
+    __half *ol = a.lo + ((dim >> 3) * a.pitch + r0) * 8 + (dim & 7);
     RowCodes<LL> cn[kDecU], dn[EVEN ? 1 : kDecU];
     auto fetch = [&](int r) {
 #pragma unroll
@@ -280,13 +291,217 @@ __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeAr
           e0 = __fmul_rn(e0, se);
           e1 = __fmul_rn(e1, se);
         }
-        const __half2 h = __floats2half2_rn(e0, e1);
-        const float2 f = __half22float2(h);
-        const __half2 lw = __floats2half2_rn(__fsub_rn(e0, f.x), __fsub_rn(e1, f.y));
-        // rows are padded to whole vectors, so a pair past D has its place; a
-        // group starts on a pair unless gs ds is odd (one group then)
-        *reinterpret_cast<__half2 *>(oh + (int64_t)x * pitch) = h;
-        *reinterpret_cast<__half2 *>(ol + (int64_t)x * pitch) = lw;
+        // columns are padded to 8 dims, so a pair past D has its place; a group
+        // starts on a pair unless gs ds is odd (one group then)
+        uint32_t hw, lw;
+        split_pair(e0, e1, hw, lw);
+        *reinterpret_cast<uint32_t *>(oh + (int64_t)x * 8) = hw;
+        *reinterpret_cast<uint32_t *>(ol + (int64_t)x * 8) = lw;
+      }
+    }
+  }
+  // zeros to a column of 8 dims and a row of 8
+  const int D = a.M * ds, D8 = (D + 7) & ~7;
+  const int64_t rows8 = (a.rows + 7) & ~7ll, threads = (int64_t)gridDim.x * kDecThreads;
+  auto clear = [&](int dim, int64_t r) {
+    const int64_t at = ((dim >> 3) * a.pitch + r) * 8 + (dim & 7);
+    a.hi[at] = a.lo[at] = __ushort_as_half(0);
+  };
+  for (int64_t i = (int64_t)blockIdx.x * kDecThreads + tid; i < rows8 * (D8 - D); i += threads)
+    clear(D + (int)(i / rows8), i % rows8);
+  for (int64_t i = (int64_t)blockIdx.x * kDecThreads + tid; i < (rows8 - a.rows) * D8; i += threads)
+    clear((int)(i % D8), a.rows + i / D8);
+}
+
+// Rows of E, a thread a row.  A CTA takes one unit of G subspaces, whose dims
+// fill Q whole columns of the planes, and a chunk of rows.  The codebooks lie
+// in shared memory split into parts of four, two and one dims, so that a
+// codeword of six is one 16- and one 8-byte access: random codewords meet in a
+// bank 2.6 times per 128 bytes so, 3.1 times in 8-byte accesses.  A row's codes
+// come in wide loads, a row ahead; a warp's stores are 32 neighbouring rows of
+// a column, 512 bytes at once.  Bound by shared memory's data path (41 million
+// passes of 128 bytes per 65536 rows of 2304 dims, two levels of 1024: 27 for
+// the gathers, 7 for codes, 5 for the stores): 207 us (10-bit codes 238), where a
+// thread per pair of dims and row-major planes take 272.  512 threads rather
+// than 1024: 4 % slower on uint16 codes, 7 % faster on 10-bit ones and a fifth
+// on few rows.
+struct DecodeRows {
+  CodeSrc cs;
+  const float *C;
+  int M, units, items, chunk;
+  int bits;            // of a code in the 32-bit words that hold a row's (VEC > 0)
+  int64_t v0, rows, pitch;
+  const float *amax;
+  __half *hi, *lo;
+  int cols;            // of the planes
+  int pairs;           // codebooks may be copied two floats at a time
+};
+
+constexpr int kRowThreads = 512;
+
+template <int DS>
+struct RowUnit {
+  static constexpr int G = DS % 8 == 0 ? 1 : DS % 4 == 0 ? 2 : DS % 2 == 0 ? 4 : 8;
+  static constexpr int Q = G * DS / 8;
+  static constexpr int V4 = DS / 4, V2 = DS % 4 / 2, V1 = DS % 2;
+};
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(float *dst, const float *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src),
+               "n"(BYTES)
+               : "memory");
+}
+
+// VEC: a row's codes of the unit come in the aligned words of 16 bytes (4) or 4
+// (1) that hold them, or one by one (0; a last unit of fewer subspaces too).
+template <int DS, int LL, int VEC>
+__global__ void __launch_bounds__(kRowThreads) loss_decode_rows_kernel(const DecodeRows a) {
+  using U = RowUnit<DS>;
+  constexpr int N = U::G * LL;                       // codes of a row
+  constexpr int S = VEC == 4 ? 128 : 32;             // bits of a word as loaded
+  constexpr int W10 = (N * 10 + 2 * S - 4) / S, W16 = (N * 16 + 2 * S - 18) / S;
+  constexpr int W = (W10 > W16 ? W10 : W16) * (S / 32);
+  extern __shared__ __align__(16) float books[];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int K = a.cs.K, tid = threadIdx.x, P = a.cs.P;
+  const float se = scale_e(a.amax, LL);
+  const int book = (K * DS + 3) & ~3;                // a codebook's floats
+  // where dim j of codeword k lies
+  auto place = [&](int k, int j) {
+    return j < U::V4 * 4             ? (j >> 2) * 4 * K + 4 * k + (j & 3)
+           : j < U::V4 * 4 + U::V2 * 2 ? U::V4 * 4 * K + 2 * k + (j & 1)
+                                       : (DS - 1) * K + k;
+  };
+  for (int u = blockIdx.x; u < a.items; u += gridDim.x) {
+    const int g = u % a.units, m0 = g * U::G, p0 = m0 * LL;
+    const bool whole = m0 + U::G <= a.M;
+    const int64_t r0 = (int64_t)(u / a.units) * a.chunk;
+    const int64_t left = a.rows - r0, full = ((a.rows + 7) & ~7ll) - r0;   // zeros to a row of 8
+    const int n = (int)(left < a.chunk ? left : a.chunk);
+    const int n8 = (int)(full < a.chunk ? full : a.chunk);
+    // the words with the unit's codes in the chunk's first row, the first
+    // code's place in them
+    const int64_t step = ((int64_t)a.bits * P + 7) / 8;
+    const int bit = a.bits * p0, sh = bit & (S - 1), nw = (sh + a.bits * N + S - 1) / S;
+    const uint8_t *src =
+        static_cast<const uint8_t *>(a.cs.codes) + (a.v0 + r0) * step + bit / S * (S / 8);
+    const bool each = VEC == 0 || !whole;
+    uint32_t next[W];
+    auto fetch = [&](int r) {
+      if (each || r >= n) return;
+      const uint8_t *p = src + r * step;
+      if (VEC == 4) {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+          if (i < nw) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            next[4 * i] = x.x;
+            next[4 * i + 1] = x.y;
+            next[4 * i + 2] = x.z;
+            next[4 * i + 3] = x.w;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (i < nw) next[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+      }
+    };
+    fetch(tid);
+    __syncthreads();                                 // the last item's books are read
+    const int have = whole ? N : (a.M - m0) * LL;    // codebooks; zeros for the rest
+    const float *c0 = a.C + (int64_t)p0 * K * DS;
+    for (int b = 0; b < N; ++b) {
+      float *d = books + b * book;
+      const float *c = c0 + (int64_t)b * K * DS;
+      if (b >= have) {
+        for (int i = tid; i < book; i += kRowThreads) d[i] = 0.f;
+      } else if (DS % 2 == 0 && a.pairs) {
+        for (int i = 2 * tid; i < K * DS; i += 2 * kRowThreads)
+          copy_async<8>(d + place(i / DS, i % DS), c + i);
+      } else {
+        for (int i = tid; i < K * DS; i += kRowThreads) copy_async<4>(d + place(i / DS, i % DS), c + i);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    for (int r = tid; r < n8; r += kRowThreads) {
+      uint32_t c[N];
+      if (each) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = r < n && p0 + i < P ? a.cs.raw(a.v0 + r0 + r, p0 + i) : 0u;
+      } else {
+        uint32_t w[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = next[i];
+        if (sh) {
+          if (S > 32 && (sh & 64)) {
+#pragma unroll
+            for (int i = 0; i + 2 < W; ++i) w[i] = w[i + 2];
+          }
+          if (S > 32 && (sh & 32)) {
+#pragma unroll
+            for (int i = 0; i + 1 < W; ++i) w[i] = w[i + 1];
+          }
+#pragma unroll
+          for (int i = 0; i + 1 < W; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], sh & 31);
+          w[W - 1] >>= sh & 31;
+        }
+        if (a.bits == 16) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) c[i] = w[i / 2] >> (16 * (i & 1)) & 0xFFFFu;
+        } else if (a.bits == 8) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) c[i] = w[i / 4] >> (8 * (i & 3)) & 0xFFu;
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            c[i] = __funnelshift_r(w[10 * i / 32], 10 * i / 32 + 1 < W ? w[10 * i / 32 + 1] : 0u,
+                                   10 * i % 32) & 1023u;
+        }
+      }
+      fetch(r + kRowThreads);
+      float e[U::G * DS];
+#pragma unroll
+      for (int m = 0; m < U::G; ++m) {
+#pragma unroll
+        for (int l = 0; l < LL; ++l) {
+          const int k = (int)a.cs.fix(c[m * LL + l]);
+          const float *b = books + (m * LL + l) * book;
+          float x[DS];
+#pragma unroll
+          for (int v = 0; v < U::V4; ++v) {
+            const float4 y = *reinterpret_cast<const float4 *>(b + v * 4 * K + 4 * k);
+            x[4 * v] = y.x;
+            x[4 * v + 1] = y.y;
+            x[4 * v + 2] = y.z;
+            x[4 * v + 3] = y.w;
+          }
+          if (U::V2) {
+            const float2 y = *reinterpret_cast<const float2 *>(b + U::V4 * 4 * K + 2 * k);
+            x[U::V4 * 4] = y.x;
+            x[U::V4 * 4 + (U::V2 ? 1 : 0)] = y.y;
+          }
+          if (U::V1) x[DS - 1] = b[(DS - 1) * K + k];
+#pragma unroll
+          for (int j = 0; j < DS; ++j)
+            e[m * DS + j] = l == 0 ? x[j] : __fadd_rn(e[m * DS + j], x[j]);
+        }
+      }
+      const float f = r < n ? se : 0.f;
+#pragma unroll
+      for (int q = 0; q < U::Q; ++q) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          split_pair(__fmul_rn(e[8 * q + 2 * i], f), __fmul_rn(e[8 * q + 2 * i + 1], f), h[i], l[i]);
+        if (g * U::Q + q < a.cols) {
+          const int64_t at = ((g * U::Q + q) * a.pitch + r0 + r) * 8;
+          *reinterpret_cast<uint4 *>(a.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4 *>(a.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
       }
     }
   }
@@ -608,9 +823,93 @@ const void *decode_fn(int L) {
 }
 }  // namespace
 
+namespace {
+template <int DS, int LL>
+const void *rows_fn(int vec) {
+  if (vec == 4) return reinterpret_cast<const void *>(&loss_decode_rows_kernel<DS, LL, 4>);
+  if (vec) return reinterpret_cast<const void *>(&loss_decode_rows_kernel<DS, LL, 1>);
+  return reinterpret_cast<const void *>(&loss_decode_rows_kernel<DS, LL, 0>);
+}
+template <int DS>
+const void *rows_fn(int L, int vec) {
+  return L == 1 ? rows_fn<DS, 1>(vec) : L == 2 ? rows_fn<DS, 2>(vec) : L == 3 ? rows_fn<DS, 3>(vec)
+                                                                            : nullptr;
+}
+
+// Rows per chunk: the shortest time of the last CTA, where an item costs its
+// rows and `fill` more for its codebooks.
+int64_t chunk_rows(int64_t rows, int64_t groups, int64_t ctas, int64_t step, int64_t fill,
+                   int64_t most) {
+  int64_t best = 0, chunk = step;
+  for (int64_t c = step; c - step < rows && c <= most; c += step) {
+    const int64_t waves = ((rows + c - 1) / c * groups + ctas - 1) / ctas;
+    const int64_t cost = waves * (c + fill);
+    if (best == 0 || cost < best) {
+      best = cost;
+      chunk = c;
+    }
+  }
+  return chunk;
+}
+}  // namespace
+
+// A thread a row: dims and levels that it is compiled for, where a unit's
+// codebooks fit in shared memory.  False: not here.
+static bool launch_decode_rows(const CodeSrc &cs, const float *C, int M, int L, int ds, int64_t v0,
+                               int64_t rows, int64_t pitch, const float *amax, __half *hi,
+                               __half *lo, const DevInfo &di, cudaStream_t s, cudaError_t *err) {
+  const int g = ds % 8 == 0 ? 1 : ds % 4 == 0 ? 2 : ds % 2 == 0 ? 4 : 8, n = g * L;
+  const size_t smem = (size_t)n * ((cs.K * ds + 3) & ~3) * 4;
+  if (smem > 220 * 1024) return false;
+  const int64_t bits = cs.fmt == RQ_CODES_U16       ? 16
+                       : cs.fmt == RQ_CODES_U8       ? 8
+                       : cs.fmt == RQ_CODES_PACKED10 ? 10
+                                                     : 0;
+  const int64_t row = (bits * cs.P + 7) / 8;
+  const int vec = bits == 0 ? 0 : row % 16 == 0 ? 4 : row % 4 == 0 ? 1 : 0;
+  const void *fn = ds == 2   ? rows_fn<2>(L, vec)
+                   : ds == 3 ? rows_fn<3>(L, vec)
+                   : ds == 4 ? rows_fn<4>(L, vec)
+                   : ds == 5 ? rows_fn<5>(L, vec)
+                   : ds == 6 ? rows_fn<6>(L, vec)
+                   : ds == 8 ? rows_fn<8>(L, vec)
+                             : nullptr;
+  if (!fn) return false;
+  DecodeRows a;
+  a.cs = cs;
+  a.C = C;
+  a.M = M;
+  a.units = (M + g - 1) / g;
+  a.bits = (int)bits;
+  a.v0 = v0;
+  a.rows = rows;
+  a.pitch = pitch;
+  a.amax = amax;
+  a.hi = hi;
+  a.lo = lo;
+  a.cols = (M * ds + 7) / 8;
+  a.pairs = (reinterpret_cast<uintptr_t>(C) & 7) == 0 && cs.K * ds % 2 == 0;
+  if ((*err = ensure_smem_limit(fn, di.device, smem)) != cudaSuccess) return true;
+  const int64_t ctas = (int64_t)di.sms * occupancy_cached(fn, di.device, kRowThreads, smem);
+  a.chunk = (int)chunk_rows(rows, a.units, ctas, kRowThreads,
+                            (int64_t)(650 * smem / (192 * 1024)) + 64, 16384);
+  const int64_t items = (rows + a.chunk - 1) / a.chunk * a.units;
+  if (items > 0x7fffffff) {
+    *err = cudaErrorInvalidValue;
+    return true;
+  }
+  a.items = (int)items;
+  void *args[] = {&a};
+  *err = launch_maybe_pdl(fn, dim3((unsigned)(items < ctas ? items : ctas)), dim3(kRowThreads), smem,
+                          s, args, true);
+  return true;
+}
+
 cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, int ds, int64_t v0,
                                int64_t rows, int64_t pitch, const float *amax, __half *hi,
                                __half *lo, const DevInfo &di, cudaStream_t s) {
+  cudaError_t done = cudaSuccess;
+  if (launch_decode_rows(cs, C, M, L, ds, v0, rows, pitch, amax, hi, lo, di, s, &done)) return done;
   DecodeArgs a;
   a.cs = cs;
   a.C = C;
@@ -654,15 +953,7 @@ cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, 
   // and the load of its books (as long as about 300 rows of 48 KB books a
   // subspace, less for smaller ones)
   const int64_t load = in_smem ? 300 * a.book / (2 * 1024 * 6) + 32 : 32;
-  int64_t best = 0, chunk = 1;
-  for (int64_t c = rstep; c - rstep < rows && c <= 4096; c += rstep) {
-    const int64_t waves = ((rows + c - 1) / c * a.groups + ctas - 1) / ctas;
-    const int64_t cost = waves * (c + load);
-    if (best == 0 || cost < best) {
-      best = cost;
-      chunk = c;
-    }
-  }
+  const int64_t chunk = chunk_rows(rows, a.groups, ctas, rstep, load, 4096);
   a.chunk = (int)chunk;
   const int64_t items = (rows + chunk - 1) / chunk * a.groups;
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
