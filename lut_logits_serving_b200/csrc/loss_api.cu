@@ -106,9 +106,10 @@ struct Choice {
 
 // Estimated microseconds of the ways, from measurements at 256000 rows of 768
 // codes (V P = 197 million) and at heads a few hundred times smaller:
-//   decoding           1070 for 295 million pairs of dims, two levels
-//   a tensor product   V D 128 per token tile at 1.1 PFLOP/s (a third more
-//                      for the first and the last wave of small ones: 12)
+//   decoding           810 for 295 million pairs of dims, two levels; 1070
+//                      where a thread has a pair of dims, not a row
+//   a tensor product   per million elements of E 0.33 to read them and 0.47
+//                      per tile of 128 tokens
 //   serving, B <= 4    116 per token (tables in shared memory)
 //   serving, groups    tables through L2: 14 TB/s, and at least 0.09 (10 bits
 //                      0.13, bytes 0.24) per column and row a thread has;
@@ -118,10 +119,11 @@ struct Choice {
 // The serving kernels' fallback for odd layouts walks a row's codes one by one
 // (385 where the tensor cores take 45) and is never chosen.
 double decode_us(const rq_dims &d) {
-  return 8 + (double)d.V * d.D / 2e6 * (2.2 + 0.7 * d.L) * ((d.D / d.M) % 2 ? 1.25 : 1.0);
+  return 8 + (double)d.V * d.D / 2e6 * (1.5 + 0.6 * d.L) *
+                 (decode_rows_ok(d.K, d.L, d.D / d.M) ? 1.0 : 1.35);
 }
 double product_us(const rq_dims &d, int N) {
-  return 12 + 3.0 * 2 * 128 * ((N + 127) / 128) * (double)d.V * d.D / 1.1e9;
+  return 12 + (0.33 + 0.47 * ((N + 127) / 128)) * (double)d.V * d.D / 1e6;
 }
 double sums_us(const rq_dims &d, int pairs) {
   return 8 + 1.95 * pairs * (double)d.V * d.M * d.L / 1e6;

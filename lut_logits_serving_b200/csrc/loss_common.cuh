@@ -149,6 +149,7 @@ cudaError_t launch_loss_gemm(int mode, const GemmPlanes &A, const GemmPlanes &B,
 // Rows of a piece decoded into fp16 hi / lo planes and the other row-wise
 // kernels (loss_rows.cu).
 cudaError_t launch_loss_widen_h(const void *h, int64_t n, float *out, cudaStream_t s);
+bool decode_rows_ok(int K, int L, int ds);   // the faster of its kernels has the size
 cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, int ds, int64_t v0,
                                int64_t rows, int64_t pitch, const float *amax, __half *hi,
                                __half *lo, const DevInfo &di, cudaStream_t s);

@@ -853,14 +853,23 @@ int64_t chunk_rows(int64_t rows, int64_t groups, int64_t ctas, int64_t step, int
 }
 }  // namespace
 
+// Subspaces whose dims fill whole columns of 8.
+static int unit_subspaces(int ds) { return ds % 8 == 0 ? 1 : ds % 4 == 0 ? 2 : ds % 2 == 0 ? 4 : 8; }
+
+static size_t unit_bytes(int K, int L, int ds) {
+  return (size_t)unit_subspaces(ds) * L * (((size_t)K * ds + 3) & ~(size_t)3) * 4;
+}
+
 // A thread a row: dims and levels that it is compiled for, where a unit's
-// codebooks fit in shared memory.  False: not here.
-static bool launch_decode_rows(const CodeSrc &cs, const float *C, int M, int L, int ds, int64_t v0,
+// codebooks fit in shared memory.
+bool decode_rows_ok(int K, int L, int ds) {
+  return (ds == 8 || (ds >= 2 && ds <= 6)) && L <= 3 && unit_bytes(K, L, ds) <= 220 * 1024;
+}
+
+static cudaError_t launch_decode_rows(const CodeSrc &cs, const float *C, int M, int L, int ds, int64_t v0,
                                int64_t rows, int64_t pitch, const float *amax, __half *hi,
-                               __half *lo, const DevInfo &di, cudaStream_t s, cudaError_t *err) {
-  const int g = ds % 8 == 0 ? 1 : ds % 4 == 0 ? 2 : ds % 2 == 0 ? 4 : 8, n = g * L;
-  const size_t smem = (size_t)n * ((cs.K * ds + 3) & ~3) * 4;
-  if (smem > 220 * 1024) return false;
+                               __half *lo, const DevInfo &di, cudaStream_t s) {
+  const size_t smem = unit_bytes(cs.K, L, ds);
   const int64_t bits = cs.fmt == RQ_CODES_U16       ? 16
                        : cs.fmt == RQ_CODES_U8       ? 8
                        : cs.fmt == RQ_CODES_PACKED10 ? 10
@@ -874,12 +883,12 @@ static bool launch_decode_rows(const CodeSrc &cs, const float *C, int M, int L, 
                    : ds == 6 ? rows_fn<6>(L, vec)
                    : ds == 8 ? rows_fn<8>(L, vec)
                              : nullptr;
-  if (!fn) return false;
+  if (!fn) return cudaErrorInvalidValue;
   DecodeRows a;
   a.cs = cs;
   a.C = C;
   a.M = M;
-  a.units = (M + g - 1) / g;
+  a.units = (M + unit_subspaces(ds) - 1) / unit_subspaces(ds);
   a.bits = (int)bits;
   a.v0 = v0;
   a.rows = rows;
@@ -889,27 +898,24 @@ static bool launch_decode_rows(const CodeSrc &cs, const float *C, int M, int L, 
   a.lo = lo;
   a.cols = (M * ds + 7) / 8;
   a.pairs = (reinterpret_cast<uintptr_t>(C) & 7) == 0 && cs.K * ds % 2 == 0;
-  if ((*err = ensure_smem_limit(fn, di.device, smem)) != cudaSuccess) return true;
+  const cudaError_t e = ensure_smem_limit(fn, di.device, smem);
+  if (e != cudaSuccess) return e;
   const int64_t ctas = (int64_t)di.sms * occupancy_cached(fn, di.device, kRowThreads, smem);
   a.chunk = (int)chunk_rows(rows, a.units, ctas, kRowThreads,
                             (int64_t)(650 * smem / (192 * 1024)) + 64, 16384);
   const int64_t items = (rows + a.chunk - 1) / a.chunk * a.units;
-  if (items > 0x7fffffff) {
-    *err = cudaErrorInvalidValue;
-    return true;
-  }
+  if (items > 0x7fffffff) return cudaErrorInvalidValue;
   a.items = (int)items;
   void *args[] = {&a};
-  *err = launch_maybe_pdl(fn, dim3((unsigned)(items < ctas ? items : ctas)), dim3(kRowThreads), smem,
+  return launch_maybe_pdl(fn, dim3((unsigned)(items < ctas ? items : ctas)), dim3(kRowThreads), smem,
                           s, args, true);
-  return true;
 }
 
 cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, int ds, int64_t v0,
                                int64_t rows, int64_t pitch, const float *amax, __half *hi,
                                __half *lo, const DevInfo &di, cudaStream_t s) {
-  cudaError_t done = cudaSuccess;
-  if (launch_decode_rows(cs, C, M, L, ds, v0, rows, pitch, amax, hi, lo, di, s, &done)) return done;
+  if (decode_rows_ok(cs.K, L, ds))
+    return launch_decode_rows(cs, C, M, L, ds, v0, rows, pitch, amax, hi, lo, di, s);
   DecodeArgs a;
   a.cs = cs;
   a.C = C;
