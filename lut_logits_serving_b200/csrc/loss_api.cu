@@ -226,13 +226,10 @@ Layout layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
     x.fused = a.take((int64_t)x.fused_bytes);
   }
   if (!grad) {
-    int parts = loss_stat_parts(d.V);
     if (!x.how.serve) {
-      parts = total_parts(d, n, rows);
+      int parts = total_parts(d, n, rows);
       if (total_parts(d, last, rows) > parts) parts = total_parts(d, last, rows);
-    }
-    x.stat = a.take((int64_t)parts * n * 8);
-    if (!x.how.serve) {
+      x.stat = a.take((int64_t)parts * n * 8);
       x.sid = a.take(n * k * 4);
       x.sj = a.take(n * k * 4);
     }
@@ -420,7 +417,7 @@ cudaError_t tensor_loss(const Problem &all, const Layout &x, float *loss, float 
       part0 += loss_stats_parts(q.N, rows);
       return launch_loss_gemm(kGemmStats, h_planes(q, x, ws), w_planes(q, x, rows, ws), g, di, s);
     }));
-    RQ_TRY(launch_loss_finish(at<float2>(ws, x.stat), part0, (int)x.chunk, q.N, d.V, q.t, y, false,
+    RQ_TRY(launch_loss_finish(at<float2>(ws, x.stat), part0, (int)x.chunk, q.N, d.V, q.t, y,
                               loss + n0, lse + n0, di.err, s));
   }
   return cudaSuccess;
@@ -601,12 +598,8 @@ int run_loss(const Problem &q, float *loss, float *lse, void *ws, size_t ws_byte
   if (!x.how.serve) return status_of(tensor_loss(q, x, loss, lse, ws, di, s));
   const int st = serve_logits(q, x, ws, s);
   if (st != RQ_OK) return st;
-  e = launch_loss_logit_stats(at<float>(ws, x.logits), q.N, q.d.V, q.t.beta, at<float2>(ws, x.stat),
-                              q.N, s);
-  if (e == cudaSuccess)
-    e = launch_loss_finish(at<float2>(ws, x.stat), loss_stat_parts(q.d.V), q.N, q.N, q.d.V, q.t,
-                           at<float>(ws, x.logits), true, loss, lse, di.err, s);
-  return status_of(e);
+  return status_of(
+      launch_loss_logits(at<float>(ws, x.logits), q.N, q.d.V, q.t, loss, lse, di.err, s));
 }
 
 int run_grad(const Problem &q, const float *lse, const float *w, const void *index, void *dh,

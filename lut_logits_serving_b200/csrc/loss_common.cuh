@@ -153,11 +153,6 @@ bool decode_rows_ok(int K, int L, int ds);   // the faster of its kernels has th
 cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, int ds, int64_t v0,
                                int64_t rows, int64_t pitch, const float *amax, __half *hi,
                                __half *lo, const DevInfo &di, cudaStream_t s);
-// (max, sum) parts of logits [N][V] at 1 / T = beta
-int loss_stat_parts(int64_t V);
-cudaError_t launch_loss_logit_stats(const float *logits, int64_t N, int64_t V, float beta,
-                                    float2 *stat, int stat_ld, cudaStream_t s);
-
 // The sparse probabilities of a loss: target ids (k = 1, val null) or a
 // teacher's lists.
 struct LossTargets {
@@ -195,11 +190,13 @@ struct SplitArgs {
   __half *hi, *lo, *dhi, *dlo;   // lo and dlo null: bf16 h, which one plane holds
 };
 cudaError_t launch_loss_split(const SplitArgs &a, cudaStream_t s);
-// lse and loss from the parts and the listed ids' logits: y[n * k + j], or, with
-// y_is_logits, y[n * V + id].
+// lse and loss from logits [N][V] of a few tokens, or from the parts of
+// kGemmStats and the listed ids' logits y [N][k]
+cudaError_t launch_loss_logits(const float *logits, int64_t N, int64_t V, const LossTargets &t,
+                               float *loss, float *lse, unsigned *err, cudaStream_t s);
 cudaError_t launch_loss_finish(const float2 *stat, int parts, int stat_ld, int64_t N, int64_t V,
-                               const LossTargets &t, const float *y, bool y_is_logits, float *loss,
-                               float *lse, unsigned *err, cudaStream_t s);
+                               const LossTargets &t, const float *y, float *loss, float *lse,
+                               unsigned *err, cudaStream_t s);
 // logits [N][V] -> their gradients [N][pitch], dense part
 cudaError_t launch_loss_dz(const float *logits, int64_t N, int64_t V, const float *lse,
                            const float *f, float beta, float cap, float *dz, int64_t pitch,

@@ -549,39 +549,6 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
   return make_float2(m, a.y * expf(a.x - m) + b.y * expf(b.x - m));
 }
 
-constexpr int kStatCols = 2048;   // logits one block folds into a part
-
-__global__ void __launch_bounds__(256) loss_logit_stats_kernel(const float *__restrict__ logits,
-                                                               int64_t V, float beta,
-                                                               float2 *__restrict__ stat,
-                                                               int stat_ld) {
-  griddep_launch_dependents();
-  griddep_wait();
-  __shared__ float2 red[8];
-  const int64_t n = blockIdx.y, c0 = (int64_t)blockIdx.x * kStatCols;
-  float x[kStatCols / 256], m = -INFINITY, s = 0.f;
-#pragma unroll
-  for (int i = 0; i < kStatCols / 256; ++i) {
-    const int64_t c = c0 + i * 256 + threadIdx.x;
-    x[i] = c < V ? __fmul_rn(logits[n * V + c], beta) : -INFINITY;
-    m = fmaxf(m, x[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < kStatCols / 256; ++i)
-    s += m > -INFINITY ? expf(x[i] - m) : (x[i] != x[i] ? x[i] : 0.f);
-  float2 p = make_float2(m, s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    p = join(p, make_float2(__shfl_xor_sync(0xffffffffu, p.x, o),
-                            __shfl_xor_sync(0xffffffffu, p.y, o)));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = p;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 8; ++w) p = join(p, red[w]);
-    stat[(int64_t)blockIdx.x * stat_ld + n] = p;
-  }
-}
-
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -597,34 +564,11 @@ __device__ __forceinline__ float warp_max(float x) {
 // logit is above -inf.
 __device__ __forceinline__ bool listed(int32_t id, int64_t V) { return id >= 0 && id < V; }
 
-// Rows 32 b .. 32 b + 31: the parts joined by 32 threads a row, then one warp
-// per row forms the loss.
-__global__ void __launch_bounds__(1024) loss_finish_kernel(const float2 *__restrict__ stat,
-                                                           int parts, int stat_ld, int64_t N,
-                                                           int64_t V, const LossTargets t,
-                                                           const float *__restrict__ y,
-                                                           int y_is_logits,
-                                                           float *__restrict__ loss,
-                                                           float *__restrict__ lse, unsigned *err) {
-  griddep_launch_dependents();
-  griddep_wait();
-  __shared__ float2 red[32][33];
-  const int r = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t row = (int64_t)blockIdx.x * 32 + r;
-  float2 p = make_float2(-INFINITY, 0.f);
-  if (row < N) {
-#pragma unroll 4
-    for (int i = w; i < parts; i += 32) p = join(p, stat[(int64_t)i * stat_ld + row]);
-  }
-  red[w][r] = p;
-  __syncthreads();
-  const int64_t n = (int64_t)blockIdx.x * 32 + w;   // this warp's row
-  if (n >= N) return;
-  p = red[r][w];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    p = join(p, make_float2(__shfl_xor_sync(0xffffffffu, p.x, o),
-                            __shfl_xor_sync(0xffffffffu, p.y, o)));
+// A row's loss and log-sum-exp from its statistics p, by one warp.
+__device__ void finish_row(float2 p, int64_t n, int64_t V, const LossTargets &t,
+                           const float *__restrict__ y, bool y_is_logits, float *__restrict__ loss,
+                           float *__restrict__ lse, unsigned *err) {
+  const int lane = threadIdx.x & 31;
   // lse = p.x + ls.  A loss takes p.x - y first: where a listed logit is the
   // maximum that is exactly 0, and a confident row's small loss keeps its bits
   // (the listed logits are those that the statistics were made of).
@@ -633,25 +577,25 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const float2 *__restr
   auto logit = [&](int j) { return y_is_logits ? y[n * V + id[j]] : y[n * t.k + j]; };
   float out = 0.f;
   if (t.val == nullptr) {
-    if (r == 0) {
+    if (lane == 0) {
       if (id[0] >= V) atomicOr(err, RQ_DEVERR_BAD_ID);
       if (listed(id[0], V)) out = (p.x - __fmul_rn(logit(0), t.beta)) + ls;
     }
   } else {
     const float *val = t.val + n * t.k;
     float m = -INFINITY;
-    for (int j = r; j < t.k; j += 32) {
+    for (int j = lane; j < t.k; j += 32) {
       if (id[j] >= V) atomicOr(err, RQ_DEVERR_BAD_ID);
       if (listed(id[j], V)) m = fmaxf(m, val[j] * t.beta);
     }
     m = warp_max(m);
     float z = 0.f, a = 0.f;
     if (m > -INFINITY) {
-      for (int j = r; j < t.k; j += 32)
+      for (int j = lane; j < t.k; j += 32)
         if (listed(id[j], V)) z += expf(val[j] * t.beta - m);
       z = warp_sum(z);
       const float logz = logf(z);
-      for (int j = r; j < t.k; j += 32) {
+      for (int j = lane; j < t.k; j += 32) {
         if (!listed(id[j], V)) continue;
         const float d = val[j] * t.beta - m, e = expf(d);
         if (e > 0.f || e != e)
@@ -660,10 +604,122 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const float2 *__restr
       out = warp_sum(a) / z * t.T * t.T;
     }
   }
-  if (r == 0) {
+  if (lane == 0) {
     loss[n] = out;
     lse[n] = l;
   }
+}
+
+__device__ __forceinline__ float2 warp_join(float2 p) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    p = join(p, make_float2(__shfl_xor_sync(0xffffffffu, p.x, o),
+                            __shfl_xor_sync(0xffffffffu, p.y, o)));
+  return p;
+}
+
+// Few tokens' logits [N][V]: a cluster a row, each CTA a share of its columns,
+// the shares joined in the first CTA's shared memory.  One launch for two (parts
+// in global memory, joined by a second kernel) is 3 us of a small call's 28;
+// with 256000 columns 32 rows take 16.6 us instead of 17.8, a single row 7.9
+// instead of 6.
+constexpr int kServeCtas = 8;
+
+__global__ void __cluster_dims__(kServeCtas, 1, 1) __launch_bounds__(1024, 2)
+    loss_logits_kernel(const float *__restrict__ logits, int64_t V, const LossTargets t,
+                       float *__restrict__ loss, float *__restrict__ lse, unsigned *err) {
+  __shared__ float2 red[32];
+  __shared__ __align__(8) float2 shares[kServeCtas];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t n = blockIdx.y, share = ((V + kServeCtas - 1) / kServeCtas + 3) & ~3ll;
+  const int rank = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c0 = rank * share, c1 = c0 + share < V ? c0 + share : V;
+  const float *row = logits + n * V;
+  const bool quads = V % 4 == 0;                     // (the rows then start on 16 bytes)
+  float2 p = make_float2(-INFINITY, 0.f);
+  for (int64_t c = c0; c < c1; c += 16 * 1024) {
+    float x[16], m = -INFINITY, s = 0.f;
+    // all loads under way before the first use
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int64_t q = c + ((int64_t)i * 1024 + threadIdx.x * 4);
+      if (quads) {
+        const float4 v = q < c1 ? *reinterpret_cast<const float4 *>(row + q)
+                                : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        x[i] = v.x;
+        x[i + 1] = v.y;
+        x[i + 2] = v.z;
+        x[i + 3] = v.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i + j] = q + j < c1 ? row[q + j] : -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      x[i] = __fmul_rn(x[i], t.beta);
+      m = fmaxf(m, x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += m > -INFINITY ? expf(x[i] - m) : (x[i] != x[i] ? x[i] : 0.f);
+    p = join(p, make_float2(m, s));
+  }
+  p = warp_join(p);
+  if (lane == 0) red[warp] = p;
+  __syncthreads();
+  if (warp == 0) {
+    p = warp_join(red[lane]);
+    if (lane == 0) {
+      uint32_t at;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_addr(shares + rank)));
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(p.x), "f"(p.y)
+                   : "memory");
+    }
+  }
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+  if (rank != 0 || warp != 0) return;
+  p = warp_join(lane < kServeCtas ? shares[lane] : make_float2(-INFINITY, 0.f));
+  finish_row(p, n, V, t, logits, true, loss, lse, err);
+}
+
+// Rows 8 b .. 8 b + 7: the parts joined by 128 threads a row, then one warp a
+// row forms the loss.
+constexpr int kFinishRows = 8;
+
+__global__ void __launch_bounds__(1024) loss_finish_kernel(const float2 *__restrict__ stat,
+                                                           int parts, int stat_ld, int64_t N,
+                                                           int64_t V, const LossTargets t,
+                                                           const float *__restrict__ y,
+                                                           float *__restrict__ loss,
+                                                           float *__restrict__ lse, unsigned *err) {
+  constexpr int kLanes = 1024 / kFinishRows;
+  __shared__ float2 red[kLanes][kFinishRows + 1];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int r = threadIdx.x % kFinishRows, w = threadIdx.x / kFinishRows;
+  const int64_t row = (int64_t)blockIdx.x * kFinishRows + r;
+  float2 p = make_float2(-INFINITY, 0.f);
+  if (row < N) {
+#pragma unroll 8
+    for (int i = w; i < parts; i += kLanes) p.x = fmaxf(p.x, stat[(int64_t)i * stat_ld + row].x);
+#pragma unroll 8
+    for (int i = w; i < parts; i += kLanes) {
+      const float2 q = stat[(int64_t)i * stat_ld + row];
+      p.y += p.x > -INFINITY ? q.y * expf(q.x - p.x) : q.y;
+    }
+  }
+  red[w][r] = p;
+  __syncthreads();
+  const int lane = threadIdx.x & 31, v = threadIdx.x >> 5;
+  const int64_t n = (int64_t)blockIdx.x * kFinishRows + v;      // this warp's row
+  if (v >= kFinishRows || n >= N) return;
+  p = red[lane][v];
+#pragma unroll
+  for (int i = 32; i < kLanes; i += 32) p = join(p, red[lane + i][v]);
+  finish_row(warp_join(p), n, V, t, y, false, loss, lse, err);
 }
 
 // ------------------------------------------------------------- gradient, sparse part
@@ -973,17 +1029,17 @@ cudaError_t launch_loss_split(const SplitArgs &a, cudaStream_t s) {
   return pdl_launch(loss_split_kernel, dim3((unsigned)a.N), dim3(256), (size_t)0, s, a);
 }
 
-int loss_stat_parts(int64_t V) { return (int)((V + kStatCols - 1) / kStatCols); }
-
-cudaError_t launch_loss_logit_stats(const float *logits, int64_t N, int64_t V, float beta,
-                                    float2 *stat, int stat_ld, cudaStream_t s) {
-  return pdl_launch(loss_logit_stats_kernel, dim3(loss_stat_parts(V), (unsigned)N), dim3(256), (size_t)0, s, logits, V, beta, stat, stat_ld);
+cudaError_t launch_loss_logits(const float *logits, int64_t N, int64_t V, const LossTargets &t,
+                               float *loss, float *lse, unsigned *err, cudaStream_t s) {
+  return pdl_launch(loss_logits_kernel, dim3(kServeCtas, (unsigned)N), dim3(1024), (size_t)0, s,
+                    logits, V, t, loss, lse, err);
 }
 
 cudaError_t launch_loss_finish(const float2 *stat, int parts, int stat_ld, int64_t N, int64_t V,
-                               const LossTargets &t, const float *y, bool y_is_logits, float *loss,
-                               float *lse, unsigned *err, cudaStream_t s) {
-  return pdl_launch(loss_finish_kernel, dim3(blocks_of(N, 32)), dim3(1024), (size_t)0, s, stat, parts, stat_ld, N, V, t, y, y_is_logits, loss, lse, err);
+                               const LossTargets &t, const float *y, float *loss, float *lse,
+                               unsigned *err, cudaStream_t s) {
+  return pdl_launch(loss_finish_kernel, dim3(blocks_of(N, kFinishRows)), dim3(1024), (size_t)0, s,
+                    stat, parts, stat_ld, N, V, t, y, loss, lse, err);
 }
 
 cudaError_t launch_loss_dz(const float *logits, int64_t N, int64_t V, const float *lse,
