@@ -321,8 +321,8 @@ Problem slice(const Problem &q, int64_t n0, int64_t n) {
 }
 
 // The sorted lists of a sweep's tokens, of a gradient with their probabilities
-// and weights, and (`scales`) the scales of the tensor cores' operands; those of
-// the codebooks with the first sweep.
+// and weights, and (`scales`) the hidden states as planes and the tensor cores'
+// scales; those of the codebooks with the first sweep.
 cudaError_t begin(const Problem &q, const Layout &x, bool scales, bool first, bool grad,
                   const float *w, void *ws, const DevInfo &di, cudaStream_t s) {
   BeginArgs a{};
@@ -332,7 +332,12 @@ cudaError_t begin(const Problem &q, const Layout &x, bool scales, bool first, bo
   a.h = q.h;
   a.bf16 = q.bf16;
   a.D = q.d.D;
-  a.sh = scales ? at<float>(ws, x.sh) : nullptr;
+  a.pitch = x.hp;
+  if (scales) {
+    a.hi = at<__half>(ws, x.hh);
+    a.lo = q.bf16 ? nullptr : at<__half>(ws, x.hl);
+    a.sh = at<float>(ws, x.sh);
+  }
   a.hw = grad && !x.how.sums ? at<float>(ws, x.hw) : nullptr;
   a.t = q.t;
   a.rows = q.N;
@@ -346,33 +351,26 @@ cudaError_t begin(const Problem &q, const Layout &x, bool scales, bool first, bo
   return launch_loss_begin(a, s);
 }
 
-// The hidden states as planes, with `dw` also as h^T dz takes them.
-cudaError_t split(const Problem &q, const Layout &x, bool dw, void *ws, cudaStream_t s) {
-  SplitArgs a{};
-  a.h = q.h;
-  a.bf16 = q.bf16;
-  a.N = q.N;
-  a.D = q.d.D;
-  a.pitch = x.hp;
-  a.sh = at<float>(ws, x.sh);
-  a.hi = at<__half>(ws, x.hh);
-  a.lo = q.bf16 ? nullptr : at<__half>(ws, x.hl);
-  if (dw) {
-    a.hw = at<float>(ws, x.hw);
-    a.f = at<float>(ws, x.f);
-    a.sdw = at<float>(ws, x.amax) + kAmaxBlocks;
-    a.dhi = at<__half>(ws, x.gh);
-    a.dlo = q.bf16 ? nullptr : at<__half>(ws, x.gl);
-  }
-  return launch_loss_split(a, s);
-}
-
-// Piece [v0, v0 + rows) decoded.
-cudaError_t decode(const Problem &q, const Layout &x, int64_t v0, int64_t rows, void *ws,
+// Piece [v0, v0 + rows) decoded; with `dw` also the hidden states as h^T dz
+// takes them.
+cudaError_t decode(const Problem &q, const Layout &x, int64_t v0, int64_t rows, bool dw, void *ws,
                    const DevInfo &di, cudaStream_t s) {
+  DwPlanes p{};
+  if (dw) {
+    p.h = q.h;
+    p.bf16 = q.bf16;
+    p.N = q.N;
+    p.D = q.d.D;
+    p.pitch = x.hp;
+    p.hw = at<float>(ws, x.hw);
+    p.f = at<float>(ws, x.f);
+    p.sdw = at<float>(ws, x.amax) + kAmaxBlocks;
+    p.hi = at<__half>(ws, x.gh);
+    p.lo = q.bf16 ? nullptr : at<__half>(ws, x.gl);
+  }
   return launch_loss_decode(q.src(), q.C, q.d.M, q.d.L, q.ds(), v0, rows, x.zp,
-                            at<float>(ws, x.amax), at<__half>(ws, x.wh), at<__half>(ws, x.wl), di,
-                            s);
+                            at<float>(ws, x.amax), at<__half>(ws, x.wh), at<__half>(ws, x.wl), p,
+                            di, s);
 }
 
 // h and the decoded piece, the factors of the logits.
@@ -399,10 +397,9 @@ cudaError_t tensor_loss(const Problem &all, const Layout &x, float *loss, float 
     const Problem q = slice(all, n0, all.N - n0 < x.chunk ? all.N - n0 : x.chunk);
     const rq_dims &d = q.d;
     RQ_TRY(begin(q, x, true, n0 == 0, false, nullptr, ws, di, s));
-    RQ_TRY(split(q, x, false, ws, s));
     int part0 = 0;
     RQ_TRY(for_pieces(d, x, [&](int64_t v0, int64_t rows) {
-      RQ_TRY(decode(q, x, v0, rows, ws, di, s));
+      RQ_TRY(decode(q, x, v0, rows, false, ws, di, s));
       GemmArgs g = gemm_args(q, x, ws, di);
       g.rows = q.N;
       g.cols = (int)rows;
@@ -437,9 +434,8 @@ cudaError_t products_grad(const Problem &all, const Layout &x, const float *lse,
     const float *ql = lse + n0;
     const int splits = dh_splits(d, q.N, x.piece);
     RQ_TRY(begin(q, x, true, n0 == 0, true, w ? w + n0 : nullptr, ws, di, s));
-    RQ_TRY(split(q, x, dC != nullptr, ws, s));
     RQ_TRY(for_pieces(d, x, [&](int64_t v0, int64_t rows) {
-      RQ_TRY(decode(q, x, v0, rows, ws, di, s));
+      RQ_TRY(decode(q, x, v0, rows, dC && v0 == 0, ws, di, s));
       GemmArgs g = gemm_args(q, x, ws, di);
       g.rows = q.N;
       g.cols = (int)rows;
@@ -509,9 +505,8 @@ cudaError_t sums_grad(const Problem &q, const Layout &x, const float *lse, const
     RQ_TRY(launch_loss_dz(y, q.N, d.V, lse, f, q.t.beta, q.cap, dz, x.vp, s));
     RQ_TRY(launch_loss_fix(sid, sq, y, q.t.k, q.N, d.V, lse, f, q.t.beta, q.cap, dz, x.vp, s));
   } else {
-    RQ_TRY(split(q, x, false, ws, s));
     RQ_TRY(for_pieces(d, x, [&](int64_t v0, int64_t rows) {
-      RQ_TRY(decode(q, x, v0, rows, ws, di, s));
+      RQ_TRY(decode(q, x, v0, rows, false, ws, di, s));
       GemmArgs g = gemm_args(q, x, ws, di);
       g.rows = q.N;
       g.cols = (int)rows;

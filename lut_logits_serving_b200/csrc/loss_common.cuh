@@ -58,8 +58,7 @@ struct CodeSrc {
 // h_n sdw / scale_z(f_n) with one sdw for all rows (zero where the row has no
 // gradient), and the sums leave divided by sdw.  E has one scale.
 //
-// loss_begin_kernel leaves kAmaxBlocks partial maxima of |C|; behind them
-// loss_split_kernel writes sdw.
+// loss_begin_kernel leaves kAmaxBlocks partial maxima of |C|; sdw follows them.
 constexpr int kAmaxBlocks = 128;
 
 // Largest power of two s (clamped to 2^-60 .. 2^60) with bound s < 2^14; 1 for
@@ -148,11 +147,21 @@ cudaError_t launch_loss_gemm(int mode, const GemmPlanes &A, const GemmPlanes &B,
 
 // Rows of a piece decoded into fp16 hi / lo planes and the other row-wise
 // kernels (loss_rows.cu).
+//
+// h as h^T dz takes it, and its scale *sdw: written by the CTAs of a decoding.
+struct DwPlanes {
+  const void *h;
+  int bf16, N, D;       // N = 0: none
+  int64_t pitch;
+  const float *hw, *f;
+  float *sdw;
+  __half *hi, *lo;      // lo null: bf16 h
+};
 cudaError_t launch_loss_widen_h(const void *h, int64_t n, float *out, cudaStream_t s);
 bool decode_rows_ok(int K, int L, int ds);   // the faster of its kernels has the size
 cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, int ds, int64_t v0,
                                int64_t rows, int64_t pitch, const float *amax, __half *hi,
-                               __half *lo, const DevInfo &di, cudaStream_t s);
+                               __half *lo, const DwPlanes &dw, const DevInfo &di, cudaStream_t s);
 // The sparse probabilities of a loss: target ids (k = 1, val null) or a
 // teacher's lists.
 struct LossTargets {
@@ -161,16 +170,19 @@ struct LossTargets {
   int k;
   float T, beta;
 };
-// The first launch: maxima of |C| (amax null: none); the scales sh of h's rows
-// (null: none); the sorted lists, for a gradient (sq set) merged, with q and
-// f = weight T (0 for rows without a target) and, with sh, hw = the rows'
-// largest |h| / scale_z(f), for a loss with their places sj
+// The first launch: maxima of |C| (amax null: none); h's rows as planes hi, lo
+// (lo null: bf16 h, which one plane holds; hi null: neither) and their scales
+// sh; the sorted lists, for a gradient (sq set) merged, with q and f = weight T
+// (0 for rows without a target) and, for h^T dz (hw set), the rows' largest
+// |h| / scale_z(f), for a loss with their places sj
 struct BeginArgs {
   const float *C;
   int64_t nc;
   float *amax;
   const void *h;
   int bf16, D;
+  int64_t pitch;
+  __half *hi, *lo;
   float *sh, *hw;
   LossTargets t;
   int64_t rows, V;
@@ -180,16 +192,6 @@ struct BeginArgs {
   unsigned *err;
 };
 cudaError_t launch_loss_begin(const BeginArgs &a, cudaStream_t s);
-// h as planes; for a gradient (dhi set) also as h^T dz takes it, and *sdw
-struct SplitArgs {
-  const void *h;
-  int bf16, N, D;
-  int64_t pitch;
-  const float *sh, *hw, *f;
-  float *sdw;
-  __half *hi, *lo, *dhi, *dlo;   // lo and dlo null: bf16 h, which one plane holds
-};
-cudaError_t launch_loss_split(const SplitArgs &a, cudaStream_t s);
 // lse and loss from logits [N][V] of a few tokens, or from the parts of
 // kGemmStats and the listed ids' logits y [N][k]
 cudaError_t launch_loss_logits(const float *logits, int64_t N, int64_t V, const LossTargets &t,

@@ -53,8 +53,8 @@ __device__ __forceinline__ float abs_max(const float *x, int64_t n, int b, int b
 __device__ float sparse_row(const BeginArgs &a, int64_t n, float *lists);
 
 // The first kernel of a call.  With a.amax, blocks [0, kAmaxBlocks) take the
-// partial maxima of |C|; the blocks after those a row each: its lists and the
-// scale of its hidden state.
+// partial maxima of |C|; the blocks after those a row each: its lists, and its
+// hidden state as planes.
 __global__ void __launch_bounds__(256) loss_begin_kernel(const BeginArgs a) {
   extern __shared__ float lists[];
   __shared__ float red[32];
@@ -68,18 +68,49 @@ __global__ void __launch_bounds__(256) loss_begin_kernel(const BeginArgs a) {
   }
   const int64_t n = (int)blockIdx.x - c_blocks;
   float m = 0.f;
-  if (a.sh && a.bf16) {
+  if (a.hi && a.bf16) {
     for (int i = threadIdx.x; i < a.D; i += blockDim.x)
       m = fmaxf(m, fabsf(load_h(a.h, 1, n * a.D + i)));
-  } else if (a.sh) {
+  } else if (a.hi) {
     m = abs_max(static_cast<const float *>(a.h) + n * a.D, a.D, 0, 1);
   }
   const float f = sparse_row(a, n, lists);
-  if (!a.sh) return;
+  if (!a.hi) return;
   m = block_max(m, red);
   if (threadIdx.x == 0) {
-    a.sh[n] = pow2_scale(m);
+    red[0] = a.sh[n] = pow2_scale(m);
     if (a.hw) a.hw[n] = f != 0.f ? m / scale_z(f) : 0.f;
+  }
+  __syncthreads();
+  const float s = red[0];
+  for (int i = threadIdx.x; i < a.D; i += blockDim.x) {
+    __half x, y;
+    split_f16(__fmul_rn(load_h(a.h, a.bf16, n * a.D + i), s), x, y);
+    a.hi[n * a.pitch + i] = x;
+    if (a.lo) a.lo[n * a.pitch + i] = y;
+  }
+}
+
+// The scale of all rows of a.h as h^T dz takes them; the whole block calls it.
+__device__ float dw_scale(const DwPlanes &a) {
+  __shared__ float red[32];
+  float m = 0.f;
+  for (int i = threadIdx.x; i < a.N; i += blockDim.x) m = fmaxf(m, a.hw[i]);
+  m = block_max(m, red);
+  __syncthreads();
+  if (threadIdx.x == 0) red[0] = m;
+  __syncthreads();
+  return pow2_scale(red[0]);
+}
+
+__device__ void dw_row(const DwPlanes &a, int64_t n, float sdw) {
+  const float f = a.f[n], s = f != 0.f ? sdw / scale_z(f) : 0.f;
+  if (n == 0 && threadIdx.x == 0) *a.sdw = sdw;
+  for (int i = threadIdx.x; i < a.D; i += blockDim.x) {
+    __half x, y;
+    split_f16(s != 0.f ? __fmul_rn(load_h(a.h, a.bf16, n * a.D + i), s) : 0.f, x, y);
+    a.hi[n * a.pitch + i] = x;
+    if (a.lo) a.lo[n * a.pitch + i] = y;
   }
 }
 
@@ -127,6 +158,7 @@ struct DecodeArgs {
   const float *amax;
   __half *hi, *lo;
   int64_t book;        // floats of one subspace's codebooks, L K ds
+  DwPlanes dw;
   int quad;            // codebooks may be copied 16 bytes at a time
 };
 
@@ -207,8 +239,14 @@ __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeAr
   const int w = tid % words, lrow = tid / words;
   const int sub = 2 * w / ds, sub1 = EVEN ? sub : (2 * w + 1) / ds;
   const int j = 2 * w - sub * ds, j1 = 2 * w + 1 - sub1 * ds;
-  for (int u = blockIdx.x; u < a.items; u += gridDim.x) {
-    const int g = u % a.groups;
+  float sdw = 0.f;
+  for (int64_t u = blockIdx.x; u < (int64_t)a.items + a.dw.N; u += gridDim.x) {
+    if (u >= a.items) {
+      if (sdw == 0.f) sdw = dw_scale(a.dw);
+      dw_row(a.dw, u - a.items, sdw);
+      continue;
+    }
+    const int g = (int)(u % a.groups);
     const int64_t r0 = (int64_t)(u / a.groups) * a.chunk;
     const int64_t r1 = r0 + a.chunk < a.rows ? r0 + a.chunk : a.rows;
     const int m0 = g * a.gs, ms = a.M - m0 < a.gs ? a.M - m0 : a.gs;
@@ -335,6 +373,7 @@ struct DecodeRows {
   __half *hi, *lo;
   int cols;            // of the planes
   int pairs;           // codebooks may be copied two floats at a time
+  DwPlanes dw;
 };
 
 constexpr int kRowThreads = 512;
@@ -374,8 +413,14 @@ __global__ void __launch_bounds__(kRowThreads) loss_decode_rows_kernel(const Dec
            : j < U::V4 * 4 + U::V2 * 2 ? U::V4 * 4 * K + 2 * k + (j & 1)
                                        : (DS - 1) * K + k;
   };
-  for (int u = blockIdx.x; u < a.items; u += gridDim.x) {
-    const int g = u % a.units, m0 = g * U::G, p0 = m0 * LL;
+  float sdw = 0.f;
+  for (int64_t u = blockIdx.x; u < (int64_t)a.items + a.dw.N; u += gridDim.x) {
+    if (u >= a.items) {
+      if (sdw == 0.f) sdw = dw_scale(a.dw);
+      dw_row(a.dw, u - a.items, sdw);
+      continue;
+    }
+    const int g = (int)(u % a.units), m0 = g * U::G, p0 = m0 * LL;
     const bool whole = m0 + U::G <= a.M;
     const int64_t r0 = (int64_t)(u / a.units) * a.chunk;
     const int64_t left = a.rows - r0, full = ((a.rows + 7) & ~7ll) - r0;   // zeros to a row of 8
@@ -503,40 +548,6 @@ __global__ void __launch_bounds__(kRowThreads) loss_decode_rows_kernel(const Dec
           *reinterpret_cast<uint4 *>(a.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
         }
       }
-    }
-  }
-}
-
-// ------------------------------------------------------------- hidden planes
-
-__global__ void __launch_bounds__(256) loss_split_kernel(const SplitArgs a) {
-  __shared__ float red[32];
-  griddep_launch_dependents();
-  griddep_wait();
-  const int64_t n = blockIdx.x;
-  const float s = a.sh[n];
-  float sd = 0.f;          // of h^T dz
-  if (a.dhi) {
-    float m = 0.f;
-    for (int i = threadIdx.x; i < a.N; i += blockDim.x) m = fmaxf(m, a.hw[i]);
-    m = block_max(m, red);
-    if (threadIdx.x == 0) red[0] = m;
-    __syncthreads();
-    const float sdw = pow2_scale(red[0]), f = a.f[n];
-    if (f != 0.f) sd = sdw / scale_z(f);
-    if (n == 0 && threadIdx.x == 0) *a.sdw = sdw;
-  }
-  for (int i = threadIdx.x; i < a.D; i += blockDim.x) {
-    const float y = load_h(a.h, a.bf16, n * a.D + i);
-    const int64_t at = n * a.pitch + i;
-    __half x, r;
-    split_f16(__fmul_rn(y, s), x, r);
-    a.hi[at] = x;
-    if (a.lo) a.lo[at] = r;
-    if (a.dhi) {
-      split_f16(sd != 0.f ? __fmul_rn(y, sd) : 0.f, x, r);
-      a.dhi[at] = x;
-      if (a.dlo) a.dlo[at] = r;
     }
   }
 }
@@ -924,7 +935,7 @@ bool decode_rows_ok(int K, int L, int ds) {
 
 static cudaError_t launch_decode_rows(const CodeSrc &cs, const float *C, int M, int L, int ds, int64_t v0,
                                int64_t rows, int64_t pitch, const float *amax, __half *hi,
-                               __half *lo, const DevInfo &di, cudaStream_t s) {
+                               __half *lo, const DwPlanes &dw, const DevInfo &di, cudaStream_t s) {
   const size_t smem = unit_bytes(cs.K, L, ds);
   const int64_t bits = cs.fmt == RQ_CODES_U16       ? 16
                        : cs.fmt == RQ_CODES_U8       ? 8
@@ -953,6 +964,7 @@ static cudaError_t launch_decode_rows(const CodeSrc &cs, const float *C, int M, 
   a.hi = hi;
   a.lo = lo;
   a.cols = (M * ds + 7) / 8;
+  a.dw = dw;
   a.pairs = (reinterpret_cast<uintptr_t>(C) & 7) == 0 && cs.K * ds % 2 == 0;
   const cudaError_t e = ensure_smem_limit(fn, di.device, smem);
   if (e != cudaSuccess) return e;
@@ -963,15 +975,16 @@ static cudaError_t launch_decode_rows(const CodeSrc &cs, const float *C, int M, 
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
   a.items = (int)items;
   void *args[] = {&a};
-  return launch_maybe_pdl(fn, dim3((unsigned)(items < ctas ? items : ctas)), dim3(kRowThreads), smem,
+  const int64_t all = items + dw.N;
+  return launch_maybe_pdl(fn, dim3((unsigned)(all < ctas ? all : ctas)), dim3(kRowThreads), smem,
                           s, args, true);
 }
 
 cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, int ds, int64_t v0,
                                int64_t rows, int64_t pitch, const float *amax, __half *hi,
-                               __half *lo, const DevInfo &di, cudaStream_t s) {
+                               __half *lo, const DwPlanes &dw, const DevInfo &di, cudaStream_t s) {
   if (decode_rows_ok(cs.K, L, ds))
-    return launch_decode_rows(cs, C, M, L, ds, v0, rows, pitch, amax, hi, lo, di, s);
+    return launch_decode_rows(cs, C, M, L, ds, v0, rows, pitch, amax, hi, lo, dw, di, s);
   DecodeArgs a;
   a.cs = cs;
   a.C = C;
@@ -985,6 +998,7 @@ cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, 
   a.hi = hi;
   a.lo = lo;
   a.book = (int64_t)L * cs.K * ds;
+  a.dw = dw;
   // as many subspaces as their codebooks fit in shared memory, at most a pair
   // per thread, and a whole number of pairs unless one group has them all
   const int64_t fit = 220 * 1024 / 4 / a.book;
@@ -1021,12 +1035,9 @@ cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, 
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
   a.items = (int)items;
   void *args[] = {&a};
-  return launch_maybe_pdl(fn, dim3((unsigned)(items < ctas ? items : ctas)), dim3(kDecThreads), smem,
+  const int64_t all = items + dw.N;
+  return launch_maybe_pdl(fn, dim3((unsigned)(all < ctas ? all : ctas)), dim3(kDecThreads), smem,
                           s, args, true);
-}
-
-cudaError_t launch_loss_split(const SplitArgs &a, cudaStream_t s) {
-  return pdl_launch(loss_split_kernel, dim3((unsigned)a.N), dim3(256), (size_t)0, s, a);
 }
 
 cudaError_t launch_loss_logits(const float *logits, int64_t N, int64_t V, const LossTargets &t,
