@@ -193,7 +193,7 @@ struct Layout {
   size_t dz, S, dhp;                               // sums by code
   size_t hw, gh, gl, zh, zl, dw, cpart, part;      // products
   size_t total;
-  int64_t hp, zp, vp;  // row pitches: D, the piece's rows, V
+  int64_t hp, gp, zp, vp;  // row pitches: D, D in whole pairs, the piece's rows, V
   int64_t chunk;       // tokens per sweep
   int64_t piece;       // rows of the vocabulary per piece
   int splits;          // shares of the sums by code
@@ -239,16 +239,17 @@ Layout layout(const rq_dims &d, int N, int fmt, int k, bool grad) {
     x.f = a.take(n * 4);
     if (x.how.sums) {
       x.splits = codebook_sum_splits(d.V, d.M, d.L, d.K, N);
-      x.dz = a.take((int64_t)N * x.vp * 4);
+      x.dz = a.take((int64_t)(N + 1) / 2 * x.vp * 8);
       x.S = a.take((int64_t)(N + 1) / 2 * x.splits * P * d.K * 8);
       x.dhp = a.take((int64_t)P * N * ds * 4);
     } else {
       x.hw = a.take(n * 4);
-      x.gh = a.take(n * x.hp * 2);
-      x.gl = a.take(n * x.hp * 2);
+      x.gp = pitch16((int64_t)d.M * ((ds + 1) & ~1));
+      x.gh = a.take(n * x.gp * 2);
+      x.gl = a.take(n * x.gp * 2);
       x.zh = a.take(n * x.zp * 2);
       x.zl = a.take(n * x.zp * 2);
-      x.dw = a.take((int64_t)d.D * x.zp * 4);
+      x.dw = a.take((int64_t)d.M * ((ds + 1) / 2) * x.zp * 8);
       x.splits = codebook_rows_splits(d.V, rows, d.M, d.L, d.K, ds);
       x.cpart = a.take(x.splits > 1 ? (int64_t)x.splits * P * d.K * ds * 4 : 0);
       // with fewer tokens there are more shares
@@ -351,7 +352,7 @@ cudaError_t begin(const Problem &q, const Layout &x, bool scales, bool first, bo
   return launch_loss_begin(a, s);
 }
 
-// Piece [v0, v0 + rows) decoded; with `dw` also the hidden states as h^T dz
+// Piece [v0, v0 + rows) decoded; with `dw` also the hidden states as dz^T h
 // takes them.
 cudaError_t decode(const Problem &q, const Layout &x, int64_t v0, int64_t rows, bool dw, void *ws,
                    const DevInfo &di, cudaStream_t s) {
@@ -360,8 +361,9 @@ cudaError_t decode(const Problem &q, const Layout &x, int64_t v0, int64_t rows, 
     p.h = q.h;
     p.bf16 = q.bf16;
     p.N = q.N;
-    p.D = q.d.D;
-    p.pitch = x.hp;
+    p.M = q.d.M;
+    p.ds = q.ds();
+    p.pitch = x.gp;
     p.hw = at<float>(ws, x.hw);
     p.f = at<float>(ws, x.f);
     p.sdw = at<float>(ws, x.amax) + kAmaxBlocks;
@@ -468,14 +470,14 @@ cudaError_t products_grad(const Problem &all, const Layout &x, const float *lse,
       }
       if (dC) {
         GemmArgs p = gemm_args(q, x, ws, di);
-        p.rows = d.D;
-        p.cols = (int)rows;
+        p.rows = (int)rows;
+        p.cols = d.M * ((q.ds() + 1) & ~1);
         p.out = at<float>(ws, x.dw);
         p.out_pitch = x.zp;
         RQ_TRY(launch_loss_gemm(
-            kGemmDw,
-            planes(at<void>(ws, x.gh), q.bf16 ? nullptr : at<void>(ws, x.gl), q.N, d.D, x.hp),
-            planes(zh, zl, q.N, rows, x.zp), p, di, s));
+            kGemmDw, planes(zh, zl, q.N, rows, x.zp),
+            planes(at<void>(ws, x.gh), q.bf16 ? nullptr : at<void>(ws, x.gl), q.N, p.cols, x.gp),
+            p, di, s));
         RQ_TRY(launch_codebook_rows(at<float>(ws, x.dw), x.zp, v0, rows, index, d.V, d.M, d.L, d.K,
                                     q.ds(), x.splits, n0 > 0 || v0 > 0,
                                     x.splits > 1 ? at<float>(ws, x.cpart) : dC, di, s));
@@ -516,7 +518,7 @@ cudaError_t sums_grad(const Problem &q, const Layout &x, const float *lse, const
       g.sq = sq;
       g.lse = lse;
       g.f = f;
-      g.dz = dz + v0;
+      g.dz = dz + 2 * v0;
       g.dz_pitch = x.vp;
       return launch_loss_gemm(kGemmGrad32, h_planes(q, x, ws), w_planes(q, x, rows, ws), g, di, s);
     }));

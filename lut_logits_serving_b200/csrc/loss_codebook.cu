@@ -25,9 +25,10 @@
 //                            more; theirs are [over[1 + s], over[2 + s]) of the
 //                            entries that follow the slices
 //   uint16 entry[]           4 x the rows' local numbers, ascending per lane
+//                            (half the distance between rows' pairs of values)
 //
 // Two uses of one kernel.  launch_codebook_rows sums the rows of a piece's
-// dE^T [D][rows] (the tensor cores' h^T dz); launch_codebook_sums, for a few
+// dE in pairs of dims (the tensor cores' dz^T h); launch_codebook_sums, for a few
 // tokens, sums the logits' gradients themselves, S[p][k][t] = sum of dz[t][v],
 // from which both gradients follow without the V x D matrix of either kind:
 //   dC[m][l][k] = sum_t S[p][k][t] h_t (subspace m)
@@ -226,22 +227,24 @@ __global__ void __launch_bounds__(256) prepare_grad_kernel(const CodeSrc cs, con
 
 // ------------------------------------------------------------- sums by code
 //
-// A CTA takes a pair of value rows [2][V] (two dims of a subspace, or two
-// tokens) and the subspace's L columns, and walks the blocks: per block the
-// values (64 KB) and per column the unit (21 KB at K = 1024) arrive by bulk
-// copies, each into the buffer that the step before last left, so that the
-// copies run under the gathers.  A warp has a slice, a lane a list; the sums
-// of all blocks are kept in shared memory and leave once.  An odd last row is
-// gathered beside what its buffer's other half holds (finite or not, it is
-// not stored).  (First version,
-// sums added in global memory list by list: 3.8 ms where the gathers alone
-// need 0.5; without the pipeline 2.3 ms for the 768 columns and 2304 dims of
-// 256000 rows.)
-constexpr int kPairPitch = kGradRows + 4;    // the row of zeros, vectors kept whole
+// A CTA takes values in pairs [V][2] (two dims of a subspace, or two tokens)
+// and the subspace's L columns, and walks the blocks: per block the values (64
+// KB) and per column the unit (21 KB at K = 1024) arrive by bulk copies, each
+// into the buffer that the step before last left, so that the copies run under
+// the gathers.  A warp has a slice, a lane a list; the sums of all blocks are
+// kept in shared memory and leave once.  A last dim or token without a partner
+// is summed beside whatever its other half holds, which is not stored.
+//
+// Bound by the random 8-byte reads of shared memory (half a warp's meet in a
+// bank 3.1 times).  256000 rows, 768 columns of 1024 codes: 660 us for four
+// tokens (a value row of its own for either of a pair, read 4 bytes at a time:
+// 720), 1000 us for 2304 dims, where the first version, which added its sums in
+// global memory list by list, took 3.8 ms, and one without the pipeline 2.3 ms.
+constexpr int kPairFloats = 2 * kGradRows + 4;    // and the row of zeros, vectors kept whole
 constexpr int kGatherThreads = 1024;
 
 struct GatherArgs {
-  const float *vals;        // value rows, `pitch` floats apart
+  const float *vals;        // values in pairs of value rows, [pair][pitch][2]
   int64_t pitch;
   const void *index;
   IndexShape x;
@@ -260,10 +263,9 @@ struct GatherArgs {
 };
 
 // Shared memory by 32-bit address, an immediate offset apart.
-template <int OFF>
-__device__ __forceinline__ float lds_f32(uint32_t a) {
-  float x;
-  asm volatile("ld.shared.f32 %0, [%1+%2];" : "=f"(x) : "r"(a), "n"(OFF));
+__device__ __forceinline__ float2 lds_f32x2(uint32_t a) {
+  float2 x;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(a));
   return x;
 }
 template <int OFF>
@@ -318,8 +320,8 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = a.x.K, g = a.x.lanes, gsh = __ffs(g) - 1, nb = a.buffers;
   unsigned char *units = smem;                                     // [nb] units
-  float *vals = reinterpret_cast<float *>(smem + nb * a.x.unit);   // [2][2][kPairPitch]
-  float2 *stage = reinterpret_cast<float2 *>(vals + 4 * kPairPitch);   // [levels][K]
+  float *vals = reinterpret_cast<float *>(smem + nb * a.x.unit);   // [2][kPairFloats]
+  float2 *stage = reinterpret_cast<float2 *>(vals + 2 * kPairFloats);  // [levels][K]
   __shared__ uint64_t bars[3 + 2 + 2];        // units, values, steps done (all warps)
   __shared__ volatile int abort_flag;
   auto ubar = [&](int i) { return smem_addr(&bars[i]); };
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
     fence_mbar_init();
     abort_flag = 0;
   }
-  if (tid < 4) vals[tid * kPairPitch + kGradRows] = 0.f;
+  if (tid < 4) vals[(tid >> 1) * kPairFloats + 2 * kGradRows + (tid & 1)] = 0.f;
   griddep_launch_dependents();
   __syncthreads();
   griddep_wait();
@@ -358,13 +360,11 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
   auto issue_vals = [&]() {
     if (nv.u >= a.units) return;
     const int64_t r0 = (int64_t)nv.b * kGradRows, left = a.rows - r0;
-    const uint32_t bytes = (uint32_t)align_up(left < kGradRows ? left : kGradRows, 4) * 4;
-    const int w = a.ds - nv.q.j < 2 ? 1 : 2, i = iv & 1;
-    mbar_arrive_expect_tx(vbar(i), bytes * w);
-    for (int k = 0; k < w; ++k)
-      bulk_g2s(smem_addr(vals + (i * 2 + k) * kPairPitch),
-               a.vals + (int64_t)((a.per_subspace ? nv.q.m * a.ds : 0) + nv.q.j + k) * a.pitch + r0,
-               bytes, vbar(i));
+    const uint32_t bytes = (uint32_t)align_up(left < kGradRows ? left : kGradRows, 2) * 8;
+    const int i = iv & 1;
+    const int64_t pair = (a.per_subspace ? (int64_t)nv.q.m * a.pairs : 0) + nv.q.j / 2;
+    mbar_arrive_expect_tx(vbar(i), bytes);
+    bulk_g2s(smem_addr(vals + i * kPairFloats), a.vals + (pair * a.pitch + r0) * 2, bytes, vbar(i));
     ++iv;
     nv.block(a);
   };
@@ -407,17 +407,15 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
           const uint16_t *code = reinterpret_cast<const uint16_t *>(un + a.x.code_at);
           const uint16_t *over = reinterpret_cast<const uint16_t *>(un + a.x.over_at);
           const uint32_t entry = smem_addr(un) + (uint32_t)a.x.entry_at + (uint32_t)lane * 4;
-          const uint32_t v0 = vals_at + (uint32_t)(vt & 1) * (2 * kPairPitch * 4);
+          const uint32_t v0 = vals_at + (uint32_t)(vt & 1) * (kPairFloats * 4);
           float2 *st = stage + (size_t)(l - q.l0) * K;
           // one word of entries: two rows of either value row
           auto add = [&](uint32_t w, float &s0, float &s1) {
-            const uint32_t p = v0 + (w & 0xFFFFu), r = v0 + (w >> 16);
-            const float x0 = lds_f32<0>(p), x1 = lds_f32<4 * kPairPitch>(p);
-            const float y0 = lds_f32<0>(r), y1 = lds_f32<4 * kPairPitch>(r);
-            s0 += x0;
-            s1 += x1;
-            s0 += y0;
-            s1 += y1;
+            const float2 x = lds_f32x2(v0 + (w & 0xFFFFu) * 2), y = lds_f32x2(v0 + (w >> 16) * 2);
+            s0 += x.x;
+            s1 += x.y;
+            s0 += y.x;
+            s1 += y.y;
           };
           const int full = over[0];
           for (int sl = warp; sl < a.x.slices; sl += kWarps) {
@@ -462,9 +460,9 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
                   reinterpret_cast<const uint16_t *>(un + a.x.entry_at) + off[a.x.slices] * 64;
               float r0 = 0.f, r1 = 0.f;
               for (int k = over[1 + f] + lane; k < over[2 + f]; k += 32) {
-                const uint32_t p = v0 + rest[k];
-                r0 += lds_f32<0>(p);
-                r1 += lds_f32<4 * kPairPitch>(p);
+                const float2 x = lds_f32x2(v0 + rest[k] * 2u);
+                r0 += x.x;
+                r1 += x.y;
               }
 #pragma unroll
               for (int o = 16; o > 0; o >>= 1) {
@@ -662,7 +660,7 @@ struct GatherPlan {
 GatherPlan gather_plan(const IndexShape &x, int blocks, int sources, int pairs, int L) {
   GatherPlan p;
   const auto bytes = [&](int levels, int buffers = 2) {
-    return buffers * x.unit + (size_t)4 * kPairPitch * 4 + (size_t)levels * x.K * 8;
+    return buffers * x.unit + (size_t)2 * kPairFloats * 4 + (size_t)levels * x.K * 8;
   };
   p.units = (int64_t)sources * pairs;
   p.by_level = L > 1 && (bytes(L) > 225 * 1024 || p.units < 148);
@@ -704,12 +702,12 @@ int codebook_rows_splits(int64_t V, int64_t rows, int M, int L, int K, int ds) {
   return gather_plan(index_shape(V, M * L, K), blocks_of(rows), M, (ds + 1) / 2, L).splits;
 }
 
-cudaError_t launch_codebook_rows(const float *dwt, int64_t pitch, int64_t v0, int64_t rows,
+cudaError_t launch_codebook_rows(const float *dw, int64_t pitch, int64_t v0, int64_t rows,
                                  const void *index, int64_t V, int M, int L, int K, int ds,
                                  int splits, bool accumulate, float *out, const DevInfo &di,
                                  cudaStream_t s) {
   GatherArgs a = {};
-  a.vals = dwt;
+  a.vals = dw;
   a.pitch = pitch;
   a.index = index;
   a.x = index_shape(V, M * L, K);

@@ -54,7 +54,7 @@ struct CodeSrc {
 // Scales.  Every row of h has its own, and so has every row of the logits'
 // gradients, bounded by |w| T: a row's scale divides out where its sums leave,
 // so that neither a row of large values nor what padding holds costs the other
-// rows their bits.  h^T dz sums over the rows; there h_n goes in as
+// rows their bits.  dz^T h sums over the rows; there h_n goes in as
 // h_n sdw / scale_z(f_n) with one sdw for all rows (zero where the row has no
 // gradient), and the sums leave divided by sdw.  E has one scale.
 //
@@ -102,8 +102,8 @@ enum LossGemm {
   kGemmStats = 0,   // y = softcap(h E^T): per row and part max and sum of exp(y / T)
   kGemmGrad = 1,    // y again, gradients of the logits as fp16 hi / lo planes
   kGemmDh = 2,      // dz E, fp32, split over the vocabulary
-  kGemmDw = 3,      // (h^T dz), fp32 [D][rows]
-  kGemmGrad32 = 4   // kGemmGrad with fp32 gradients, unscaled
+  kGemmDw = 3,      // dz^T h, fp32, pairs of dims: [pair][rows][2]
+  kGemmGrad32 = 4   // kGemmGrad with fp32 gradients, unscaled, pairs of tokens
 };
 
 // fp16 planes; lo may be null.  Row-major, rows `pitch` elements apart, but for
@@ -127,7 +127,7 @@ struct GemmArgs {
   int stat_part0;            // first part of this launch
   const float *lse, *f;      // per row: log-sum-exp, w T (0: no gradient)
   __half *dz_hi, *dz_lo;
-  float *dz;
+  float *dz;                 // [token / 2][dz_pitch][2]
   int64_t dz_pitch;
   // listed ids, ascending per row; columns are rows v0 .. of the vocabulary
   const int32_t *sid, *sj;   // [rows][k], places in y's rows (a loss)
@@ -135,7 +135,7 @@ struct GemmArgs {
   float *y;                  // [rows][k], their logits (a loss)
   int k, v0;
   float *out;                // fp32 output
-  int64_t out_pitch, out_split;   // row pitch; stride between splits
+  int64_t out_pitch, out_split;   // row pitch (kGemmDw: of pairs); stride between splits
   int accumulate;
   unsigned *err;
 };
@@ -148,10 +148,11 @@ cudaError_t launch_loss_gemm(int mode, const GemmPlanes &A, const GemmPlanes &B,
 // Rows of a piece decoded into fp16 hi / lo planes and the other row-wise
 // kernels (loss_rows.cu).
 //
-// h as h^T dz takes it, and its scale *sdw: written by the CTAs of a decoding.
+// h as dz^T h takes it, subspaces of odd dims filled up by a zero, and its scale
+// *sdw: written by the CTAs of a decoding.
 struct DwPlanes {
   const void *h;
-  int bf16, N, D;       // N = 0: none
+  int bf16, N, M, ds;   // N = 0: none
   int64_t pitch;
   const float *hw, *f;
   float *sdw;
@@ -173,7 +174,7 @@ struct LossTargets {
 // The first launch: maxima of |C| (amax null: none); h's rows as planes hi, lo
 // (lo null: bf16 h, which one plane holds; hi null: neither) and their scales
 // sh; the sorted lists, for a gradient (sq set) merged, with q and f = weight T
-// (0 for rows without a target) and, for h^T dz (hw set), the rows' largest
+// (0 for rows without a target) and, for dz^T h (hw set), the rows' largest
 // |h| / scale_z(f), for a loss with their places sj
 struct BeginArgs {
   const float *C;
@@ -199,11 +200,12 @@ cudaError_t launch_loss_logits(const float *logits, int64_t N, int64_t V, const 
 cudaError_t launch_loss_finish(const float2 *stat, int parts, int stat_ld, int64_t N, int64_t V,
                                const LossTargets &t, const float *y, float *loss, float *lse,
                                unsigned *err, cudaStream_t s);
-// logits [N][V] -> their gradients [N][pitch], dense part
+// logits [N][V] -> their gradients in pairs of tokens, [(N + 1) / 2][pitch][2],
+// dense part
 cudaError_t launch_loss_dz(const float *logits, int64_t N, int64_t V, const float *lse,
                            const float *f, float beta, float cap, float *dz, int64_t pitch,
                            cudaStream_t s);
-// dz [N][pitch] at the listed ids, from the logits
+// the same at the listed ids
 cudaError_t launch_loss_fix(const int32_t *sid, const float *sq, const float *logits, int k,
                             int64_t N, int64_t V, const float *lse, const float *f, float beta,
                             float cap, float *dz, int64_t pitch, cudaStream_t s);
@@ -213,18 +215,20 @@ cudaError_t launch_loss_dh_sum(const float *part, int splits, int64_t stride, in
 // Rows by code (loss_codebook.cu).
 size_t grad_index_bytes(int64_t V, int P, int K);
 cudaError_t launch_prepare_grad(const CodeSrc &cs, void *index, const DevInfo &di, cudaStream_t s);
-// out[split] (+)= the columns of dwt [D][pitch] (rows v0 .. v0 + rows of the
+// out[split] (+)= the columns of dw (pairs of dims of a subspace, an odd last
+// one half empty: [M][(ds + 1) / 2][pitch][2]; rows v0 .. v0 + rows of the
 // vocabulary, v0 % kGradRows == 0) summed by code, each share of the piece's
 // blocks in an array like dC; with one share out is dC itself, else
 // launch_codebook_join adds them up
 int codebook_rows_splits(int64_t V, int64_t rows, int M, int L, int K, int ds);
-cudaError_t launch_codebook_rows(const float *dwt, int64_t pitch, int64_t v0, int64_t rows,
+cudaError_t launch_codebook_rows(const float *dw, int64_t pitch, int64_t v0, int64_t rows,
                                  const void *index, int64_t V, int M, int L, int K, int ds,
                                  int splits, bool accumulate, float *out, const DevInfo &di,
                                  cudaStream_t s);
 cudaError_t launch_codebook_join(const float *part, int splits, int64_t n, float *dC,
                                  cudaStream_t s);
-// S[pair][split][p][k][2] = sums of dz [N][pitch] by code, tokens in pairs
+// S[pair][split][p][k][2] = sums of dz [(N + 1) / 2][pitch][2] by code, tokens in
+// pairs
 int codebook_sum_splits(int64_t V, int M, int L, int K, int N);
 cudaError_t launch_codebook_sums(const float *dz, int64_t pitch, int N, const void *index, int64_t V,
                                  int M, int L, int K, float *S, const DevInfo &di, cudaStream_t s);

@@ -6,7 +6,7 @@
 //   kGemmGrad   y again; dz = w T exp(y / T - lse) (1 - (y / cap)^2), as fp16
 //               planes for the next two, or (kGemmGrad32) in fp32
 //   kGemmDh     dz E       (contraction over the rows of the vocabulary)
-//   kGemmDw     h^T dz     (contraction over the tokens)
+//   kGemmDw     dz^T h     (contraction over the tokens)
 //
 // Mathematics.  Every operand is an fp16 hi / lo pair of planes scaled by a
 // power of two (loss_common.cuh), so a product of two fp32 operands is three
@@ -196,10 +196,9 @@ __device__ __forceinline__ void stg32(void *p, const uint32_t *v) {
                : "memory");
 }
 
-// Outgoing tiles leave through shared memory as TMA stores: a thread has a row,
-// and stored directly a warp's words go to 32 rows, a sector each, which keeps
-// the threads from the next tile's sums (h^T dz of 500 tokens: 396 us, 261
-// without any store).
+// The gradients' planes leave through shared memory as TMA stores: a thread has
+// a row, and stored directly a warp's words go to 32 rows, a sector each, which
+// keeps the threads from the next tile's sums.
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
@@ -276,7 +275,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                      const __grid_constant__ CUtensorMap b_hi, const __grid_constant__ CUtensorMap b_lo,
                      const __grid_constant__ CUtensorMap o_hi, const __grid_constant__ CUtensorMap o_lo,
                      const GemmArgs g) {
-  constexpr bool STAGED = MODE == kGemmGrad || MODE == kGemmDw;   // output through TMA
+  constexpr bool STAGED = MODE == kGemmGrad;                    // output through TMA
   constexpr bool LOGITS = MODE == kGemmStats || MODE == kGemmGrad || MODE == kGemmGrad32;
   constexpr bool A_MN = MODE == kGemmDw;                        // contraction down the rows of A
   constexpr bool B_MN = MODE == kGemmDh || MODE == kGemmDw;     // and of B
@@ -338,6 +337,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   // CTA (or pair) `unit` of `units` takes every units-th tile
   const int unit = blockIdx.x / CG, units = gridDim.x / CG;
   const int mn = g.m_tiles * g.n_tiles, total = mn * g.splits;
+  // the operand with fewer tiles stays in the L2, so its tiles change fastest
+  auto m_tile = [&](int r) { return MODE == kGemmDw ? r / g.n_tiles : r % g.m_tiles; };
+  auto n_tile = [&](int r) { return MODE == kGemmDw ? r % g.n_tiles : r / g.m_tiles; };
   bool to = false;
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (!to && !mbar_try_wait(bar, parity) && !mbar_wait_bounded(bar, parity)) {
@@ -358,8 +360,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         int it = 0;
         for (int t = unit; t < total && !abort_flag; t += units) {
           const int sp = t / mn, r = t % mn;
-          const int n0 = r / g.m_tiles * TN + rank * BN;
-          const int m0 = (r % g.m_tiles * CG + rank) * kTM;
+          const int n0 = n_tile(r) * TN + rank * BN;
+          const int m0 = (m_tile(r) * CG + rank) * kTM;
           const int k0 = (int)((int64_t)g.kblocks * sp / g.splits);
           const int k1 = (int)((int64_t)g.kblocks * (sp + 1) / g.splits);
           for (int k = k0; k < k1; ++k, ++it) {
@@ -479,9 +481,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     float acc[HALF];
     int c = 0;
     for (int t = unit; t < total && !to; t += units) {
-      const int sp = t / mn, r = t % mn, nt = r / g.m_tiles;
+      const int sp = t / mn, r = t % mn, nt = n_tile(r);
       const int col0 = nt * TN + half * HALF;
-      const int row = (r % g.m_tiles * CG + rank) * kTM + q * 32 + lane;
+      const int row = (m_tile(r) * CG + rank) * kTM + q * 32 + lane;
       const int k0 = (int)((int64_t)g.kblocks * sp / g.splits);
       const int k1 = (int)((int64_t)g.kblocks * (sp + 1) / g.splits);
       // what the epilogue needs of the row, on its way while the MMAs run: the
@@ -584,7 +586,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           g.stat[(int64_t)(g.stat_part0 + nt * 2 + half) * g.stat_ld + row] = make_float2(mx, sum);
       } else if (LOGITS) {
         const float fs = MODE == kGemmGrad ? f * scale_z(f) : f;
-        const int64_t at = (int64_t)row * g.dz_pitch + col0;
+        const int64_t at = ((int64_t)(row >> 1) * g.dz_pitch + col0) * 2 + (row & 1);   // fp32
 #pragma unroll 1
         for (int j0 = 0; j0 < HALF; j0 += 32) {
           if (STAGED) {
@@ -606,9 +608,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               x[j] = f != 0.f ? ex2(fmaf(y, beta, -lse) * kLog2e) * slope * fs : 0.f;
             }
             if (MODE == kGemmGrad32) {
-              if (in && col0 + j0 + 16 * k < g.cols) {          // the rows' pitch is 16 floats
-                stg32(g.dz + at + j0 + 16 * k, reinterpret_cast<const uint32_t *>(x));
-                stg32(g.dz + at + j0 + 16 * k + 8, reinterpret_cast<const uint32_t *>(x + 8));
+              if (in && col0 + j0 + 16 * k < g.cols) {          // the pitch is 16 columns
+#pragma unroll
+                for (int j = 0; j < 16; ++j) g.dz[at + 2 * (j0 + 16 * k + j)] = x[j];
               }
             } else {
               uint32_t hi[8], lo[8];
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const float d =
                 f != 0.f ? (p - __ldg(g.sq + (int64_t)row * g.k + li)) * (1.f - th * th) * fs : 0.f;
             if (MODE == kGemmGrad32) {
-              g.dz[at + j0 + c] = d;
+              g.dz[at + 2 * (j0 + c)] = d;
             } else {
               __half dh, dl;
               split_f16(d, dh, dl);
@@ -672,26 +674,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           for (int j = 0; j + 32 < HALF; ++j) acc[j] = acc[j + 32];
         }
       } else if (MODE == kGemmDw) {
+        // a thread has a row of the vocabulary and stores pairs of dims, a warp
+        // 32 neighbouring rows of a pair
+        if (in) {
+          float2 *o = reinterpret_cast<float2 *>(g.out) + (int64_t)(col0 / 2) * g.out_pitch + row;
 #pragma unroll
-        for (int j0 = 0; j0 < HALF; j0 += 32) {
-          if (q == 0 && lane == 0) store_wait_read();
-          group_sync(1 + half);
-          // rows of 128 bytes, 16-byte pieces swizzled by row
-          const uint32_t r = staging + (uint32_t)(half * kStoreBytes + (q * 32 + lane) * 128);
-#pragma unroll
-          for (int p = 0; p < 8; ++p)
-            sts16(r + (((uint32_t)p ^ ((uint32_t)lane & 7u)) << 4),
-                  __float_as_uint(acc[j0 + 4 * p] * inv), __float_as_uint(acc[j0 + 4 * p + 1] * inv),
-                  __float_as_uint(acc[j0 + 4 * p + 2] * inv),
-                  __float_as_uint(acc[j0 + 4 * p + 3] * inv));
-          async_fence();
-          group_sync(1 + half);
-          if (q == 0 && lane == 0) {
-            // 32-bit elements as pairs of 16
-            if (col0 + j0 < g.cols && row < g.rows)
-              store_tile(&o_hi, staging + half * kStoreBytes, 2 * (col0 + j0), row);
-            store_commit();
-          }
+          for (int j = 0; j < HALF; j += 2, o += g.out_pitch)
+            if (col0 + j < g.cols) *o = make_float2(acc[j] * inv, acc[j + 1] * inv);
         }
       } else if (in) {
         float *o = g.out + (int64_t)sp * g.out_split + (int64_t)row * g.out_pitch + col0;
@@ -810,12 +799,8 @@ cudaError_t launch_tile(const GemmPlanes &A, const GemmPlanes &B, GemmArgs a, co
        !encode_tmap_2d_u16(&ol, a.dz_lo, (uint64_t)a.cols, (uint64_t)a.rows,
                            (uint64_t)a.dz_pitch * 2, 32, kTM, CU_TENSOR_MAP_SWIZZLE_64B)))
     return cudaErrorInvalidValue;
-  if (MODE == kGemmDw &&
-      !encode_tmap_2d_u16(&oh, a.out, (uint64_t)a.cols * 2, (uint64_t)a.rows,
-                          (uint64_t)a.out_pitch * 4, 64, kTM, CU_TENSOR_MAP_SWIZZLE_128B))
-    return cudaErrorInvalidValue;
   const size_t stage = (size_t)a.a_planes * kABytes + (size_t)a.b_planes * (BN * kTK * 2);
-  const size_t tail = kGemmSmemTail + (MODE == kGemmGrad || MODE == kGemmDw ? 2 * kStoreBytes : 0);
+  const size_t tail = kGemmSmemTail + (MODE == kGemmGrad ? 2 * kStoreBytes : 0);
   int st = (int)((kGemmSmemMax - tail) / stage);
   a.stages = st > kMaxStages ? kMaxStages : st;
   const size_t smem = tail + a.stages * stage;

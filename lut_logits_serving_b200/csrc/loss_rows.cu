@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(256) loss_begin_kernel(const BeginArgs a) {
   }
 }
 
-// The scale of all rows of a.h as h^T dz takes them; the whole block calls it.
+// The scale of all rows of a.h as dz^T h takes them; the whole block calls it.
 __device__ float dw_scale(const DwPlanes &a) {
   __shared__ float red[32];
   float m = 0.f;
@@ -106,9 +106,14 @@ __device__ float dw_scale(const DwPlanes &a) {
 __device__ void dw_row(const DwPlanes &a, int64_t n, float sdw) {
   const float f = a.f[n], s = f != 0.f ? sdw / scale_z(f) : 0.f;
   if (n == 0 && threadIdx.x == 0) *a.sdw = sdw;
-  for (int i = threadIdx.x; i < a.D; i += blockDim.x) {
+  const int even = (a.ds + 1) & ~1;
+  for (int i = threadIdx.x; i < a.M * even; i += blockDim.x) {
+    const int m = i / even, j = i - m * even;
     __half x, y;
-    split_f16(s != 0.f ? __fmul_rn(load_h(a.h, a.bf16, n * a.D + i), s) : 0.f, x, y);
+    split_f16(s != 0.f && j < a.ds
+                  ? __fmul_rn(load_h(a.h, a.bf16, (n * a.M + m) * a.ds + j), s)
+                  : 0.f,
+              x, y);
     a.hi[n * a.pitch + i] = x;
     if (a.lo) a.lo[n * a.pitch + i] = y;
   }
@@ -535,13 +540,17 @@ __global__ void __launch_bounds__(kRowThreads) loss_decode_rows_kernel(const Dec
             e[m * DS + j] = l == 0 ? x[j] : __fadd_rn(e[m * DS + j], x[j]);
         }
       }
-      const float f = r < n ? se : 0.f;
+      if (r >= n) {
+#pragma unroll
+        for (int i = 0; i < U::G * DS; ++i) e[i] = 0.f;
+      }
 #pragma unroll
       for (int q = 0; q < U::Q; ++q) {
         uint32_t h[4], l[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          split_pair(__fmul_rn(e[8 * q + 2 * i], f), __fmul_rn(e[8 * q + 2 * i + 1], f), h[i], l[i]);
+          split_pair(__fmul_rn(e[8 * q + 2 * i], se), __fmul_rn(e[8 * q + 2 * i + 1], se), h[i],
+                     l[i]);
         if (g * U::Q + q < a.cols) {
           const int64_t at = ((g * U::Q + q) * a.pitch + r0 + r) * 8;
           *reinterpret_cast<uint4 *>(a.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
@@ -824,17 +833,23 @@ __device__ __forceinline__ float dz_at(float y, float q, float lse, float f, flo
   return f != 0.f ? (expf(fmaf(y, beta, -lse)) - q) * (1.f - th * th) * f : 0.f;
 }
 
-__global__ void __launch_bounds__(256) loss_dz_kernel(const float *__restrict__ logits, int64_t V,
+__global__ void __launch_bounds__(256) loss_dz_kernel(const float *__restrict__ logits, int64_t N,
+                                                      int64_t V,
                                                       const float *__restrict__ lse,
                                                       const float *__restrict__ f, float beta,
                                                       float cap, float *__restrict__ dz,
                                                       int64_t pitch) {
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t n = blockIdx.y;
-  const float l = lse[n], w = f[n];
+  const int64_t n = 2 * (int64_t)blockIdx.y;
+  const bool two = n + 1 < N;
+  const float l0 = lse[n], w0 = f[n], l1 = two ? lse[n + 1] : 0.f, w1 = two ? f[n + 1] : 0.f;
+  const float *y0 = logits + n * V, *y1 = y0 + (two ? V : 0);
+  float2 *out = reinterpret_cast<float2 *>(dz) + blockIdx.y * pitch;
   for (int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x; v < pitch; v += (int64_t)gridDim.x * 256)
-    dz[n * pitch + v] = v < V ? dz_at(logits[n * V + v], 0.f, l, w, beta, cap) : 0.f;
+    out[v] = v < V ? make_float2(dz_at(y0[v], 0.f, l0, w0, beta, cap),
+                                 dz_at(y1[v], 0.f, l1, w1, beta, cap))
+                   : make_float2(0.f, 0.f);
 }
 
 __global__ void __launch_bounds__(256) loss_fix_kernel(
@@ -846,7 +861,7 @@ __global__ void __launch_bounds__(256) loss_fix_kernel(
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= count || sid[i] == kNoId) return;
   const int64_t n = i / k, v = sid[i];
-  dz[n * pitch + v] = dz_at(logits[n * V + v], sq[i], lse[n], f[n], beta, cap);
+  dz[(n / 2 * pitch + v) * 2 + n % 2] = dz_at(logits[n * V + v], sq[i], lse[n], f[n], beta, cap);
 }
 
 __global__ void __launch_bounds__(256) loss_dh_sum_kernel(const float *__restrict__ part,
@@ -1056,7 +1071,8 @@ cudaError_t launch_loss_finish(const float2 *stat, int parts, int stat_ld, int64
 cudaError_t launch_loss_dz(const float *logits, int64_t N, int64_t V, const float *lse,
                            const float *f, float beta, float cap, float *dz, int64_t pitch,
                            cudaStream_t s) {
-  return pdl_launch(loss_dz_kernel, dim3(blocks_of(pitch, 1024), (unsigned)N), dim3(256), (size_t)0, s, logits, V, lse, f, beta, cap, dz, pitch);
+  return pdl_launch(loss_dz_kernel, dim3(blocks_of(pitch, 1024), (unsigned)((N + 1) / 2)), dim3(256),
+                    (size_t)0, s, logits, N, V, lse, f, beta, cap, dz, pitch);
 }
 
 cudaError_t launch_loss_fix(const int32_t *sid, const float *sq, const float *logits, int k,
