@@ -461,3 +461,17 @@ def test_unaligned_tensors(N, dtype):
     rq.rq_distill_grad(*x.args(), x.val, x.idx, off(want["lse"]), x.index, temperature=1.0,
                        weight=x.weight, dh=dh, dC=dC)
     assert torch.equal(dh, want["dh"]) and torch.equal(dC, want["dC"])
+
+
+@pytest.mark.parametrize("c", [
+    (5, 6, 2, 100, "u16"), (6, 6, 2, 64, "u8"), (8, 5, 1, 50, "packed10"), (16, 2, 2, 300, "packed10"),
+    (13, 2, 3, 40, "u16"), (22, 2, 1, 40, "u16"), (9, 8, 3, 30, "u8"), (12, 8, 3, 30, "u8"),
+    (16, 3, 2, 70, "packed10"), (24, 4, 3, 33, "u8"), (32, 5, 3, 200, "u8"), (64, 3, 1, 20, "u8"),
+    (64, 4, 1, 20, "packed10"), (32, 6, 1, 1000, "packed10"), (32, 3, 2, 300, "sched"),
+    (64, 4, 1, 512, "rot10"), (10, 7, 2, 60, "u16"), (3, 16, 4, 20, "u8"), (7, 6, 2, 4000, "u16")])
+def test_decoding(c):
+    """Rows rebuilt for the tensor cores from codes in words of 16 and 4 bytes
+    and one by one, units of subspaces that end early, columns filled up."""
+    M, ds, L, K, fmt = c
+    x = Head(777, M, ds, L, K, 66, fmt=fmt, seed=15)
+    x.check()
