@@ -13,7 +13,9 @@
 // tensor-core products, a_hi b_hi + a_lo b_hi + a_hi b_lo (two where one
 // operand is bf16, which a scaled fp16 plane holds exactly).  The tensor
 // core's fp32 accumulator does not round to nearest and its error grows with
-// the chain of MMAs, so a chain has 12 to 36 of them; a finished chain is
+// the chain of MMAs, so a chain has 12 to 48 of them, the small products of each
+// block first (each MMA costs the running sum half a unit in its last place;
+// with a_hi b_hi first the errors are half as large again); a finished chain is
 // added to fp32 registers, round to nearest, while the next one runs into the
 // other half of tensor memory.
 //
@@ -56,12 +58,14 @@ constexpr int kGemmThreads = (kEpiWarps + 4) * 32;   // + copy, MMA, two idle: w
 constexpr int kMaxStages = 8;
 constexpr int kABytes = kTM * kTK * 2;
 // MMAs of one accumulation chain.  Errors of dC and dh against 64 bits (500
-// fp32 tokens, 256000 rows): chains of 48 1.4e-6 and 1.4e-6, of 24 7.8e-7 and
-// 8.0e-7, for 5 to 8 % of a step's time; an fp32 library product leaves 8.4e-7
-// and 1.6e-6.  So the sums that only pass through one product get longer ones,
-// and short contractions (up to 4 blocks, where nothing is left to overlap)
-// the shortest.
-constexpr int kChainMmas = 36, kChainMmasDw = 24, kChainMmasShort = 12;
+// fp32 tokens, 256000 rows): chains of 48 (dz^T h 36) 6.7e-7 and 7.1e-7, of 36
+// (24) 4.7e-7 and 5.4e-7 for 2 to 8 % of a product's time; an fp32 library
+// product leaves 8.4e-7 and 1.6e-6.  Short contractions (up to 4 blocks, where
+// nothing is left to overlap) take short chains.  So do the logits of up to 128
+// tokens, which the planes of E bound: 130 us per 65536 rows instead of 122, and
+// a single confident row, whose logit all MMAs round in one direction, keeps a
+// relative error of its loss of 1e-6 (3e-6 with longer ones).
+constexpr int kChainMmas = 48, kChainMmasDw = 36, kChainMmasShort = 12;
 constexpr size_t kGemmSmemMax = 226 * 1024;      // 227 KB less the static part
 constexpr int kStoreBytes = 16384;               // a warpgroup's outgoing 128 rows x 128 bytes
 constexpr size_t kGemmSmemTail = 1024 + 256;     // alignment slack, barriers
@@ -434,19 +438,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                   : B_MN  ? block_desc(sb, 128, 1024)
                                           : block_desc(sb, BN * 16, 128);
               const uint64_t al = ah + kABytes / 16, bl = bh + B_BYTES / 16;
-#pragma unroll
-              for (int j = 0; j < kTK / 16; ++j)
-                mma_f16_ss<CG>(d, ah + j * a_step, bh + j * b_step, idesc, k > ka || j > 0);
-              if (g.a_planes > 1) {
-#pragma unroll
-                for (int j = 0; j < kTK / 16; ++j)
-                  mma_f16_ss<CG>(d, al + j * a_step, bh + j * b_step, idesc, 1u);
-              }
+              // the small products first
+              uint32_t on = k > ka;
               if (g.b_planes > 1) {
 #pragma unroll
-                for (int j = 0; j < kTK / 16; ++j)
-                  mma_f16_ss<CG>(d, ah + j * a_step, bl + j * b_step, idesc, 1u);
+                for (int j = 0; j < kTK / 16; ++j, on = 1u)
+                  mma_f16_ss<CG>(d, ah + j * a_step, bl + j * b_step, idesc, on);
               }
+              if (g.a_planes > 1) {
+#pragma unroll
+                for (int j = 0; j < kTK / 16; ++j, on = 1u)
+                  mma_f16_ss<CG>(d, al + j * a_step, bh + j * b_step, idesc, on);
+              }
+#pragma unroll
+              for (int j = 0; j < kTK / 16; ++j, on = 1u)
+                mma_f16_ss<CG>(d, ah + j * a_step, bh + j * b_step, idesc, on);
               tc_commit<CG>(empty(st));
             }
             if (to) break;
@@ -789,7 +795,8 @@ cudaError_t launch_tile(const GemmPlanes &A, const GemmPlanes &B, GemmArgs a, co
   a.m_tiles = (int)(((A_MN ? A.cols : A.rows) + kTM * CG - 1) / (kTM * CG));
   a.n_tiles = (int)(((B_MN ? B.cols : B.rows) + TN - 1) / TN);
   a.kblocks = (int)((k + kTK - 1) / kTK);
-  const int mmas = a.kblocks <= 4 ? kChainMmasShort : MODE == kGemmDw ? kChainMmasDw : kChainMmas;
+  const bool few = (MODE != kGemmDh && MODE != kGemmDw && a.rows <= kTM) || a.kblocks <= 4;
+  const int mmas = few ? kChainMmasShort : MODE == kGemmDw ? kChainMmasDw : kChainMmas;
   a.chain = mmas / (kTK / 16 * (a.a_planes + a.b_planes - 1));
   if (a.splits > a.kblocks) a.splits = a.kblocks;
   CUtensorMap oh = ah, ol = ah;
