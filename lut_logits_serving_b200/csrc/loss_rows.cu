@@ -361,13 +361,12 @@ __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeAr
 // in shared memory split into parts of four, two and one dims, so that a
 // codeword of six is one 16- and one 8-byte access: random codewords meet in a
 // bank 2.6 times per 128 bytes so, 3.1 times in 8-byte accesses.  A row's codes
-// come in wide loads, a row ahead; a warp's stores are 32 neighbouring rows of
-// a column, 512 bytes at once.  Bound by shared memory's data path (41 million
-// passes of 128 bytes per 65536 rows of 2304 dims, two levels of 1024: 27 for
-// the gathers, 7 for codes, 5 for the stores): 207 us (10-bit codes 238), where a
-// thread per pair of dims and row-major planes take 272.  512 threads rather
-// than 1024: 4 % slower on uint16 codes, 7 % faster on 10-bit ones and a fifth
-// on few rows.
+// come in wide words, rows ahead; a warp's stores are 32 neighbouring rows of a
+// column, 512 bytes at once.  Bound by shared memory's data path and the stores
+// (per 65536 rows of 2304 dims, two levels of 1024: 27 million passes of 128
+// bytes for the gathers, 5 for the stores; without the stores 142 us): 182 us,
+// 10-bit codes 238, where a thread per pair of dims and row-major planes take
+// 272.  512 threads rather than 1024: a fifth faster on few rows.
 struct DecodeRows {
   CodeSrc cs;
   const float *C;
@@ -378,10 +377,13 @@ struct DecodeRows {
   __half *hi, *lo;
   int cols;            // of the planes
   int pairs;           // codebooks may be copied two floats at a time
+  int stages;          // VEC 16: rows that a thread has under way
+  unsigned *err;
   DwPlanes dw;
 };
 
-constexpr int kRowThreads = 512;
+constexpr int kRowThreads = 512, kRowWarps = kRowThreads / 32;
+constexpr int kRowStages = 4;
 
 template <int DS>
 struct RowUnit {
@@ -399,17 +401,32 @@ __device__ __forceinline__ void copy_async(float *dst, const float *src) {
 
 // VEC: a row's codes of the unit come in the aligned words of 16 bytes (4) or 4
 // (1) that hold them, or one by one (0; a last unit of fewer subspaces too).
+// 16: a single word of 16 bytes, which comes by TMA, a box of 32 rows for each
+// warp, up to four of them ahead, into a ring of its own: 32 rows' words lie in
+// 32 lines, which as loads cost as many passes through the data path, and their
+// latency behind the stores (65536 rows of uint16 codes 210 us so, 185 by TMA;
+// with two boxes a row, 10-bit codes, 276, by loads 238).
 template <int DS, int LL, int VEC>
-__global__ void __launch_bounds__(kRowThreads) loss_decode_rows_kernel(const DecodeRows a) {
+__global__ void __launch_bounds__(kRowThreads)
+    loss_decode_rows_kernel(const __grid_constant__ CUtensorMap map, const DecodeRows a) {
   using U = RowUnit<DS>;
   constexpr int N = U::G * LL;                       // codes of a row
-  constexpr int S = VEC == 4 ? 128 : 32;             // bits of a word as loaded
+  constexpr int S = VEC >= 4 ? 128 : 32;             // bits of a word as loaded
   constexpr int W10 = (N * 10 + 2 * S - 4) / S, W16 = (N * 16 + 2 * S - 18) / S;
-  constexpr int W = (W10 > W16 ? W10 : W16) * (S / 32);
+  constexpr int W = VEC == 16 ? 4 : (W10 > W16 ? W10 : W16) * (S / 32);
   extern __shared__ __align__(16) float books[];
+  __shared__ uint64_t bars[VEC == 16 ? kRowWarps * kRowStages : 1];
+  const int K = a.cs.K, tid = threadIdx.x, P = a.cs.P, lane = tid & 31, warp = tid >> 5;
+  if (VEC == 16) {
+    if (tid == 0) {
+      prefetch_tmap(&map);
+      for (int i = 0; i < kRowWarps * a.stages; ++i) mbar_init(smem_addr(&bars[i]), 1);
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
   griddep_launch_dependents();
   griddep_wait();
-  const int K = a.cs.K, tid = threadIdx.x, P = a.cs.P;
   const float se = scale_e(a.amax, LL);
   const int book = (K * DS + 3) & ~3;                // a codebook's floats
   // where dim j of codeword k lies
@@ -418,6 +435,36 @@ __global__ void __launch_bounds__(kRowThreads) loss_decode_rows_kernel(const Dec
            : j < U::V4 * 4 + U::V2 * 2 ? U::V4 * 4 * K + 2 * k + (j & 1)
                                        : (DS - 1) * K + k;
   };
+  // the warp's ring of boxes, 16 bytes of 32 rows each: issued and used so far, and
+  // the rows issued last, irow of item iu
+  const uint32_t ring = ((smem_addr(books) + (uint32_t)(N * book) * 4 + 127u) & ~127u) +
+                        (uint32_t)(warp * a.stages) * 512u;
+  const uint32_t bar0 = smem_addr(bars) + 8u * (uint32_t)(warp * a.stages);
+  const int64_t rows8 = (a.rows + 7) & ~7ll;
+  int64_t iu = (int64_t)blockIdx.x - gridDim.x;
+  int irow = 0, iend = 0, issued = 0, used = 0;
+  bool lost = false;
+  auto issue = [&]() {                               // by lane 0
+    irow += kRowThreads;
+    while (irow >= iend) {                           // the next item's rows
+      iu += gridDim.x;
+      if (iu >= a.items) {
+        iu -= gridDim.x;                             // none left
+        irow = iend;
+        return;
+      }
+      const int64_t full = rows8 - iu / a.units * a.chunk;
+      irow = warp * 32;
+      iend = (int)(full < a.chunk ? full : a.chunk);
+    }
+    const uint32_t st = (uint32_t)(issued % a.stages);
+    mbar_arrive_expect_tx(bar0 + 8u * st, 512u);
+    tma_load_2d(ring + st * 512u, &map, a.bits * N * (int)(iu % a.units) / S * 8,
+                (int)(a.v0 + iu / a.units * a.chunk + irow), bar0 + 8u * st, l2_policy_evict_last());
+    ++issued;
+  };
+  if (VEC == 16 && lane == 0)
+    for (int i = 0; i < a.stages; ++i) issue();
   float sdw = 0.f;
   for (int64_t u = blockIdx.x; u < (int64_t)a.items + a.dw.N; u += gridDim.x) {
     if (u >= a.items) {
@@ -428,7 +475,7 @@ __global__ void __launch_bounds__(kRowThreads) loss_decode_rows_kernel(const Dec
     const int g = (int)(u % a.units), m0 = g * U::G, p0 = m0 * LL;
     const bool whole = m0 + U::G <= a.M;
     const int64_t r0 = (int64_t)(u / a.units) * a.chunk;
-    const int64_t left = a.rows - r0, full = ((a.rows + 7) & ~7ll) - r0;   // zeros to a row of 8
+    const int64_t left = a.rows - r0, full = rows8 - r0;     // zeros to a row of 8
     const int n = (int)(left < a.chunk ? left : a.chunk);
     const int n8 = (int)(full < a.chunk ? full : a.chunk);
     // the words with the unit's codes in the chunk's first row, the first
@@ -437,10 +484,10 @@ __global__ void __launch_bounds__(kRowThreads) loss_decode_rows_kernel(const Dec
     const int bit = a.bits * p0, sh = bit & (S - 1), nw = (sh + a.bits * N + S - 1) / S;
     const uint8_t *src =
         static_cast<const uint8_t *>(a.cs.codes) + (a.v0 + r0) * step + bit / S * (S / 8);
-    const bool each = VEC == 0 || !whole;
+    const bool each = VEC == 0 || (VEC != 16 && !whole);
     uint32_t next[W];
     auto fetch = [&](int r) {
-      if (each || r >= n) return;
+      if (VEC == 16 || each || r >= n) return;
       const uint8_t *p = src + r * step;
       if (VEC == 4) {
 #pragma unroll
@@ -477,8 +524,24 @@ __global__ void __launch_bounds__(kRowThreads) loss_decode_rows_kernel(const Dec
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    for (int r = tid; r < n8; r += kRowThreads) {
+    for (int base = warp * 32; base < n8; base += kRowThreads) {
+      const int r = base + lane;
       uint32_t c[N];
+      if (VEC == 16) {
+        const uint32_t st = (uint32_t)(used % a.stages), bar = bar0 + 8u * st;
+        const uint32_t parity = (uint32_t)(used / a.stages) & 1u;
+        if (!lost && !mbar_try_wait(bar, parity) && !mbar_wait_bounded(bar, parity)) lost = true;
+        lost = __any_sync(0xffffffffu, lost);
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(next[0]), "=r"(next[1]), "=r"(next[2]), "=r"(next[3])
+                     : "r"(ring + st * 512u + (uint32_t)lane * 16u)
+                     : "memory");
+        __syncwarp();                                // all have read: the stage is free
+        if (!lost) {
+          ++used;
+          if (lane == 0) issue();
+        }
+      }
       if (each) {
 #pragma unroll
         for (int i = 0; i < N; ++i) c[i] = r < n && p0 + i < P ? a.cs.raw(a.v0 + r0 + r, p0 + i) : 0u;
@@ -551,13 +614,19 @@ __global__ void __launch_bounds__(kRowThreads) loss_decode_rows_kernel(const Dec
         for (int i = 0; i < 4; ++i)
           split_pair(__fmul_rn(e[8 * q + 2 * i], se), __fmul_rn(e[8 * q + 2 * i + 1], se), h[i],
                      l[i]);
-        if (g * U::Q + q < a.cols) {
+        if (g * U::Q + q < a.cols && r < n8) {
           const int64_t at = ((g * U::Q + q) * a.pitch + r0 + r) * 8;
           *reinterpret_cast<uint4 *>(a.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
           *reinterpret_cast<uint4 *>(a.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
         }
       }
     }
+  }
+  if (VEC == 16 && lost && lane == 0) {
+    // the copies in flight land before the shared memory goes
+    for (; used < issued; ++used)
+      mbar_wait_bounded(bar0 + 8u * (uint32_t)(used % a.stages), (uint32_t)(used / a.stages) & 1u);
+    atomicOr(a.err, RQ_DEVERR_TIMEOUT);
   }
 }
 
@@ -908,7 +977,10 @@ const void *decode_fn(int L) {
 namespace {
 template <int DS, int LL>
 const void *rows_fn(int vec) {
-  if (vec == 4) return reinterpret_cast<const void *>(&loss_decode_rows_kernel<DS, LL, 4>);
+  constexpr int N = RowUnit<DS>::G * LL;
+  if (vec == 16 && N <= 16)      // (of a byte; 8 of two)
+    return reinterpret_cast<const void *>(&loss_decode_rows_kernel<DS, LL, N <= 16 ? 16 : 4>);
+  if (vec >= 4) return reinterpret_cast<const void *>(&loss_decode_rows_kernel<DS, LL, 4>);
   if (vec) return reinterpret_cast<const void *>(&loss_decode_rows_kernel<DS, LL, 1>);
   return reinterpret_cast<const void *>(&loss_decode_rows_kernel<DS, LL, 0>);
 }
@@ -951,13 +1023,22 @@ bool decode_rows_ok(int K, int L, int ds) {
 static cudaError_t launch_decode_rows(const CodeSrc &cs, const float *C, int M, int L, int ds, int64_t v0,
                                int64_t rows, int64_t pitch, const float *amax, __half *hi,
                                __half *lo, const DwPlanes &dw, const DevInfo &di, cudaStream_t s) {
-  const size_t smem = unit_bytes(cs.K, L, ds);
+  size_t smem = unit_bytes(cs.K, L, ds);
+  const int units = (M + unit_subspaces(ds) - 1) / unit_subspaces(ds);
   const int64_t bits = cs.fmt == RQ_CODES_U16       ? 16
                        : cs.fmt == RQ_CODES_U8       ? 8
                        : cs.fmt == RQ_CODES_PACKED10 ? 10
                                                      : 0;
   const int64_t row = (bits * cs.P + 7) / 8;
-  const int vec = bits == 0 ? 0 : row % 16 == 0 ? 4 : row % 4 == 0 ? 1 : 0;
+  int vec = bits == 0 ? 0 : row % 16 == 0 ? 4 : row % 4 == 0 ? 1 : 0;
+  // by TMA where a unit's codes never cross a word (they start at multiples of
+  // gcd(their bits, 128)), two stages fit beside the books and a thread has rows
+  // enough (8192 rows of 96 units, 10 a thread: 39 us, 36 by loads; 32768 99, 104)
+  const int64_t unit = bits * unit_subspaces(ds) * L, low = unit & -unit;
+  const int64_t fit = (226 * 1024 - 128 - (int64_t)smem) / (kRowWarps * 512);
+  if (vec == 4 && unit + 128 - (low < 128 ? low : 128) <= 128 && fit >= 2 &&
+      M % unit_subspaces(ds) == 0 && rows * units >= 24 * (int64_t)di.sms * kRowThreads)
+    vec = 16;
   const void *fn = ds == 2   ? rows_fn<2>(L, vec)
                    : ds == 3 ? rows_fn<3>(L, vec)
                    : ds == 4 ? rows_fn<4>(L, vec)
@@ -970,7 +1051,7 @@ static cudaError_t launch_decode_rows(const CodeSrc &cs, const float *C, int M, 
   a.cs = cs;
   a.C = C;
   a.M = M;
-  a.units = (M + unit_subspaces(ds) - 1) / unit_subspaces(ds);
+  a.units = units;
   a.bits = (int)bits;
   a.v0 = v0;
   a.rows = rows;
@@ -981,6 +1062,15 @@ static cudaError_t launch_decode_rows(const CodeSrc &cs, const float *C, int M, 
   a.cols = (M * ds + 7) / 8;
   a.dw = dw;
   a.pairs = (reinterpret_cast<uintptr_t>(C) & 7) == 0 && cs.K * ds % 2 == 0;
+  a.err = di.err;
+  a.stages = fit < kRowStages ? (int)fit : kRowStages;
+  CUtensorMap map = {};
+  if (vec == 16) {
+    smem += 128 + (size_t)a.stages * kRowWarps * 512;
+    if (!encode_tmap_2d_u16(&map, cs.codes, (uint64_t)row / 2, (uint64_t)cs.V, (uint64_t)row, 8, 32,
+                            CU_TENSOR_MAP_SWIZZLE_NONE))
+      return cudaErrorInvalidValue;
+  }
   const cudaError_t e = ensure_smem_limit(fn, di.device, smem);
   if (e != cudaSuccess) return e;
   const int64_t ctas = (int64_t)di.sms * occupancy_cached(fn, di.device, kRowThreads, smem);
@@ -989,7 +1079,7 @@ static cudaError_t launch_decode_rows(const CodeSrc &cs, const float *C, int M, 
   const int64_t items = (rows + a.chunk - 1) / a.chunk * a.units;
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
   a.items = (int)items;
-  void *args[] = {&a};
+  void *args[] = {&map, &a};
   const int64_t all = items + dw.N;
   return launch_maybe_pdl(fn, dim3((unsigned)(all < ctas ? all : ctas)), dim3(kRowThreads), smem,
                           s, args, true);

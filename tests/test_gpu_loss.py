@@ -475,3 +475,15 @@ def test_decoding(c):
     M, ds, L, K, fmt = c
     x = Head(777, M, ds, L, K, 66, fmt=fmt, seed=15)
     x.check()
+
+
+@pytest.mark.parametrize("c", [
+    (30005, 256, 6, 2, 32, "u16"), (30001, 256, 6, 2, 32, "u8"), (20003, 96, 8, 2, 40, "u16"),
+    (20003, 96, 8, 3, 40, "u8"), (31001, 256, 4, 1, 20, "packed10"), (61000, 256, 2, 3, 25, "u8"),
+    (125000, 128, 3, 2, 30, "u8")])
+def test_decoding_many_rows(c):
+    """The same where codes are fetched many rows ahead, with chunks that end
+    unevenly and a second piece."""
+    V, M, ds, L, K, fmt = c
+    x = Head(V, M, ds, L, K, 66, fmt=fmt, seed=16)
+    x.check()
