@@ -61,13 +61,15 @@ struct Arena {
   }
 };
 
-// Rows of the vocabulary per piece, whole index blocks: 65536, or more where
-// rows are short, up to what 600 MB of planes hold (8 blocks measured fastest
-// for rows of 2304 and 256 to 2048 tokens: 9.9 ms where 4 take 10.3, 2 take
-// 10.9, 1 takes 12.0; fewer launches and ends of waves).
+// Rows of the vocabulary per piece, whole index blocks: 131072, or more where
+// rows are short, up to what 1.2 GB of planes and gradients hold.  Fewer pieces
+// are fewer launches and ends of waves, more hold more memory (rows of 2304: 1.2
+// GB for a loss, 2.4 GB and 0.5 MB per token for gradients).  Rows of 2304, 500
+// tokens: 3 blocks a piece 9.1 ms a step, 5 8.7, 8 8.4, 16 8.2; 64 tokens' loss
+// 1.60, 1.62, 1.32 and 1.25 ms.
 int64_t piece_rows(const rq_dims &d, int64_t tokens) {
-  const int64_t fit = 600000000 / (8 * (int64_t)d.D + 4 * tokens) / kGradRows;
-  const int64_t rows = (fit < 8 ? 8 : fit) * kGradRows;
+  const int64_t fit = 1200000000 / (8 * (int64_t)d.D + 4 * tokens) / kGradRows;
+  const int64_t rows = (fit < 16 ? 16 : fit) * kGradRows;
   return d.V < rows ? d.V : rows;
 }
 int64_t pitch16(int64_t n) { return align_up(n, 16); }   // fp16 rows of whole sectors
