@@ -108,8 +108,9 @@ struct Choice {
 
 // Estimated microseconds of the ways, from measurements at 256000 rows of 768
 // codes (V P = 197 million) and at heads a few hundred times smaller:
-//   decoding           810 for 295 million pairs of dims, two levels; 1070
-//                      where a thread has a pair of dims, not a row
+//   decoding           710 (uint16 codes) to 930 (10 bits) for 295 million pairs
+//                      of dims, two levels; 1070 where a thread has a pair of
+//                      dims, not a row
 //   a tensor product   per million elements of E 0.33 to read them and 0.47
 //                      per tile of 128 tokens
 //   serving, B <= 4    116 per token (tables in shared memory)
