@@ -536,7 +536,15 @@ __global__ void __launch_bounds__(kRowThreads)
                      : "=r"(next[0]), "=r"(next[1]), "=r"(next[2]), "=r"(next[3])
                      : "r"(ring + st * 512u + (uint32_t)lane * 16u)
                      : "memory");
-        __syncwarp();                                // all have read: the stage is free
+        // The stage is free once every lane has its words: the vote needs them
+        // (a barrier alone would let loads still under way meet the next copy,
+        // which no order but this holds back)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %0, 0;\n\tvote.sync.any.pred q, p, "
+            "0xffffffff;\n\tfence.proxy.async.shared::cta;\n\t}\n" ::"r"(next[0] ^ next[1] ^
+                                                                         next[2] ^ next[3])
+            : "memory");
+        __syncwarp();
         if (!lost) {
           ++used;
           if (lane == 0) issue();

@@ -487,3 +487,15 @@ def test_decoding_many_rows(c):
     V, M, ds, L, K, fmt = c
     x = Head(V, M, ds, L, K, 66, fmt=fmt, seed=16)
     x.check()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_same_bits_every_time(dtype):
+    """Copies that run ahead of their readers meet none of them: a head whose
+    codes come rows ahead, forty calls."""
+    x = Head(70001, 256, 6, 2, 1024, 200, dtype, seed=17)
+    want = x.run()
+    for _ in range(40):
+        got = x.run()
+        for n in want:
+            assert torch.equal(got[n], want[n]), n
