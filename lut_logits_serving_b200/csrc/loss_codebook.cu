@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(256) prepare_grad_kernel(const CodeSrc cs, con
 // global memory list by list, took 3.8 ms, and one without the pipeline 2.3 ms.
 constexpr int kPairFloats = 2 * kGradRows + 4;    // and the row of zeros, vectors kept whole
 constexpr int kGatherThreads = 1024;
+constexpr size_t kGatherSmemMax = 226 * 1024;     // 227 KB less the static part
 
 struct GatherArgs {
   const float *vals;        // values in pairs of value rows, [pair][pitch][2]
@@ -259,6 +260,7 @@ struct GatherArgs {
   int64_t out_pair;                  // pair (0: its two columns lie at 2 pair)
   int accumulate;
   int buffers;              // for units: 2, or 3 (see the kernel)
+  int value_buffers;        // for values: 2, or 1 where codebooks are largest
   unsigned *err;
 };
 
@@ -318,10 +320,10 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int kWarps = kGatherThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int K = a.x.K, g = a.x.lanes, gsh = __ffs(g) - 1, nb = a.buffers;
+  const int K = a.x.K, g = a.x.lanes, gsh = __ffs(g) - 1, nb = a.buffers, nv = a.value_buffers;
   unsigned char *units = smem;                                     // [nb] units
-  float *vals = reinterpret_cast<float *>(smem + nb * a.x.unit);   // [2][kPairFloats]
-  float2 *stage = reinterpret_cast<float2 *>(vals + 2 * kPairFloats);  // [levels][K]
+  float *vals = reinterpret_cast<float *>(smem + nb * a.x.unit);   // [nv][kPairFloats]
+  float2 *stage = reinterpret_cast<float2 *>(vals + nv * kPairFloats);  // [levels][K]
   __shared__ uint64_t bars[3 + 2 + 2];        // units, values, steps done (all warps)
   __shared__ volatile int abort_flag;
   auto ubar = [&](int i) { return smem_addr(&bars[i]); };
@@ -333,44 +335,45 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
     fence_mbar_init();
     abort_flag = 0;
   }
-  if (tid < 4) vals[(tid >> 1) * kPairFloats + 2 * kGradRows + (tid & 1)] = 0.f;
+  if (tid < 2 * nv) vals[(tid >> 1) * kPairFloats + 2 * kGradRows + (tid & 1)] = 0.f;
   griddep_launch_dependents();
   __syncthreads();
   griddep_wait();
   // The last warp, whose lists are the shortest, issues the copies: a step
   // (units) and a block (values) ahead.  With three unit buffers the warps may
   // be a step apart (`lag` 2: a step starts when all have finished the last but
-  // one), so that nobody waits for the longest list of every step.
+  // one), so that nobody waits for the longest list of every step.  With one
+  // value buffer (lag 1) a block's values come once the last block is done.
   const int lag = nb - 1;
   const uint32_t vals_at = smem_addr(vals);
   const bool issuer = tid == kGatherThreads - 32;
-  GatherAhead nu{}, nv{};
+  GatherAhead au{}, av{};
   int it = 0, iv = 0;        // copies issued
   auto issue_unit = [&]() {
-    if (nu.u >= a.units) return;
+    if (au.u >= a.units) return;
     const int i = it % nb;
     mbar_arrive_expect_tx(ubar(i), (uint32_t)a.x.unit);
     bulk_g2s(smem_addr(units + i * a.x.unit),
              static_cast<const unsigned char *>(a.index) +
-                 ((size_t)(a.block0 + nu.b) * a.x.P + nu.q.m * a.L + nu.l) * a.x.unit,
+                 ((size_t)(a.block0 + au.b) * a.x.P + au.q.m * a.L + au.l) * a.x.unit,
              (uint32_t)a.x.unit, ubar(i));
     ++it;
-    nu.step(a);
+    au.step(a);
   };
   auto issue_vals = [&]() {
-    if (nv.u >= a.units) return;
-    const int64_t r0 = (int64_t)nv.b * kGradRows, left = a.rows - r0;
+    if (av.u >= a.units) return;
+    const int64_t r0 = (int64_t)av.b * kGradRows, left = a.rows - r0;
     const uint32_t bytes = (uint32_t)align_up(left < kGradRows ? left : kGradRows, 2) * 8;
-    const int i = iv & 1;
-    const int64_t pair = (a.per_subspace ? (int64_t)nv.q.m * a.pairs : 0) + nv.q.j / 2;
+    const int i = iv & (nv - 1);
+    const int64_t pair = (a.per_subspace ? (int64_t)av.q.m * a.pairs : 0) + av.q.j / 2;
     mbar_arrive_expect_tx(vbar(i), bytes);
     bulk_g2s(smem_addr(vals + i * kPairFloats), a.vals + (pair * a.pitch + r0) * 2, bytes, vbar(i));
     ++iv;
-    nv.block(a);
+    av.block(a);
   };
   if (issuer) {
-    nu.unit(a, blockIdx.x);
-    nv = nu;
+    au.unit(a, blockIdx.x);
+    av = au;
     issue_unit();
     issue_vals();
   }
@@ -393,21 +396,22 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
         if (abort_flag) ok = false;      // (the loops go on, without work, to meet at their ends)
         // everyone has finished step t - lag: its unit buffer takes the next
         // unit, its lists' sums are in the stage, and, a step into a block (at
-        // lag 1 at once), nobody reads the last block's values any more
+        // lag 1 at once), nobody reads the last block's values any more, in
+        // whose place go the next block's (of one buffer, this block's)
         if (t >= lag) wait(dbar((t - lag) & 1), (uint32_t)((t - lag) >> 1) & 1u);
         if (issuer && ok) {
           issue_unit();
-          if (l == q.l0 + (lag > 1 ? 1 : 0)) issue_vals();
+          if (l == q.l0 + (lag > 1 ? 1 : 0) && (nv > 1 || vt > 0)) issue_vals();
         }
         wait(ubar(ub), uphase);
-        if (l == q.l0) wait(vbar(vt & 1), (uint32_t)(vt >> 1) & 1u);
+        if (l == q.l0) wait(vbar(vt & (nv - 1)), (uint32_t)(vt >> (nv - 1)) & 1u);
         if (ok) {
           const unsigned char *un = units + ub * a.x.unit;
           const uint16_t *off = reinterpret_cast<const uint16_t *>(un);
           const uint16_t *code = reinterpret_cast<const uint16_t *>(un + a.x.code_at);
           const uint16_t *over = reinterpret_cast<const uint16_t *>(un + a.x.over_at);
           const uint32_t entry = smem_addr(un) + (uint32_t)a.x.entry_at + (uint32_t)lane * 4;
-          const uint32_t v0 = vals_at + (uint32_t)(vt & 1) * (kPairFloats * 4);
+          const uint32_t v0 = vals_at + (uint32_t)(vt & (nv - 1)) * (kPairFloats * 4);
           float2 *st = stage + (size_t)(l - q.l0) * K;
           // one word of entries: two rows of either value row
           auto add = [&](uint32_t w, float &s0, float &s1) {
@@ -505,8 +509,8 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
     // the copies in flight land before the shared memory goes
     for (int i = 1; i <= nb; ++i)
       if (it >= i) mbar_wait_bounded(ubar((it - i) % nb), (uint32_t)((it - i) / nb) & 1u);
-    for (int i = 1; i <= 2; ++i)
-      if (iv >= i) mbar_wait_bounded(vbar((iv - i) & 1), (uint32_t)((iv - i) >> 1) & 1u);
+    for (int i = 1; i <= nv; ++i)
+      if (iv >= i) mbar_wait_bounded(vbar((iv - i) & (nv - 1)), (uint32_t)((iv - i) >> (nv - 1)) & 1u);
     atomicOr(a.err, RQ_DEVERR_TIMEOUT);
   }
 }
@@ -649,18 +653,20 @@ namespace {
 
 // Units of a gather and how they split: a column of its own where a subspace's
 // L sums do not fit, or where whole subspaces would leave SMs idle; then
-// shares of the blocks.
+// shares of the blocks.  From 3841 codewords on (8192 rows or more) two blocks'
+// values no longer fit beside a column's sums, and one does up to kMaxGradK:
+// 2 x 35712 bytes of units, 65552 of values and 32768 of sums.
 struct GatherPlan {
   bool by_level;
-  int splits, buffers;
+  int splits, buffers, value_buffers;
   int64_t units;
   size_t smem;
 };
 
 GatherPlan gather_plan(const IndexShape &x, int blocks, int sources, int pairs, int L) {
   GatherPlan p;
-  const auto bytes = [&](int levels, int buffers = 2) {
-    return buffers * x.unit + (size_t)2 * kPairFloats * 4 + (size_t)levels * x.K * 8;
+  const auto bytes = [&](int levels, int buffers = 2, int value_buffers = 2) {
+    return buffers * x.unit + (size_t)value_buffers * kPairFloats * 4 + (size_t)levels * x.K * 8;
   };
   p.units = (int64_t)sources * pairs;
   p.by_level = L > 1 && (bytes(L) > 225 * 1024 || p.units < 148);
@@ -668,8 +674,9 @@ GatherPlan gather_plan(const IndexShape &x, int blocks, int sources, int pairs, 
   // warps a step apart need a third unit buffer, and two levels: a step's sums
   // and values are then not those of the step before
   const int levels = p.by_level ? 1 : L;
-  p.buffers = levels > 1 && bytes(levels, 3) <= 226 * 1024 ? 3 : 2;
-  p.smem = bytes(levels, p.buffers);
+  p.buffers = levels > 1 && bytes(levels, 3) <= kGatherSmemMax ? 3 : 2;
+  p.value_buffers = bytes(levels, p.buffers) <= kGatherSmemMax ? 2 : 1;
+  p.smem = bytes(levels, p.buffers, p.value_buffers);
   p.splits = 1;
   if (p.units < 148) {
     const int64_t n = 148 / p.units;
@@ -680,10 +687,11 @@ GatherPlan gather_plan(const IndexShape &x, int blocks, int sources, int pairs, 
 }
 
 cudaError_t launch_gather(GatherArgs a, const GatherPlan &p, const DevInfo &di, cudaStream_t s) {
-  if (p.units > 0x7fffffff || p.smem > 226 * 1024) return cudaErrorInvalidValue;
+  if (p.units > 0x7fffffff || p.smem > kGatherSmemMax) return cudaErrorInvalidValue;
   a.by_level = p.by_level ? 1 : 0;
   a.splits = p.splits;
   a.buffers = p.buffers;
+  a.value_buffers = p.value_buffers;
   a.units = (int)p.units;
   a.err = di.err;
   const void *fn = reinterpret_cast<const void *>(&codebook_gather_kernel);

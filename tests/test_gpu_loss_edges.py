@@ -1,0 +1,50 @@
+"""GPU tests of the losses on the RQ-coded head at the ends of their ranges:
+large codebooks, wide subspaces, rows of E with a common part, values of any
+size, lists of a teacher that hold the type's lowest value or NaN.  References
+and heads as in test_gpu_loss.py."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import lut_logits_serving_b200 as rq  # noqa: E402
+from tests import loss_ref  # noqa: E402
+from tests.test_gpu_loss import Head, compare  # noqa: E402
+
+
+@pytest.fixture(autouse=True)
+def _clear():
+    rq.rq_device_error()
+    yield
+
+
+# V, M, ds, L, K, N
+BOOKS = [
+    (9001, 2, 2, 1, 3840, 4), (9001, 2, 2, 1, 3841, 4), (9001, 2, 2, 2, 3841, 70),
+    (70001, 4, 3, 2, 4096, 5), (70001, 4, 3, 2, 4096, 70),       # shares of the blocks, an odd dim
+    (25001, 400, 2, 1, 4096, 66),                                # several units a CTA, blocks each
+    (25001, 75, 4, 3, 4000, 66), (8192, 5, 8, 2, 4096, 3), (8193, 3, 1, 1, 4096, 20),
+    (150001, 2, 4, 1, 4096, 66),                                 # a second piece
+]
+
+
+@pytest.mark.parametrize("c", BOOKS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_large_codebooks(c, dtype):
+    """Up to 4096 codewords on more rows than one block of the index has."""
+    V, M, ds, L, K, N = c
+    Head(V, M, ds, L, K, N, dtype, seed=20).check()
+
+
+@pytest.mark.parametrize("N", [4, 70])
+def test_large_codebooks_of_few_used_codewords(N):
+    """A quarter of the rows share a codeword: lists that go on past their lanes."""
+    x = Head(20001, 3, 4, 2, 4096, N, seed=21)
+    x.codes[::4] = 4095
+    x.packed = x.codes.to(torch.int16).view(torch.uint16).view(x.V, -1)
+    x.index = rq.rq_prepare_grad(x.packed, x.fmt, x.d)
+    a, _ = x.check()
+    for _ in range(5):
+        b = x.run()
+        for n in a:
+            assert torch.equal(a[n], b[n]), n

@@ -1,0 +1,17 @@
+"""Host-only checks of the losses at the ends of their ranges (no GPU): sizes
+that every accepted shape has to fit, refusals before any launch, and that a
+refused call leaves the caller's device and arguments alone."""
+import pytest
+
+import lut_logits_serving_b200 as rq
+
+
+@pytest.mark.parametrize("V", [1, 3000, 8191, 8192, 256000])
+def test_every_accepted_codebook_has_room(V):
+    """The sums by code keep two units of the index, the values of a block of
+    8192 rows and a column's sums in shared memory (226 KB)."""
+    blocks = (V + 8191) // 8192
+    for K in range(1, 4097):
+        unit = rq.rq_grad_index_bytes(rq.dims(V, 1, 1, 1, K)) // blocks
+        assert 0 < 2 * unit + (2 * 8192 + 4) * 4 + 8 * K <= 226 * 1024, K
+    assert rq.rq_grad_index_bytes(rq.dims(V, 1, 1, 1, 4097)) == 0
