@@ -48,3 +48,27 @@ def test_large_codebooks_of_few_used_codewords(N):
         b = x.run()
         for n in a:
             assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("k", [0, 12])
+@pytest.mark.parametrize("N", [80, 300])
+def test_bf16_gradient_of_rows_with_a_common_part(N, k):
+    """Rows of E that share a component 200 times their spread.  dz sums to zero
+    over the vocabulary without a softcap, so dh holds none of it: what is lost
+    of dz or E shows.  Within the bounds of float operands and one rounding to
+    bf16."""
+    x = Head(3000, 16, 6, 2, 100, N, torch.bfloat16, seed=22)
+    g = torch.Generator("cuda").manual_seed(1)
+    # 200 x the spread of an element (1 / sqrt(D) and a quarter of that)
+    x.C[:, 0] += 200 * (1.0 / x.d.D) ** 0.5 * torch.randn(16, 1, 6, generator=g, device="cuda").sign()
+    x.h = (1e-4 * x.h.float()).bfloat16()
+    ids, val = x.target, None
+    if k:
+        x.teacher(k)
+        x.val /= 4
+        ids, val = x.idx, x.val
+    got = x.run(cap=0.0)
+    ref = loss_ref.losses(x.h, x.C, x.codes, ids, val, 1.0, 0.0)
+    lim = loss_ref.bounds(ref, False)["dh"] + 2.0 ** -8 * ref["dh"].abs()
+    off = (got["dh"].double() - ref["dh"]).abs()
+    assert (off <= lim).all(), (off / lim).max().item()
