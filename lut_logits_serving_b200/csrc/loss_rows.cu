@@ -240,10 +240,9 @@ __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeAr
   const int ds = a.ds, L = LL > 0 ? LL : a.L, K = a.cs.K, tid = threadIdx.x;
   const float se = scale_e(a.amax, a.L);
   const int words = (a.gs * ds + 1) / 2;            // pairs of a row's group
-  const int rstep = kDecThreads / words;            // rows the CTA takes at once
-  const int w = tid % words, lrow = tid / words;
-  const int sub = 2 * w / ds, sub1 = EVEN ? sub : (2 * w + 1) / ds;
-  const int j = 2 * w - sub * ds, j1 = 2 * w + 1 - sub1 * ds;
+  const int span = words < kDecThreads ? words : kDecThreads;
+  const int rstep = kDecThreads / span;             // rows the CTA takes at once
+  const int lrow = tid / span;
   float sdw = 0.f;
   for (int64_t u = blockIdx.x; u < (int64_t)a.items + a.dw.N; u += gridDim.x) {
     if (u >= a.items) {
@@ -275,71 +274,78 @@ __global__ void __launch_bounds__(kDecThreads) loss_decode_kernel(const DecodeAr
       for (int i = i0 + tid; i < n; i += kDecThreads) books[i] = src[i] * se;
       __syncthreads();
     }
-    if (lrow >= rstep || sub >= ms) continue;
-    const bool second = EVEN || sub1 < ms;          // an odd last pair has one dim
-    const float *b0 = (SMEM ? books + sub * a.book : a.C + (m0 + sub) * a.book) + j;
-    const float *b1 = (SMEM ? books + sub1 * a.book : a.C + (m0 + sub1) * a.book) + j1;
-    const int m = m0 + sub, m1 = m0 + sub1;
-    const int64_t vc = a.v0 + r0;
-    const int n = (int)(r1 - r0);
-    const CodeRow ca(a.cs, vc, m, L), cb(a.cs, vc, EVEN ? m : m1, L);
-    const int dim = m0 * ds + 2 * w;
-    __half *oh = a.hi + ((dim >> 3) * a.pitch + r0) * 8 + (dim & 7);
-    __half *ol = a.lo + ((dim >> 3) * a.pitch + r0) * 8 + (dim & 7);
-    RowCodes<LL> cn[kDecU], dn[EVEN ? 1 : kDecU];
-    auto fetch = [&](int r) {
+    // (wide subspaces have more pairs than the CTA threads)
+    if (lrow >= rstep) continue;
+#pragma unroll 1
+    for (int w = tid % span; w < words; w += kDecThreads) {
+      const int sub = 2 * w / ds, sub1 = EVEN ? sub : (2 * w + 1) / ds;
+      const int j = 2 * w - sub * ds, j1 = 2 * w + 1 - sub1 * ds;
+      if (sub >= ms) break;
+      const bool second = EVEN || sub1 < ms;          // an odd last pair has one dim
+      const float *b0 = (SMEM ? books + sub * a.book : a.C + (m0 + sub) * a.book) + j;
+      const float *b1 = (SMEM ? books + sub1 * a.book : a.C + (m0 + sub1) * a.book) + j1;
+      const int m = m0 + sub, m1 = m0 + sub1;
+      const int64_t vc = a.v0 + r0;
+      const int n = (int)(r1 - r0);
+      const CodeRow ca(a.cs, vc, m, L), cb(a.cs, vc, EVEN ? m : m1, L);
+      const int dim = m0 * ds + 2 * w;
+      __half *oh = a.hi + ((dim >> 3) * a.pitch + r0) * 8 + (dim & 7);
+      __half *ol = a.lo + ((dim >> 3) * a.pitch + r0) * 8 + (dim & 7);
+      RowCodes<LL> cn[kDecU], dn[EVEN ? 1 : kDecU];
+      auto fetch = [&](int r) {
 #pragma unroll
-      for (int i = 0; i < kDecU; ++i) {
-        const int x = r + i * rstep;
-        if (LL > 0 && x < n) {
-          cn[i].load(a.cs, ca, x, vc + x, m);
-          if (!EVEN && second) dn[EVEN ? 0 : i].load(a.cs, cb, x, vc + x, m1);
-        }
-      }
-    };
-    fetch(lrow);
-    for (int r = lrow; r < n; r += kDecU * rstep) {
-      RowCodes<LL> c[kDecU], d[EVEN ? 1 : kDecU];
-#pragma unroll
-      for (int i = 0; i < kDecU; ++i) {
-        c[i] = cn[i];
-        if (!EVEN) d[EVEN ? 0 : i] = dn[EVEN ? 0 : i];
-      }
-      fetch(r + kDecU * rstep);
-#pragma unroll
-      for (int i = 0; i < kDecU; ++i) {
-        const int x = r + i * rstep;
-        if (x >= n) break;
-        float e0 = 0.f, e1 = 0.f;
-#pragma unroll(LL > 0 ? LL : 1)
-        for (int l = 0; l < L; ++l) {
-          const uint32_t cl = LL > 0 ? c[i].get(a.cs, ca, l) : a.cs(vc + x, m * L + l);
-          const float *p0 = b0 + (int64_t)(l * K + (int)cl) * ds;
-          if (EVEN && SMEM) {
-            const float2 y = *reinterpret_cast<const float2 *>(p0);
-            e0 = __fadd_rn(e0, y.x);
-            e1 = __fadd_rn(e1, y.y);
-          } else {
-            e0 = __fadd_rn(e0, *p0);
-            if (EVEN) {
-              e1 = __fadd_rn(e1, p0[1]);
-            } else if (second) {
-              const uint32_t dl = LL > 0 ? d[EVEN ? 0 : i].get(a.cs, cb, l)
-                                         : a.cs(vc + x, m1 * L + l);
-              e1 = __fadd_rn(e1, b1[(int64_t)(l * K + (int)dl) * ds]);
-            }
+        for (int i = 0; i < kDecU; ++i) {
+          const int x = r + i * rstep;
+          if (LL > 0 && x < n) {
+            cn[i].load(a.cs, ca, x, vc + x, m);
+            if (!EVEN && second) dn[EVEN ? 0 : i].load(a.cs, cb, x, vc + x, m1);
           }
         }
-        if (!SMEM) {
-          e0 = __fmul_rn(e0, se);
-          e1 = __fmul_rn(e1, se);
+      };
+      fetch(lrow);
+      for (int r = lrow; r < n; r += kDecU * rstep) {
+        RowCodes<LL> c[kDecU], d[EVEN ? 1 : kDecU];
+#pragma unroll
+        for (int i = 0; i < kDecU; ++i) {
+          c[i] = cn[i];
+          if (!EVEN) d[EVEN ? 0 : i] = dn[EVEN ? 0 : i];
         }
-        // columns are padded to 8 dims, so a pair past D has its place; a group
-        // starts on a pair unless gs ds is odd (one group then)
-        uint32_t hw, lw;
-        split_pair(e0, e1, hw, lw);
-        *reinterpret_cast<uint32_t *>(oh + (int64_t)x * 8) = hw;
-        *reinterpret_cast<uint32_t *>(ol + (int64_t)x * 8) = lw;
+        fetch(r + kDecU * rstep);
+#pragma unroll
+        for (int i = 0; i < kDecU; ++i) {
+          const int x = r + i * rstep;
+          if (x >= n) break;
+          float e0 = 0.f, e1 = 0.f;
+#pragma unroll(LL > 0 ? LL : 1)
+          for (int l = 0; l < L; ++l) {
+            const uint32_t cl = LL > 0 ? c[i].get(a.cs, ca, l) : a.cs(vc + x, m * L + l);
+            const float *p0 = b0 + (int64_t)(l * K + (int)cl) * ds;
+            if (EVEN && SMEM) {
+              const float2 y = *reinterpret_cast<const float2 *>(p0);
+              e0 = __fadd_rn(e0, y.x);
+              e1 = __fadd_rn(e1, y.y);
+            } else {
+              e0 = __fadd_rn(e0, *p0);
+              if (EVEN) {
+                e1 = __fadd_rn(e1, p0[1]);
+              } else if (second) {
+                const uint32_t dl = LL > 0 ? d[EVEN ? 0 : i].get(a.cs, cb, l)
+                                           : a.cs(vc + x, m1 * L + l);
+                e1 = __fadd_rn(e1, b1[(int64_t)(l * K + (int)dl) * ds]);
+              }
+            }
+          }
+          if (!SMEM) {
+            e0 = __fmul_rn(e0, se);
+            e1 = __fmul_rn(e1, se);
+          }
+          // columns are padded to 8 dims, so a pair past D has its place; a group
+          // starts on a pair unless gs ds is odd (one group then)
+          uint32_t hw, lw;
+          split_pair(e0, e1, hw, lw);
+          *reinterpret_cast<uint32_t *>(oh + (int64_t)x * 8) = hw;
+          *reinterpret_cast<uint32_t *>(ol + (int64_t)x * 8) = lw;
+        }
       }
     }
   }
@@ -1112,17 +1118,18 @@ cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, 
   a.lo = lo;
   a.book = (int64_t)L * cs.K * ds;
   a.dw = dw;
-  // as many subspaces as their codebooks fit in shared memory, at most a pair
-  // per thread, and a whole number of pairs unless one group has them all
+  // as many subspaces as their codebooks fit in shared memory, a whole number of
+  // pairs unless one group has them all, and at most a pair per thread unless
+  // the fewest have more
   const int64_t fit = 220 * 1024 / 4 / a.book;
   const bool even = ds % 2 == 0;
-  const bool in_smem = fit >= (even || M == 1 ? 1 : 2);
+  const int64_t fewest = even || M == 1 ? 1 : 2;
+  const bool in_smem = fit >= fewest;
   int64_t gs = in_smem ? fit : M;
   if (gs > M) gs = M;
   if (gs * ds > 2 * kDecThreads) gs = 2 * kDecThreads / ds;
-  if (gs < 1) return cudaErrorInvalidValue;
+  if (gs < fewest) gs = fewest;
   if (!even && gs < M) gs -= gs % 2;
-  if (gs < 1) return cudaErrorInvalidValue;
   a.gs = (int)gs;
   a.groups = (M + a.gs - 1) / a.gs;
   // even groups: fewer leftovers
@@ -1136,7 +1143,8 @@ cudaError_t launch_loss_decode(const CodeSrc &cs, const float *C, int M, int L, 
   cudaError_t e = ensure_smem_limit(fn, di.device, smem);
   if (e != cudaSuccess) return e;
   const int occ = occupancy_cached(fn, di.device, kDecThreads, smem);
-  const int rstep = kDecThreads / ((a.gs * ds + 1) / 2);
+  const int words = (a.gs * ds + 1) / 2;
+  const int rstep = words < kDecThreads ? kDecThreads / words : 1;
   const int64_t ctas = (int64_t)di.sms * occ;
   // rows per chunk: the shortest time of the last CTA, an item costing its rows
   // and the load of its books (as long as about 300 rows of 48 KB books a

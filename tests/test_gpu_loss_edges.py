@@ -72,3 +72,16 @@ def test_bf16_gradient_of_rows_with_a_common_part(N, k):
     lim = loss_ref.bounds(ref, False)["dh"] + 2.0 ** -8 * ref["dh"].abs()
     off = (got["dh"].double() - ref["dh"]).abs()
     assert (off <= lim).all(), (off / lim).max().item()
+
+
+@pytest.mark.parametrize("c", [
+    (600, 1, 2050, 1, 4, 66, "u16"),       # codebooks in shared memory
+    (600, 1, 2050, 2, 40, 2, "u8"),        # too large for it
+    (500, 2, 1025, 1, 16, 66, "u16"), (500, 2, 1025, 2, 10, 66, "packed10"),
+    (300, 3, 1025, 2, 300, 67, "u16"), (300, 5, 1027, 3, 7, 3, "u8"),
+    (130, 1, 6145, 1, 9, 70, "u16"), (130, 2, 4098, 4, 5, 70, "u8")])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_wide_subspaces(c, dtype):
+    """More pairs of dims in a group of subspaces than a CTA has threads."""
+    V, M, ds, L, K, N, fmt = c
+    Head(V, M, ds, L, K, N, dtype, fmt, seed=23).check()
