@@ -116,8 +116,12 @@ struct Choice {
 //   serving, B <= 4    116 per token (tables in shared memory)
 //   serving, groups    tables through L2: 14 TB/s, and at least 0.09 (10 bits
 //                      0.13, bytes 0.24) per column and row a thread has;
-//                      decoded groups: 450 (32 tokens, 1024 rows per SM), 340
-//                      (64, 512)
+//                      a rest of tokens behind a group of 32 at least 5 per
+//                      million codes (it reads that group's wide tables);
+//                      decoded groups: 450 (32 tokens or a rest of 17 and more,
+//                      1024 rows per SM), 340 (64, 512).  33 to 63 tokens are two
+//                      groups: 63 tokens of 227000 rows 1784 us served, 1093 as
+//                      a product; 33 of 256000 1958 and 1246
 //   sums by code       1.95 per million codes and pair (of tokens or dims)
 // The serving kernels' fallback for odd layouts walks a row's codes one by one
 // (385 where the tensor cores take 45) and is never chosen.
@@ -147,16 +151,19 @@ double serve_us(const rq_dims &d, int N, int fmt) {
                     : fmt == RQ_CODES_U8    ? P % 16 == 0
                                             : P % 64 == 0;
   if (!fast) return never;
-  const bool tc = decode_mma_shape_ok(fmt, d.V, d.D, d.M, d.L, d.K);
+  const bool shape = decode_mma_shape_ok(fmt, d.V, d.D, d.M, d.L, d.K);
+  const auto fits = [&](int n) { return decode_mma_smem(d.K, n, fmt) <= (size_t)di.max_smem_optin; };
+  const bool tc = shape && fits(32), tc64 = shape && fits(64);
   const int64_t per_sm = (d.V + kSms - 1) / kSms;
   double us = 8;
   for (int left = N; left > 0;) {
-    if (tc && left > 32) {
+    const int nd = decode_group(left, tc, tc64, false, kTcPartialMin);
+    if (nd == 64) {
       us += 340.0 * ((per_sm + 511) / 512) * P / 768 + 40;
       left -= 64;
-    } else if (tc && left > 16) {
+    } else if (nd > 0) {
       us += 450.0 * ((per_sm + 1023) / 1024) * P / 768 + 40;
-      left -= 32;
+      left -= nd;
     } else {
       int tok = 4;
       while (tok < left && tok < 32) tok *= 2;
@@ -164,7 +171,8 @@ double serve_us(const rq_dims &d, int N, int fmt) {
       const int64_t steps = (d.V + grid * (1024 / tok) - 1) / (grid * (1024 / tok));
       const double wait = (fmt == RQ_CODES_U8 ? 0.24 : fmt == RQ_CODES_U16 ? 0.09 : 0.13) * steps * P;
       const double move = codes * tok * 4 / 14;
-      us += 10 + (wait > move ? wait : move);
+      const double rest = left < N ? 5 * codes : 0;
+      us += 10 + (wait > move ? (wait > rest ? wait : rest) : (move > rest ? move : rest));
       left -= tok;
     }
   }

@@ -161,6 +161,23 @@ cudaError_t launch_logits_decode_mma(const float *h, const float *C, const void 
 size_t decode_mma_smem(int K, int N, int fmt);
 size_t decode_mma_hop_bytes(int M, int N, int K);
 
+// Smallest partial token group (fewer than 32 tokens) that the fused calls
+// send to the tensor cores by default: from the size where the tables
+// measured slower.
+constexpr int kTcPartialMin = 17;
+
+// Tokens of the next group of a fused call with `rem` left that are decoded and
+// multiplied: 64 or 32 on the tensor cores, 32 in FP32, or a rest of at least
+// `least` on the tensor cores, whose time hardly depends on the group's fill
+// where the tables' grows with it.  0: a group through tables.  (tc64: groups of
+// 64 have room.)
+inline int decode_group(int rem, bool tc, bool tc64, bool fma, int least) {
+  return tc && tc64 && rem >= 64    ? 64
+         : (tc || fma) && rem >= 32 ? 32
+         : tc && rem >= least       ? rem
+                                    : 0;
+}
+
 // Batched pass with the LUT read through L2 (token groups of <= 32).
 cudaError_t launch_logits_l2(const void *codes, int fmt, int64_t V, int P, int K,
                              const float *lut, int Bs, int lut_t0, int out_t0, int nb,

@@ -238,10 +238,8 @@ size_t table_region_bytes(const rq_dims &d, int B, int fmt) {
   return n;
 }
 
-// Smallest partial token group (fewer than 32 tokens) that the fused calls
-// send to the tensor cores: with RQ_PATH_DECODE_TC every group does (down to
-// one token); by default from the size where the tables measured slower.
-constexpr int kTcPartialMin = 17;
+// With RQ_PATH_DECODE_TC every partial token group goes to the tensor cores
+// (down to one token).
 int tc_partial_min(int path) { return path == RQ_PATH_DECODE_TC ? 1 : kTcPartialMin; }
 
 
@@ -295,13 +293,7 @@ int run_fused(const float *h, const float *C, const void *codes, int fmt, const 
   bool marked = false;   // the profile start goes before the first logits kernel
   for (int b0 = 0; b0 < B && e == cudaSuccess;) {
     const int rem = B - b0;
-    // a group of fewer than 32 tokens also takes the tensor cores from
-    // kTcPartialMin tokens on: their time hardly depends on the group's fill,
-    // the tables' grows with it
-    const int nd = use_tc && tc64 && rem >= 64                 ? 64
-                   : (use_tc || use_fma) && rem >= 32          ? 32
-                   : use_tc && rem >= tc_partial_min(path)     ? rem
-                                                               : 0;
+    const int nd = decode_group(rem, use_tc, tc64, use_fma, tc_partial_min(path));
     if (nd > 0) {
       if (!marked && (e = prof_mark(t_prof_start, s)) != cudaSuccess) break;
       marked = true;

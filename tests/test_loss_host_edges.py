@@ -15,3 +15,15 @@ def test_every_accepted_codebook_has_room(V):
         unit = rq.rq_grad_index_bytes(rq.dims(V, 1, 1, 1, K)) // blocks
         assert 0 < 2 * unit + (2 * 8192 + 4) * 4 + 8 * K <= 226 * 1024, K
     assert rq.rq_grad_index_bytes(rq.dims(V, 1, 1, 1, 4097)) == 0
+
+
+@pytest.mark.parametrize("N,V", [(63, 227000), (48, 75000), (40, 120000), (33, 20000), (33, 256000)])
+def test_logits_of_33_to_63_tokens_are_not_priced_as_one_group(N, V):
+    """The serving kernels take 64 tokens in one pass, 33 to 63 in two, which
+    is slower than one product; a call on the serving kernels' logits needs
+    little more workspace than those, one on products the decoded rows."""
+    d = rq.dims(V, 2304, 384, 2, 1024)
+    planes = 4 * 2304 * min(V, 131072)
+    assert rq.rq_loss_workspace_bytes(d, N, rq.U16) > planes
+    one = rq.dims(256000, 2304, 384, 2, 1024)
+    assert rq.rq_loss_workspace_bytes(one, 32, rq.U16) < 4 * 2304 * 131072
