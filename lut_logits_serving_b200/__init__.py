@@ -498,6 +498,11 @@ def _loss_sizes(V, D, M, L, K, fmt, N, k, grad):
             rq_loss_workspace_bytes(d, N, fmt, k, grad))
 
 
+def _stream_on(stream, device, name):
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream on {stream.device}, {name} on {device}")
+
+
 class _LossCall:
     """Checks and pointers of one call of the losses: every tensor on h's
     device, which is made current with the call's stream for the call's time
@@ -520,11 +525,10 @@ class _LossCall:
         if self.h.is_cuda:
             torch = _torch()
             if self.stream is not None or torch.cuda.current_device() != self.device.index:
+                _stream_on(self.stream, self.device, "h")    # before anything is entered
                 self.stack = contextlib.ExitStack()
                 self.stack.enter_context(torch.cuda.device(self.device))
                 if self.stream is not None:
-                    if self.stream.device != self.device:
-                        raise ValueError(f"stream on {self.stream.device}, h on {self.device}")
                     self.stack.enter_context(torch.cuda.stream(self.stream))
         return self
 

@@ -27,3 +27,55 @@ def test_logits_of_33_to_63_tokens_are_not_priced_as_one_group(N, V):
     assert rq.rq_loss_workspace_bytes(d, N, rq.U16) > planes
     one = rq.dims(256000, 2304, 384, 2, 1024)
     assert rq.rq_loss_workspace_bytes(one, 32, rq.U16) < 4 * 2304 * 131072
+
+
+class _OnDevice:
+    """What a tensor or a stream of another GPU says of itself."""
+    is_cuda = True
+
+    def __init__(self, index, N=3, D=192):
+        import torch
+        self.device, self.shape, self.dtype = torch.device("cuda", index), (N, D), torch.float32
+        self.cuda_stream = 0
+
+    def dim(self):
+        return 2
+
+
+@pytest.fixture
+def devices(monkeypatch):
+    """torch.cuda's current device and stream without a GPU; the list of devices
+    entered and left."""
+    torch = pytest.importorskip("torch")
+    log = []
+
+    class Context:
+        def __init__(self, what):
+            self.what = what
+
+        def __enter__(self):
+            log.append(("enter", self.what))
+
+        def __exit__(self, *exc):
+            log.append(("leave", self.what))
+
+    monkeypatch.setattr(torch.cuda, "device", lambda d: Context(str(d)))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: Context("stream of " + str(s.device)))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    return log
+
+
+def test_a_stream_of_another_device_leaves_the_current_one(devices):
+    """The refusal comes before the tensors' device is made current: no context
+    is left behind by a call that raises."""
+    call = rq._LossCall.__new__(rq._LossCall)
+    call.h, call.stream, call.stack = _OnDevice(1), _OnDevice(0), None
+    call.device = call.h.device
+    with pytest.raises(ValueError, match="stream on cuda:0, h on cuda:1"):
+        with call:
+            raise AssertionError("entered")
+    assert devices == []
+    call.stream = _OnDevice(1)
+    with call:
+        pass
+    assert [what for what, _ in devices] == ["enter", "enter", "leave", "leave"]
