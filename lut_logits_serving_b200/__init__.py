@@ -619,16 +619,19 @@ def rq_prepare_grad(codes, fmt: int, d: RqDims, out=None, stream=None):
     """Codes in any layout -> the index uint8 [rq_grad_index_bytes(d)] that
     the gradients of the losses sum the vocabulary's rows by."""
     torch = _torch()
+    if not isinstance(codes, torch.Tensor):
+        raise ValueError("codes: expected a torch.Tensor")
     nbytes = rq_grad_index_bytes(d)
+    _stream_on(stream, codes.device, "codes")
     with torch.cuda.device(codes.device) if codes.is_cuda else contextlib.nullcontext():
         with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
             if out is None:
                 out = _empty((nbytes,), torch.uint8, codes)
+            args = (_cuda(codes, _codes_dtype(fmt), "codes", rq_codes_bytes(d, fmt)), fmt, d,
+                    _cuda(out, torch.uint8, "index", nbytes))
             if out.device != codes.device:
                 raise ValueError(f"out: on {out.device}, codes on {codes.device}")
-            _check("rq_prepare_grad", lib().rq_prepare_grad(
-                _cuda(codes, _codes_dtype(fmt), "codes", rq_codes_bytes(d, fmt)), fmt, d,
-                _cuda(out, torch.uint8, "index", nbytes), _stream(None)))
+            _check("rq_prepare_grad", lib().rq_prepare_grad(*args, _stream(None)))
     return out
 
 

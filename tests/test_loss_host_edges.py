@@ -79,3 +79,31 @@ def test_a_stream_of_another_device_leaves_the_current_one(devices):
     with call:
         pass
     assert [what for what, _ in devices] == ["enter", "enter", "leave", "leave"]
+
+
+def test_prepare_grad_on_a_stream_of_another_device(devices, monkeypatch):
+    torch = pytest.importorskip("torch")
+    d = rq.dims(3, 192, 32, 2, 64)
+
+    class Codes(torch.Tensor):
+        is_cuda = True
+        device = torch.device("cuda", 1)
+
+    def codes():
+        return torch.zeros((3, 64), dtype=torch.uint16).as_subclass(Codes)
+
+    launched = []
+    monkeypatch.setattr(rq, "_on_device", lambda t: True)
+    monkeypatch.setattr(rq, "_stream", lambda s: None)
+    monkeypatch.setattr(rq, "_check", lambda name, status: launched.append(name))
+    out = torch.zeros(rq.rq_grad_index_bytes(d), dtype=torch.uint8).as_subclass(Codes)
+    with pytest.raises(ValueError, match="stream on cuda:0, codes on cuda:1"):
+        rq.rq_prepare_grad(codes(), rq.U16, d, out=out, stream=_OnDevice(0))
+    assert devices == [] and launched == []
+    with pytest.raises(ValueError, match="codes: expected a torch.Tensor"):
+        rq.rq_prepare_grad([1, 2], rq.U16, d)
+    with pytest.raises(ValueError, match="index: expected a torch.Tensor"):
+        rq.rq_prepare_grad(codes(), rq.U16, d, out=[0])
+    with pytest.raises(ValueError, match="out: on cpu, codes on cuda:1"):
+        rq.rq_prepare_grad(codes(), rq.U16, d, out=torch.zeros_like(torch.empty(out.shape, dtype=torch.uint8)))
+    assert launched == []
