@@ -557,6 +557,8 @@ class _LossCall:
         return self.h.new_empty(shape, dtype=dtype) if t is None else t
 
     def workspace(self, ws):
+        if ws is not None and not isinstance(ws, self.tensor):
+            raise ValueError("ws: expected a torch.Tensor")
         if ws is None or ws.nbytes < self.ws_bytes:
             ws = self.h.new_empty((self.ws_bytes,), dtype=_torch().uint8)
         return ws, self.ptr(ws, ws.dtype, "ws", self.ws_bytes), ws.nbytes
@@ -578,6 +580,9 @@ def _lists(call, val, idx, temperature):
 
 
 def _lists_k(h, val, idx):
+    for t, name in ((h, "h"), (val, "teacher_val"), (idx, "teacher_idx")):
+        if not isinstance(t, _torch().Tensor):
+            raise ValueError(f"{name}: expected a torch.Tensor")
     if idx.dim() != 2 or idx.shape[0] != (h.shape[0] if h.dim() == 2 else 1) or \
             val.shape != idx.shape:
         raise ValueError("teacher_val, teacher_idx: [N, k] expected")

@@ -107,3 +107,29 @@ def test_prepare_grad_on_a_stream_of_another_device(devices, monkeypatch):
     with pytest.raises(ValueError, match="out: on cpu, codes on cuda:1"):
         rq.rq_prepare_grad(codes(), rq.U16, d, out=torch.zeros_like(torch.empty(out.shape, dtype=torch.uint8)))
     assert launched == []
+
+
+@pytest.mark.parametrize("wrong", [None, [0, 1], 3.0])
+def test_arguments_that_are_no_tensors_are_named(wrong, monkeypatch):
+    torch = pytest.importorskip("torch")
+    d, N, k = rq.dims(4096, 192, 32, 2, 256), 3, 4
+    f32, i32 = torch.float32, torch.int32
+    good = {"h": torch.zeros(N, d.D), "C": torch.zeros(32, 2, 256, 6),
+            "codes": torch.zeros((d.V, 64), dtype=torch.uint16), "teacher_val": torch.zeros(N, k),
+            "teacher_idx": torch.zeros(N, k, dtype=i32), "lse": torch.zeros(N, dtype=f32),
+            "index": torch.zeros(rq.rq_grad_index_bytes(d), dtype=torch.uint8)}
+    monkeypatch.setattr(rq, "_on_device", lambda x: True)
+    for name in good:
+        a = dict(good)
+        a[name] = wrong
+        head = (a["h"], a["C"], a["codes"], rq.U16, d, a["teacher_val"], a["teacher_idx"])
+        with pytest.raises(ValueError, match=f"{name}: expected a torch.Tensor"):
+            rq.rq_distill_grad(*head, a["lse"], a["index"])
+        if name not in ("lse", "index"):
+            with pytest.raises(ValueError, match=f"{name}: expected a torch.Tensor"):
+                rq.rq_distill(*head)
+    if wrong is not None:
+        a = good
+        with pytest.raises(ValueError, match="ws: expected a torch.Tensor"):
+            rq.rq_distill(a["h"], a["C"], a["codes"], rq.U16, d, a["teacher_val"], a["teacher_idx"],
+                          ws=wrong)
