@@ -185,8 +185,13 @@ def _torch():
 
 def _stream(stream):
     torch = _torch()
-    if stream is None:      # without a Stream object around it, 2 us of a small call
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    if stream is None:
+        # without a Stream object around it, 2 us of a small call; not a public
+        # name of torch, so where it is missing the public call serves
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return ctypes.c_void_p(raw(torch.cuda.current_device()))
+        stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
 

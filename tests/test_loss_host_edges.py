@@ -133,3 +133,15 @@ def test_arguments_that_are_no_tensors_are_named(wrong, monkeypatch):
         with pytest.raises(ValueError, match="ws: expected a torch.Tensor"):
             rq.rq_distill(a["h"], a["C"], a["codes"], rq.U16, d, a["teacher_val"], a["teacher_idx"],
                           ws=wrong)
+
+
+def test_current_stream_without_torch_s_private_name(monkeypatch):
+    torch = pytest.importorskip("torch")
+    stream = _OnDevice(0)
+    stream.cuda_stream = 0x1230
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: stream)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0x4560, raising=False)
+    assert rq._stream(None).value == 0x4560
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert rq._stream(None).value == 0x1230 and rq._stream(stream).value == 0x1230
