@@ -664,7 +664,8 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 // An id of the lists counts when it lies in [0, V) and, for a teacher, its
-// logit is above -inf.
+// logit is above -inf.  A teacher's logits are taken from their largest before
+// the temperature divides them, which finite ones of any size survive.
 __device__ __forceinline__ bool listed(int32_t id, int64_t V) { return id >= 0 && id < V; }
 
 // A row's loss and log-sum-exp from its statistics p, by one warp.
@@ -689,18 +690,18 @@ __device__ void finish_row(float2 p, int64_t n, int64_t V, const LossTargets &t,
     float m = -INFINITY;
     for (int j = lane; j < t.k; j += 32) {
       if (id[j] >= V) atomicOr(err, RQ_DEVERR_BAD_ID);
-      if (listed(id[j], V)) m = fmaxf(m, val[j] * t.beta);
+      if (listed(id[j], V)) m = fmaxf(m, val[j]);
     }
     m = warp_max(m);
     float z = 0.f, a = 0.f;
     if (m > -INFINITY) {
       for (int j = lane; j < t.k; j += 32)
-        if (listed(id[j], V)) z += expf(val[j] * t.beta - m);
+        if (listed(id[j], V)) z += expf((val[j] - m) * t.beta);
       z = warp_sum(z);
       const float logz = logf(z);
       for (int j = lane; j < t.k; j += 32) {
         if (!listed(id[j], V)) continue;
-        const float d = val[j] * t.beta - m, e = expf(d);
+        const float d = (val[j] - m) * t.beta, e = expf(d);
         if (e > 0.f || e != e)
           a = fmaf(e, (d - logz) + ((p.x - __fmul_rn(logit(j), t.beta)) + ls), a);
       }
@@ -842,7 +843,7 @@ __device__ float sparse_row(const BeginArgs &a, int64_t n, float *lists) {
   float m = -INFINITY;
   for (int j = tid; j < k; j += nt) {
     int32_t v = id[j];
-    float x = t.val ? t.val[n * k + j] * t.beta : 0.f;
+    float x = t.val ? t.val[n * k + j] : 0.f;
     if (grad && v >= a.V) atomicOr(a.err, RQ_DEVERR_BAD_ID);
     if (!listed(v, a.V)) {
       v = kNoId;
@@ -863,7 +864,7 @@ __device__ float sparse_row(const BeginArgs &a, int64_t n, float *lists) {
     some = m > -INFINITY;
     if (some)
       for (int j = tid; j < k; j += nt) {
-        const float e = ids[j] != kNoId ? expf(q[j] - m) : 0.f;
+        const float e = ids[j] != kNoId ? expf((q[j] - m) * t.beta) : 0.f;
         q[j] = e;
         z += e;
       }

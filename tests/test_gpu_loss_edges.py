@@ -85,3 +85,19 @@ def test_wide_subspaces(c, dtype):
     """More pairs of dims in a group of subspaces than a CTA has threads."""
     V, M, ds, L, K, N, fmt = c
     Head(V, M, ds, L, K, N, dtype, fmt, seed=23).check()
+
+
+@pytest.mark.parametrize("T", [0.5, 1.0, 3.0])
+@pytest.mark.parametrize("N", [3, 70])
+def test_teacher_of_lowest_and_largest_values(N, T):
+    """Finite logits that the temperature takes out of float's range: only their
+    differences count.  (-inf alone stands for no entry.)"""
+    low = torch.finfo(torch.float32).min
+    x = Head(900, 8, 6, 2, 32, N, seed=24).teacher(6)
+    same = x.val.clone()
+    x.val[0], same[0] = low, 0.0                       # a row of it: all alike
+    x.val[1], same[1] = -low, 0.0
+    x.val[2, 1:], same[2, 1:] = low, -torch.inf        # beside another: nothing
+    got = x.run(T, weight=x.weight)
+    ref = loss_ref.losses(x.h, x.C, x.codes, x.idx, same, T, 30.0, x.weight)
+    compare(got, ref, False)
