@@ -668,6 +668,10 @@ __device__ __forceinline__ float warp_max(float x) {
 // the temperature divides them, which finite ones of any size survive.
 __device__ __forceinline__ bool listed(int32_t id, int64_t V) { return id >= 0 && id < V; }
 
+// A list's entry as its maximum takes it: fmaxf would pass over a NaN, and a list
+// of nothing else would pass for an empty one.
+__device__ __forceinline__ float list_top(float x) { return x != x ? INFINITY : x; }
+
 // A row's loss and log-sum-exp from its statistics p, by one warp.
 __device__ void finish_row(float2 p, int64_t n, int64_t V, const LossTargets &t,
                            const float *__restrict__ y, bool y_is_logits, float *__restrict__ loss,
@@ -690,7 +694,7 @@ __device__ void finish_row(float2 p, int64_t n, int64_t V, const LossTargets &t,
     float m = -INFINITY;
     for (int j = lane; j < t.k; j += 32) {
       if (id[j] >= V) atomicOr(err, RQ_DEVERR_BAD_ID);
-      if (listed(id[j], V)) m = fmaxf(m, val[j]);
+      if (listed(id[j], V)) m = fmaxf(m, list_top(val[j]));
     }
     m = warp_max(m);
     float z = 0.f, a = 0.f;
@@ -851,7 +855,7 @@ __device__ float sparse_row(const BeginArgs &a, int64_t n, float *lists) {
     }
     ids[j] = v;
     q[j] = x;
-    m = fmaxf(m, x);
+    m = fmaxf(m, list_top(x));
   }
   bool some = true;
   float z = 0.f;

@@ -101,3 +101,20 @@ def test_teacher_of_lowest_and_largest_values(N, T):
     got = x.run(T, weight=x.weight)
     ref = loss_ref.losses(x.h, x.C, x.codes, x.idx, same, T, 30.0, x.weight)
     compare(got, ref, False)
+
+
+@pytest.mark.parametrize("N", [3, 70])
+def test_teacher_of_nan(N):
+    """A list with NaN gives NaN in its row, one of nothing but NaN too, and in
+    no other row."""
+    x = Head(900, 8, 6, 2, 32, N, seed=25).teacher(6)
+    ref = loss_ref.losses(x.h, x.C, x.codes, x.idx, x.val, 1.3, 30.0)
+    x.val[0] = torch.nan
+    x.val[1, 3] = torch.nan
+    x.idx[1, :2] = -1
+    got = x.run(1.3)
+    assert got["loss"][:2].isnan().all() and got["dC"].isnan().any()
+    assert got["dh"][:2].isnan().all()
+    ok = {n: got[n][2:] for n in ("loss", "dh")}
+    compare(ok | {"lse": got["lse"][2:]}, {n: ref[n][2:] if n in ("loss", "lse", "dh", "dh_mag") else ref[n]
+                                           for n in ref}, False)
