@@ -61,14 +61,16 @@ struct CodeSrc {
 // loss_begin_kernel leaves kAmaxBlocks partial maxima of |C|; sdw follows them.
 constexpr int kAmaxBlocks = 128;
 
-// Largest power of two s (clamped to 2^-60 .. 2^60) with bound s < 2^14; 1 for
-// a bound that is zero, infinite or NaN.
+// Largest power of two s (clamped to 2^-114 .. 2^112) with bound s < 2^14; 1 for
+// a bound that is zero, infinite or NaN.  2^-114 serves the largest floats;
+// below 2^-98 the planes lose bits.  A product of two scales or their reciprocals
+// may leave float's range where what it scales does not.
 __device__ __forceinline__ float pow2_scale(float bound) {
   if (!(bound > 0.f) || !(bound <= FLT_MAX)) return 1.f;
   int e;
   frexpf(bound, &e);
   int k = 14 - e;
-  k = k < -60 ? -60 : (k > 60 ? 60 : k);
+  k = k < -114 ? -114 : (k > 112 ? 112 : k);
   return ldexpf(1.f, k);
 }
 

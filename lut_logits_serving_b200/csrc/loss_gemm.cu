@@ -496,10 +496,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       // next listed id at or after col0, its weight and log-sum-exp
       const bool in = row < g.rows;
       int li = 0, next = kNoId;
-      float f = 0.f, lse = 0.f, inv = 1.f;
+      float f = 0.f, lse = 0.f, inv = 1.f, inv2 = 1.f;
       if (MODE == kGemmDw) inv = 1.f / __ldg(g.amax + kAmaxBlocks);
-      if (MODE == kGemmDh && in) inv = 1.f / (scale_z(g.f[row]) * se);
-      if (LOGITS && in) inv = 1.f / (g.sh[row] * se);
+      if (MODE == kGemmDh && in) {         // one after the other, the smaller first
+        const float a = 1.f / scale_z(g.f[row]), b = 1.f / se;
+        inv = fminf(a, b);
+        inv2 = fmaxf(a, b);
+      }
+      if (LOGITS && in) inv = fminf(1.f / (g.sh[row] * se), FLT_MAX);
       if (LOGITS && in) {
         const int32_t *list = g.sid + (int64_t)row * g.k;
         const int want = g.v0 + col0;
@@ -695,7 +699,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (col0 + j < g.out_pitch) {
             float v[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) v[x] = acc[j + x] * inv;
+            for (int x = 0; x < 8; ++x) v[x] = acc[j + x] * inv * inv2;
             if (g.accumulate) {
 #pragma unroll
               for (int x = 0; x < 8; x += 4) {

@@ -104,7 +104,7 @@ __device__ float dw_scale(const DwPlanes &a) {
 }
 
 __device__ void dw_row(const DwPlanes &a, int64_t n, float sdw) {
-  const float f = a.f[n], s = f != 0.f ? sdw / scale_z(f) : 0.f;
+  const float f = a.f[n], s = f != 0.f ? fminf(sdw / scale_z(f), FLT_MAX) : 0.f;
   if (n == 0 && threadIdx.x == 0) *a.sdw = sdw;
   const int even = (a.ds + 1) & ~1;
   for (int i = threadIdx.x; i < a.M * even; i += blockDim.x) {

@@ -118,3 +118,25 @@ def test_teacher_of_nan(N):
     ok = {n: got[n][2:] for n in ("loss", "dh")}
     compare(ok | {"lse": got["lse"][2:]}, {n: ref[n][2:] if n in ("loss", "lse", "dh", "dh_mag") else ref[n]
                                            for n in ref}, False)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N", [4, 24, 90])
+def test_powers_of_two(N, dtype):
+    """Hidden states up and codebooks down by a power of two, and weights by
+    one: the same bits of the loss, gradients times the power."""
+    x = Head(2500, 16, 6, 2, 64, N, dtype, seed=26)
+    h, C = x.h, x.C
+    want = x.run(weight=x.weight)
+    for e in (83, -83, 30):
+        s = 2.0 ** e
+        x.h, x.C = (h.float() * s).to(dtype), C / s
+        got = x.run(weight=x.weight)
+        for n, f in (("loss", 1.0), ("lse", 1.0), ("dh", 1 / s), ("dC", s)):
+            assert torch.equal(got[n].double(), want[n].double() * f), (e, n)
+    x.h, x.C = h, C
+    for e in (-60, 40, 80):
+        s = 2.0 ** e
+        got = x.run(weight=x.weight * s)
+        for n in ("dh", "dC"):
+            assert torch.equal(got[n].double(), want[n].double() * s), (e, n)
