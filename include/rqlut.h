@@ -125,6 +125,7 @@ enum rq_status {
 /* Bits of the device error word. */
 #define RQ_DEVERR_TIMEOUT 0x1u  /* a bounded wait inside a kernel expired */
 #define RQ_DEVERR_BAD_ID  0x2u  /* rq_decode_rows saw an id outside [0,V), a loss one >= V */
+#define RQ_DEVERR_BAD_INDEX 0x4u  /* a loss's gradient met an index that is not of its sizes */
 
 /* Human-readable name of a status code (static string, never NULL). */
 RQ_API const char *rq_status_string(int status);
@@ -445,7 +446,8 @@ RQ_API int rq_prepare_rot10(const uint16_t *codes_u16, rq_dims d, uint8_t *out,
  *   dh      (device) [N][D] in h's type, or NULL; dC (device) float
  *           [M][L][K][ds], or NULL; at least one of the two.  Both are
  *           overwritten.
- *   index   (device) as written by rq_prepare_grad for the codes
+ *   index   (device) as written by rq_prepare_grad for the codes (anything else
+ *           gives wrong sums and, where its layout shows it, RQ_DEVERR_BAD_INDEX)
  *   ws      (device) >= rq_loss_workspace_bytes(d, N, fmt, k, grad) bytes,
  *           256-byte aligned, contents need no initialisation (k = 1 for
  *           cross entropy; grad = 1: enough for the gradient and the loss)

@@ -321,9 +321,9 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
   constexpr int kWarps = kGatherThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = a.x.K, g = a.x.lanes, gsh = __ffs(g) - 1, nb = a.buffers, nv = a.value_buffers;
-  unsigned char *units = smem;                                     // [nb] units
-  float *vals = reinterpret_cast<float *>(smem + nb * a.x.unit);   // [nv][kPairFloats]
-  float2 *stage = reinterpret_cast<float2 *>(vals + nv * kPairFloats);  // [levels][K]
+  float *vals = reinterpret_cast<float *>(smem);                   // [nv][kPairFloats]
+  unsigned char *units = smem + nv * kPairFloats * 4;              // [nb] units
+  float2 *stage = reinterpret_cast<float2 *>(units + nb * a.x.unit);  // [levels][K]
   __shared__ uint64_t bars[3 + 2 + 2];        // units, values, steps done (all warps)
   __shared__ volatile int abort_flag;
   auto ubar = [&](int i) { return smem_addr(&bars[i]); };
@@ -379,6 +379,13 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
   }
   int t = 0, vt = 0, ub = 0;     // steps and blocks so far; the step's unit buffer
   uint32_t uphase = 0;           // and its phase
+  // What the index names is held to its places, so that one that rq_prepare_grad
+  // did not write for these sizes gives wrong sums and mostly an error, but no
+  // access out of bounds.  An entry's two low bits do not count, and the values
+  // come first in shared memory that goes on as far as 16 bits reach (a minimum
+  // per entry took 2 % of a step); a slice's end is one compare (a minimum there,
+  // in the way of the loop's length, 8 % of this kernel; so 1 % or less).
+  const int steps = (int)((a.x.unit - a.x.entry_at) / 128);   // rows of 64 entries
   bool ok = true;
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (ok && !mbar_try_wait(bar, parity) && !mbar_wait_bounded(bar, parity)) {
@@ -415,15 +422,19 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
           float2 *st = stage + (size_t)(l - q.l0) * K;
           // one word of entries: two rows of either value row
           auto add = [&](uint32_t w, float &s0, float &s1) {
-            const float2 x = lds_f32x2(v0 + (w & 0xFFFFu) * 2), y = lds_f32x2(v0 + (w >> 16) * 2);
+            const float2 x = lds_f32x2(v0 + (w & 0xFFFCu) * 2), y = lds_f32x2(v0 + (w >> 18) * 8);
             s0 += x.x;
             s1 += x.y;
             s0 += y.x;
             s1 += y.y;
           };
-          const int full = over[0];
+          const int full = min((int)over[0], a.x.most);
           for (int sl = warp; sl < a.x.slices; sl += kWarps) {
-            const int e0 = off[sl], n = off[sl + 1] - e0;
+            const int e0 = off[sl], e1 = off[sl + 1], n = e1 - e0;
+            if (e1 > steps) {
+              if (lane == 0) atomicOr(a.err, RQ_DEVERR_BAD_INDEX);
+              break;
+            }
             uint32_t e = entry + (uint32_t)e0 * 128;
             const int s = (sl * 32 + lane) >> gsh;
             float s0 = 0.f, s1 = 0.f;
@@ -440,15 +451,16 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
               const uint32_t w0 = lds_b32<0>(e), w1 = lds_b32<128>(e);
               add(w0, s0, s1);
               add(w1, s0, s1);
+              i += 2;
               e += 256;
             }
-            if (n & 1) add(lds_b32<0>(e), s0, s1);
+            if (i < n) add(lds_b32<0>(e), s0, s1);
             for (int o = g >> 1; o > 0; o >>= 1) {
               s0 += __shfl_xor_sync(0xffffffffu, s0, o);
               s1 += __shfl_xor_sync(0xffffffffu, s1, o);
             }
             if ((lane & (g - 1)) == 0 && s < K) {
-              const int c = code[s];
+              const int c = min((int)code[s], K - 1);
               if (b > q.b0) {
                 const float2 d = st[c];
                 s0 += d.x;
@@ -460,11 +472,12 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
             const int f1 = (sl + 1) * 32 >> gsh;
             for (int f = sl * 32 >> gsh; f < f1 && f < full; ++f) {
               __syncwarp();
-              const uint16_t *rest =
-                  reinterpret_cast<const uint16_t *>(un + a.x.entry_at) + off[a.x.slices] * 64;
+              const int at = min((int)off[a.x.slices], steps) * 64;
+              const uint16_t *rest = reinterpret_cast<const uint16_t *>(un + a.x.entry_at) + at;
+              const int end = min((int)over[2 + f], steps * 64 - at);
               float r0 = 0.f, r1 = 0.f;
-              for (int k = over[1 + f] + lane; k < over[2 + f]; k += 32) {
-                const float2 x = lds_f32x2(v0 + rest[k] * 2u);
+              for (int k = over[1 + f] + lane; k < end; k += 32) {
+                const float2 x = lds_f32x2(v0 + (rest[k] & 0xFFFCu) * 2);
                 r0 += x.x;
                 r1 += x.y;
               }
@@ -474,8 +487,9 @@ __global__ void __launch_bounds__(kGatherThreads, 1) codebook_gather_kernel(cons
                 r1 += __shfl_xor_sync(0xffffffffu, r1, o);
               }
               if (lane == 0) {
-                const float2 d = st[code[f]];
-                st[code[f]] = make_float2(d.x + r0, d.y + r1);
+                const int c = min((int)code[f], K - 1);
+                const float2 d = st[c];
+                st[c] = make_float2(d.x + r0, d.y + r1);
               }
             }
           }
@@ -677,6 +691,8 @@ GatherPlan gather_plan(const IndexShape &x, int blocks, int sources, int pairs, 
   p.buffers = levels > 1 && bytes(levels, 3) <= kGatherSmemMax ? 3 : 2;
   p.value_buffers = bytes(levels, p.buffers) <= kGatherSmemMax ? 2 : 1;
   p.smem = bytes(levels, p.buffers, p.value_buffers);
+  const size_t reach = (size_t)(p.value_buffers - 1) * kPairFloats * 4 + 65536 * 2;
+  if (p.smem < reach) p.smem = reach;      // (of any 16-bit entry in the last buffer)
   p.splits = 1;
   if (p.units < 148) {
     const int64_t n = 148 / p.units;

@@ -140,3 +140,32 @@ def test_powers_of_two(N, dtype):
         got = x.run(weight=x.weight * s)
         for n in ("dh", "dC"):
             assert torch.equal(got[n].double(), want[n].double() * s), (e, n)
+
+
+# V, M, ds, L, K: lists shared by lanes, by level, three unit buffers, one value buffer
+@pytest.mark.parametrize("c", [(9000, 16, 6, 2, 256), (9000, 5, 3, 2, 40), (9001, 160, 4, 2, 1024),
+                               (9001, 2, 4, 1, 4096), (700, 8, 6, 1, 64)])
+@pytest.mark.parametrize("N", [4, 70])
+def test_index_of_other_sizes(c, N):
+    """An index that is none of these codes': an error, and the next call as ever."""
+    V, M, ds, L, K = c
+    x = Head(V, M, ds, L, K, N, seed=27)
+    want, mine = x.run(), x.index
+    other = Head(V, M, ds, L, 2 * K if K < 4096 else K // 2, 1, seed=28).index
+    n = mine.numel()
+    g = torch.Generator("cuda").manual_seed(2)
+    for name, index in (("ones", torch.full_like(mine, 255)),
+                        ("noise", torch.randint(0, 256, (n,), generator=g, device="cuda", dtype=torch.uint8)),
+                        ("other", torch.cat([other, mine])[:n].contiguous()),
+                        ("shifted", torch.roll(mine, 2)), ("zeros", torch.zeros_like(mine))):
+        x.index = index
+        got = x.run()
+        torch.cuda.synchronize()
+        err = rq.rq_device_error()
+        assert err in ((4,) if name in ("ones", "noise") else (0, 4)), (name, err)
+        assert torch.equal(got["loss"], want["loss"])
+    x.index = mine
+    got = x.run()
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
+    assert rq.rq_device_error() == 0
