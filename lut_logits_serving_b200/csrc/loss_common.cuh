@@ -124,7 +124,7 @@ struct GemmArgs {
   int L;
   // epilogues
   float inv_cap, cap, beta;
-  float2 *stat;              // [parts][stat_ld] (max, sum), base 2
+  float2 *stat;              // [parts][stat_ld] (max of y / T, sum of exp(y / T - max))
   int stat_ld;
   int stat_part0;            // first part of this launch
   const float *lse, *f;      // per row: log-sum-exp, w T (0: no gradient)
