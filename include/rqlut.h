@@ -457,10 +457,10 @@ RQ_API int rq_prepare_rot10(const uint16_t *codes_u16, rq_dims d, uint8_t *out,
  * for float h, dh carry fp32 accuracy; a bf16 dh is rounded once.  Sums run in
  * a fixed order: the same call gives the same bits.
  * Errors: RQ_ERR_INVALID_ARGUMENT (null pointer, N < 1, k, T or h_bf16 out of
- * range, bad dims or format, an output or ws that overlaps another argument),
- * RQ_ERR_UNSUPPORTED (the format cannot hold the
- * shape, k > 1024; gradients: K > 4096), RQ_ERR_MISALIGNED,
- * RQ_ERR_WORKSPACE_TOO_SMALL, RQ_ERR_CUDA.
+ * range, a positive softcap that is infinite or has an infinite reciprocal, bad
+ * dims or format, an output or ws that overlaps another argument),
+ * RQ_ERR_UNSUPPORTED (the format cannot hold the shape, k > 1024; gradients:
+ * K > 4096), RQ_ERR_MISALIGNED, RQ_ERR_WORKSPACE_TOO_SMALL, RQ_ERR_CUDA.
  */
 RQ_API size_t rq_loss_workspace_bytes(rq_dims d, int N, int fmt, int k, int grad);
 RQ_API int rq_xent(const void *h, int h_bf16, const float *C, const void *codes, int fmt,

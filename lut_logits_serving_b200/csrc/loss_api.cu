@@ -552,6 +552,8 @@ int check(const Problem &q, const void *ws) {
   if (q.t.k < 1 || q.t.k > q.d.V) return RQ_ERR_INVALID_ARGUMENT;
   if (!(q.t.T > 0.f) || !(q.t.T <= FLT_MAX) || !(q.t.beta > 0.f) || !(q.t.beta <= FLT_MAX))
     return RQ_ERR_INVALID_ARGUMENT;
+  // cap tanh(z / cap) needs either factor finite
+  if (q.cap > 0.f && !(q.cap <= FLT_MAX && 1.f / q.cap <= FLT_MAX)) return RQ_ERR_INVALID_ARGUMENT;
   if (rq_codes_bytes(q.d, q.fmt) == 0 || q.t.k > kMaxList) return RQ_ERR_UNSUPPORTED;
   if (!aligned(q.h, q.bf16 ? 2 : 4) || !aligned(q.C, 4) || !aligned(q.codes, 16) ||
       !aligned(q.t.id, 4) || (q.t.val && !aligned(q.t.val, 4)) || (ws && !aligned(ws, 256)))

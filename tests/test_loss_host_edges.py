@@ -145,3 +145,22 @@ def test_current_stream_without_torch_s_private_name(monkeypatch):
     assert rq._stream(None).value == 0x4560
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
     assert rq._stream(None).value == 0x1230 and rq._stream(stream).value == 0x1230
+
+
+def test_softcaps_without_a_finite_value_are_refused():
+    """cap tanh(z / cap) of an infinite cap is infinity times 0, of one whose
+    reciprocal is infinite a NaN at z = 0; none or a negative one is off."""
+    import ctypes
+    a, null = ctypes.c_void_p(0x100000), ctypes.c_void_p(None)
+    d = rq.dims(4096, 192, 32, 2, 256)
+
+    def xent(cap):
+        return rq.lib().rq_xent(a, 0, a, a, 0, d, 8, cap, a, a, a, null, 0, null)
+
+    def xent_grad(cap):
+        return rq.lib().rq_xent_grad(a, 0, a, a, 0, d, 8, cap, a, a, null, a, a, a, null, 0, null)
+
+    for f in (xent, xent_grad):
+        assert f(float("inf")) == 1 and f(1e-39) == 1
+        for cap in (30.0, 0.0, -1.0, -float("inf"), 1e-37, 3e38):
+            assert f(cap) == 3, cap                     # on to the missing workspace
